@@ -230,6 +230,21 @@ int rx_step_finish(rx_radix* t, int32_t batch, const int32_t* tokens, const int6
                    const rx_node* last_nodes, const void* h_stage, const rx_step_layout* layout,
                    int64_t evict_tokens, int64_t* out_evicted);
 
+/* Change the pool's size to new_num_slots (1 .. 2^31-1), keeping everything cached.
+ * Growing appends the new slots to the free list in ascending order.  Shrinking takes the slots
+ * from new_num_slots on out of the allocator; cached tokens that sit there move to free slots below
+ * (moved slots in ascending order get the usable free slots in free-list order), and the moves are
+ * returned for kv_pool_copy (page size 1) to carry out in the pools of every layer: out_src[i] ->
+ * out_dst[i], i < *out_n; a destination was free, so no destination is a source.  The free list
+ * keeps the order of what is left.  The tree names the new slots at once, so the copy has to be
+ * enqueued before any kernel that uses a later match (on the same stream).
+ *  - RX_EINVAL and no change if cap < the moves needed (*out_n receives that number; out_src, out_dst
+ *    may be NULL with cap 0), or a slot to be removed is held by the caller (allocated, not inserted).
+ *  - RX_ELOCKED and no change if a token to be moved belongs to a pinned node (a step in flight).
+ *  - RX_ENOMEM and no change if fewer free slots are left below than tokens have to move: evict
+ *    first. */
+int radix_resize(rx_radix* t, int64_t new_num_slots, int32_t* out_src, int32_t* out_dst, int64_t cap, int64_t* out_n);
+
 int radix_stats(const rx_radix* t, rx_stats* out);
 
 /* Check the tree's invariants (edges, parents, slot ownership, stamps, locks);
@@ -270,6 +285,107 @@ int kv_pool_write(const rx_attn_desc* desc, int32_t batch,
                   void* d_k_pool, void* d_v_pool,
                   int32_t* d_req_to_token, int64_t r2t_stride, int64_t total_new,
                   int32_t* d_status, void* stream);
+
+/* Rotary positions.  Channels are turned in pairs: pair i of a query or key row (0 <= i <
+ * rot_dim / 2) is (a, b) = channels (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `interleaved`, and
+ * becomes (a cos t - b sin t, b cos t + a sin t) with t = position * w_i, w_i = base^(-2 i /
+ * rot_dim) or inv_freq[i].  Channels from rot_dim on are not turned.  A token has n_axes positions
+ * (text: one; images and video: time, height, width) and pair i takes the position of one axis:
+ * sections[a] pairs take axis a, in blocks (the first sections[0] pairs axis 0, the next axis 1,
+ * ...), or with `cyclic` in turn (axis 0, 1, ..., n_axes - 1, 0, ...; an axis that has its share
+ * drops out).  inv_freq (host, [rot_dim / 2], optional) is read during the call only. */
+#define RX_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t n_axes;              /* 1 .. RX_ROPE_MAX_AXES */
+    int32_t rot_dim;             /* a multiple of 16, at most head_dim */
+    int32_t sections[RX_ROPE_MAX_AXES];   /* pairs of each axis, together rot_dim / 2 */
+    int32_t cyclic, interleaved;
+    double base;                 /* > 0; not used with inv_freq */
+    const double* inv_freq;
+} rx_rope_desc;
+
+/* kv_pool_write for rows whose rotary positions are still to be applied: turns the new keys on
+ * their way into the pool, copies the new values, turns the queries, and builds the slot table,
+ * in one launch (decode steps of one token per request and whole prompts alike).
+ * The batch, slot lists, pools, table and their errors are those of kv_pool_write; d_req_to_token
+ * NULL makes no table, and d_new_slots NULL writes no pool (then no table either): only rows are
+ * turned.  Rows are [T, hq | hkv, head_dim] with the heads of a row contiguous and `stride` elements
+ * between rows, so that they can be parts of one projection's output; strides and addresses are
+ * multiples of 16 bytes.  d_positions: int32 [n_axes, pos_stride], entry (a, t) the position of row
+ * t along axis a; any 32-bit value, negative ones too.
+ *  - d_q -> d_q_out (both or neither): may be the same rows (same address and stride: in place);
+ *    d_k_out, optional: the turned keys as rows too (needed where no pool is written), likewise in
+ *    place or apart.  Otherwise no output may overlap an input.
+ *  - Rows before qo_indptr[0] and from qo_indptr[batch] on (a padded batch) are left as they were;
+ *    qo_indptr[batch] > total_new is RX_DEV_BAD_LENGTH, and the rows up to total_new are done.
+ *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, that row's pool entries are not written.
+ *  - Two rows with the same slot: that slot holds parts of either.
+ * Angles are exact but for the rounding of the frequency to double (2^-52 of the angle) and of the
+ * reduced angle to float (2^-25 turn); results are rounded once from 32 bits. */
+int kv_pool_write_rope(const rx_attn_desc* desc, const rx_rope_desc* rope, int32_t batch,
+                       const int32_t* d_prefix_slots, const int64_t* d_prefix_indptr,
+                       const int32_t* d_new_slots, const int64_t* d_qo_indptr,
+                       const int32_t* d_positions, int64_t pos_stride,
+                       const void* d_q, int64_t q_stride, const void* d_k_new, int64_t k_stride,
+                       const void* d_v_new, int64_t v_stride,
+                       void* d_q_out, int64_t q_out_stride, void* d_k_out, int64_t k_out_stride,
+                       void* d_k_pool, void* d_v_pool,
+                       int32_t* d_req_to_token, int64_t r2t_stride, int64_t total_new,
+                       int32_t* d_status, void* stream);
+
+/* Copy pages of KV pools to other pages of the same pools: for every i < n and every pool,
+ * page d_dst[i] = page d_src[i], page x being the page_size slots from x * page_size on (page_size
+ * 1: slots).  The mover of compaction (radix_resize makes the lists), of a copied prefix, of
+ * anything that takes cached tokens to other slots; one launch for the pools of all layers (per
+ * 256 of them).  pools: HOST array of n_pools device addresses (each layer's K pool and V pool; all
+ * different), read during the call only; each pool is [num_slots, hkv, head_dim].
+ *  - A source may be named more than once.  Destinations are named once each and are nobody's
+ *    source (but its own: src == dst is left alone): the copies run at the same time.
+ *  - A page outside [0, num_slots / page_size): RX_DEV_BAD_SLOT, that pair is skipped. */
+int kv_pool_copy(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, int64_t page_size, int64_t n,
+                 const int32_t* d_src, const int32_t* d_dst, int32_t* d_status, void* stream);
+
+/* Fork sequences: build the slot tables of n_rows sequences that continue others -- answers sampled
+ * from one prompt, beams that part -- from the table their parents are in, and copy the K/V of the
+ * tokens that they do not share.  Output row f continues row parents[f] of d_r2t_in [in_rows,
+ * in_stride]: its first keep_lens[f] tokens keep the parent's slots, its tokens keep_lens[f] ..
+ * kv_lens[f] - 1 get the slots d_tail_slots[d_tail_indptr[f] : d_tail_indptr[f+1]] and in every pool
+ * a copy of the parent's K/V rows, and entries from kv_lens[f] on are -1.  (With pages of p slots a
+ * child keeps its parent's whole pages, keep_lens = len - len % p, and copies the last; kv_lens ==
+ * keep_lens copies nothing.)  d_r2t_out: [n_rows, out_stride], which may not overlap d_r2t_in.
+ * pools as for kv_pool_copy; n_pools may be 0 (tables only).  total_tail (host) >=
+ * d_tail_indptr[n_rows].  Tail slots are named once each and hold no row that is read.
+ *  - A parent or length that does not fit the tables or the tail list: RX_DEV_BAD_LENGTH, that row
+ *    becomes -1 and its rows are not copied.
+ *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, -1 in the table, that row is not copied. */
+int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, int32_t n_rows,
+                 const int32_t* d_parents, const int32_t* d_keep_lens, const int32_t* d_kv_lens,
+                 const int64_t* d_tail_indptr, const int32_t* d_tail_slots,
+                 const int32_t* d_r2t_in, int32_t in_rows, int64_t in_stride,
+                 int32_t* d_r2t_out, int64_t out_stride, int64_t total_tail, int32_t* d_status, void* stream);
+
+/* Attention over whole prompts that have no cached prefix, straight from the projections' rows (no
+ * pool, no slot table): row i of sequence b, rows indptr[b] + 0 .. n_b - 1 with n_b = indptr[b+1] -
+ * indptr[b], computes per query head
+ *   o = softmax(scale * q K[0..i]^T) V[0..i]
+ * over the rows of its own sequence (packed sequences of different lengths; lengths of 0 and 1
+ * included); query head h reads kv head h / (hq / hkv), any ratio.  d_q: [total, hq, head_dim], d_k,
+ * d_v: [total, hkv, head_dim], d_out: [total, hq, head_dim], each with the heads of a row contiguous
+ * and its own stride in elements between rows (multiples of 16 bytes, as the addresses are); d_lse:
+ * optional [total, hq] float32 natural-log log-sum-exp.  d_out overlaps no input.
+ * bf16 runs on tcgen05 tensor cores (sm_103a), f32 on CUDA cores in 32-bit arithmetic; softmax
+ * statistics and sums are 32-bit.  No workspace; calls on several streams, or captured into graphs
+ * that run at once, share nothing.
+ *  - A row's result depends on rows 0..i of its own sequence alone: an infinity or NaN in another
+ *    row, or in rows that no sequence has, does not reach it.
+ *  - Rows before indptr[0] and from indptr[batch] on are left as they were.
+ *  - indptr [batch+1] must not decrease and lie in [0, total] (total <= 2^31-1 rows): a sequence that
+ *    does not is RX_DEV_BAD_LENGTH and is skipped.
+ *  - scale is finite and not negative (RX_EINVAL). */
+int prompt_attention(const rx_attn_desc* desc, int32_t batch, const void* d_q, int64_t q_stride,
+                     const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride,
+                     const int64_t* d_indptr, void* d_out, int64_t out_stride, float* d_lse, int64_t total,
+                     int32_t* d_status, void* stream);
 
 /* Optional description of requests that share a leading run of KV (a cached prefix), for
  * decode_attention and prefix_extend_attention.  Members of group g have identical

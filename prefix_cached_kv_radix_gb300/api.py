@@ -19,6 +19,7 @@ RX_OK, RX_EINVAL, RX_ENOMEM, RX_ECUDA, RX_ELOCKED, RX_ETIMEOUT, RX_EDEVICE = 0, 
 RX_DEV_OK, RX_DEV_BAD_SLOT, RX_DEV_BAD_LENGTH, RX_DEV_TIMEOUT = 0, 1, 2, 3
 RX_F32, RX_BF16 = 0, 1
 RX_DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20   # include/radix_attn.h
+RX_ROPE_MAX_AXES = 4
 
 EXPORTS = ("radix_create", "radix_destroy", "match_prefix", "match_prefix_len", "match_prefix_len_batch", "radix_set_page_size",
            "radix_lock", "radix_unlock", "alloc_slots",
@@ -28,7 +29,7 @@ EXPORTS = ("radix_create", "radix_destroy", "match_prefix", "match_prefix_len", 
            "rx_step_workspace_bytes", "rx_step_launch", "rx_step_prefetch", "rx_step_ranges", "rx_stage_wait", "rx_step_run",
            "kv_pool_write", "prefix_extend_attention", "extend_workspace_bytes", "decode_workspace_bytes",
            "decode_attention",
-           "decode_attention_noalloc",
+           "decode_attention_noalloc", "kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention", "radix_resize",
            "rx_last_error", "rx_version", "rx_wait_selftest", "rx_set_tracing")
 
 
@@ -41,6 +42,12 @@ class RxError(RuntimeError):
 class rx_attn_desc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("num_slots", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class rx_rope_desc(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("sections", ctypes.c_int32 * RX_ROPE_MAX_AXES),
+                ("cyclic", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("base", ctypes.c_double),
+                ("inv_freq", ctypes.c_void_p)]
 
 
 class rx_stats(ctypes.Structure):
@@ -141,6 +148,12 @@ def load(path: str = LIB_PATH):
         "decode_workspace_bytes": (SZ, [P, I32, I32, P]),
         "decode_attention": (ctypes.c_int, [P, I32, P, P, I64, P, P, P, P, P, P, I32, P, SZ, P, P]),
         "decode_attention_noalloc": (ctypes.c_int, [P, I32, P, P, I64, P, P, P, P, P, P, I32, P, P]),
+        "kv_pool_write_rope": (ctypes.c_int, [P, P, I32, P, P, P, P, P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, P, I64,
+                                              I64, P, P]),
+        "kv_pool_copy": (ctypes.c_int, [P, I32, P, I64, I64, P, P, P, P]),
+        "kv_pool_fork": (ctypes.c_int, [P, I32, P, I32, P, P, P, P, P, P, I32, I64, P, I64, I64, P, P]),
+        "prompt_attention": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, P, P, I64, P, I64, P, P]),
+        "radix_resize": (ctypes.c_int, [P, I64, P, P, I64, P]),
         "rx_last_error": (ctypes.c_char_p, []),
         "rx_version": (ctypes.c_char_p, []),
         "rx_wait_selftest": (ctypes.c_int, [P, U64, P]),
@@ -369,6 +382,17 @@ def radix_shared_groups(tree, last_nodes, min_shared: int = 1):
     return gof[:b].copy(), glen[: ng.value].copy()
 
 
+def radix_resize(tree, num_slots: int):
+    """Grow or shrink the pool.  Returns (src, dst): the slots whose K/V rows kv_pool_copy has to
+    move (page size 1) before a later match is used."""
+    st = radix_stats(tree)
+    cap = max(0, min(st["cached_tokens"], st["num_slots"] - num_slots))
+    src, dst = np.empty(max(cap, 1), np.int32), np.empty(max(cap, 1), np.int32)
+    n = I64()
+    _check("radix_resize", load().radix_resize(tree, num_slots, _addr(src), _addr(dst), cap, ctypes.byref(n)))
+    return src[: n.value].copy(), dst[: n.value].copy()
+
+
 def rx_step_stage_bytes(batch: int, total_tokens: int) -> int:
     return int(load().rx_step_stage_bytes(batch, total_tokens))
 
@@ -538,6 +562,11 @@ class RadixTree:
     def unlock_batch(self, nodes):
         return radix_unlock_batch(self.h, nodes)
 
+    def resize(self, num_slots):
+        moves = radix_resize(self.h, num_slots)
+        self.num_slots = num_slots
+        return moves
+
     def stats(self):
         return radix_stats(self.h)
 
@@ -609,3 +638,137 @@ def decode_attention_noalloc(desc, batch, q, req_to_token, kv_lens, k_pool, v_po
         ctypes.byref(desc), batch, _ptr(q), _ptr(req_to_token), stride, _ptr(kv_lens),
         ctypes.byref(groups) if groups is not None else None, _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(lse),
         max_kv_len, _ptr(status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- rows, pages, prompts
+_NBYTES = {RX_F32: 4, RX_BF16: 2}
+_INTS = {"torch.int32": 4, "torch.int64": 8}
+
+
+def _rows(name, t, heads: int, desc, total: int):
+    """(address, elements between rows) of rows [>= total, heads, head_dim] of the descriptor's
+    type, the heads of a row contiguous; the rows may be part of wider ones."""
+    if t is None:
+        return None, 0
+    d = desc.head_dim
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or t.element_size() != _NBYTES[desc.dtype] or not t.is_floating_point():
+        raise ValueError(f"{name}: not rows of the descriptor's type on a CUDA device")
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < total or stride[2] != 1 or \
+            (heads > 1 and stride[1] != d):
+        raise ValueError(f"{name}: shape {tuple(shape)}, strides {stride}: want [{total}, {heads}, {d}] with contiguous heads")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+
+
+def _ints(name, t, size: int, count: int):
+    """Address of a contiguous device array of `count` or more integers of `size` bytes (or a
+    device address as it is)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or _INTS.get(str(t.dtype)) != size or not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name}: want {count} contiguous int{8 * size} on a CUDA device")
+    return t.data_ptr()
+
+
+def _here(*tensors):
+    """Every tensor on the current device: the launch goes there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _pool_list(desc, pools):
+    n = desc.num_slots * desc.hkv * desc.head_dim
+    for p in pools:
+        if not p.is_cuda or not p.is_contiguous() or p.numel() != n or p.element_size() != _NBYTES[desc.dtype]:
+            raise ValueError("pools: want contiguous [num_slots, hkv, head_dim] of the descriptor's type on a CUDA device")
+    return (ctypes.c_void_p * max(len(pools), 1))(*[p.data_ptr() for p in pools])
+
+
+def rope_desc(sections, base: float = 10000.0, cyclic: bool = False, interleaved: bool = False, inv_freq=None) -> rx_rope_desc:
+    """Rotary positions: sections[a] channel pairs take position axis a (one entry: text).  base, or
+    the pairs' frequencies themselves in inv_freq.  See include/radix_attn.h."""
+    sections = [sections] if isinstance(sections, int) else [int(x) for x in sections]
+    if not 1 <= len(sections) <= RX_ROPE_MAX_AXES:
+        raise ValueError(f"rope_desc: 1 to {RX_ROPE_MAX_AXES} axes")
+    r = rx_rope_desc(len(sections), 2 * sum(sections), (ctypes.c_int32 * RX_ROPE_MAX_AXES)(*sections), int(cyclic),
+                     int(interleaved), float(base), None)
+    if inv_freq is not None:
+        f = np.ascontiguousarray(np.asarray(inv_freq, np.float64))
+        if f.shape != (sum(sections),):
+            raise ValueError("rope_desc: one frequency per channel pair")
+        r.inv_freq = f.ctypes.data
+        r._keep = f                      # the descriptor points into it
+    return r
+
+
+def kv_pool_write_rope(desc, rope, batch, prefix_slots, prefix_indptr, new_slots, qo_indptr, positions, q, k_new, v_new, q_out,
+                       k_out, k_pool, v_pool, req_to_token, total_new, status, stream=None, r2t_stride=None) -> None:
+    """kv_pool_write with rotary positions: turned keys and the values into the pools, turned
+    queries into q_out (may be q; q and q_out may be None), optionally turned keys into k_out (may be
+    k_new), and the slot table.  positions: int32 [axes, >= total_new].  new_slots None writes no
+    pool, req_to_token None makes no table.  Rows may be parts of wider ones (strided)."""
+    qa, qs = _rows("q", q, desc.hq, desc, total_new)
+    oa, os_ = _rows("q_out", q_out, desc.hq, desc, total_new)
+    ka, ks = _rows("k_new", k_new, desc.hkv, desc, total_new)
+    va, vs = _rows("v_new", v_new, desc.hkv, desc, total_new)
+    xa, xs = _rows("k_out", k_out, desc.hkv, desc, total_new)
+    if positions.dim() != 2 or positions.shape[0] != rope.n_axes or positions.shape[1] < total_new:
+        raise ValueError(f"positions: want [{rope.n_axes}, {total_new}]")
+    pool_rows = desc.num_slots if new_slots is not None else 0
+    kp, _ = _rows("k_pool", k_pool, desc.hkv, desc, pool_rows)
+    vp, _ = _rows("v_pool", v_pool, desc.hkv, desc, pool_rows)
+    if any(x is not None and not x.is_contiguous() for x in (k_pool, v_pool)):
+        raise ValueError("pools: not contiguous")
+    stride = 0
+    if req_to_token is not None:
+        stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride
+    _here(k_new, positions, qo_indptr, k_pool, q, status)
+    _check("kv_pool_write_rope", load().kv_pool_write_rope(
+        ctypes.byref(desc), ctypes.byref(rope), batch, _ints("prefix_slots", prefix_slots, 4, 0),
+        _ints("prefix_indptr", prefix_indptr, 8, batch + 1), _ints("new_slots", new_slots, 4, total_new),
+        _ints("qo_indptr", qo_indptr, 8, batch + 1), _ints("positions", positions, 4, 0), positions.shape[1], qa, qs, ka, ks,
+        va, vs, oa, os_, xa, xs, kp, vp, _ints("req_to_token", req_to_token, 4, batch * stride), stride, total_new,
+        _ints("status", status, 4, 1), _stream(stream)))
+
+
+def kv_pool_copy(desc, pools, src, dst, page_size, status, stream=None) -> None:
+    """Pages of every pool to other pages of the same pool: pool[dst[i]] = pool[src[i]] (pages of
+    page_size slots).  pools: the layers' K and V pools."""
+    if src.numel() != dst.numel():
+        raise ValueError("src, dst: one destination per source")
+    _here(src, dst, status, *pools)
+    _check("kv_pool_copy", load().kv_pool_copy(
+        ctypes.byref(desc), len(pools), _pool_list(desc, pools), page_size, src.numel(), _ints("src", src, 4, 0),
+        _ints("dst", dst, 4, 0), _ints("status", status, 4, 1), _stream(stream)))
+
+
+def kv_pool_fork(desc, pools, parents, keep_lens, kv_lens, tail_indptr, tail_slots, r2t_in, r2t_out, total_tail, status,
+                 stream=None) -> None:
+    """Slot tables (and copied K/V rows) of sequences that continue others: row f of r2t_out keeps
+    the first keep_lens[f] slots of row parents[f] of r2t_in and has its own tail slots, holding
+    copies, up to kv_lens[f]."""
+    n = r2t_out.shape[0]
+    _here(parents, r2t_in, r2t_out, status, *pools)
+    _check("kv_pool_fork", load().kv_pool_fork(
+        ctypes.byref(desc), len(pools), _pool_list(desc, pools), n, _ints("parents", parents, 4, n),
+        _ints("keep_lens", keep_lens, 4, n), _ints("kv_lens", kv_lens, 4, n), _ints("tail_indptr", tail_indptr, 8, n + 1),
+        _ints("tail_slots", tail_slots, 4, total_tail), _ints("r2t_in", r2t_in, 4, 0), r2t_in.shape[0], r2t_in.shape[1],
+        _ints("r2t_out", r2t_out, 4, 0), r2t_out.shape[1], total_tail, _ints("status", status, 4, 1), _stream(stream)))
+
+
+def prompt_attention(desc, batch, q, k, v, indptr, out, lse, total, status, stream=None) -> None:
+    """Causal attention over packed prompts, each row over rows 0.. itself of its own sequence
+    (rows indptr[b] .. indptr[b+1]-1), straight from the projections' rows; rows may be strided."""
+    qa, qs = _rows("q", q, desc.hq, desc, total)
+    ka, ks = _rows("k", k, desc.hkv, desc, total)
+    va, vs = _rows("v", v, desc.hkv, desc, total)
+    oa, os_ = _rows("out", out, desc.hq, desc, total)
+    if lse is not None and (not lse.is_contiguous() or lse.numel() < total * desc.hq or lse.element_size() != 4):
+        raise ValueError(f"lse: want contiguous float32 [{total}, {desc.hq}]")
+    _here(q, k, v, out, indptr, status)
+    _check("prompt_attention", load().prompt_attention(
+        ctypes.byref(desc), batch, qa, qs, ka, ks, va, vs, _ints("indptr", indptr, 8, batch + 1), oa, os_,
+        None if lse is None else lse.data_ptr(), total, _ints("status", status, 4, 1), _stream(stream)))

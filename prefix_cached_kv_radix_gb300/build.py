@@ -25,7 +25,7 @@ LIB_NAME = "libradixattn.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 
 CU_SOURCES = ["kv_pool_write.cu", "attention_simt.cu", "extend_attention.cu", "decode_attention.cu", "step_runtime.cu",
-              "wait_selftest.cu"]
+              "wait_selftest.cu", "kv_pool_rope.cu", "kv_pool_move.cu", "prompt_simt.cu", "prompt_attention.cu"]
 CPP_SOURCES = ["radix_tree.cpp"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 # the per-step marshalling as a CPython extension (optional: the ctypes binding does the same)

@@ -971,6 +971,79 @@ int rx_step_finish(rx_radix* t, int32_t batch, const int32_t* tokens, const int6
     return radix_unlock_batch(t, last_nodes, batch);
 }
 
+int radix_resize(rx_radix* t, int64_t new_num_slots, int32_t* out_src, int32_t* out_dst, int64_t cap, int64_t* out_n) {
+    RX_TRACE("radix_resize");
+    RX_REQUIRE(t && out_n && cap >= 0 && (cap == 0 || (out_src && out_dst)), "radix_resize: bad arguments");
+    RX_REQUIRE(new_num_slots >= 1 && new_num_slots <= INT32_MAX, "radix_resize: num_slots %lld out of range",
+               (long long)new_num_slots);
+    *out_n = 0;
+    const int64_t old = t->num_slots, n = new_num_slots;
+    try {
+        // each cached token to be moved: its slot, and where its node keeps it
+        struct Moved {
+            int32_t slot;
+            int32_t* place;
+        };
+        std::vector<Moved> moved;
+        std::vector<rx::Node*> stack;
+        std::vector<int32_t> ring;      // the free slots that stay, in order
+        ring.reserve((size_t)std::max(old, n));
+        std::vector<uint8_t> is_free((size_t)n, 0);
+        int64_t gone = 0;               // free slots that are removed
+        for (int64_t i = 0; i < t->count; ++i) {
+            const int32_t s = t->ring[(size_t)t->ring_pos(i)];
+            if (s < n) ring.push_back(s);
+            else ++gone;
+        }
+        if (n < old) {
+            bool locked = false;
+            stack.push_back(&t->root);
+            while (!stack.empty()) {
+                rx::Node* x = stack.back();
+                stack.pop_back();
+                for (int32_t& s : x->slots)
+                    if (s >= n) {
+                        moved.push_back({s, &s});
+                        locked |= x->ref > 0;
+                    }
+                x->children.for_each([&](int32_t, rx::Node* c) { stack.push_back(c); });
+            }
+            RX_REQUIRE((int64_t)moved.size() + gone == old - n, "radix_resize: %lld slots from %lld on are held by the caller",
+                       (long long)(old - n - gone - (int64_t)moved.size()), (long long)n);
+            if (locked) {
+                set_error("radix_resize: tokens to be moved belong to pinned nodes");
+                return RX_ELOCKED;
+            }
+            if (moved.size() > ring.size()) {
+                set_error("radix_resize: %zu tokens to move, %zu free slots below %lld", moved.size(), ring.size(), (long long)n);
+                return RX_ENOMEM;
+            }
+            *out_n = (int64_t)moved.size();
+            RX_REQUIRE((int64_t)moved.size() <= cap, "radix_resize: room for %lld moves, %zu needed", (long long)cap, moved.size());
+            std::sort(moved.begin(), moved.end(), [](const Moved& a, const Moved& b) { return a.slot < b.slot; });
+        }
+        // nothing fails from here on
+        for (size_t i = 0; i < moved.size(); ++i) {
+            out_src[i] = moved[i].slot;
+            out_dst[i] = *moved[i].place = ring[i];
+        }
+        ring.erase(ring.begin(), ring.begin() + (int64_t)moved.size());
+        for (int64_t s = old; s < n; ++s) ring.push_back((int32_t)s);      // within what was reserved
+        for (int32_t s : ring) is_free[(size_t)s] = 1;
+        t->count = (int64_t)ring.size();
+        t->head = 0;
+        ring.resize((size_t)n);         // at most max(old, n), as reserved
+        t->ring.swap(ring);
+        t->is_free.swap(is_free);
+        t->num_slots = n;
+        t->st.num_slots = n;
+    } catch (const std::bad_alloc&) {
+        set_error("radix_resize: out of host memory");
+        return RX_ENOMEM;
+    }
+    return RX_OK;
+}
+
 int radix_stats(const rx_radix* t, rx_stats* out) {
     RX_REQUIRE(t && out, "radix_stats: bad arguments");
     *out = t->st;

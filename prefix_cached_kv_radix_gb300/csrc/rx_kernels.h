@@ -102,6 +102,22 @@ struct SmallExtendArgs {
 };
 int launch_extend_small(const SmallExtendArgs& a, cudaStream_t stream);
 
+// Causal attention over packed prompts (prompt_attention): sequence b's rows are
+// indptr[b] .. indptr[b+1]-1 of q, k, v and out, strides in elements between rows.
+struct PromptParams {
+    int32_t batch, hq, hkv;
+    int64_t total;                // rows of the buffers
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int64_t* indptr;
+    float* lse;                   // natural log, [total, hq], optional
+    float scale;
+    int32_t* status;
+};
+int launch_prompt_simt(const PromptParams& p, int head_dim, cudaStream_t stream);
 
 // kv_pool_write for the requests of one call whose new tokens are t_begin .. t_end-1 (index
 // arrays absolute: a slice of a step's requests passes its offset pointers).  With stage_bytes

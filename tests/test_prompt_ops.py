@@ -1,0 +1,654 @@
+"""Whole-prompt attention, rotary pool writes, and pool-row moves: host checks on CPU, and the
+kernels against plain 64-bit definitions on the GPU.
+
+No configuration of the pages names these; they stand beside kv_pool_write and the attention
+entry points and share their conventions.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from prefix_cached_kv_radix_gb300 import api
+from tests.prompt_cases import attention, close, rotate
+
+api.load()
+gpu = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+A = 0x1000        # stands for an aligned device address in calls that are refused before any launch
+
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda")
+
+
+def desc_of(dt, hq, hkv, d, slots=64, scale=None):
+    return api.make_desc(api.RX_F32 if dt == F else api.RX_BF16, hq, hkv, d, slots, 1 / math.sqrt(d) if scale is None else scale)
+
+
+def indptr(lens, dev, start=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]) + start, dtype=torch.int64, device=dev)
+
+
+def i32(v, dev):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=dev)
+
+
+# ============================================================================ refusals (CPU)
+def refused(fn, *args):
+    rc = getattr(api.load(), fn)(*args)
+    assert rc == api.RX_EINVAL, (fn, rc)
+    assert fn in api.load().rx_last_error().decode()
+
+
+def test_prompt_attention_refuses():
+    def call(desc=None, batch=1, q=A, qs=256, k=A, ks=128, v=A, vs=128, ind=A, out=A, os_=256, total=4):
+        refused("prompt_attention", ctypes.byref(desc or desc_of(BF, 4, 2, 64)), batch, q, qs, k, ks, v, vs, ind, out, os_,
+                None, total, None, None)
+    for kw in (dict(batch=-1), dict(total=-1), dict(total=1 << 31), dict(q=None), dict(k=None), dict(v=None), dict(ind=None),
+               dict(out=None), dict(q=A + 8), dict(k=A + 2), dict(qs=255), dict(ks=127), dict(ks=64), dict(os_=248),
+               dict(vs=132), dict(desc=desc_of(BF, 4, 3, 64)), dict(desc=desc_of(BF, 4, 0, 64)), dict(desc=desc_of(BF, 4, 2, 96)),
+               dict(desc=desc_of(BF, 4, 2, 64, scale=-1.0)), dict(desc=desc_of(BF, 4, 2, 64, scale=math.inf)),
+               dict(desc=desc_of(BF, 4, 2, 64, scale=math.nan)), dict(desc=api.make_desc(7, 4, 2, 64, 4, 1.0))):
+        call(**kw)
+
+
+def test_kv_pool_write_rope_refuses():
+    base = dict(desc=desc_of(BF, 4, 2, 64), rope=api.rope_desc(32), batch=1, ps=A, pi=A, ns=A, qi=A, pos=A, pstr=4, q=A, qs=256,
+                k=A, ks=128, v=A, vs=128, qo=2 * A, qos=256, ko=None, kos=0, kp=A, vp=A, r2t=A, stride=8, total=4)
+
+    def call(**kw):
+        c = dict(base, **kw)
+        refused("kv_pool_write_rope", ctypes.byref(c["desc"]), ctypes.byref(c["rope"]), *[c[x] for x in list(base)[2:]], None, None)
+
+    def rope(**kw):
+        r = api.rope_desc(kw.pop("sections", 32))
+        for x, y in kw.items():
+            setattr(r, x, y)
+        return r
+    for kw in (dict(batch=-1), dict(total=-1), dict(stride=-1), dict(qi=None), dict(pos=None), dict(pstr=3), dict(k=None),
+               dict(v=None), dict(kp=None), dict(vp=None), dict(pi=None), dict(ns=None), dict(q=None), dict(qo=None),
+               dict(ns=None, r2t=None), dict(q=A + 4), dict(ks=120), dict(vs=129), dict(qo=A, qos=264), dict(ko=A, kos=136),
+               dict(kp=A + 8), dict(desc=desc_of(BF, 4, 2, 80)), dict(desc=api.make_desc(3, 4, 2, 64, 4, 1.0)),
+               dict(rope=rope(n_axes=0)), dict(rope=rope(n_axes=5)), dict(rope=rope(rot_dim=24)), dict(rope=rope(rot_dim=128)),
+               dict(rope=rope(rot_dim=0)), dict(rope=rope(rot_dim=32)), dict(rope=rope(base=0.0)), dict(rope=rope(base=math.nan)),
+               dict(rope=rope(sections=[40, -8], rot_dim=64)), dict(rope=api.rope_desc(32, inv_freq=[math.inf] * 32))):
+        call(**kw)
+    with pytest.raises(ValueError):
+        api.rope_desc([8] * 5)
+    with pytest.raises(ValueError):
+        api.rope_desc(32, inv_freq=[1.0] * 31)
+
+
+def test_kv_pool_copy_and_fork_refuse():
+    d = desc_of(BF, 4, 2, 64)
+
+    def pools(*a):
+        return (ctypes.c_void_p * max(len(a), 1))(*a)
+    for kw in (dict(n=-1), dict(page=0), dict(page=65), dict(np_=-1), dict(pl=None), dict(pl=pools(A, None)), dict(pl=pools(A, A + 8)),
+               dict(pl=pools(A, A)), dict(src=None), dict(dst=None), dict(desc=desc_of(BF, 4, 1, 4)), dict(desc=desc_of(BF, 4, 2, 64, 0))):
+        c = dict(dict(desc=d, np_=2, pl=pools(A, 2 * A), page=1, n=3, src=A, dst=A), **kw)
+        refused("kv_pool_copy", ctypes.byref(c["desc"]), c["np_"], c["pl"], c["page"], c["n"], c["src"], c["dst"], None, None)
+    base = dict(np_=2, pl=pools(A, 2 * A), rows=2, par=A, keep=A, lens=A, ti=A, ts=A, rin=A, inr=2, ins=8, rout=2 * A, outs=8, tail=3)
+    for kw in (dict(rows=-1), dict(inr=-1), dict(ins=-1), dict(outs=-1), dict(tail=-1), dict(par=None), dict(keep=None),
+               dict(lens=None), dict(ti=None), dict(ts=None), dict(rin=None), dict(rout=None), dict(pl=pools(A, A)),
+               dict(rout=A), dict(rout=A + 60), dict(rin=2 * A + 60)):
+        c = dict(base, **kw)
+        refused("kv_pool_fork", ctypes.byref(d), *[c[x] for x in base], None, None)
+
+
+def test_empty_calls_need_no_gpu():
+    d, L = desc_of(BF, 4, 2, 64), api.load()
+    r = api.rope_desc([16, 8, 8])
+    assert L.prompt_attention(ctypes.byref(d), 0, None, 0, None, 0, None, 0, None, None, 0, None, 5, None, None) == api.RX_OK
+    assert L.prompt_attention(ctypes.byref(d), 3, None, 0, None, 0, None, 0, A, None, 0, None, 0, None, None) == api.RX_OK
+    assert L.kv_pool_write_rope(ctypes.byref(d), ctypes.byref(r), 0, *[None] * 5, 0, None, 0, None, 0, None, 0, None, 0, None, 0,
+                                None, None, None, 0, 0, None, None) == api.RX_OK
+    assert L.kv_pool_copy(ctypes.byref(d), 0, None, 1, 5, A, A, None, None) == api.RX_OK
+    assert L.kv_pool_copy(ctypes.byref(d), 1, (ctypes.c_void_p * 1)(A), 1, 0, None, None, None, None) == api.RX_OK
+    assert L.kv_pool_fork(ctypes.byref(d), 0, None, 0, *[None] * 6, 0, 0, None, 0, 0, None, None) == api.RX_OK
+
+
+# ============================================================================ radix_resize (CPU)
+def filled(num_slots, seed, seqs):
+    t = api.RadixTree(num_slots, seed)
+    for toks in seqs:
+        sl, m, _ = t.match_prefix(toks)
+        t.insert(toks, np.concatenate([sl, t.alloc_slots(len(toks) - m)]))
+    return t
+
+
+def free_order(t):
+    n = t.stats()["free_slots"]
+    sl = t.alloc_slots(n)
+    t.free_slots(sl)
+    return sl.tolist()
+
+
+@pytest.mark.parametrize("seed,num,new", [(1, 64, 40), (2, 64, 27), (3, 200, 30), (4, 31, 31), (5, 40, 90), (6, 40, 41)])
+def test_resize_against_model(seed, num, new):
+    rng = np.random.default_rng(seed)
+    seqs = [np.concatenate([[7, 7, 7], rng.integers(0, 3, rng.integers(1, 6))]).astype(np.int32) for _ in range(5)]
+    t = filled(num, seed, seqs)
+    before = {i: t.match_prefix(s)[0].tolist() for i, s in enumerate(seqs)}
+    free = free_order(t)
+    used = sorted({x for v in before.values() for x in v})
+    src, dst = t.resize(new)
+    # the model: used slots from `new` on, ascending, take the usable free slots in their order
+    want_src = [x for x in used if x >= new]
+    left = [x for x in free if x < new]
+    assert src.tolist() == want_src and dst.tolist() == left[:len(want_src)]
+    moved = dict(zip(want_src, dst.tolist()))
+    for i, s in enumerate(seqs):
+        assert t.match_prefix(s)[0].tolist() == [moved.get(x, x) for x in before[i]]
+    t.check()
+    assert t.stats()["num_slots"] == t.num_slots == new
+    assert free_order(t) == left[len(want_src):] + list(range(num, new))
+    assert not set(src.tolist()) & set(dst.tolist())
+
+
+def test_resize_refuses_and_leaves_the_tree():
+    t = filled(64, 9, [np.arange(20, dtype=np.int32)])
+    held, n = t.alloc_slots(3), ctypes.c_int64()
+    free, cached = t.stats()["free_slots"], t.match_prefix(np.arange(20, dtype=np.int32))[0].tolist()
+
+    def code(new):
+        with pytest.raises(api.RxError) as e:
+            t.resize(new)
+        t.check()
+        assert t.stats()["num_slots"] == 64 and t.stats()["free_slots"] == free
+        assert t.match_prefix(np.arange(20, dtype=np.int32))[0].tolist() == cached
+        return e.value.code
+    assert code(0) == code(-1) == code(1 << 31) == api.RX_EINVAL
+    assert code(int(held.max())) == api.RX_EINVAL          # held by the caller
+    t.free_slots(held)
+    free = t.stats()["free_slots"]
+    assert code(19) == api.RX_ENOMEM                       # 20 tokens are cached
+    _, m, node = t.match_prefix(np.arange(20, dtype=np.int32))
+    t.lock(node)
+    assert code(max(cached)) == api.RX_ELOCKED
+    t.unlock(node)
+    need = sum(x >= 30 for x in cached)
+    assert need > 1
+    buf = np.empty(64, np.int32)
+    args = (t.h, 30, api._addr(buf), api._addr(buf[32:]))
+    assert api.load().radix_resize(*args, need - 1, ctypes.byref(n)) == api.RX_EINVAL and n.value == need
+    assert api.load().radix_resize(t.h, 30, None, None, 0, ctypes.byref(n)) == api.RX_EINVAL and n.value == need
+    assert api.load().radix_resize(*args, need, ctypes.byref(n)) == api.RX_OK and n.value == need
+    t.check()
+
+
+def test_resize_then_serve():
+    """A shrunk pool fills, evicts, and grows again."""
+    t = filled(50, 3, [np.arange(i, i + 10, dtype=np.int32) for i in (0, 100, 200)])
+    t.resize(30)
+    assert t.stats()["free_slots"] == 0
+    freed = t.evict(10)
+    assert len(freed) == 10 and freed.max() < 30
+    assert t.resize(33)[0].size == 0
+    sl = t.alloc_slots(13)
+    assert sorted(sl.tolist()) == sorted(freed.tolist() + [30, 31, 32])
+    t.insert(np.arange(300, 313, dtype=np.int32), sl)
+    t.check()
+
+
+# ============================================================================ kv_pool_copy, kv_pool_fork
+def some_pools(gen, n, num, hkv, d, dt):
+    x = torch.randn(n, num, hkv, d, generator=gen, device="cuda").to(dt)
+    return x, [x[i] for i in range(n)]
+
+
+@gpu
+@pytest.mark.parametrize("dt,hkv,d", [(BF, 1, 64), (BF, 3, 64), (BF, 8, 128), (F, 1, 64), (F, 5, 128), (BF, 12, 64)])
+@pytest.mark.parametrize("page,pages,n", [(1, 50, 1), (1, 4000, 1999), (16, 37, 18), (64, 9, 4), (7, 20, 6)])
+@pytest.mark.parametrize("pools", [1, 2, 6])
+def test_copy(dev, dt, hkv, d, page, pages, n, pools):
+    gen = torch.Generator("cuda").manual_seed(n + d)
+    num = pages * page + (page - 1)                       # a last page that is not whole
+    x, lst = some_pools(gen, pools, num, hkv, d, dt)
+    ids = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+    src, dst, st = ids[:n].clone(), ids[n:2 * n].clone(), i32([0], "cuda")
+    if n > 2:
+        src[1] = src[0]                                   # one source, two destinations
+        dst[2] = src[2]                                   # left where it is
+    want = x.clone()
+    w = want[:, :pages * page].unflatten(1, (pages, page))      # a view
+    w[:, dst.long()] = w[:, src.long()].clone()
+    api.kv_pool_copy(desc_of(dt, hkv, hkv, d, num), lst, src, dst, page, st)
+    assert int(st.item()) == 0 and torch.equal(x, want)
+
+
+@gpu
+def test_copy_many_pools_and_bad_pages(dev):
+    gen = torch.Generator("cuda").manual_seed(1)
+    x, lst = some_pools(gen, 300, 40, 1, 64, BF)
+    src, dst, st = i32([5, 40, 3, -1, 9], "cuda"), i32([20, 21, 40, 22, 23], "cuda"), i32([0], "cuda")
+    want = x.clone()
+    want[:, 20], want[:, 23] = x[:, 5], x[:, 9]
+    api.kv_pool_copy(desc_of(BF, 1, 1, 64, 40), lst, src, dst, 1, st)
+    assert int(st.item()) == api.RX_DEV_BAD_SLOT and torch.equal(x, want)
+
+
+@gpu
+def test_copy_far_rows(dev):
+    """Byte offsets past 2^32 in one pool."""
+    num = (5 << 30) // 2048
+    pool = torch.empty(num, 8, 128, dtype=BF, device="cuda")
+    pool[num - 1] = 3.0
+    pool[num // 2] = 4.0
+    src, dst, st = i32([num - 1, num // 2], "cuda"), i32([0, num - 2], "cuda"), i32([0], "cuda")
+    api.kv_pool_copy(desc_of(BF, 8, 8, 128, num), [pool], src, dst, 1, st)
+    assert (pool[0] == 3).all() and (pool[num - 2] == 4).all() and int(st.item()) == 0
+
+
+def fork_case(gen, parents, children, ctx, page, extra=11):
+    rng = np.random.default_rng(parents * 7 + children)
+    lens = rng.integers(0, ctx + 1, parents)
+    rows = [(p, int(lens[p])) for p in range(parents) for _ in range(children)]
+    rng.shuffle(rows)
+    rows = [(int(p), int(n)) for p, n in rows]
+    keep = [n - n % page if rng.random() < 0.7 else int(rng.integers(0, n + 1)) for _, n in rows]
+    tails = [n - k for (_, n), k in zip(rows, keep)]
+    num = int(lens.sum() + sum(tails) + extra)
+    ids = torch.randperm(num, generator=gen, device="cuda").to(torch.int32)
+    table = torch.full((parents, ctx + 2), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for p, n in enumerate(lens):
+        table[p, :n] = ids[at:at + n]
+        at += n
+    return rows, keep, tails, num, table, ids[at:at + max(sum(tails), 1)].contiguous()
+
+
+@gpu
+@pytest.mark.parametrize("dt,hkv,d,pools", [(BF, 2, 64, 2), (BF, 8, 128, 4), (F, 3, 128, 1), (BF, 1, 64, 0)])
+@pytest.mark.parametrize("parents,children,ctx,page", [(1, 1, 5, 4), (3, 4, 70, 16), (40, 3, 50, 16), (2, 600, 20, 8), (2, 2, 2600, 64)])
+def test_fork(dev, dt, hkv, d, pools, parents, children, ctx, page):
+    gen = torch.Generator("cuda").manual_seed(ctx)
+    rows, keep, tails, num, table, tail_slots = fork_case(gen, parents, children, ctx, page)
+    x, lst = some_pools(gen, pools, num, hkv, d, dt) if pools else (torch.zeros(1), [])
+    want = x.clone()
+    out, st = torch.full((len(rows), ctx + 5), 99, dtype=torch.int32, device="cuda"), i32([0], "cuda")
+    api.kv_pool_fork(desc_of(dt, hkv, hkv, d, num), lst, i32([p for p, _ in rows], "cuda"), i32(keep, "cuda"),
+                     i32([n for _, n in rows], "cuda"), indptr(tails, "cuda"), tail_slots, table, out, sum(tails), st)
+    at, T, tl, got = 0, table.tolist(), tail_slots.tolist(), out.tolist()
+    src, dst = [], []
+    for f, (p, n) in enumerate(rows):
+        tail = tl[at:at + tails[f]]
+        assert got[f] == T[p][:keep[f]] + tail + [-1] * (ctx + 5 - n)
+        src += T[p][keep[f]:n]
+        dst += tail
+        at += tails[f]
+    if pools:
+        want[:, dst] = want[:, src].clone()
+        assert torch.equal(x, want)
+    assert int(st.item()) == 0
+
+
+@gpu
+def test_fork_bad_rows(dev):
+    gen = torch.Generator("cuda").manual_seed(2)
+    x, lst = some_pools(gen, 2, 64, 2, 64, BF)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").reshape(2, 10)
+    tails = torch.arange(40, 60, dtype=torch.int32, device="cuda")
+    # rows: a good one, a parent too high, keep past the length, a length past the table, a tail list too long, a good one
+    par, keep, lens = [1, 2, 0, 0, 0, 0], [7, 1, 6, 4, 8, 9], [9, 3, 5, 11, 10, 10]
+    ti = torch.tensor([0, 2, 4, 4, 11, 12, 13], device="cuda")
+    out, st, want = torch.empty(6, 12, dtype=torch.int32, device="cuda"), i32([0], "cuda"), x.clone()
+    api.kv_pool_fork(desc_of(BF, 2, 2, 64, 64), lst, i32(par, "cuda"), i32(keep, "cuda"), i32(lens, "cuda"), ti, tails, table, out, 13, st)
+    assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+    assert out[0].tolist() == list(range(10, 17)) + [40, 41] + [-1] * 3
+    assert (out[1:5] == -1).all()
+    assert out[5].tolist() == list(range(9)) + [52] + [-1] * 2
+    want[:, [40, 41, 52]] = x[:, [17, 18, 9]]
+    assert torch.equal(x, want)
+    # a slot outside the pool, in the parent's row and in the tail
+    st.zero_()
+    table[0, 9], tails[0] = 64, -1
+    want = x.clone()
+    api.kv_pool_fork(desc_of(BF, 2, 2, 64, 64), lst, i32([0, 1], "cuda"), i32([9, 9], "cuda"), i32([10, 10], "cuda"),
+                     torch.tensor([0, 1, 2], device="cuda"), tails, table, out[:2].contiguous(), 2, st)
+    want[:, 41] = x[:, 19]
+    assert int(st.item()) == api.RX_DEV_BAD_SLOT and torch.equal(x, want)
+
+
+# ============================================================================ kv_pool_write_rope
+def rope_case(gen, dt, hq, hkv, d, new, pre, axes_pos, slots_extra=9, wide=1):
+    T, P = sum(new), sum(pre)
+    ids = torch.randperm(T + P + slots_extra, generator=gen, device="cuda").to(torch.int32)
+    x = torch.randn(T, hq + 2 * hkv + wide, d, generator=gen, device="cuda").to(dt)
+    return dict(q=x[:, :hq], k=x[:, hq:hq + hkv], v=x[:, hq + hkv:hq + 2 * hkv], x=x, num=T + P + slots_extra,
+                ps=ids[:P].contiguous(), ns=ids[P:P + T].contiguous(), pi=indptr(pre, "cuda"), qi=indptr(new, "cuda"),
+                pos=axes_pos.to(torch.int32).contiguous())
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d,sections,cyclic,inter", [
+    (4, 4, 64, [32], False, False), (4, 4, 64, [32], False, True), (8, 2, 128, [16, 24, 24], False, False),
+    (8, 2, 128, [24, 20, 20], True, False), (7, 1, 128, [12, 11, 5, 4], True, True), (3, 1, 64, [3, 0, 5], False, False),
+    (5, 5, 128, [32], False, False), (1, 1, 64, [0, 8], True, True)])
+@pytest.mark.parametrize("new,pre", [([1], [0]), ([1] * 70, [3] * 70), ([0, 5, 1, 0, 33], [2, 0, 1100, 7, 0]), ([1300], [9])])
+def test_rope_write(dev, dt, hq, hkv, d, sections, cyclic, inter, new, pre):
+    gen = torch.Generator("cuda").manual_seed(len(new) + d)
+    T = sum(new)
+    far = torch.tensor([0, 5, -100000, 2 ** 31 - 3000])[:len(sections), None].cuda()
+    pos = torch.randint(0, 3000, (len(sections), T + 5), generator=gen, device="cuda") + far
+    c = rope_case(gen, dt, hq, hkv, d, new, pre, pos)
+    desc = desc_of(dt, hq, hkv, d, c["num"])
+    rope = api.rope_desc(sections, 10000.0, cyclic=cyclic, interleaved=inter)
+    kp, vp = (torch.full((c["num"], hkv, d), 7.5, dtype=dt, device="cuda") for _ in range(2))
+    qo, ko = torch.empty(T, hq, d, dtype=dt, device="cuda"), torch.empty(T, hkv, d, dtype=dt, device="cuda")
+    stride = max(a + b for a, b in zip(new, pre)) + 3
+    r2t, st = torch.full((len(new), stride), 99, dtype=torch.int32, device="cuda"), i32([0], "cuda")
+    keep = c["x"].clone()
+    api.kv_pool_write_rope(desc, rope, len(new), c["ps"], c["pi"], c["ns"], c["qi"], c["pos"], c["q"], c["k"], c["v"], qo, ko, kp,
+                           vp, r2t, T, st)
+    assert int(st.item()) == 0 and torch.equal(c["x"], keep)
+    half = sum(sections)
+    freq = 10000.0 ** (-2.0 * torch.arange(half, dtype=torch.float64, device="cuda") / (2 * half))
+    for got, src in ((qo, c["q"]), (ko, c["k"])):
+        want, tol = rotate(src, c["pos"][:, :T], sections, freq, cyclic, inter)
+        close(got, want, tol)
+    at = c["ns"].long()
+    assert torch.equal(kp[at], ko) and torch.equal(vp[at], c["v"])
+    other = torch.ones(c["num"], dtype=torch.bool, device="cuda")
+    other[at] = False
+    assert (kp[other] == 7.5).all() and (vp[other] == 7.5).all()
+    p0, q0 = np.cumsum([0] + pre), np.cumsum([0] + new)
+    for b in range(len(new)):
+        row = torch.cat([c["ps"][p0[b]:p0[b + 1]], c["ns"][q0[b]:q0[b + 1]]]).tolist()
+        assert r2t[b].tolist() == row + [-1] * (stride - len(row))
+    # the table and values are kv_pool_write's
+    k2, v2, t2 = torch.empty_like(kp), torch.empty_like(vp), torch.empty_like(r2t)
+    api.kv_pool_write(desc, len(new), c["ps"] if c["ps"].numel() else None, c["pi"], c["ns"], c["qi"], ko, c["v"].contiguous(), k2,
+                      v2, t2, T, st)
+    assert torch.equal(t2, r2t) and torch.equal(k2[at], kp[at]) and torch.equal(v2[at], vp[at]) and int(st.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("T", [5, 2000])
+def test_rope_in_place_alone_and_padded(dev, dt, T):
+    """In place in the projection's rows, without pool and table; rows outside the batch stay; own
+    frequencies."""
+    gen = torch.Generator("cuda").manual_seed(T)
+    hq, hkv, d, a, z = 6, 2, 64, 2, 1
+    pos = torch.randint(0, 1 << 20, (1, T), generator=gen, device="cuda")
+    c = rope_case(gen, dt, hq, hkv, d, [T], [0], pos)
+    freq = torch.rand(16, generator=gen, device="cuda", dtype=torch.float64) * 40 - 20
+    rope = api.rope_desc(16, inv_freq=freq.cpu().numpy())
+    desc, st, before = desc_of(dt, hq, hkv, d, c["num"]), i32([0], "cuda"), c["x"].clone()
+    qi = torch.tensor([a, a, T - z], device="cuda")
+    args = (desc, rope, 2, None, None, None, qi, c["pos"])
+    api.kv_pool_write_rope(*args, c["q"], c["k"], None, c["q"], c["k"], None, None, None, T, st)
+    for name, lo, h in (("q", 0, hq), ("k", hq, hkv)):
+        src = before[:, lo:lo + h]
+        want, tol = rotate(src, c["pos"], [16], freq)
+        close(c[name][a:T - z], want[a:T - z], tol[a:T - z], name)
+        assert torch.equal(c[name][:a], src[:a]) and torch.equal(c[name][T - z:], src[T - z:])
+    assert torch.equal(c["x"][:, hq + hkv:], before[:, hq + hkv:]) and int(st.item()) == 0
+    # keys only, into the pool; the queries left to someone else
+    kp, vp = (torch.zeros(c["num"], hkv, d, dtype=dt, device="cuda") for _ in range(2))
+    api.kv_pool_write_rope(desc, rope, 2, None, None, c["ns"], qi, c["pos"], None, before[:, hq:hq + hkv], c["v"], None, None, kp, vp,
+                           None, T, st)
+    at = c["ns"][a:T - z].long()
+    assert torch.equal(kp[at], c["k"][a:T - z]) and torch.equal(vp[at], c["v"][a:T - z]) and int(st.item()) == 0
+    assert kp.abs().sum(dim=(1, 2)).ne(0).sum() == T - z - a
+
+
+@gpu
+def test_rope_bad_slots_and_lengths(dev):
+    gen = torch.Generator("cuda").manual_seed(8)
+    c = rope_case(gen, BF, 2, 2, 64, [40], [0], torch.arange(40, device="cuda")[None])
+    desc, rope = desc_of(BF, 2, 2, 64, c["num"]), api.rope_desc(32)
+    kp, vp = (torch.full((c["num"], 2, 64), 7.5, dtype=BF, device="cuda") for _ in range(2))
+    ns = c["ns"].clone()
+    ns[3], ns[17] = -1, c["num"]
+    qo, st = torch.empty(40, 2, 64, dtype=BF, device="cuda"), i32([0], "cuda")
+    r2t = torch.empty(1, 40, dtype=torch.int32, device="cuda")
+    api.kv_pool_write_rope(desc, rope, 1, None, c["pi"], ns, c["qi"], c["pos"], c["q"], c["k"], c["v"], qo, None, kp, vp, r2t, 40, st)
+    assert int(st.item()) == api.RX_DEV_BAD_SLOT
+    assert r2t[0, 3] == r2t[0, 17] == -1
+    assert (kp != 7.5).any(dim=2).any(dim=1).sum() == 38
+    st.zero_()
+    for table in (r2t, None):
+        api.kv_pool_write_rope(desc, rope, 1, None, c["pi"], c["ns"], torch.tensor([0, 41], device="cuda"), c["pos"], c["q"], c["k"],
+                               c["v"], qo, None, kp, vp, table, 40, st)
+        assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+        st.zero_()
+
+
+@gpu
+def test_binding_refuses(dev):
+    d, st = desc_of(BF, 4, 2, 64, 10), i32([0], "cuda")
+    q, k = torch.zeros(8, 4, 64, dtype=BF, device="cuda"), torch.zeros(8, 2, 64, dtype=BF, device="cuda")
+    ip = torch.tensor([0, 8], device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:7]), dict(k=q), dict(out=q.transpose(0, 1)), dict(ip=ip.int()), dict(ip=ip[:1]),
+                dict(lse=torch.zeros(7, 4, device="cuda")), dict(q=q.cpu()), dict(st=st.long())):
+        a = dict(dict(q=q, k=k, out=torch.empty_like(q), ip=ip, lse=None, st=st), **bad)
+        with pytest.raises(ValueError):
+            api.prompt_attention(d, 1, a["q"], a["k"], k, a["ip"], a["out"], a["lse"], 8, a["st"])
+    with pytest.raises(ValueError):
+        api.kv_pool_copy(d, [k], i32([1], "cuda"), i32([2], "cuda"), 1, st)      # not num_slots rows
+    pool = torch.zeros(10, 2, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        api.kv_pool_copy(d, [pool], i32([1, 2], "cuda"), i32([2], "cuda"), 1, st)
+    with pytest.raises(ValueError):
+        api.kv_pool_write_rope(d, api.rope_desc(32), 1, None, None, None, ip, torch.zeros(2, 8, dtype=torch.int32, device="cuda"), q, k,
+                               None, q, k, None, None, None, 8, st)
+
+
+# ============================================================================ prompt_attention
+def rows_of(gen, T, hq, hkv, d, dt, wide=0):
+    """q, k, v as parts of one projection's rows (wide more columns than needed between them)."""
+    x = torch.randn(T, hq + 2 * hkv + wide, d, generator=gen, device="cuda").to(dt)
+    return x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:hq + 2 * hkv]
+
+
+def run_prompt(q, k, v, lens, desc, start=0, total=None, lse=True):
+    total = q.shape[0] if total is None else total
+    out = torch.full((q.shape[0], desc.hq, desc.head_dim), 7.5, dtype=q.dtype, device="cuda")
+    L = torch.full((q.shape[0], desc.hq), 7.5, device="cuda") if lse else None
+    st = i32([0], "cuda")
+    api.prompt_attention(desc, len(lens), q, k, v, indptr(lens, "cuda", start), out, L, total, st)
+    torch.cuda.synchronize()
+    return out, L, int(st.item())
+
+
+def check_prompt(q, k, v, lens, desc, start=0):
+    out, lse, st = run_prompt(q, k, v, lens, desc, start)
+    assert st == 0
+    want, wl, to, tl = attention(q, k, v, lens, desc.scale, start)
+    a, b = start, start + sum(lens)
+    close(out[a:b], want[a:b], to[a:b], "out")
+    close(lse[a:b], wl[a:b], tl[a:b], "lse")
+    assert (out[:a] == 7.5).all() and (out[b:] == 7.5).all() and (lse[:a] == 7.5).all() and (lse[b:] == 7.5).all()
+    return out, lse
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (4, 1, 128), (6, 2, 128), (14, 2, 64), (1, 1, 128), (16, 2, 128)])
+def test_prompt_lengths(dev, dt, hq, hkv, d):
+    gen = torch.Generator("cuda").manual_seed(hq * 100 + d)
+    for lens in ([1], [0, 1, 2, 0], [127, 128, 129], [255, 1, 256, 257], [33, 0, 300, 64, 65], [700]):
+        q, k, v = rows_of(gen, sum(lens), hq, hkv, d, dt, wide=3)
+        check_prompt(q, k, v, lens, desc_of(dt, hq, hkv, d))
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,hkv", [(71, 1), (128, 1), (150, 1), (130, 2), (260, 2)])
+def test_prompt_many_heads_per_kv_head(dev, dt, hq, hkv):
+    """Up to and past the 128 rows of a tile."""
+    gen = torch.Generator("cuda").manual_seed(hq)
+    lens = [3, 130, 1]
+    q, k, v = rows_of(gen, sum(lens), hq, hkv, 64, dt)
+    check_prompt(q, k, v, lens, desc_of(dt, hq, hkv, 64))
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_many_sequences(dev, dt):
+    """Enough items that a block takes several, and more sequences than a warp looks at at once."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 60, 400)] + [513] + [int(x) for x in rng.integers(0, 3, 800)]
+    q, k, v = rows_of(gen, sum(lens), 4, 2, 64, dt)
+    check_prompt(q, k, v, lens, desc_of(dt, 4, 2, 64))
+
+
+@gpu
+@pytest.mark.parametrize("dt,hq,hkv,d,n", [(F, 4, 4, 128, 2500), (BF, 8, 2, 128, 6000), (BF, 12, 12, 64, 3001), (BF, 64, 8, 128, 2100)])
+def test_prompt_long(dev, dt, hq, hkv, d, n):
+    gen = torch.Generator("cuda").manual_seed(n)
+    q, k, v = rows_of(gen, n, hq, hkv, d, dt)
+    check_prompt(q, k, v, [n], desc_of(dt, hq, hkv, d))
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_leaves_other_rows(dev, dt):
+    """Rows before the first and behind the last sequence, NaN inside: neither read nor written."""
+    gen = torch.Generator("cuda").manual_seed(1)
+    lens = [200, 57]
+    q, k, v = rows_of(gen, 400, 4, 2, 128, dt)
+    for x in (q, k, v):
+        x[:70] = math.nan
+        x[70 + 257:] = math.nan
+    check_prompt(q, k, v, lens, desc_of(dt, 4, 2, 128), start=70)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 128), (8, 2, 64), (6, 2, 128)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_prompt_non_finite_values_stay_in_their_place(dev, dt, hq, hkv, d, bad):
+    """A non-finite value reaches the rows of its sequence from its own on; a non-finite key's row is
+    hidden from earlier rows and other sequences as well."""
+    gen = torch.Generator("cuda").manual_seed(2)
+    lens = [150, 301, 90]
+    q, k, v = rows_of(gen, sum(lens), hq, hkv, d, dt)
+    for at in (40, 149, 150 + 200, 150 + 255, 150 + 300, 451):
+        v[at, (at % hkv), at % d] = bad
+    v[451, 0, 3] = math.nan
+    check_prompt(q, k, v, lens, desc_of(dt, hq, hkv, d))
+    k[150 + 280:150 + 301] = math.nan             # the tail of the second sequence: those rows are NaN
+    out, lse, st = run_prompt(q, k, v, lens, desc_of(dt, hq, hkv, d))
+    want, wl, to, tl = attention(q, k, v, lens, desc_of(dt, hq, hkv, d).scale)
+    rows = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    rows[150 + 280:150 + 301] = False
+    close(out[rows], want[rows], to[rows], "out")
+    close(lse[rows], wl[rows], tl[rows], "lse")
+    assert torch.isnan(out[~rows].float()).all() and torch.isnan(lse[~rows]).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_growing_and_extreme_scores(dev, dt):
+    """Scores whose maximum keeps growing (the running maximum moves at every tile), one that falls,
+    the type's lowest values as keys, and a scale of zero."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    n, d = 700, 64
+    q, k, v = (x.contiguous() for x in rows_of(gen, n, 2, 1, d, dt))
+    ramp = torch.linspace(0.1, 6, n, device="cuda")[:, None, None]
+    q0 = q[:1].expand_as(q).contiguous()
+    for kk in (q0[:, :1] * ramp, q0[:, :1] * ramp.flip(0)):
+        check_prompt(q0, kk.to(dt).contiguous(), v, [n], desc_of(dt, 2, 1, d))
+    check_prompt(q, k, v, [n], desc_of(dt, 2, 1, d, scale=0.0))
+    low = torch.full_like(k, torch.finfo(dt).min)
+    low[0] = 0
+    pos = q.abs() + 0.1
+    out, lse, st = run_prompt(pos, low, v, [n], desc_of(dt, 2, 1, d))
+    assert torch.equal(out, v[:1].expand(n, 2, d))        # every later key underflows: row 0's value exactly
+    assert (lse == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_far_rows(dev, dt):
+    """Element offsets past 2^32: 5000 rows, a million elements apart."""
+    n, gap = 5000, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    big = torch.empty(n * gap, dtype=dt, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(4)
+    rows = big.as_strided((n, 4, 64), (gap, 64, 1))
+    rows[-300:] = torch.randn(300, 4, 64, generator=gen, device="cuda").to(dt)
+    q, k, v = rows[:, :2], rows[:, 2:3], rows[:, 3:4]
+    out = torch.full((n, 2, 64), 7.5, dtype=dt, device="cuda")
+    st = i32([0], "cuda")
+    desc = desc_of(dt, 2, 1, 64)
+    api.prompt_attention(desc, 2, q, k, v, indptr([100, 200], "cuda", n - 300), out, None, n, st)
+    want, _, to, _ = attention(q[-300:], k[-300:], v[-300:], [100, 200], desc.scale)
+    close(out[-300:], want, to)
+    wide = big.as_strided((n, 2, 64), (gap, 64, 1), 1024)   # and written that far apart
+    api.prompt_attention(desc, 2, q, k, v, indptr([100, 200], "cuda", n - 300), wide, None, n, st)
+    assert torch.equal(wide[-300:], out[-300:]) and int(st.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_bad_boundaries_are_reported_and_skipped(dev, dt):
+    gen = torch.Generator("cuda").manual_seed(6)
+    q, k, v = rows_of(gen, 300, 4, 2, 64, dt)
+    desc = desc_of(dt, 4, 2, 64)
+    for ind in ([0, 100, 301], [0, 100, 1 << 40], [-5, 100, 300]):
+        out = torch.full((300, 4, 64), 7.5, dtype=dt, device="cuda")
+        st = i32([0], "cuda")
+        api.prompt_attention(desc, 2, q, k, v, torch.tensor(ind, device="cuda"), out, None, 300, st)
+        assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+        good = slice(0, 100) if ind[0] == 0 else slice(100, 300)
+        want, _, to, _ = attention(q[good], k[good], v[good], [good.stop - good.start], desc.scale)
+        close(out[good], want, to)
+        rest = torch.ones(300, dtype=torch.bool, device="cuda")
+        rest[good] = False
+        assert (out[rest] == 7.5).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_streams_and_graphs(dev, dt):
+    """Calls on several streams at once, and two graphs captured on one stream and replayed on two,
+    give the first call's bits."""
+    gen = torch.Generator("cuda").manual_seed(7)
+    desc = desc_of(dt, 8, 2, 128)
+    sets = []
+    for lens in ([900, 300, 77], [64] * 40 + [1500]):
+        q, k, v = rows_of(gen, sum(lens), 8, 2, 128, dt)
+        out, lse, st = run_prompt(q, k, v, lens, desc)
+        assert st == 0
+        sets.append((q, k, v, lens, out, indptr(lens, "cuda")))
+    st = i32([0], "cuda")
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = []
+    torch.cuda.synchronize()
+    for r in range(3):
+        for i, s in enumerate(streams):
+            q, k, v, lens, _, ip = sets[i % 2]
+            with torch.cuda.stream(s):
+                o = torch.empty_like(sets[i % 2][4])
+                api.prompt_attention(desc, len(lens), q, k, v, ip, o, None, q.shape[0], st)
+                outs.append((i % 2, o))
+    torch.cuda.synchronize()
+    for i, o in outs:
+        assert torch.equal(o, sets[i][4])
+    graphs = []
+    for q, k, v, lens, want, ip in sets:
+        g, o = torch.cuda.CUDAGraph(), torch.zeros_like(want)
+        with torch.cuda.graph(g, stream=streams[0]):
+            api.prompt_attention(desc, len(lens), q, k, v, ip, o, None, q.shape[0], st)
+        graphs.append((g, o, want))
+    for r in range(5):
+        for (g, o, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, o, want in graphs:
+        assert torch.equal(o, want)
+    assert int(st.item()) == 0
