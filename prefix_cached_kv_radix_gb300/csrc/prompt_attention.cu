@@ -713,7 +713,8 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     p.hb = std::min(p.group, 128);
     p.nhb = (p.group + p.hb - 1) / p.hb;
     p.tpt = 128 / p.hb;
-    p.scale_log2 = a.scale * PT_LOG2E;
+    // a scale of zero as the least normal number: masked scores are -inf, and -inf times it has to stay so
+    p.scale_log2 = std::max(a.scale * PT_LOG2E, 0x1p-126f);
     const int64_t heads = (int64_t)a.hkv * p.nhb;
     // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn; one a piece
     // when there would be fewer such items than SMs.
