@@ -468,6 +468,21 @@ def rx_step_run(args) -> int:
     return rc
 
 
+def _load_ext(name: str):
+    """A CPython extension built next to the library, or False where it was not built."""
+    from .build import pystep_path
+    path = pystep_path(name)
+    if not os.path.exists(path):
+        return False
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    spec = importlib.util.spec_from_file_location(name, path, loader=loader)
+    m = importlib.util.module_from_spec(spec)
+    loader.exec_module(m)
+    return m
+
+
 _step_ext = None
 
 
@@ -477,18 +492,9 @@ def step_ext():
     None when it was not built (the ctypes path then makes the same call)."""
     global _step_ext
     if _step_ext is None:
-        from .build import pystep_path
-        path = pystep_path()
-        _step_ext = False
-        if os.path.exists(path):
-            import importlib.machinery
-            import importlib.util
-            loader = importlib.machinery.ExtensionFileLoader("_rxstep", path)
-            spec = importlib.util.spec_from_file_location("_rxstep", path, loader=loader)
-            m = importlib.util.module_from_spec(spec)
-            loader.exec_module(m)
-            m.bind(ctypes.cast(load().rx_step_run, ctypes.c_void_p).value)
-            _step_ext = m
+        _step_ext = _load_ext("_rxstep")
+        if _step_ext:
+            _step_ext.bind(ctypes.cast(load().rx_step_run, ctypes.c_void_p).value)
     return _step_ext or None
 
 
@@ -643,6 +649,31 @@ def decode_attention_noalloc(desc, batch, q, req_to_token, kv_lens, k_pool, v_po
 # ---------------------------------------------------------------------------- rows, pages, prompts
 _NBYTES = {RX_F32: 4, RX_BF16: 2}
 _INTS = {"torch.int32": 4, "torch.int64": 8}
+_ops_ext = None
+
+
+def ops_ext():
+    """The _rxops extension (the checks and marshalling of the operators below in C), bound to
+    torch's types and the loaded library; None when it was not built (the Python code below then
+    makes the same checks and the same calls)."""
+    global _ops_ext
+    if _ops_ext is None:
+        ext = _load_ext("_rxops")
+        if ext:
+            import torch
+            names = {n: ctypes.cast(getattr(load(), n), ctypes.c_void_p).value
+                     for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention")}
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+            dev = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+            torch.cuda.init()
+            ext.bind(dict(names, int32=torch.int32, int64=torch.int64, float32=torch.float32, bfloat16=torch.bfloat16,
+                          get_device=dev, raw_stream=raw))
+        _ops_ext = ext
+    return _ops_ext or None
+
+
+def _stream_of(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _rows(name, t, heads: int, desc, total: int):
@@ -710,6 +741,11 @@ def kv_pool_write_rope(desc, rope, batch, prefix_slots, prefix_indptr, new_slots
     queries into q_out (may be q; q and q_out may be None), optionally turned keys into k_out (may be
     k_new), and the slot table.  positions: int32 [axes, >= total_new].  new_slots None writes no
     pool, req_to_token None makes no table.  Rows may be parts of wider ones (strided)."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("kv_pool_write_rope", ext.kv_pool_write_rope(
+            ctypes.addressof(desc), ctypes.addressof(rope), batch, prefix_slots, prefix_indptr, new_slots, qo_indptr, positions, q,
+            k_new, v_new, q_out, k_out, k_pool, v_pool, req_to_token, total_new, status, r2t_stride, _stream_of(stream)))
     qa, qs = _rows("q", q, desc.hq, desc, total_new)
     oa, os_ = _rows("q_out", q_out, desc.hq, desc, total_new)
     ka, ks = _rows("k_new", k_new, desc.hkv, desc, total_new)
@@ -737,6 +773,10 @@ def kv_pool_write_rope(desc, rope, batch, prefix_slots, prefix_indptr, new_slots
 def kv_pool_copy(desc, pools, src, dst, page_size, status, stream=None) -> None:
     """Pages of every pool to other pages of the same pool: pool[dst[i]] = pool[src[i]] (pages of
     page_size slots).  pools: the layers' K and V pools."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("kv_pool_copy", ext.kv_pool_copy(ctypes.addressof(desc), pools, src, dst, page_size, status,
+                                                       _stream_of(stream)))
     if src.numel() != dst.numel():
         raise ValueError("src, dst: one destination per source")
     _here(src, dst, status, *pools)
@@ -750,6 +790,10 @@ def kv_pool_fork(desc, pools, parents, keep_lens, kv_lens, tail_indptr, tail_slo
     """Slot tables (and copied K/V rows) of sequences that continue others: row f of r2t_out keeps
     the first keep_lens[f] slots of row parents[f] of r2t_in and has its own tail slots, holding
     copies, up to kv_lens[f]."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("kv_pool_fork", ext.kv_pool_fork(ctypes.addressof(desc), pools, parents, keep_lens, kv_lens, tail_indptr,
+                                                       tail_slots, r2t_in, r2t_out, total_tail, status, _stream_of(stream)))
     n = r2t_out.shape[0]
     _here(parents, r2t_in, r2t_out, status, *pools)
     _check("kv_pool_fork", load().kv_pool_fork(
@@ -762,6 +806,10 @@ def kv_pool_fork(desc, pools, parents, keep_lens, kv_lens, tail_indptr, tail_slo
 def prompt_attention(desc, batch, q, k, v, indptr, out, lse, total, status, stream=None) -> None:
     """Causal attention over packed prompts, each row over rows 0.. itself of its own sequence
     (rows indptr[b] .. indptr[b+1]-1), straight from the projections' rows; rows may be strided."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("prompt_attention", ext.prompt_attention(ctypes.addressof(desc), batch, q, k, v, indptr, out, lse, total,
+                                                               status, _stream_of(stream)))
     qa, qs = _rows("q", q, desc.hq, desc, total)
     ka, ks = _rows("k", k, desc.hkv, desc, total)
     va, vs = _rows("v", v, desc.hkv, desc, total)

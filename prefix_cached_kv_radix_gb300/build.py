@@ -4,8 +4,8 @@
 
 Translation units compile in parallel; the result is prefix_cached_kv_radix_gb300/_build/
 libradixattn.so (git-ignored).  nvcc: -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo.  Also
-_build/_rxstep*.so, the per-step call's marshalling as a CPython extension, where the Python
-headers are installed.
+_build/_rxstep*.so and _rxops*.so, the per-step call's and the row, page and prompt operators'
+marshalling as CPython extensions, where the Python headers are installed.
 """
 from __future__ import annotations
 
@@ -30,11 +30,13 @@ CPP_SOURCES = ["radix_tree.cpp"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 # the per-step marshalling as a CPython extension (optional: the ctypes binding does the same)
 PYSTEP_SRC = "pystep.c"
+# the row, page and prompt operators' marshalling, likewise
+PYOPS_SRC = "pyops.c"
 
 
-def pystep_path() -> str:
+def pystep_path(name: str = "_rxstep") -> str:
     import sysconfig
-    return os.path.join(OUT_DIR, "_rxstep" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+    return os.path.join(OUT_DIR, name + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
 def nvcc() -> str:
@@ -102,16 +104,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
               "-ldl"], verbose)
         os.replace(tmp, LIB_PATH)
     build_pystep(force, verbose)
+    build_pystep(force, verbose, PYOPS_SRC, "_rxops")
     return LIB_PATH
 
 
-def build_pystep(force: bool = False, verbose: bool = False) -> str | None:
-    """The _rxstep extension next to the library, when the Python headers are installed."""
+def build_pystep(force: bool = False, verbose: bool = False, source: str = PYSTEP_SRC, name: str = "_rxstep") -> str | None:
+    """A CPython extension next to the library, when the Python headers are installed."""
     import sysconfig
     inc = sysconfig.get_paths().get("include")
     if not inc or not os.path.exists(os.path.join(inc, "Python.h")):
         return None
-    src, out = os.path.join(CSRC, PYSTEP_SRC), pystep_path()
+    src, out = os.path.join(CSRC, source), pystep_path(name)
     if force or _stale(out, src):
         tmp = out + f".tmp{os.getpid()}"
         _run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", inc, "-I", INCLUDE, src, "-o", tmp], verbose)

@@ -424,7 +424,11 @@ def test_rope_bad_slots_and_lengths(dev):
 
 
 @gpu
-def test_binding_refuses(dev):
+@pytest.mark.parametrize("in_c", [True, False])
+def test_binding_refuses(dev, in_c, monkeypatch):
+    """The same refusals from the extension and from the Python code that stands in for it."""
+    if not in_c:
+        monkeypatch.setattr(api, "_ops_ext", False)
     d, st = desc_of(BF, 4, 2, 64, 10), i32([0], "cuda")
     q, k = torch.zeros(8, 4, 64, dtype=BF, device="cuda"), torch.zeros(8, 2, 64, dtype=BF, device="cuda")
     ip = torch.tensor([0, 8], device="cuda")
@@ -441,6 +445,35 @@ def test_binding_refuses(dev):
     with pytest.raises(ValueError):
         api.kv_pool_write_rope(d, api.rope_desc(32), 1, None, None, None, ip, torch.zeros(2, 8, dtype=torch.int32, device="cuda"), q, k,
                                None, q, k, None, None, None, 8, st)
+
+
+@gpu
+def test_binding_in_python_makes_the_same_calls(dev, monkeypatch):
+    """Every operator through the extension and through the Python code: the same results."""
+    gen = torch.Generator("cuda").manual_seed(11)
+    c = rope_case(gen, BF, 4, 2, 64, [30, 50], [3, 0], torch.arange(80, device="cuda")[None])
+    desc, rope, st = desc_of(BF, 4, 2, 64, c["num"]), api.rope_desc(32), i32([0], "cuda")
+    stream, results = torch.cuda.Stream(), []
+    for ext in (None, False):
+        monkeypatch.setattr(api, "_ops_ext", ext)
+        x, lst = some_pools(torch.Generator("cuda").manual_seed(12), 2, c["num"], 2, 64, BF)
+        qo, ko, r2t = torch.empty(80, 4, 64, dtype=BF, device="cuda"), torch.empty(80, 2, 64, dtype=BF, device="cuda"), i32([[0] * 56] * 2, "cuda")
+        out, lse, fork = torch.empty_like(qo), torch.empty(80, 4, device="cuda"), i32([[0] * 60] * 2, "cuda")
+        torch.cuda.synchronize()
+        for s in (None, stream, stream.cuda_stream):
+            api.kv_pool_write_rope(desc, rope, 2, c["ps"], c["pi"], c["ns"], c["qi"], c["pos"], c["q"], c["k"], c["v"], qo, ko, *lst, r2t, 80,
+                                   st, stream=s)
+            api.kv_pool_write_rope(desc, rope, 2, c["ps"].data_ptr(), c["pi"].data_ptr(), c["ns"], c["qi"], c["pos"], c["q"], c["k"], c["v"],
+                                   qo, ko, *lst, r2t.data_ptr(), 80, st, stream=s, r2t_stride=56)
+            api.prompt_attention(desc, 2, qo, ko, c["v"], c["qi"], out, lse, 80, st, stream=s)
+            api.kv_pool_copy(desc, lst, c["ps"], c["ns"][:3].contiguous(), 1, st, stream=s)
+            api.kv_pool_fork(desc, lst, i32([1, 0], "cuda"), i32([40, 33], "cuda"), i32([50, 33], "cuda"), indptr([10, 0], "cuda"), c["ns"][:10].contiguous(),
+                             r2t, fork, 10, st, stream=s)
+            torch.cuda.synchronize()
+        results.append((x, qo, ko, r2t, out, lse, fork))
+    assert int(st.item()) == 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 # ============================================================================ prompt_attention
