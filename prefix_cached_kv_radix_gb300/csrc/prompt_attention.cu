@@ -135,6 +135,42 @@ __device__ __forceinline__ int clc_answer(uint32_t answer) {
     return ok ? (int)x : -1;
 }
 
+// ---------------------------------------------------------------- tensor core instructions of a warp
+// The whole warp runs the issuing code, so that addresses and descriptors stay warp-uniform, and
+// one elected lane issues.  Descriptors (sdesc_sw128) come as their low word (start address, leading
+// offset); the high word (stride offset 1024 bytes, version, 128-byte swizzle) is the same for all.
+constexpr uint32_t PT_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void pt_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(PT_DESC_HI)
+        : "memory");
+}
+
+__device__ __forceinline__ void pt_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(PT_DESC_HI)
+        : "memory");
+}
+
+__device__ __forceinline__ void pt_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_constant__ PromptTcParams p) {
     using LY = PtLayout<D>;
@@ -257,51 +293,51 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ tcgen05.mma
-            if (lane == 0) {
+            {
                 constexpr uint32_t IDESC_S = idesc_bf16_f32(128, PT_BN, 0, 0);
                 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
-                const uint64_t qd0 = sdesc_sw128(base + LY::OFF_Q, 16, 1024);
-                const uint64_t kd0 = sdesc_sw128(base + LY::OFF_K, 16, 1024);
-                const uint64_t vd0 = sdesc_sw128(base + LY::OFF_V, PT_BN * 128, 1024);
+                const uint32_t qd0 = (uint32_t)sdesc_sw128(base + LY::OFF_Q, 16, 1024);
+                const uint32_t kd0 = (uint32_t)sdesc_sw128(base + LY::OFF_K, 16, 1024);
+                const uint32_t vd0 = (uint32_t)sdesc_sw128(base + LY::OFF_V, PT_BN * 128, 1024);
                 auto issue_s = [&](int t, int ks) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        umma_f16_ss(tmem + t * PT_BN,
-                                    qd0 + (uint64_t)((t * LY::Q_TILE + (s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
-                                    kd0 + (uint64_t)((ks * LY::KV_TILE + (s >> 2) * PT_BN * 128 + (s & 3) * 32) >> 4), IDESC_S,
+                        pt_mma_ss(tmem + t * PT_BN,
+                                    qd0 + (uint32_t)((t * LY::Q_TILE + (s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
+                                    kd0 + (uint32_t)((ks * LY::KV_TILE + (s >> 2) * PT_BN * 128 + (s & 3) * 32) >> 4), IDESC_S,
                                     s > 0 ? 1u : 0u);
-                    umma_commit(bar(LY::BAR_S + t));
+                    pt_commit(bar(LY::BAR_S + t));
                 };
                 auto issue_pv = [&](int t, int vs, int j, int h) {   // keys 64h .. 64h+63 of the tile
 #pragma unroll
                     for (int s = h * (PT_BN / 32); s < (h + 1) * (PT_BN / 32); ++s)
-                        umma_f16_ts(tmem + LY::COL_O0 + t * D, tmem + t * PT_BN + s * 8,
-                                    vd0 + (uint64_t)((vs * LY::KV_TILE + s * 16 * 128) >> 4), IDESC_PV, (j > 0 || s > 0) ? 1u : 0u);
+                        pt_mma_ts(tmem + LY::COL_O0 + t * D, tmem + t * PT_BN + s * 8,
+                                    vd0 + (uint32_t)((vs * LY::KV_TILE + s * 16 * 128) >> 4), IDESC_PV, (j > 0 || s > 0) ? 1u : 0u);
                 };
                 int gt = 0, sc0 = 0, sc1 = 0;   // K/V tiles, and score steps of each Q tile, so far
                 bool ok = true;
                 for (int k = 0; ok; ++k) {
                     const int e = k % PT_RING;
-                    if (!mbar_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
+                    if (!warp_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
                     PtItem it;
                     ring_item(k, it);
                     if (it.n < 0) break;
                     const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
                     const int nkv = max(n0, n1);
-                    ok = mbar_wait(bar(LY::BAR_Q), k & 1, abort_flag, status) &&
-                         mbar_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag, status);
+                    ok = warp_wait(bar(LY::BAR_Q), k & 1, abort_flag, status) &&
+                         warp_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag, status);
                     if (!ok) break;
                     tc_fence_after();
                     issue_s(0, gt % NK);
-                    if (n0 == 1) umma_commit(bar(LY::BAR_QE));
+                    if (n0 == 1) pt_commit(bar(LY::BAR_QE));
                     if (n1 > 0) {
                         issue_s(1, gt % NK);
-                        if (n1 == 1) umma_commit(bar(LY::BAR_QE + 1));
+                        if (n1 == 1) pt_commit(bar(LY::BAR_QE + 1));
                     }
-                    umma_commit(bar(LY::BAR_KE + gt % NK));
+                    pt_commit(bar(LY::BAR_KE + gt % NK));
                     for (int j = 0; ok && j < nkv; ++j) {
                         const int u = gt + j, vs = u % NV, ks = (u + 1) % NK;
-                        ok = mbar_wait(bar(LY::BAR_VF + vs), (u / NV) & 1, abort_flag, status);
+                        ok = warp_wait(bar(LY::BAR_VF + vs), (u / NV) & 1, abort_flag, status);
                         if (!ok) break;
                         tc_fence_after();
                         bool have_k = false;
@@ -309,33 +345,33 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                             const int nt = t == 0 ? n0 : n1;
                             if (j >= nt) continue;
                             const int ph = ((t == 0 ? sc0 : sc1) + j) & 1;
-                            if (!(ok = mbar_wait(bar(LY::BAR_P + t), ph, abort_flag, status))) break;
+                            if (!(ok = warp_wait(bar(LY::BAR_P + t), ph, abort_flag, status))) break;
                             tc_fence_after();
                             issue_pv(t, vs, j, 0);
-                            if (!(ok = mbar_wait(bar(LY::BAR_P + 2 + t), ph, abort_flag, status))) break;
+                            if (!(ok = warp_wait(bar(LY::BAR_P + 2 + t), ph, abort_flag, status))) break;
                             tc_fence_after();
                             issue_pv(t, vs, j, 1);
-                            if (t == 1 || j >= n1) umma_commit(bar(LY::BAR_VE + vs));   // V(u) read by every tile
+                            if (t == 1 || j >= n1) pt_commit(bar(LY::BAR_VE + vs));   // V(u) read by every tile
                             if (j + 1 < nt) {
                                 if (!have_k) {
-                                    if (!(ok = mbar_wait(bar(LY::BAR_KF + ks), ((u + 1) / NK) & 1, abort_flag, status))) break;
+                                    if (!(ok = warp_wait(bar(LY::BAR_KF + ks), ((u + 1) / NK) & 1, abort_flag, status))) break;
                                     tc_fence_after();
                                     have_k = true;
                                 }
                                 issue_s(t, ks);
-                                if (j + 2 == nt) umma_commit(bar(LY::BAR_QE + t));   // the item's last S_t
+                                if (j + 2 == nt) pt_commit(bar(LY::BAR_QE + t));   // the item's last S_t
                             } else {
-                                umma_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
+                                pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
                             }
                         }
-                        if (ok && j + 1 < nkv) umma_commit(bar(LY::BAR_KE + ks));
+                        if (ok && j + 1 < nkv) pt_commit(bar(LY::BAR_KE + ks));
                     }
                     sc0 += n0;
                     sc1 += n1;
                     gt += nkv;
-                    mbar_arrive(bar(LY::BAR_IE + e));
+                    if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
                 }
-                umma_commit(bar(LY::BAR_DONE));
+                pt_commit(bar(LY::BAR_DONE));
             }
             __syncwarp();
         } else if (warp == 2) {
