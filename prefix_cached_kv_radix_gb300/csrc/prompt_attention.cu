@@ -15,15 +15,17 @@
 // head), two Q tiles share each K/V tile of 128 keys.  One CTA per SM; the CTAs that run take the
 // items of those that have not been launched (clusterlaunchcontrol.try_cancel), so the assignment
 // is dynamic without a counter in memory: launches on several streams and replays of captured
-// graphs share nothing.  Roles (384 threads):
+// graphs share nothing.  Roles (512 threads):
 //   warp 0      takes and decodes the items, hands them on through a ring in shared memory, and
 //               loads their Q tiles as the buffers come free
-//   warp 1      one thread issues the tcgen05.mma: per K/V tile j and Q tile t
+//   warp 1      issues the tcgen05.mma: per K/V tile j and Q tile t
 //               O_t += P_t(j) V(j) in two halves of 64 keys as P comes in (P from TMEM), then at
-//               once S_t(j+1) = Q_t K(j+1)^T over the columns P was read from
+//               once S_t(j+1) = Q_t K(j+1)^T over the columns P was read from, or the next item's
+//               first scores
 //   warp 2      loads K and V tiles into rings of their own, on into the next items
 //   warp 3      TMEM; clears what must not enter a sum (below)
-//   warps 4-7, 8-11   softmax and output of Q tile 0 and 1, a row per thread
+//   warps 4-7, 8-11   softmax of Q tile 0 and 1, a row per thread
+//   warps 12-15 the items' output from TMEM, while the others are on the next item
 // While one tile's softmax runs the tensor core works on the other's products.
 //
 // Rows that a row must not see: a masked score is replaced after the product, so nothing of a
@@ -52,12 +54,12 @@
 namespace rx {
 
 constexpr int PT_BN = 128;         // keys per K/V tile
-constexpr int PT_THREADS = 384;
+constexpr int PT_THREADS = 512;
 constexpr int PT_RING = 4;         // items in flight between the roles
-constexpr int PT_CONSUMERS = 11;   // MMA thread, K/V warp, clearing warp, eight softmax warps
+constexpr int PT_CONSUMERS = 15;   // MMA warp, K/V warp, clearing warp, eight softmax warps, four output warps
 constexpr int PT_CUT = 3;          // K/V tiles of an item that a mask or the sequence's end can cut
-// 128 * 72 + 256 * 216 = 384 * 168
-constexpr uint32_t PT_REGS_SOFTMAX = 216, PT_REGS_OTHER = 72, PT_REGS_LAUNCH = 168;
+// 2 * 128 * 80 + 2 * 128 * 176 = 512 * 128
+constexpr uint32_t PT_REGS_SOFTMAX = 176, PT_REGS_OTHER = 80, PT_REGS_LAUNCH = 128;
 constexpr float PT_LOG2E = 1.4426950408889634f;
 constexpr float PT_LN2 = 0.6931471805599453f;
 constexpr float PT_RESCALE = 8.0f;   // log2 units
@@ -81,16 +83,17 @@ struct PtLayout {
     static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
     static constexpr int OFF_V = OFF_K + NK * KV_TILE;
     static constexpr int OFF_BAR = OFF_V + NV * KV_TILE;
-    static constexpr int BAR_Q = 0, BAR_KF = 1, BAR_KE = BAR_KF + NK, BAR_VF = BAR_KE + NK, BAR_VE = BAR_VF + NV,
+    static constexpr int BAR_Q = 0, BAR_KF = 2, BAR_KE = BAR_KF + NK, BAR_VF = BAR_KE + NK, BAR_VE = BAR_VF + NV,
                          BAR_VX = BAR_VE + NV,      // a cut V tile is in, but not yet cleared
                          BAR_S = BAR_VX + NV, BAR_P = BAR_S + 2, BAR_QE = BAR_P + 4, BAR_OR = BAR_QE + 2,
-                         BAR_IF = BAR_OR + 2, BAR_IE = BAR_IF + PT_RING,
+                         BAR_OE = BAR_OR + 2, BAR_L = BAR_OE + 2, BAR_IF = BAR_L + 2, BAR_IE = BAR_IF + PT_RING,
                          BAR_IC = BAR_IE + PT_RING,   // every cut tile of an item has been cleared
                          BAR_CLC = BAR_IC + PT_RING, BAR_DONE = BAR_CLC + 1, NBAR = BAR_DONE + 1;
     static constexpr int OFF_CLC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // answer of try_cancel
     static constexpr int OFF_RING = OFF_CLC + 16;                       // int4 per entry
     static constexpr int OFF_BAD = OFF_RING + 16 * PT_RING;             // non-finite keys: PT_CUT * 4 words per entry
-    static constexpr int OFF_MISC = OFF_BAD + PT_RING * PT_CUT * 16;    // TMEM address, abort flag
+    static constexpr int OFF_INV = OFF_BAD + PT_RING * PT_CUT * 16;     // 1 / l of each row of the Q tiles
+    static constexpr int OFF_MISC = OFF_INV + 2 * 128 * 4;              // TMEM address, abort flag
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int ALLOC = BYTES + 1024;   // room to align the base to 1024 B
     static constexpr uint32_t TMEM_COLS = 512;
@@ -137,38 +140,75 @@ __device__ __forceinline__ int clc_answer(uint32_t answer) {
 
 // ---------------------------------------------------------------- tensor core instructions of a warp
 // The whole warp runs the issuing code, so that addresses and descriptors stay warp-uniform, and
-// one elected lane issues.  Descriptors (sdesc_sw128) come as their low word (start address, leading
-// offset); the high word (stride offset 1024 bytes, version, 128-byte swizzle) is the same for all.
+// one elected lane issues a group of products.  (Issued under `if (lane == 0)`, one product at a
+// time, they took 75 clocks each where the tensor core needs 64.)  Descriptors (sdesc_sw128) come as
+// their low word (start address in 16-byte units, leading offset); the high word (stride offset 1024
+// bytes, version, 128-byte swizzle) is the same for all.
 constexpr uint32_t PT_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-__device__ __forceinline__ void pt_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(PT_DESC_HI)
-        : "memory");
+#define PT_SS(DA, DB, ACC)                                                     \
+    "add.u32 a, %1, " #DA ";\n\tadd.u32 b, %2, " #DB ";\n\t"                   \
+    "mov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t"                         \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, " #ACC ";\n\t"
+#define PT_TS(TA, DB, ACC)                                                     \
+    "add.u32 a, %1, " #TA ";\n\tadd.u32 b, %2, " #DB ";\n\t"                   \
+    "mov.b64 db, {b, %4};\n\t"                                                 \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, " #ACC ";\n\t"
+#define PT_GROUP "{\n\t.reg .pred e, t, f;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\telect.sync _|e, 0xffffffff;\n\t"
+
+// S[128 x 128] = Q K^T over D channels: 16 channels (32 bytes) an instruction, 64 a 16 KB half tile.
+template <int D>
+__device__ __forceinline__ void pt_mma_s(uint32_t s, uint32_t q, uint32_t k, uint32_t idesc) {
+    if constexpr (D == 128)
+        asm volatile(PT_GROUP "setp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t" PT_SS(0, 0, f) PT_SS(2, 2, t) PT_SS(4, 4, t)
+                         PT_SS(6, 6, t) PT_SS(1024, 1024, t) PT_SS(1026, 1026, t) PT_SS(1028, 1028, t) PT_SS(1030, 1030, t) "}" ::"r"(s),
+                     "r"(q), "r"(k), "r"(idesc), "r"(PT_DESC_HI)
+                     : "memory");
+    else
+        asm volatile(PT_GROUP "setp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t" PT_SS(0, 0, f) PT_SS(2, 2, t) PT_SS(4, 4, t)
+                         PT_SS(6, 6, t) "}" ::"r"(s),
+                     "r"(q), "r"(k), "r"(idesc), "r"(PT_DESC_HI)
+                     : "memory");
 }
 
-__device__ __forceinline__ void pt_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 db, {%2, %5};\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(PT_DESC_HI)
-        : "memory");
+// O[128 x D] += P V over 64 keys: 16 keys (8 TMEM columns of P, 2 KB of V) an instruction; with
+// `fresh` the first of them overwrites O.
+__device__ __forceinline__ void pt_mma_pv(uint32_t o, uint32_t pt, uint32_t v, uint32_t idesc, bool fresh) {
+    asm volatile(PT_GROUP "setp.eq.u32 t, 0, 0;\n\tsetp.eq.u32 f, %5, 0;\n\t" PT_TS(0, 0, f) PT_TS(8, 128, t) PT_TS(16, 256, t)
+                     PT_TS(24, 384, t) "}" ::"r"(o),
+                 "r"(pt), "r"(v), "r"(idesc), "r"(PT_DESC_HI), "r"(fresh ? 1u : 0u)
+                 : "memory");
 }
+#undef PT_SS
+#undef PT_TS
+#undef PT_GROUP
 
 __device__ __forceinline__ void pt_commit(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
+}
+
+// ---------------------------------------------------------------- waits
+// A whole warp's bounded wait (2 s) on an mbarrier phase; on time-out it sets *abort, which ends
+// every role's waits and is reported once, at the end.  As short as can be: there are some thirty
+// waits in the kernel, and an item of a short sequence runs every role's code once, so that
+// fetching instructions is much of its time.
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    bool ok = mbar_try_wait(bar, parity);     // up to 100 us by itself
+    if (!ok) {
+        auto now = [] {
+            uint32_t t;
+            asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+            return t;
+        };
+        const uint32_t t0 = now();
+        do ok = mbar_try_wait(bar, parity);
+        while (!ok && !*abort && now() - t0 < 2000000000u);
+        if (!ok) *abort = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 template <int D>
@@ -185,11 +225,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + LY::OFF_MISC + 4);
     int4* ring = reinterpret_cast<int4*>(gbase + LY::OFF_RING);
     uint32_t* bad = reinterpret_cast<uint32_t*>(gbase + LY::OFF_BAD);
+    float* inv_l = reinterpret_cast<float*>(gbase + LY::OFF_INV);
     int32_t* const status = p.a.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(LY::BAR_Q), 1);
         for (int i = 0; i < NK; ++i) {
             mbar_init(bar(LY::BAR_KF + i), 1);
             mbar_init(bar(LY::BAR_KE + i), 1);
@@ -200,11 +240,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             mbar_init(bar(LY::BAR_VX + i), 1);
         }
         for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(LY::BAR_Q + t), 1);
             mbar_init(bar(LY::BAR_S + t), 1);
             mbar_init(bar(LY::BAR_P + t), 4);          // one arrival per softmax warp, keys 0-63
             mbar_init(bar(LY::BAR_P + 2 + t), 4);      // keys 64-127
             mbar_init(bar(LY::BAR_QE + t), 1);         // Q buffer t read by its item's last S
             mbar_init(bar(LY::BAR_OR + t), 1);         // O_t of an item complete
+            mbar_init(bar(LY::BAR_OE + t), 4);         // and read by the output warps
+            mbar_init(bar(LY::BAR_L + t), 4);          // 1 / l of an item's rows written
         }
         for (int i = 0; i < PT_RING; ++i) {
             mbar_init(bar(LY::BAR_IF + i), 1);
@@ -234,7 +277,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         regs_decrease<PT_REGS_OTHER>();
         if (warp == 0) {
             // ------------------------------------------------------------ items and Q
-            int64_t place = blockIdx.x;
+            int place = (int)blockIdx.x;
+            PromptFinder finder;
             int k = 0, use0 = 0, use1 = 0, asked = 0;
             bool ok = true;
             for (;;) {
@@ -244,33 +288,33 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     clc_try_cancel(base + LY::OFF_CLC, bar(LY::BAR_CLC));
                 }
                 PromptItem w;
-                if (prompt_item(p.a, place, p.tpt * p.tiles, p.a.hkv * p.nhb, w)) {
+                if (finder.find(p.a, place, p.tpt * p.tiles, p.a.hkv * p.nhb, w)) {
                     PtItem it;
-                    it.start = (int)w.start, it.n = w.n, it.t0 = w.tile * p.tpt * p.tiles, it.head = w.head;
+                    it.start = w.start, it.n = w.n, it.t0 = w.tile * p.tpt * p.tiles, it.head = w.head;
                     const int e = k % PT_RING;
-                    ok = k < PT_RING || warp_wait(bar(LY::BAR_IE + e), ((k / PT_RING) - 1) & 1, abort_flag, status);
+                    ok = k < PT_RING || pt_wait(bar(LY::BAR_IE + e), ((k / PT_RING) - 1) & 1, abort_flag);
                     if (ok && lane == 0) {
                         ring[e] = make_int4(it.start, it.n, it.t0, it.head);
                         mbar_arrive(bar(LY::BAR_IF + e));
                     }
                     ++k;
                     const bool two = p.tiles > 1 && it.nkv(1, p.tpt) > 0;
-                    ok = ok && (use0 == 0 || warp_wait(bar(LY::BAR_QE), (use0 - 1) & 1, abort_flag, status));
-                    ok = ok && (!two || use1 == 0 || warp_wait(bar(LY::BAR_QE + 1), (use1 - 1) & 1, abort_flag, status));
-                    if (!ok) break;
-                    ++use0;
-                    use1 += two ? 1 : 0;
-                    if (lane == 0) {
-                        const int g = it.head / p.nhb, h0 = g * p.group + (it.head - g * p.nhb) * p.hb;
-                        const int nt = two ? 2 : 1;
-                        mbar_arrive_expect_tx(bar(LY::BAR_Q), (uint32_t)(nt * p.hb * p.tpt * D * 2));
-                        for (int t = 0; t < nt; ++t)
+                    const int g = it.head / p.nhb, h0 = g * p.group + (it.head - g * p.nhb) * p.hb;
+                    for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+                        int& use = t == 0 ? use0 : use1;
+                        ok = use == 0 || pt_wait(bar(LY::BAR_QE + t), (use - 1) & 1, abort_flag);
+                        if (!ok) break;
+                        ++use;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(LY::BAR_Q + t), (uint32_t)(p.hb * p.tpt * D * 2));
                             for (int c = 0; c < D / 64; ++c)
                                 tma_load_3d(base + LY::OFF_Q + t * LY::Q_TILE + c * 128 * 128, &p.q_map, c * 64, h0,
-                                            it.start + it.t0 + t * p.tpt, bar(LY::BAR_Q));
+                                            it.start + it.t0 + t * p.tpt, bar(LY::BAR_Q + t));
+                        }
                     }
+                    if (!ok) break;
                 }
-                ok = warp_wait(bar(LY::BAR_CLC), asked & 1, abort_flag, status);
+                ok = pt_wait(bar(LY::BAR_CLC), asked & 1, abort_flag);
                 if (!ok) break;
                 ++asked;
                 place = clc_answer(base + LY::OFF_CLC);
@@ -280,7 +324,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             }
             if (ok) {
                 const int e = k % PT_RING;
-                ok = k < PT_RING || warp_wait(bar(LY::BAR_IE + e), ((k / PT_RING) - 1) & 1, abort_flag, status);
+                ok = k < PT_RING || pt_wait(bar(LY::BAR_IE + e), ((k / PT_RING) - 1) & 1, abort_flag);
                 if (ok && lane == 0) {
                     ring[e] = make_int4(0, -1, 0, 0);
                     mbar_arrive(bar(LY::BAR_IF + e));
@@ -288,91 +332,116 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             }
             if (*abort_flag) {                // what was asked for may still be on its way
                 volatile int no_abort = 0;
-                if (use0 > 0) warp_wait(bar(LY::BAR_Q), (use0 - 1) & 1, &no_abort, status, 100000000ull);
-                if (place >= 0) warp_wait(bar(LY::BAR_CLC), asked & 1, &no_abort, status, 100000000ull);
+                if (use0 > 0) pt_wait(bar(LY::BAR_Q), (use0 - 1) & 1, &no_abort);
+                if (use1 > 0) pt_wait(bar(LY::BAR_Q + 1), (use1 - 1) & 1, &no_abort);
+                if (place >= 0) pt_wait(bar(LY::BAR_CLC), asked & 1, &no_abort);
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ tcgen05.mma
-            {
-                constexpr uint32_t IDESC_S = idesc_bf16_f32(128, PT_BN, 0, 0);
-                constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
-                const uint32_t qd0 = (uint32_t)sdesc_sw128(base + LY::OFF_Q, 16, 1024);
-                const uint32_t kd0 = (uint32_t)sdesc_sw128(base + LY::OFF_K, 16, 1024);
-                const uint32_t vd0 = (uint32_t)sdesc_sw128(base + LY::OFF_V, PT_BN * 128, 1024);
-                auto issue_s = [&](int t, int ks) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        pt_mma_ss(tmem + t * PT_BN,
-                                    qd0 + (uint32_t)((t * LY::Q_TILE + (s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
-                                    kd0 + (uint32_t)((ks * LY::KV_TILE + (s >> 2) * PT_BN * 128 + (s & 3) * 32) >> 4), IDESC_S,
-                                    s > 0 ? 1u : 0u);
-                    pt_commit(bar(LY::BAR_S + t));
-                };
-                auto issue_pv = [&](int t, int vs, int j, int h) {   // keys 64h .. 64h+63 of the tile
-#pragma unroll
-                    for (int s = h * (PT_BN / 32); s < (h + 1) * (PT_BN / 32); ++s)
-                        pt_mma_ts(tmem + LY::COL_O0 + t * D, tmem + t * PT_BN + s * 8,
-                                    vd0 + (uint32_t)((vs * LY::KV_TILE + s * 16 * 128) >> 4), IDESC_PV, (j > 0 || s > 0) ? 1u : 0u);
-                };
-                int gt = 0, sc0 = 0, sc1 = 0;   // K/V tiles, and score steps of each Q tile, so far
-                bool ok = true;
-                for (int k = 0; ok; ++k) {
-                    const int e = k % PT_RING;
-                    if (!warp_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
-                    PtItem it;
-                    ring_item(k, it);
-                    if (it.n < 0) break;
-                    const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
-                    const int nkv = max(n0, n1);
-                    ok = warp_wait(bar(LY::BAR_Q), k & 1, abort_flag, status) &&
-                         warp_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag, status);
+            constexpr uint32_t IDESC_S = idesc_bf16_f32(128, PT_BN, 0, 0);
+            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
+            const uint32_t qd0 = (uint32_t)sdesc_sw128(base + LY::OFF_Q, 16, 1024);
+            const uint32_t kd0 = (uint32_t)sdesc_sw128(base + LY::OFF_K, 16, 1024);
+            const uint32_t vd0 = (uint32_t)sdesc_sw128(base + LY::OFF_V, PT_BN * 128, 1024);
+            auto issue_s = [&](int t, uint32_t ks, bool last) {     // last: no later S of this item reads Q_t
+                pt_mma_s<D>(tmem + t * PT_BN, qd0 + t * (uint32_t)(LY::Q_TILE >> 4), kd0 + ks * (uint32_t)(LY::KV_TILE >> 4), IDESC_S);
+                pt_commit(bar(LY::BAR_S + t));
+                if (last) pt_commit(bar(LY::BAR_QE + t));
+            };
+            auto issue_pv = [&](int t, uint32_t vs, int h, bool fresh) {   // keys 64h .. 64h+63 of the tile
+                pt_mma_pv(tmem + LY::COL_O0 + t * D, tmem + t * PT_BN + h * 32, vd0 + vs * (uint32_t)(LY::KV_TILE >> 4) + h * 512u,
+                          IDESC_PV, fresh);
+            };
+            auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
+            // ring positions: the next K tile to be multiplied by Q, the V tile of the current step
+            uint32_t ks = 0, kph = 0, vs = 0, vph = 0;
+            auto k_next = [&](uint32_t& slot, uint32_t& ph) {
+                if (++slot == NK) slot = 0, ph ^= 1;
+            };
+            uint32_t pph = 0;               // phases of the P barriers (bit t), a step each
+            int items0 = 0, items1 = 0;     // items of each Q tile so far
+            bool s0_issued = false;         // S_0 of the coming item's first K tile is on its way
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int e = k % PT_RING;
+                if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+                PtItem it;
+                ring_item(k, it);
+                if (it.n < 0) break;
+                const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
+                const int nkv = max(n0, n1);
+                if (!s0_issued) {
+                    ok = pt_wait(bar(LY::BAR_Q), items0 & 1, abort_flag) &&
+                         pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_s(0, gt % NK);
-                    if (n0 == 1) pt_commit(bar(LY::BAR_QE));
-                    if (n1 > 0) {
-                        issue_s(1, gt % NK);
-                        if (n1 == 1) pt_commit(bar(LY::BAR_QE + 1));
-                    }
-                    pt_commit(bar(LY::BAR_KE + gt % NK));
-                    for (int j = 0; ok && j < nkv; ++j) {
-                        const int u = gt + j, vs = u % NV, ks = (u + 1) % NK;
-                        ok = warp_wait(bar(LY::BAR_VF + vs), (u / NV) & 1, abort_flag, status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        bool have_k = false;
-                        for (int t = 0; ok && t < 2; ++t) {
-                            const int nt = t == 0 ? n0 : n1;
-                            if (j >= nt) continue;
-                            const int ph = ((t == 0 ? sc0 : sc1) + j) & 1;
-                            if (!(ok = warp_wait(bar(LY::BAR_P + t), ph, abort_flag, status))) break;
+                    issue_s(0, ks, n0 == 1);
+                }
+                s0_issued = false;
+                if (n1 > 0) {
+                    if (!(ok = pt_wait(bar(LY::BAR_Q + 1), items1 & 1, abort_flag))) break;
+                    tc_fence_after();
+                    issue_s(1, ks, n1 == 1);
+                }
+                pt_commit(bar(LY::BAR_KE + ks));
+                k_next(ks, kph);
+                for (int j = 0; ok && j < nkv; ++j) {
+                    if (!(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t == 0 ? n0 : n1, before = t == 0 ? items0 : items1;
+                        if (!ok || j >= nt) continue;
+                        // the previous item's O_t has been read out
+                        if (j == 0 && before > 0 && !(ok = pt_wait(bar(LY::BAR_OE + t), (before - 1) & 1, abort_flag)))
+                            continue;
+                        const uint32_t ph = (pph >> t) & 1;
+#pragma unroll 1
+                        for (int h = 0; ok && h < 2; ++h) {
+                            ok = pt_wait(bar(LY::BAR_P + 2 * h + t), ph, abort_flag);
                             tc_fence_after();
-                            issue_pv(t, vs, j, 0);
-                            if (!(ok = warp_wait(bar(LY::BAR_P + 2 + t), ph, abort_flag, status))) break;
+                            if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
+                        }
+                        if (!ok) continue;
+                        pph ^= 1u << t;
+                        if (t == 1 || j >= n1) pt_commit(bar(LY::BAR_VE + vs));   // V read by every tile
+                        if (j + 1 < nt) {
+                            if ((t == 0 || j + 1 >= n0) && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) continue;
                             tc_fence_after();
-                            issue_pv(t, vs, j, 1);
-                            if (t == 1 || j >= n1) pt_commit(bar(LY::BAR_VE + vs));   // V(u) read by every tile
-                            if (j + 1 < nt) {
-                                if (!have_k) {
-                                    if (!(ok = warp_wait(bar(LY::BAR_KF + ks), ((u + 1) / NK) & 1, abort_flag, status))) break;
-                                    tc_fence_after();
-                                    have_k = true;
+                            issue_s(t, ks, j + 2 == nt);
+                        } else {
+                            pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
+                            if (t == 0) {
+                                // the next item's first scores at once, if all they need is here already:
+                                // their softmax then runs under this item's last products of the other tile
+                                uint32_t ks2 = ks, kph2 = kph;
+                                for (int i = j + 1; i < nkv; ++i) k_next(ks2, kph2);
+                                const int e2 = (k + 1) % PT_RING;
+                                if (ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1)) {
+                                    PtItem nx;
+                                    ring_item(k + 1, nx);
+                                    if (nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
+                                        tc_fence_after();
+                                        issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
+                                        s0_issued = true;
+                                    }
                                 }
-                                issue_s(t, ks);
-                                if (j + 2 == nt) pt_commit(bar(LY::BAR_QE + t));   // the item's last S_t
-                            } else {
-                                pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
                             }
                         }
-                        if (ok && j + 1 < nkv) pt_commit(bar(LY::BAR_KE + ks));
                     }
-                    sc0 += n0;
-                    sc1 += n1;
-                    gt += nkv;
-                    if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
+                    if (!ok) break;
+                    if (j + 1 < nkv) {
+                        pt_commit(bar(LY::BAR_KE + ks));
+                        k_next(ks, kph);
+                    }
+                    if (++vs == NV) vs = 0, vph ^= 1;
                 }
-                pt_commit(bar(LY::BAR_DONE));
+                ++items0;
+                items1 += n1 > 0 ? 1 : 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
             }
+            pt_commit(bar(LY::BAR_DONE));
             __syncwarp();
         } else if (warp == 2) {
             // ------------------------------------------------------------ K and V tiles
@@ -380,7 +449,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int e = k % PT_RING;
-                if (!warp_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
+                if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
                 PtItem it;
                 ring_item(k, it);
                 if (it.n < 0) break;
@@ -388,7 +457,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const int g = it.head / p.nhb, cut = it.first_cut();
                 for (int j = 0; j < nkv; ++j) {
                     const int u = gt + j, ks = u % NK, vs = u % NV;
-                    ok = u < NK || warp_wait(bar(LY::BAR_KE + ks), ((u / NK) - 1) & 1, abort_flag, status);
+                    ok = u < NK || pt_wait(bar(LY::BAR_KE + ks), ((u / NK) - 1) & 1, abort_flag);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(LY::BAR_KF + ks), LY::KV_TILE);
@@ -396,7 +465,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                             tma_load_3d(base + LY::OFF_K + ks * LY::KV_TILE + c * PT_BN * 128, &p.k_map, c * 64, g,
                                         it.start + j * PT_BN, bar(LY::BAR_KF + ks));
                     }
-                    ok = u < NV || warp_wait(bar(LY::BAR_VE + vs), ((u / NV) - 1) & 1, abort_flag, status);
+                    ok = u < NV || pt_wait(bar(LY::BAR_VE + vs), ((u / NV) - 1) & 1, abort_flag);
                     if (!ok) break;
                     // a cut tile goes to warp 3 first, which hands it on (at most one per slot is on its way)
                     const uint32_t full = bar((j >= cut ? LY::BAR_VX : LY::BAR_VF) + vs);
@@ -424,7 +493,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int e = k % PT_RING;
-                if (!warp_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
+                if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
                 PtItem it;
                 ring_item(k, it);
                 if (it.n < 0) break;
@@ -434,7 +503,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 __syncwarp();
                 for (int j = cut; j < nkv; ++j) {
                     const int vs = (gt + j) % NV;
-                    ok = warp_wait(bar(LY::BAR_VX + vs), (ph >> vs) & 1, abort_flag, status);
+                    ok = pt_wait(bar(LY::BAR_VX + vs), (ph >> vs) & 1, abort_flag);
                     ph ^= 1u << vs;
                     if (!ok) break;
                     uint4* tile = reinterpret_cast<uint4*>(gbase + LY::OFF_V + vs * LY::KV_TILE);   // [D / 64][128 rows][8]
@@ -490,7 +559,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 }
             }
         }
-    } else {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ softmax warpgroups
         regs_increase<PT_REGS_SOFTMAX>();
         const int t = (warp >> 2) - 1;
@@ -498,14 +567,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         const int r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + t * PT_BN;   // scores, then P over them
-        const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;
+        const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;   // rescaled here, read out by the output warps
         const float sl = p.scale_log2;
         const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
         int sc = 0, oc = 0;                   // score steps and items of this Q tile so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int e = k % PT_RING;
-            if (!warp_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag, status)) break;
+            if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
             PtItem it;
             ring_item(k, it);
             if (it.n < 0) break;
@@ -514,7 +583,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             const int pos = min(tok, it.n - 1);          // attends keys 0..pos
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nkv; ++j) {
-                if (!warp_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag, status)) { ok = false; break; }
+                if (!pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 float s[PT_BN];
 #pragma unroll
@@ -523,8 +592,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const int lim = pos - j * PT_BN;   // columns past lim are masked
                 if (lim < PT_BN - 1) {
 #pragma unroll
-                    for (int c = 0; c < PT_BN; ++c)
-                        if (c > lim) s[c] = -INFINITY;
+                    for (int c = 0; c < PT_BN; c += 32) {
+                        const int left = lim - c;      // of these 32 columns, 0 .. left are seen
+                        const uint32_t see = left >= 31 ? 0xffffffffu : left < 0 ? 0u : (2u << left) - 1u;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!((see >> x) & 1u)) s[c + x] = -INFINITY;
+                    }
                 }
                 float mx8[8];
 #pragma unroll
@@ -587,48 +661,68 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             if (!ok) break;
             sc += nkv;
             if (nkv > 0) {
-                const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
-                const bool valid = row_tok < p.tpt && tok < it.n && hh < p.group;
-                // The item's O_t is complete once its last PV has: it is read while the tensor core
-                // works on the next item's scores; the next item's first PV (which overwrites O_t)
-                // waits for P that this warpgroup publishes after the reads.
-                if (!warp_wait(bar(LY::BAR_OR + t), oc & 1, abort_flag, status) ||
-                    !warp_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag, status))
-                    break;
+                // 1 / l for the output warps, once they have read the last item's
+                if (oc > 0 && !pt_wait(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
                 oc += 1;
+                inv_l[t * 128 + r] = 1.f / l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(LY::BAR_L + t));
+                const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
+                if (p.a.lse && row_tok < p.tpt && tok < it.n && hh < p.group)
+                    p.a.lse[((int64_t)it.start + tok) * p.a.hq + g * p.group + hh] = (m_ref + log2f(l)) * PT_LN2;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
+        }
+    } else {
+        // ------------------------------------------------------------ output
+        regs_decrease<PT_REGS_OTHER>();
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
+        int done[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int e = k % PT_RING;
+            if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+            PtItem it;
+            ring_item(k, it);
+            if (it.n < 0) break;
+            const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
+            const uint32_t* mask = bad + e * PT_CUT * 4;
+            uint32_t any = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!ok || (t > 0 && (p.tiles < 2 || it.nkv(1, p.tpt) == 0))) continue;
+                ok = pt_wait(bar(LY::BAR_L + t), done[t] & 1, abort_flag) &&
+                     pt_wait(bar(LY::BAR_OR + t), done[t] & 1, abort_flag) &&
+                     (t > 0 || pt_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag));
+                if (!ok) continue;
+                ++done[t];
                 tc_fence_after();
-                const uint32_t* mask = bad + e * PT_CUT * 4;
-                uint32_t any = 0;
+                if (t == 0) {
 #pragma unroll
-                for (int w = 0; w < PT_CUT * 4; ++w) any |= mask[w];
-                const float inv = 1.f / l;
-                const int64_t row = (int64_t)it.start + tok;
-                const int h = g * p.group + hh;
-                __nv_bfloat16* orow = (__nv_bfloat16*)p.a.out + row * p.a.out_stride + (int64_t)h * D;
-#pragma unroll
+                    for (int w = 0; w < PT_CUT * 4; ++w) any |= mask[w];
+                }
+                const float inv = inv_l[t * 128 + r];
+                const int tok = it.t0 + t * p.tpt + row_tok;
+                const bool valid = row_tok < p.tpt && tok < it.n && hh < p.group;
+                const uint32_t o_addr = tmem + ((uint32_t)(quarter * 32) << 16) + LY::COL_O0 + t * D;
+                __nv_bfloat16* orow =
+                    (__nv_bfloat16*)p.a.out + ((int64_t)it.start + tok) * p.a.out_stride + (int64_t)(g * p.group + hh) * D;
+#pragma unroll 1
                 for (int cc = 0; cc < D; cc += 32) {
                     float ov[32];
                     tmem_ld32(o_addr + cc, ov);
                     tmem_wait_ld();
+                    if (cc + 32 == D) {          // read: the next item's first product may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(LY::BAR_OE + t));
+                    }
                     if (valid) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) ov[x] *= inv;
-                        if (any) {               // the non-finite values of the keys this row attends
-#pragma unroll 1
-                            for (int w = 0; w < PT_CUT * 4; ++w)
-#pragma unroll 1
-                                for (uint32_t b = mask[w]; b; b &= b - 1) {
-                                    const int key = it.first_cut() * PT_BN + w * 32 + __ffs(b) - 1;
-                                    if (key > pos) continue;
-                                    const __nv_bfloat16* vr = (const __nv_bfloat16*)p.a.v +
-                                                              ((int64_t)it.start + key) * p.a.v_stride + (int64_t)g * D + cc;
-#pragma unroll
-                                    for (int x = 0; x < 32; ++x) {
-                                        const float f = __bfloat162float(vr[x]);
-                                        if (!isfinite(f)) ov[x] += f;
-                                    }
-                                }
-                        }
 #pragma unroll
                         for (int x = 0; x < 32; x += 8) {
                             uint4 v;
@@ -639,9 +733,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                             *reinterpret_cast<uint4*>(orow + cc + x) = v;
                         }
                     }
+                    __syncwarp();                // the whole warp reads the next columns
                 }
-                if (valid && p.a.lse) p.a.lse[row * p.a.hq + h] = (m_ref + log2f(l)) * PT_LN2;
-                tc_fence_before();
+                // the non-finite values of the keys this row attends, added to what was just stored
+                if (any && valid) {
+#pragma unroll 1
+                    for (int w = 0; w < PT_CUT * 4; ++w)
+#pragma unroll 1
+                        for (uint32_t b = mask[w]; b; b &= b - 1) {
+                            const int key = it.first_cut() * PT_BN + w * 32 + __ffs(b) - 1;
+                            if (key > tok) break;
+                            const __nv_bfloat16* vr =
+                                (const __nv_bfloat16*)p.a.v + ((int64_t)it.start + key) * p.a.v_stride + (int64_t)g * D;
+#pragma unroll 1
+                            for (int x = 0; x < D; ++x) {
+                                const float f = __bfloat162float(vr[x]);
+                                if (!isfinite(f)) orow[x] = __float2bfloat16_rn(__bfloat162float(orow[x]) + f);
+                            }
+                        }
+                }
+                __syncwarp();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
@@ -650,6 +761,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     // ---------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) report(status, RX_DEV_TIMEOUT);
     if (warp == 3) {
         tc_fence_after();
         // every MMA this CTA issued has completed before TMEM is released; this wait does not stop
@@ -726,7 +838,7 @@ static int launch_pt(const PromptTcParams& p, unsigned grid, cudaStream_t stream
         }
         // the warpgroups re-split the registers the block is launched with (setmaxnreg); the shares
         // must add up to no more than that, or the increasing warps would wait forever
-        static_assert(128 * PT_REGS_OTHER + 256 * PT_REGS_SOFTMAX <= PT_THREADS * PT_REGS_LAUNCH, "register split");
+        static_assert(256 * PT_REGS_OTHER + 256 * PT_REGS_SOFTMAX <= PT_THREADS * PT_REGS_LAUNCH, "register split");
         cudaFuncAttributes fa{};
         if (cudaFuncGetAttributes(&fa, prompt_tc_kernel<D>) != cudaSuccess || fa.numRegs < (int)PT_REGS_LAUNCH) {
             set_error("prompt_attention: kernel built with %d registers per thread; the register split needs %d", fa.numRegs,

@@ -20,38 +20,67 @@ __host__ __device__ inline int64_t prompt_items(int64_t total, int32_t batch, in
 }
 
 struct PromptItem {
-    int64_t start;   // first row of the sequence
-    int n, head, tile;
+    int start, n, head, tile;   // first row and rows of the sequence, head, row tile
 };
 
-// Item `i` of the places x heads: within a sequence the heads one after another, and within a head
-// the tiles from the last, which has the most keys, to the first, so that the items that end a
-// launch are short ones.  False for a place left over, and for a sequence whose boundaries do not
-// lie in order in [0, total] (reported).  Every thread of a warp calls it with the same item.
-__device__ __forceinline__ bool prompt_item(const PromptParams& p, int64_t i, int tile_tokens, int heads, PromptItem& it) {
-    const int lane = threadIdx.x & 31;
-    auto base = [&](int b) { return p.indptr[b] / tile_tokens + b; };
-    int lo = 0, hi = p.batch;                        // base(lo) * heads <= i < base(hi) * heads, where they hold
-    while (hi - lo > 1) {                            // 32 evenly spaced sequences at a time
-        const int w = (hi - lo + 31) / 32, at = lo + lane * w;
-        const unsigned m = __ballot_sync(0xffffffffu, at < hi && (lane == 0 || base(at) * heads <= i));
-        const int last = 31 - __clz(m);
-        lo += last * w;
-        hi = min(hi, lo + w);
+// Finds the items' sequences.  A warp keeps 32 consecutive boundaries in its lanes: the items a
+// block takes one after another lie close together, so most are found without a memory access, and
+// the others in two or three rounds of loads.  32-bit arithmetic throughout: rows are below 2^31,
+// and a boundary that is not (the sequence is reported) is clamped.
+struct PromptFinder {
+    int w0 = -1;             // first boundary of the window (-1: none loaded)
+    int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last
+    bool good = false;       // it lies in [0, total]
+
+    __device__ __forceinline__ int load(const PromptParams& p, int b, bool& ok) const {
+        const int64_t x = p.indptr[b];
+        ok = x >= 0 && x <= p.total;
+        return (int)min(max(x, (int64_t)0), p.total);
     }
-    const int64_t s = p.indptr[lo], e = p.indptr[lo + 1];
-    if (s < 0 || e < s || e > p.total || e - s > INT32_MAX) {
-        if (lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
-        return false;
+
+    // Item `i` of the places x heads: within a sequence the heads one after another, and within a
+    // head the tiles from the last, which has the most keys, to the first, so that the items that
+    // end a launch are short ones.  False for a place left over, and for a sequence whose boundaries
+    // do not lie in order in [0, total] (reported).  Every thread of a warp calls it with the same item.
+    __device__ __forceinline__ bool find(const PromptParams& p, int i, int tile_tokens, int heads, PromptItem& it) {
+        const int lane = threadIdx.x & 31;
+        const int place = (unsigned)i / (unsigned)heads;      // place-major bound of the sequence: base(b) <= place
+        // the last sequence whose places start at or before this one
+        unsigned m = 0;
+        if (w0 >= 0) m = __ballot_sync(0xffffffffu, (unsigned)mine / (unsigned)tile_tokens + w0 + lane <= (unsigned)place);
+        if (m == 0 || (m >> 31)) {                            // not inside the window
+            int lo = 0, hi = p.batch;
+            bool ok;
+            while (hi - lo > 1) {                             // 32 evenly spaced sequences at a time
+                const int w = (hi - lo + 31) / 32, at = lo + lane * w;
+                const bool before = at < hi && (lane == 0 || (unsigned)load(p, at, ok) / (unsigned)tile_tokens + at <= (unsigned)place);
+                const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
+                lo += last * w;
+                hi = min(hi, lo + w);
+            }
+            w0 = lo;
+            mine = load(p, min(lo + lane, p.batch), good);
+            m = 1;
+        }
+        int l = 31 - __clz(m);
+        // beyond the last boundary every lane holds the last: the sequence is the last one
+        l = min(l, p.batch - 1 - w0);
+        const int b = w0 + l, s = __shfl_sync(0xffffffffu, mine, l), e = __shfl_sync(0xffffffffu, mine, l + 1);
+        const unsigned sound = __ballot_sync(0xffffffffu, good);
+        if (((sound >> l) & 3u) != 3u || e < s) {
+            if (lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
+            return false;
+        }
+        const unsigned first = (unsigned)s / (unsigned)tile_tokens;
+        const int places = (int)((unsigned)e / (unsigned)tile_tokens - first) + 1;
+        const int64_t at = i - (int64_t)(first + (unsigned)b) * heads;
+        if (at < 0 || at >= (int64_t)places * heads) return false;
+        it.head = (int)((unsigned)at / (unsigned)places);
+        it.tile = places - 1 - ((int)at - it.head * places);
+        it.start = s;
+        it.n = e - s;
+        return (int64_t)it.tile * tile_tokens < it.n;
     }
-    const int64_t places = e / tile_tokens - s / tile_tokens + 1;
-    const int64_t at = i - (s / tile_tokens + lo) * heads;
-    if (at < 0 || at >= places * heads) return false;
-    it.head = (int)(at / places);
-    it.tile = (int)(places - 1 - (at - it.head * places));
-    it.start = s;
-    it.n = (int)(e - s);
-    return (int64_t)it.tile * tile_tokens < it.n;
-}
+};
 
 }  // namespace rx

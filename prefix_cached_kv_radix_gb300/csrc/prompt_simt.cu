@@ -58,12 +58,13 @@ __global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_co
     extern __shared__ __align__(16) float sm[];
     const uint32_t sb = smem_u32(sm);
     PromptItem it;
-    if (!prompt_item(p, blockIdx.x, PS_BM, p.hq, it)) return;
+    PromptFinder finder;
+    if (!finder.find(p, (int)blockIdx.x, PS_BM, p.hq, it)) return;
     const int h = it.head, g = h / (p.hq / p.hkv);
     const int row0 = it.tile * PS_BM, rows = min(PS_BM, it.n - row0);
-    const float* q = (const float*)p.q + (it.start + row0) * p.q_stride + (int64_t)h * D;
-    const float* k = (const float*)p.k + it.start * p.k_stride + (int64_t)g * D;
-    const float* v = (const float*)p.v + it.start * p.v_stride + (int64_t)g * D;
+    const float* q = (const float*)p.q + (int64_t)(it.start + row0) * p.q_stride + (int64_t)h * D;
+    const float* k = (const float*)p.k + (int64_t)it.start * p.k_stride + (int64_t)g * D;
+    const float* v = (const float*)p.v + (int64_t)it.start * p.v_stride + (int64_t)g * D;
     const int keys = row0 + rows;                            // keys the block needs
     const int nkv = (keys + PS_BN - 1) / PS_BN;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;  // rows ty*8.., keys tx + 16 j, columns tx*4 + 64 c
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_co
         const int r = ty * 8 + i;
         if (r >= rows) continue;
         const float inv = 1.f / l[i];
-        float* orow = (float*)p.out + (it.start + row0 + r) * p.out_stride + (int64_t)h * D;
+        float* orow = (float*)p.out + (int64_t)(it.start + row0 + r) * p.out_stride + (int64_t)h * D;
 #pragma unroll
         for (int c = 0; c < OC; ++c) {
             float4 w;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_co
             w.x *= inv, w.y *= inv, w.z *= inv, w.w *= inv;
             *reinterpret_cast<float4*>(orow + tx * 4 + 64 * c) = w;
         }
-        if (p.lse && tx == 0) p.lse[(it.start + row0 + r) * p.hq + h] = m[i] + logf(l[i]);
+        if (p.lse && tx == 0) p.lse[(int64_t)(it.start + row0 + r) * p.hq + h] = m[i] + logf(l[i]);
     }
 }
 
