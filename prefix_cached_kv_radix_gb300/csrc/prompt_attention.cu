@@ -83,8 +83,9 @@ struct PtLayout {
     static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
     static constexpr int OFF_V = OFF_K + NK * KV_TILE;
     static constexpr int OFF_BAR = OFF_V + NV * KV_TILE;
-    static constexpr int BAR_Q = 0, BAR_KF = 2, BAR_KE = BAR_KF + NK, BAR_VF = BAR_KE + NK, BAR_VE = BAR_VF + NV,
-                         BAR_VX = BAR_VE + NV,      // a cut V tile is in, but not yet cleared
+    static constexpr int NE = 4;                   // steps whose ends the loads may wait for
+    static constexpr int BAR_Q = 0, BAR_KF = 2, BAR_VF = BAR_KF + NK, BAR_E = BAR_VF + NV,
+                         BAR_VX = BAR_E + NE,      // a cut V tile is in, but not yet cleared
                          BAR_S = BAR_VX + NV, BAR_P = BAR_S + 2, BAR_QE = BAR_P + 4, BAR_OR = BAR_QE + 2,
                          BAR_OE = BAR_OR + 2, BAR_L = BAR_OE + 2, BAR_IF = BAR_L + 2, BAR_IE = BAR_IF + PT_RING,
                          BAR_IC = BAR_IE + PT_RING,   // every cut tile of an item has been cleared
@@ -230,13 +231,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NK; ++i) {
-            mbar_init(bar(LY::BAR_KF + i), 1);
-            mbar_init(bar(LY::BAR_KE + i), 1);
-        }
+        for (int i = 0; i < NK; ++i) mbar_init(bar(LY::BAR_KF + i), 1);
+        for (int i = 0; i < LY::NE; ++i) mbar_init(bar(LY::BAR_E + i), 1);
         for (int i = 0; i < NV; ++i) {
             mbar_init(bar(LY::BAR_VF + i), 1);
-            mbar_init(bar(LY::BAR_VE + i), 1);
             mbar_init(bar(LY::BAR_VX + i), 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -353,15 +351,19 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                           IDESC_PV, fresh);
             };
             auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
-            // ring positions: the next K tile to be multiplied by Q, the V tile of the current step
-            uint32_t ks = 0, kph = 0, vs = 0, vph = 0;
+            // ring positions: the next K tile to be multiplied by Q, the V tile of the current step, the step's end
+            uint32_t ks = 0, kph = 0, vs = 0, vph = 0, es = 0;
             auto k_next = [&](uint32_t& slot, uint32_t& ph) {
                 if (++slot == NK) slot = 0, ph ^= 1;
             };
-            uint32_t pph = 0;               // phases of the P barriers (bit t), a step each
+            uint32_t pph0 = 0, pph1 = 0;    // phases of the P barriers, a step each
             int items0 = 0, items1 = 0;     // items of each Q tile so far
             bool s0_issued = false;         // S_0 of the coming item's first K tile is on its way
             bool ok = true;
+            // The tensor core works off what is issued in order and with some 400 clocks of it in its
+            // queue; what this warp does between two groups of products has to fit into that.  So the
+            // waits for K and V, which are long there, stand where the queue is full, and a step's end is
+            // committed once for the K and the V tile that it frees.
             for (int k = 0; ok; ++k) {
                 const int e = k % PT_RING;
                 if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
@@ -371,8 +373,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
                 const int nkv = max(n0, n1);
                 if (!s0_issued) {
-                    ok = pt_wait(bar(LY::BAR_Q), items0 & 1, abort_flag) &&
-                         pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
+                    ok = pt_wait(bar(LY::BAR_Q), items0 & 1, abort_flag) && pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     issue_s(0, ks, n0 == 1);
@@ -383,58 +384,64 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     tc_fence_after();
                     issue_s(1, ks, n1 == 1);
                 }
-                pt_commit(bar(LY::BAR_KE + ks));
                 k_next(ks, kph);
+                ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag);
                 for (int j = 0; ok && j < nkv; ++j) {
-                    if (!(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t == 0 ? n0 : n1, before = t == 0 ? items0 : items1;
-                        if (!ok || j >= nt) continue;
-                        // the previous item's O_t has been read out
-                        if (j == 0 && before > 0 && !(ok = pt_wait(bar(LY::BAR_OE + t), (before - 1) & 1, abort_flag)))
-                            continue;
-                        const uint32_t ph = (pph >> t) & 1;
-#pragma unroll 1
-                        for (int h = 0; ok && h < 2; ++h) {
-                            ok = pt_wait(bar(LY::BAR_P + 2 * h + t), ph, abort_flag);
-                            tc_fence_after();
-                            if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
-                        }
-                        if (!ok) continue;
-                        pph ^= 1u << t;
-                        if (t == 1 || j >= n1) pt_commit(bar(LY::BAR_VE + vs));   // V read by every tile
-                        if (j + 1 < nt) {
-                            if ((t == 0 || j + 1 >= n0) && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) continue;
-                            tc_fence_after();
-                            issue_s(t, ks, j + 2 == nt);
+                    const bool more = j + 1 < nkv;
+                    uint32_t vs1 = vs + 1, vph1 = vph;
+                    if (vs1 == NV) vs1 = 0, vph1 ^= 1;
+                    if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) break;
+                    if (j < n0) {
+                        // the previous item's O_0 has been read out
+                        if (j == 0 && items0 > 0 && !(ok = pt_wait(bar(LY::BAR_OE), (items0 - 1) & 1, abort_flag))) break;
+                        if (!(ok = pt_wait(bar(LY::BAR_P), pph0, abort_flag))) break;
+                        tc_fence_after();
+                        issue_pv(0, vs, 0, j == 0);
+                        if (!(ok = pt_wait(bar(LY::BAR_P + 2), pph0, abort_flag))) break;
+                        tc_fence_after();
+                        issue_pv(0, vs, 1, false);
+                        pph0 ^= 1;
+                        if (j + 1 < n0) {
+                            issue_s(0, ks, j + 2 == n0);
                         } else {
-                            pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
-                            if (t == 0) {
-                                // the next item's first scores at once, if all they need is here already:
-                                // their softmax then runs under this item's last products of the other tile
-                                uint32_t ks2 = ks, kph2 = kph;
-                                for (int i = j + 1; i < nkv; ++i) k_next(ks2, kph2);
-                                const int e2 = (k + 1) % PT_RING;
-                                if (ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1)) {
-                                    PtItem nx;
-                                    ring_item(k + 1, nx);
-                                    if (nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
-                                        tc_fence_after();
-                                        issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
-                                        s0_issued = true;
-                                    }
+                            pt_commit(bar(LY::BAR_OR));   // O_0 of this item complete
+                            // the next item's first scores at once, if all they need is here already:
+                            // their softmax then runs under this item's last products of the other tile
+                            uint32_t ks2 = ks, kph2 = kph;
+                            if (more) k_next(ks2, kph2);
+                            const int e2 = (k + 1) % PT_RING;
+                            if (ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1)) {
+                                PtItem nx;
+                                ring_item(k + 1, nx);
+                                if (nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
+                                    tc_fence_after();
+                                    issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
+                                    s0_issued = true;
                                 }
                             }
                         }
                     }
-                    if (!ok) break;
-                    if (j + 1 < nkv) {
-                        pt_commit(bar(LY::BAR_KE + ks));
-                        k_next(ks, kph);
+                    if (j < n1) {
+                        if (j == 0 && items1 > 0 && !(ok = pt_wait(bar(LY::BAR_OE + 1), (items1 - 1) & 1, abort_flag))) break;
+                        if (!(ok = pt_wait(bar(LY::BAR_P + 1), pph1, abort_flag))) break;
+                        tc_fence_after();
+                        issue_pv(1, vs, 0, j == 0);
+                        if (!(ok = pt_wait(bar(LY::BAR_P + 3), pph1, abort_flag))) break;
+                        tc_fence_after();
+                        issue_pv(1, vs, 1, false);
+                        pph1 ^= 1;
+                        if (more && !(ok = pt_wait(bar(LY::BAR_VF + vs1), vph1, abort_flag))) break;
+                        if (more)
+                            issue_s(1, ks, j + 2 == n1);
+                        else
+                            pt_commit(bar(LY::BAR_OR + 1));   // O_1 of this item complete
+                    } else if (more && !(ok = pt_wait(bar(LY::BAR_VF + vs1), vph1, abort_flag))) {
+                        break;
                     }
-                    if (++vs == NV) vs = 0, vph ^= 1;
+                    pt_commit(bar(LY::BAR_E + es));       // this step's V and the next one's K are read
+                    es = (es + 1) % LY::NE;
+                    if (more) k_next(ks, kph);
+                    vs = vs1, vph = vph1;
                 }
                 ++items0;
                 items1 += n1 > 0 ? 1 : 0;
@@ -445,8 +452,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             __syncwarp();
         } else if (warp == 2) {
             // ------------------------------------------------------------ K and V tiles
-            int gt = 0;
+            // Step u's end (BAR_E) means that the tensor core is done with V tile u, and with K tile u
+            // and, within the item, u + 1.
+            int gt = 0, ended = 0;        // tiles loaded, and steps whose end has been waited for, so far
             bool ok = true;
+            auto freed = [&](int steps) {
+                while (ok && ended < steps) {
+                    ok = pt_wait(bar(LY::BAR_E + ended % LY::NE), (ended / LY::NE) & 1, abort_flag);
+                    ++ended;
+                }
+                return ok;
+            };
             for (int k = 0; ok; ++k) {
                 const int e = k % PT_RING;
                 if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
@@ -457,24 +473,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const int g = it.head / p.nhb, cut = it.first_cut();
                 for (int j = 0; j < nkv; ++j) {
                     const int u = gt + j, ks = u % NK, vs = u % NV;
-                    ok = u < NK || pt_wait(bar(LY::BAR_KE + ks), ((u / NK) - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(LY::BAR_KF + ks), LY::KV_TILE);
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(base + LY::OFF_K + ks * LY::KV_TILE + c * PT_BN * 128, &p.k_map, c * 64, g,
-                                        it.start + j * PT_BN, bar(LY::BAR_KF + ks));
+                    // a cut V tile goes to warp 3 first, which hands it on (at most one per slot is on its way)
+                    const uint32_t kf = bar(LY::BAR_KF + ks), vf = bar((j >= cut ? LY::BAR_VX : LY::BAR_VF) + vs);
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        if (!freed(u + 1 - (v ? NV : NK))) break;
+                        const uint32_t full = v ? vf : kf, to = base + (v ? LY::OFF_V + vs * LY::KV_TILE : LY::OFF_K + ks * LY::KV_TILE);
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, LY::KV_TILE);
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_3d(to + c * PT_BN * 128, v ? &p.v_map : &p.k_map, c * 64, g, it.start + j * PT_BN, full);
+                        }
+                        __syncwarp();
                     }
-                    ok = u < NV || pt_wait(bar(LY::BAR_VE + vs), ((u / NV) - 1) & 1, abort_flag);
                     if (!ok) break;
-                    // a cut tile goes to warp 3 first, which hands it on (at most one per slot is on its way)
-                    const uint32_t full = bar((j >= cut ? LY::BAR_VX : LY::BAR_VF) + vs);
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(full, LY::KV_TILE);
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(base + LY::OFF_V + vs * LY::KV_TILE + c * PT_BN * 128, &p.v_map, c * 64, g,
-                                        it.start + j * PT_BN, full);
-                    }
                 }
                 gt += nkv;
                 __syncwarp();
