@@ -196,19 +196,34 @@ __device__ __forceinline__ void pt_commit(uint32_t bar) {
 // every role's waits and is reported once, at the end.  As short as can be: there are some thirty
 // waits in the kernel, and an item of a short sequence runs every role's code once, so that
 // fetching instructions is much of its time.
+__device__ __forceinline__ bool pt_wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+    auto now = [] {
+        uint32_t t;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        return t;
+    };
+    const uint32_t t0 = now();
+    bool ok;
+    do ok = mbar_try_wait(bar, parity);
+    while (!ok && !*abort && now() - t0 < 2000000000u);
+    if (!ok) *abort = 1;
+    return ok;
+}
+
+// out of line where registers allow a call (all roles but the softmax)
+__device__ __noinline__ bool pt_wait_far(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return pt_wait_on(bar, parity, abort);
+}
+
 __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
     bool ok = mbar_try_wait(bar, parity);     // up to 100 us by itself
-    if (!ok) {
-        auto now = [] {
-            uint32_t t;
-            asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-            return t;
-        };
-        const uint32_t t0 = now();
-        do ok = mbar_try_wait(bar, parity);
-        while (!ok && !*abort && now() - t0 < 2000000000u);
-        if (!ok) *abort = 1;
-    }
+    if (!ok) ok = pt_wait_far(bar, parity, abort);
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool pt_wait_near(uint32_t bar, uint32_t parity, volatile int* abort) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = pt_wait_on(bar, parity, abort);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -228,7 +243,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     uint32_t* bad = reinterpret_cast<uint32_t*>(gbase + LY::OFF_BAD);
     float* inv_l = reinterpret_cast<float*>(gbase + LY::OFF_INV);
     int32_t* const status = p.a.status;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // from a shuffle, as the items below: so that the compiler knows them the same for the whole warp
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NK; ++i) mbar_init(bar(LY::BAR_KF + i), 1);
@@ -268,7 +284,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
 
     auto ring_item = [&](int k, PtItem& it) {          // item k of this CTA
         const int4 r = ring[k % PT_RING];
-        it.start = r.x, it.n = r.y, it.t0 = r.z, it.head = r.w;
+        it.start = __shfl_sync(0xffffffffu, r.x, 0), it.n = __shfl_sync(0xffffffffu, r.y, 0);
+        it.t0 = __shfl_sync(0xffffffffu, r.z, 0), it.head = __shfl_sync(0xffffffffu, r.w, 0);
     };
 
     if (warp < 4) {
@@ -358,7 +375,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             };
             uint32_t pph0 = 0, pph1 = 0;    // phases of the P barriers, a step each
             int items0 = 0, items1 = 0;     // items of each Q tile so far
-            bool s0_issued = false;         // S_0 of the coming item's first K tile is on its way
+            bool s0_issued = false, s1_issued = false;   // S of the coming item's first K tile is on its way
+            PtItem nx{};                    // the coming item, where it was there to be read in time
+            bool have_nx = false;
             bool ok = true;
             // The tensor core works off what is issued in order and with some 400 clocks of it in its
             // queue; what this warp does between two groups of products has to fit into that.  So the
@@ -366,10 +385,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             // committed once for the K and the V tile that it frees.
             for (int k = 0; ok; ++k) {
                 const int e = k % PT_RING;
-                if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
-                PtItem it;
-                ring_item(k, it);
+                if (!have_nx) {
+                    if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+                    ring_item(k, nx);
+                }
+                const PtItem it = nx;
                 if (it.n < 0) break;
+                have_nx = false;
                 const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
                 const int nkv = max(n0, n1);
                 if (!s0_issued) {
@@ -379,18 +401,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     issue_s(0, ks, n0 == 1);
                 }
                 s0_issued = false;
-                if (n1 > 0) {
+                if (n1 > 0 && !s1_issued) {
                     if (!(ok = pt_wait(bar(LY::BAR_Q + 1), items1 & 1, abort_flag))) break;
                     tc_fence_after();
                     issue_s(1, ks, n1 == 1);
                 }
+                s1_issued = false;
                 k_next(ks, kph);
-                ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag);
+                bool have_v = false;        // the step's V has been seen to be there
                 for (int j = 0; ok && j < nkv; ++j) {
                     const bool more = j + 1 < nkv;
                     uint32_t vs1 = vs + 1, vph1 = vph;
                     if (vs1 == NV) vs1 = 0, vph1 ^= 1;
                     if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) break;
+                    if (j + 1 == n0) {                        // the coming item, for its first scores
+                        const int e2 = (k + 1) % PT_RING;
+                        have_nx = ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1);
+                        if (have_nx) ring_item(k + 1, nx);
+                    }
+                    if (!have_v && !(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
+                    have_v = false;
                     if (j < n0) {
                         // the previous item's O_0 has been read out
                         if (j == 0 && items0 > 0 && !(ok = pt_wait(bar(LY::BAR_OE), (items0 - 1) & 1, abort_flag))) break;
@@ -409,15 +439,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                             // their softmax then runs under this item's last products of the other tile
                             uint32_t ks2 = ks, kph2 = kph;
                             if (more) k_next(ks2, kph2);
-                            const int e2 = (k + 1) % PT_RING;
-                            if (ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1)) {
-                                PtItem nx;
-                                ring_item(k + 1, nx);
-                                if (nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
-                                    tc_fence_after();
-                                    issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
-                                    s0_issued = true;
-                                }
+                            if (have_nx && nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
+                                tc_fence_after();
+                                issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
+                                s0_issued = true;
                             }
                         }
                     }
@@ -430,13 +455,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         tc_fence_after();
                         issue_pv(1, vs, 1, false);
                         pph1 ^= 1;
-                        if (more && !(ok = pt_wait(bar(LY::BAR_VF + vs1), vph1, abort_flag))) break;
-                        if (more)
+                        have_v = more && ready(bar(LY::BAR_VF + vs1), vph1);
+                        if (more) {
                             issue_s(1, ks, j + 2 == n1);
-                        else
+                        } else {
                             pt_commit(bar(LY::BAR_OR + 1));   // O_1 of this item complete
-                    } else if (more && !(ok = pt_wait(bar(LY::BAR_VF + vs1), vph1, abort_flag))) {
-                        break;
+                            if (s0_issued) {                  // and the next item's K tile is there
+                                const int nn1 = nx.nkv(1, p.tpt);
+                                if (nn1 > 0 && ready(bar(LY::BAR_Q + 1), (items1 + 1) & 1)) {
+                                    tc_fence_after();
+                                    issue_s(1, ks, nn1 == 1);
+                                    s1_issued = true;
+                                }
+                            }
+                        }
                     }
                     pt_commit(bar(LY::BAR_E + es));       // this step's V and the next one's K are read
                     es = (es + 1) % LY::NE;
@@ -586,7 +618,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int e = k % PT_RING;
-            if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+            if (!pt_wait_near(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
             PtItem it;
             ring_item(k, it);
             if (it.n < 0) break;
@@ -595,7 +627,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             const int pos = min(tok, it.n - 1);          // attends keys 0..pos
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nkv; ++j) {
-                if (!pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag)) { ok = false; break; }
+                if (!pt_wait_near(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 float s[PT_BN];
 #pragma unroll
@@ -674,7 +706,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             sc += nkv;
             if (nkv > 0) {
                 // 1 / l for the output warps, once they have read the last item's
-                if (oc > 0 && !pt_wait(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
+                if (oc > 0 && !pt_wait_near(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
                 oc += 1;
                 inv_l[t * 128 + r] = 1.f / l;
                 __syncwarp();
