@@ -69,6 +69,7 @@ struct PromptTcParams {
     int32_t group;                 // query heads of a kv head
     int32_t hb, nhb;               // heads of a Q tile (at most 128), head blocks of a kv head
     int32_t tpt, tiles;            // tokens of a Q tile, Q tiles of an item
+    PromptDiv by_tokens, by_heads; // tokens of an item, heads of a place
     float scale_log2;
     CUtensorMap q_map, k_map, v_map;
 };
@@ -210,19 +211,8 @@ __device__ __forceinline__ bool pt_wait_on(uint32_t bar, uint32_t parity, volati
     return ok;
 }
 
-// out of line where registers allow a call (all roles but the softmax)
-__device__ __noinline__ bool pt_wait_far(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return pt_wait_on(bar, parity, abort);
-}
-
 __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
     bool ok = mbar_try_wait(bar, parity);     // up to 100 us by itself
-    if (!ok) ok = pt_wait_far(bar, parity, abort);
-    return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ bool pt_wait_near(uint32_t bar, uint32_t parity, volatile int* abort) {
-    bool ok = mbar_try_wait(bar, parity);
     if (!ok) ok = pt_wait_on(bar, parity, abort);
     return __all_sync(0xffffffffu, ok);
 }
@@ -303,7 +293,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     clc_try_cancel(base + LY::OFF_CLC, bar(LY::BAR_CLC));
                 }
                 PromptItem w;
-                if (finder.find(p.a, place, p.tpt * p.tiles, p.a.hkv * p.nhb, w)) {
+                if (finder.find(p.a, place, p.by_tokens, p.by_heads, w)) {
                     PtItem it;
                     it.start = w.start, it.n = w.n, it.t0 = w.tile * p.tpt * p.tiles, it.head = w.head;
                     const int e = k % PT_RING;
@@ -315,13 +305,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     ++k;
                     const bool two = p.tiles > 1 && it.nkv(1, p.tpt) > 0;
                     const int g = it.head / p.nhb, h0 = g * p.group + (it.head - g * p.nhb) * p.hb;
+#pragma unroll 1
                     for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
-                        int& use = t == 0 ? use0 : use1;
+                        const int use = t == 0 ? use0 : use1;
                         ok = use == 0 || pt_wait(bar(LY::BAR_QE + t), (use - 1) & 1, abort_flag);
                         if (!ok) break;
-                        ++use;
+                        use0 += t == 0 ? 1 : 0;
+                        use1 += t;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(bar(LY::BAR_Q + t), (uint32_t)(p.hb * p.tpt * D * 2));
+#pragma unroll 1
                             for (int c = 0; c < D / 64; ++c)
                                 tma_load_3d(base + LY::OFF_Q + t * LY::Q_TILE + c * 128 * 128, &p.q_map, c * 64, h0,
                                             it.start + it.t0 + t * p.tpt, bar(LY::BAR_Q + t));
@@ -344,12 +337,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     ring[e] = make_int4(0, -1, 0, 0);
                     mbar_arrive(bar(LY::BAR_IF + e));
                 }
-            }
-            if (*abort_flag) {                // what was asked for may still be on its way
-                volatile int no_abort = 0;
-                if (use0 > 0) pt_wait(bar(LY::BAR_Q), (use0 - 1) & 1, &no_abort);
-                if (use1 > 0) pt_wait(bar(LY::BAR_Q + 1), (use1 - 1) & 1, &no_abort);
-                if (place >= 0) pt_wait(bar(LY::BAR_CLC), asked & 1, &no_abort);
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ tcgen05.mma
@@ -513,6 +500,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         const uint32_t full = v ? vf : kf, to = base + (v ? LY::OFF_V + vs * LY::KV_TILE : LY::OFF_K + ks * LY::KV_TILE);
                         if (lane == 0) {
                             mbar_arrive_expect_tx(full, LY::KV_TILE);
+#pragma unroll 1
                             for (int c = 0; c < D / 64; ++c)
                                 tma_load_3d(to + c * PT_BN * 128, v ? &p.v_map : &p.k_map, c * 64, g, it.start + j * PT_BN, full);
                         }
@@ -523,12 +511,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 gt += nkv;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
-            }
-            if (*abort_flag) {
-                // Copies may still be on their way.  Which phase of which barrier each slot's last V
-                // went to is not worth keeping for this case: wait out the time that any copy takes.
-                const uint64_t t0 = global_ns();
-                while (global_ns() - t0 < 10000000ull) __nanosleep(1000);
             }
         } else {
             // ------------------------------------------------------------ cut V tiles
@@ -618,7 +600,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int e = k % PT_RING;
-            if (!pt_wait_near(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+            if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
             PtItem it;
             ring_item(k, it);
             if (it.n < 0) break;
@@ -627,7 +609,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             const int pos = min(tok, it.n - 1);          // attends keys 0..pos
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nkv; ++j) {
-                if (!pt_wait_near(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag)) { ok = false; break; }
+                if (!pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 float s[PT_BN];
 #pragma unroll
@@ -706,7 +688,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             sc += nkv;
             if (nkv > 0) {
                 // 1 / l for the output warps, once they have read the last item's
-                if (oc > 0 && !pt_wait_near(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
+                if (oc > 0 && !pt_wait(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
                 oc += 1;
                 inv_l[t * 128 + r] = 1.f / l;
                 __syncwarp();
@@ -724,7 +706,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
-        int done[2] = {0, 0};
+        uint32_t ph = 0;                         // phases of the tiles' barriers (bit t), an item each
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int e = k % PT_RING;
@@ -734,20 +716,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             if (it.n < 0) break;
             const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
             const uint32_t* mask = bad + e * PT_CUT * 4;
-            uint32_t any = 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!ok || (t > 0 && (p.tiles < 2 || it.nkv(1, p.tpt) == 0))) continue;
-                ok = pt_wait(bar(LY::BAR_L + t), done[t] & 1, abort_flag) &&
-                     pt_wait(bar(LY::BAR_OR + t), done[t] & 1, abort_flag) &&
-                     (t > 0 || pt_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag));
-                if (!ok) continue;
-                ++done[t];
+            const int nt = p.tiles > 1 && it.nkv(1, p.tpt) > 0 ? 2 : 1;
+#pragma unroll 1
+            for (int t = 0; t < nt; ++t) {
+                ok = pt_wait(bar(LY::BAR_L + t), (ph >> t) & 1, abort_flag) && pt_wait(bar(LY::BAR_OR + t), (ph >> t) & 1, abort_flag) &&
+                     pt_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag);
+                if (!ok) break;
+                ph ^= 1u << t;
                 tc_fence_after();
-                if (t == 0) {
-#pragma unroll
-                    for (int w = 0; w < PT_CUT * 4; ++w) any |= mask[w];
-                }
+                const bool any = __any_sync(0xffffffffu, lane < PT_CUT * 4 && mask[lane] != 0);
                 const float inv = inv_l[t * 128 + r];
                 const int tok = it.t0 + t * p.tpt + row_tok;
                 const bool valid = row_tok < p.tpt && tok < it.n && hh < p.group;
@@ -805,7 +782,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     // ---------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) report(status, RX_DEV_TIMEOUT);
+    if (*abort_flag) {
+        // Copies and an answer may still be on their way to shared memory.  What phase of which barrier
+        // each went to is not worth keeping for this case: wait out the time that any of them takes.
+        if (threadIdx.x == 0) report(status, RX_DEV_TIMEOUT);
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 10000000ull) __nanosleep(1000);
+    }
     if (warp == 3) {
         tc_fence_after();
         // every MMA this CTA issued has completed before TMEM is released; this wait does not stop
@@ -912,6 +895,8 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     // when there would be fewer such items than SMs.
     p.tiles = prompt_items(a.total, a.batch, 2 * p.tpt) * heads >= sms ? 2 : 1;
     const int64_t items = prompt_items(a.total, a.batch, p.tiles * p.tpt) * heads;
+    p.by_tokens = PromptDiv(p.tiles * p.tpt);
+    p.by_heads = PromptDiv((int)heads);
     RX_REQUIRE(items < (1ll << 31), "prompt_attention: too many rows");
     RX_REQUIRE(rows_map(&p.q_map, a.q, a.total, a.hq, head_dim, a.q_stride, p.hb, p.tpt) &&
                    rows_map(&p.k_map, a.k, a.total, a.hkv, head_dim, a.k_stride, 1, PT_BN) &&

@@ -19,6 +19,21 @@ __host__ __device__ inline int64_t prompt_items(int64_t total, int32_t batch, in
     return total / tile_tokens + batch;
 }
 
+// Division of a number below 2^31 by one fixed for the launch, as a product: with 2^(s-1) < d <= 2^s and
+// m = ceil(2^(31+s) / d) < 2^32 + 1, floor(x / d) = floor(x m / 2^(31+s)) for every 0 <= x < 2^31, since
+// m d - 2^(31+s) < d <= 2^s (Granlund and Montgomery 1994, theorem 4.2).
+struct PromptDiv {
+    int d = 1;
+    uint64_t m = 1ull << 31;
+    int s = 0;
+    PromptDiv() = default;
+    explicit PromptDiv(int divisor) : d(divisor) {
+        while ((1ll << s) < divisor) ++s;
+        m = ((1ull << (31 + s)) + (uint64_t)divisor - 1) / (uint64_t)divisor;
+    }
+    __host__ __device__ __forceinline__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> (31 + s)); }
+};
+
 struct PromptItem {
     int start, n, head, tile;   // first row and rows of the sequence, head, row tile
 };
@@ -42,18 +57,18 @@ struct PromptFinder {
     // head the tiles from the last, which has the most keys, to the first, so that the items that
     // end a launch are short ones.  False for a place left over, and for a sequence whose boundaries
     // do not lie in order in [0, total] (reported).  Every thread of a warp calls it with the same item.
-    __device__ __forceinline__ bool find(const PromptParams& p, int i, int tile_tokens, int heads, PromptItem& it) {
+    __device__ __forceinline__ bool find(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads, PromptItem& it) {
         const int lane = threadIdx.x & 31;
-        const int place = (unsigned)i / (unsigned)heads;      // place-major bound of the sequence: base(b) <= place
+        const int place = heads(i);      // place-major bound of the sequence: base(b) <= place
         // the last sequence whose places start at or before this one
         unsigned m = 0;
-        if (w0 >= 0) m = __ballot_sync(0xffffffffu, (unsigned)mine / (unsigned)tile_tokens + w0 + lane <= (unsigned)place);
+        if (w0 >= 0) m = __ballot_sync(0xffffffffu, tile_tokens(mine) + w0 + lane <= place);
         if (m == 0 || (m >> 31)) {                            // not inside the window
             int lo = 0, hi = p.batch;
             bool ok;
             while (hi - lo > 1) {                             // 32 evenly spaced sequences at a time
                 const int w = (hi - lo + 31) / 32, at = lo + lane * w;
-                const bool before = at < hi && (lane == 0 || (unsigned)load(p, at, ok) / (unsigned)tile_tokens + at <= (unsigned)place);
+                const bool before = at < hi && (lane == 0 || tile_tokens(load(p, at, ok)) + at <= place);
                 const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
                 lo += last * w;
                 hi = min(hi, lo + w);
@@ -71,15 +86,15 @@ struct PromptFinder {
             if (lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
             return false;
         }
-        const unsigned first = (unsigned)s / (unsigned)tile_tokens;
-        const int places = (int)((unsigned)e / (unsigned)tile_tokens - first) + 1;
-        const int64_t at = i - (int64_t)(first + (unsigned)b) * heads;
-        if (at < 0 || at >= (int64_t)places * heads) return false;
+        const int first = tile_tokens(s);
+        const int places = tile_tokens(e) - first + 1;
+        const int64_t at = i - (int64_t)(first + b) * heads.d;
+        if (at < 0 || at >= (int64_t)places * heads.d) return false;
         it.head = (int)((unsigned)at / (unsigned)places);
         it.tile = places - 1 - ((int)at - it.head * places);
         it.start = s;
         it.n = e - s;
-        return (int64_t)it.tile * tile_tokens < it.n;
+        return (int64_t)it.tile * tile_tokens.d < it.n;
     }
 };
 

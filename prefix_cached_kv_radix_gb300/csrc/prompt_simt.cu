@@ -52,14 +52,16 @@ __device__ __forceinline__ void ps_load(uint32_t dst, const float* src, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_constant__ PromptParams p,
+                                                                  const __grid_constant__ PromptDiv by_rows,
+                                                                  const __grid_constant__ PromptDiv by_heads) {
     using LY = PsLayout<D>;
     constexpr int LD = LY::LD, LDP = LY::LDP, OC = D / 64;   // OC: 4-column groups of a thread
     extern __shared__ __align__(16) float sm[];
     const uint32_t sb = smem_u32(sm);
     PromptItem it;
     PromptFinder finder;
-    if (!finder.find(p, (int)blockIdx.x, PS_BM, p.hq, it)) return;
+    if (!finder.find(p, (int)blockIdx.x, by_rows, by_heads, it)) return;
     const int h = it.head, g = h / (p.hq / p.hkv);
     const int row0 = it.tile * PS_BM, rows = min(PS_BM, it.n - row0);
     const float* q = (const float*)p.q + (int64_t)(it.start + row0) * p.q_stride + (int64_t)h * D;
@@ -208,7 +210,7 @@ static int launch_ps(const PromptParams& p, unsigned grid, cudaStream_t stream) 
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    prompt_simt_kernel<D><<<grid, PS_THREADS, PsLayout<D>::BYTES, stream>>>(p);
+    prompt_simt_kernel<D><<<grid, PS_THREADS, PsLayout<D>::BYTES, stream>>>(p, PromptDiv(PS_BM), PromptDiv(p.hq));
     return RX_OK;
 }
 
