@@ -1,20 +1,25 @@
 // prompt_attention in 32 bits on CUDA cores: causal attention over packed prompts.
 //
 // Row i of a sequence attends rows 0..i of the same sequence:  o = softmax(scale q K^T) V, one
-// pass over the keys with a running maximum m and sum l, the accumulator rescaled by e^(m - m')
+// pass over the keys with a running maximum m and sum l, the accumulator rescaled by 2^(m - m')
 // when the maximum moves.  Bound by the fused multiply-adds (4 head_dim flops per query head, row
 // and key); tensor cores would round the products' inputs, so they are not used for 32-bit rows.
 //
-// One block of 256 threads per (sequence, query head, 128 rows), keys in tiles of 64.  A thread
-// owns 8 rows x 4 keys of the scores and 8 rows x head_dim / 16 columns of the output, both in
-// registers: per 16 bytes it reads from shared memory it does 5 packed (two-wide) multiply-adds in
-// the first product and 8 in the second, so the arithmetic, not shared memory, sets the pace.  K is
-// fetched while the block works on P V and V while it works on Q K^T (cp.async).  Rows of Q and K
-// are padded by 16 bytes so that eight threads reading eight rows hit all banks.
+// One block of 128 threads per (sequence, query head, 64 rows), keys in tiles of 64; two (head_dim
+// 128) or three blocks share an SM, so that one's softmax runs beside another's products.  A thread
+// owns 8 rows x 4 keys of the scores and 8 rows x head_dim / 8 columns of the output, both in
+// registers: per 16 bytes it reads from shared memory it does 5 packed (two-wide) multiply-adds in the
+// first product and 8 in the second, so the arithmetic, not shared memory, sets the pace.  P takes the
+// place of the K tile it came from; where there is room (head_dim 64) the next K tile has a buffer of its
+// own and comes in meanwhile.  Rows of Q and K are padded by 16 bytes so that eight threads reading
+// eight rows hit all banks.
 //
-// A value row that a row may not see enters none of its sums: in the tiles a mask cuts, a key's
-// product is added only for the rows that attend it, so an infinity or a NaN there (a later token,
-// the next sequence's row) stays where it is.
+// Probabilities are 2^(s sl - m), sl = scale log2(e): one multiply-add, rounded once where the result
+// is small, and the special-function unit (2^-22 relative).  l is summed per thread and joined at the
+// end; the accumulator is rescaled only in tiles where a row's maximum moved.
+//
+// A value row that a row may not see enters none of its sums, so an infinity or a NaN there (a later
+// token, the next sequence's row) stays where it is.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -27,16 +32,22 @@
 
 namespace rx {
 
-constexpr int PS_BM = 128, PS_BN = 64, PS_THREADS = 256;
+constexpr int PS_BM = 64, PS_BN = 64, PS_THREADS = 128;
+constexpr float PS_LOG2E = 1.4426950408889634f;
+constexpr float PS_LN2 = 0.6931471805599453f;
 
 template <int D>
 struct PsLayout {
     static constexpr int LD = D + 4;                       // floats between rows of Q and K
-    static constexpr int OFF_K = PS_BM * LD;
-    static constexpr int OFF_V = OFF_K + PS_BN * LD;
+    static constexpr int NK = D == 64 ? 2 : 1;             // K buffers
     static constexpr int LDP = PS_BM + 4;                  // floats between keys of P (stored by key)
-    static constexpr int OFF_P = OFF_V + PS_BN * D;
-    static constexpr int BYTES = (OFF_P + PS_BN * LDP) * 4;
+    static constexpr int K_SIZE = PS_BN * LD;
+    static constexpr int OFF_K = PS_BM * LD;
+    static constexpr int OFF_V = OFF_K + NK * K_SIZE;
+    static constexpr int BYTES = (OFF_V + PS_BN * D) * 4;
+    static constexpr int BLOCKS = D == 64 ? 3 : 2;         // per SM
+    static_assert(PS_BN * LDP <= K_SIZE, "P takes the place of K");
+    static_assert(BLOCKS * (BYTES + 1024) <= 233472, "shared memory of the blocks of an SM");
 };
 
 // `rows` rows of D floats, `stride` apart, to shared rows LD apart; rows from `have` on are zeros.
@@ -52,9 +63,9 @@ __device__ __forceinline__ void ps_load(uint32_t dst, const float* src, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_constant__ PromptParams p,
-                                                                  const __grid_constant__ PromptDiv by_rows,
-                                                                  const __grid_constant__ PromptDiv by_heads) {
+__global__ void __launch_bounds__(PS_THREADS, PsLayout<D>::BLOCKS)
+    prompt_simt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptDiv by_rows,
+                       const __grid_constant__ PromptDiv by_heads) {
     using LY = PsLayout<D>;
     constexpr int LD = LY::LD, LDP = LY::LDP, OC = D / 64;   // OC: 4-column groups of a thread
     extern __shared__ __align__(16) float sm[];
@@ -70,21 +81,36 @@ __global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_co
     const int keys = row0 + rows;                            // keys the block needs
     const int nkv = (keys + PS_BN - 1) / PS_BN;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;  // rows ty*8.., keys tx + 16 j, columns tx*4 + 64 c
-
+    // a scale of zero as the least normal number: masked scores are -inf, and -inf times it has to stay so
+    const float sl = fmaxf(p.scale * PS_LOG2E, 0x1p-126f);
+    auto load_k = [&](int j) {
+        ps_load<D, LD>(sb + (LY::OFF_K + j % LY::NK * LY::K_SIZE) * 4, k + (int64_t)(j * PS_BN) * p.k_stride, p.k_stride, PS_BN,
+                       keys - j * PS_BN);
+    };
+    auto load_v = [&](int j) {
+        ps_load<D, D>(sb + LY::OFF_V * 4, v + (int64_t)(j * PS_BN) * p.v_stride, p.v_stride, PS_BN, keys - j * PS_BN);
+    };
     ps_load<D, LD>(sb, q, p.q_stride, PS_BM, rows);
-    ps_load<D, LD>(sb + LY::OFF_K * 4, k, p.k_stride, PS_BN, keys);
-    float m[8], l[8];
-    uint64_t o[8][OC * 2];
+    load_k(0);
+    load_v(0);
+    float m[8], l[8];                                        // row maximum times sl; this thread's part of the sum
+    uint64_t o[4][OC * 4];                                   // rows 2i and 2i + 1 of a column
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m[i] = -INFINITY, l[i] = 0.f;
+    for (int i = 0; i < 8; ++i) m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < OC * 2; ++c) o[i][c] = 0ull;
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < OC * 4; ++c) o[i][c] = 0ull;
     for (int j = 0; j < nkv; ++j) {
         const int k0 = j * PS_BN;
-        ps_load<D, D>(sb + LY::OFF_V * 4, v + (int64_t)k0 * p.v_stride, p.v_stride, PS_BN, keys - k0);
-        cp_async_wait<1>();                                  // Q and this tile of K are in
+        float* const kt = sm + LY::OFF_K + j % LY::NK * LY::K_SIZE;
+        if constexpr (LY::NK == 2) {
+            if (j + 1 < nkv) load_k(j + 1);
+            else cp_async_commit();
+            cp_async_wait<2>();                              // all but this tile's V and the next K
+        } else {
+            cp_async_wait<1>();
+        }
         __syncthreads();
         // scores: two channels at a time, the even and the odd ones summed apart
         uint64_t s2[8][4];
@@ -94,106 +120,138 @@ __global__ void __launch_bounds__(PS_THREADS) prompt_simt_kernel(const __grid_co
             for (int c = 0; c < 4; ++c) s2[i][c] = 0ull;
 #pragma unroll 2
         for (int d = 0; d < D; d += 4) {
-            ulonglong2 a[8], b[4];
+            ulonglong2 b[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(sm + (ty * 8 + i) * LD + d);
+            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2*>(kt + (tx + 16 * c) * LD + d);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2*>(sm + LY::OFF_K + (tx + 16 * c) * LD + d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i) {
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sm + (ty * 8 + i) * LD + d);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    s2[i][c] = f2_fma(a[i].x, b[c].x, s2[i][c]);
-                    s2[i][c] = f2_fma(a[i].y, b[c].y, s2[i][c]);
+                    s2[i][c] = f2_fma(a.x, b[c].x, s2[i][c]);
+                    s2[i][c] = f2_fma(a.y, b[c].y, s2[i][c]);
                 }
+            }
         }
         const bool cut = k0 + PS_BN - 1 > row0;              // a mask or the end of the sequence cuts this tile
         float pr[4][8];
+        bool moved = false;
+        float corr[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = row0 + ty * 8 + i;
-            float sc[4], mx = -INFINITY;
+            float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x, y;
                 f2_unpack(s2[i][c], x, y);
-                sc[c] = (x + y) * p.scale;
-                if (cut && k0 + tx + 16 * c > r) sc[c] = -INFINITY;
-                mx = fmaxf(mx, sc[c]);
+                pr[c][i] = x + y;
+                if (cut && k0 + tx + 16 * c > r) pr[c][i] = -INFINITY;
+                mx = fmaxf(mx, pr[c][i]);
             }
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float mn = fmaxf(m[i], mx);
+            const float mn = fmaxf(m[i], mx * sl);
             const float sub = mn == -INFINITY ? 0.f : mn;    // nothing but -inf so far
-            const float corr = expf(m[i] - sub);
+            corr[i] = fast_exp2(m[i] - sub);
+            moved |= mn != m[i];
+            m[i] = mn;
             float sum = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                pr[c][i] = expf(sc[c] - sub);
+                pr[c][i] = fast_exp2(fmaf(pr[c][i], sl, -sub));
                 sum += pr[c][i];
             }
-#pragma unroll
-            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            l[i] = l[i] * corr + sum;
-            m[i] = mn;
-            const uint64_t c2 = f2_pack(corr, corr);
-#pragma unroll
-            for (int c = 0; c < OC * 2; ++c) o[i][c] = f2_fma(o[i][c], c2, 0ull);
+            l[i] = fmaf(l[i], corr[i], sum);
         }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t c2 = f2_pack(corr[2 * i], corr[2 * i + 1]);
+#pragma unroll
+                for (int c = 0; c < OC * 4; ++c) o[i][c] = f2_fma(o[i][c], c2, 0ull);
+            }
+        }
+        __syncthreads();                                     // K is read: P takes its place
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 8; i += 4)
-                *reinterpret_cast<float4*>(sm + LY::OFF_P + (tx + 16 * c) * LDP + ty * 8 + i) =
+                *reinterpret_cast<float4*>(kt + (tx + 16 * c) * LDP + ty * 8 + i) =
                     make_float4(pr[c][i], pr[c][i + 1], pr[c][i + 2], pr[c][i + 3]);
-        cp_async_wait<0>();                                  // V is in
-        __syncthreads();                                     // P is written, K is read
-        if (j + 1 < nkv)
-            ps_load<D, LD>(sb + LY::OFF_K * 4, k + (int64_t)(k0 + PS_BN) * p.k_stride, p.k_stride, PS_BN, keys - k0 - PS_BN);
-        const int nk = min(PS_BN, keys - k0);
+        cp_async_wait<LY::NK == 2 ? 1 : 0>();                // V is in
+        __syncthreads();
+        // A hidden key has P = 0, and 0 times its value is 0 unless that is not finite: only a cut tile that
+        // has such a value (their sum with factors of 0 is NaN) adds key by key for the rows that attend it.
+        bool apart = false;
+        if (cut) {
+            float z = 0.f;
+            for (int i = threadIdx.x; i < PS_BN * D / 4; i += PS_THREADS) {
+                const float4 x = *reinterpret_cast<const float4*>(sm + LY::OFF_V + i * 4);
+                z = fmaf(x.x, 0.f, z), z = fmaf(x.y, 0.f, z), z = fmaf(x.z, 0.f, z), z = fmaf(x.w, 0.f, z);
+            }
+            apart = __syncthreads_or(z != z);
+        }
         auto pv = [&](int kk, bool guarded) {
-            const float4 pa = *reinterpret_cast<const float4*>(sm + LY::OFF_P + kk * LDP + ty * 8);
-            const float4 pb = *reinterpret_cast<const float4*>(sm + LY::OFF_P + kk * LDP + ty * 8 + 4);
-            const float pp[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-            ulonglong2 w[OC];
+            const ulonglong2 pa = *reinterpret_cast<const ulonglong2*>(kt + kk * LDP + ty * 8);
+            const ulonglong2 pb = *reinterpret_cast<const ulonglong2*>(kt + kk * LDP + ty * 8 + 4);
+            const uint64_t pp[4] = {pa.x, pa.y, pb.x, pb.y};
 #pragma unroll
-            for (int c = 0; c < OC; ++c) w[c] = *reinterpret_cast<const ulonglong2*>(sm + LY::OFF_V + kk * D + tx * 4 + 64 * c);
+            for (int c = 0; c < OC; ++c) {
+                const float4 w = *reinterpret_cast<const float4*>(sm + LY::OFF_V + kk * D + tx * 4 + 64 * c);
+                const uint64_t w2[4] = {f2_pack(w.x, w.x), f2_pack(w.y, w.y), f2_pack(w.z, w.z), f2_pack(w.w, w.w)};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (guarded && k0 + kk > row0 + ty * 8 + i) continue;
-                const uint64_t p2 = f2_pack(pp[i], pp[i]);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < OC; ++c) {
-                    o[i][2 * c] = f2_fma(p2, w[c].x, o[i][2 * c]);
-                    o[i][2 * c + 1] = f2_fma(p2, w[c].y, o[i][2 * c + 1]);
-                }
+                    for (int x = 0; x < 4; ++x) {
+                        const uint64_t r = f2_fma(pp[i], w2[x], o[i][c * 4 + x]);
+                        if (!guarded) {
+                            o[i][c * 4 + x] = r;
+                        } else {
+                            float lo, hi, lo0, hi0;
+                            f2_unpack(r, lo, hi);
+                            f2_unpack(o[i][c * 4 + x], lo0, hi0);
+                            const int row = row0 + ty * 8 + 2 * i;
+                            o[i][c * 4 + x] = f2_pack(k0 + kk <= row ? lo : lo0, k0 + kk <= row + 1 ? hi : hi0);
+                        }
+                    }
             }
         };
-        if (cut) {
+        if (apart) {
 #pragma unroll 1
-            for (int kk = 0; kk < nk; ++kk) pv(kk, true);
+            for (int kk = 0; kk < PS_BN; ++kk) pv(kk, true);
         } else {
 #pragma unroll 4
             for (int kk = 0; kk < PS_BN; ++kk) pv(kk, false);
         }
         __syncthreads();                                     // P and V are read
+        if (j + 1 < nkv) {
+            if constexpr (LY::NK == 1) load_k(j + 1);
+            load_v(j + 1);
+        }
     }
     cp_async_wait_all();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = ty * 8 + i;
+        float sum = l[i];
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
         if (r >= rows) continue;
-        const float inv = 1.f / l[i];
+        const float inv = 1.f / sum;
         float* orow = (float*)p.out + (int64_t)(it.start + row0 + r) * p.out_stride + (int64_t)h * D;
 #pragma unroll
         for (int c = 0; c < OC; ++c) {
-            float4 w;
-            f2_unpack(o[i][2 * c], w.x, w.y);
-            f2_unpack(o[i][2 * c + 1], w.z, w.w);
-            w.x *= inv, w.y *= inv, w.z *= inv, w.w *= inv;
-            *reinterpret_cast<float4*>(orow + tx * 4 + 64 * c) = w;
+            float w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float lo, hi;
+                f2_unpack(o[i / 2][c * 4 + x], lo, hi);
+                w[x] = (i % 2 ? hi : lo) * inv;
+            }
+            *reinterpret_cast<float4*>(orow + tx * 4 + 64 * c) = make_float4(w[0], w[1], w[2], w[3]);
         }
-        if (p.lse && tx == 0) p.lse[(int64_t)(it.start + row0 + r) * p.hq + h] = m[i] + logf(l[i]);
+        if (p.lse && tx == 0) p.lse[(int64_t)(it.start + row0 + r) * p.hq + h] = (m[i] + log2f(sum)) * PS_LN2;
     }
 }
 
