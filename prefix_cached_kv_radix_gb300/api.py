@@ -653,21 +653,16 @@ _ops_ext = None
 
 
 def ops_ext():
-    """The _rxops extension (the checks and marshalling of the operators below in C), bound to
-    torch's types and the loaded library; None when it was not built (the Python code below then
+    """The _rxops extension (the checks and marshalling of the operators below in C++), bound to the
+    loaded library; None when it was not built (the Python code below then
     makes the same checks and the same calls)."""
     global _ops_ext
     if _ops_ext is None:
+        import torch  # noqa: F401  (the extension links to it)
         ext = _load_ext("_rxops")
         if ext:
-            import torch
-            names = {n: ctypes.cast(getattr(load(), n), ctypes.c_void_p).value
-                     for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention")}
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
-            dev = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-            torch.cuda.init()
-            ext.bind(dict(names, int32=torch.int32, int64=torch.int64, float32=torch.float32, bfloat16=torch.bfloat16,
-                          get_device=dev, raw_stream=raw))
+            ext.bind({n: ctypes.cast(getattr(load(), n), ctypes.c_void_p).value
+                      for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention")})
         _ops_ext = ext
     return _ops_ext or None
 

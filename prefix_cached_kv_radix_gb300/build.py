@@ -5,7 +5,7 @@
 Translation units compile in parallel; the result is prefix_cached_kv_radix_gb300/_build/
 libradixattn.so (git-ignored).  nvcc: -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo.  Also
 _build/_rxstep*.so and _rxops*.so, the per-step call's and the row, page and prompt operators'
-marshalling as CPython extensions, where the Python headers are installed.
+marshalling as Python extensions, where the Python (and torch) headers are installed.
 """
 from __future__ import annotations
 
@@ -30,8 +30,9 @@ CPP_SOURCES = ["radix_tree.cpp"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 # the per-step marshalling as a CPython extension (optional: the ctypes binding does the same)
 PYSTEP_SRC = "pystep.c"
-# the row, page and prompt operators' marshalling, likewise
-PYOPS_SRC = "pyops.c"
+# the row, page and prompt operators' marshalling, likewise; reads torch's tensors in C++, so it wants
+# torch's headers too
+PYOPS_SRC = "pyops.cpp"
 
 
 def pystep_path(name: str = "_rxstep") -> str:
@@ -73,6 +74,7 @@ def _run(cmd, verbose):
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nv = nvcc()
+    ops = ThreadPoolExecutor(max_workers=1).submit(build_pyops, force, verbose)     # beside the kernels
     jobs = []
     objs = []
     for f in CU_SOURCES:
@@ -104,20 +106,46 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
               "-ldl"], verbose)
         os.replace(tmp, LIB_PATH)
     build_pystep(force, verbose)
-    build_pystep(force, verbose, PYOPS_SRC, "_rxops")
+    ops.result()
     return LIB_PATH
 
 
-def build_pystep(force: bool = False, verbose: bool = False, source: str = PYSTEP_SRC, name: str = "_rxstep") -> str | None:
-    """A CPython extension next to the library, when the Python headers are installed."""
+def build_pystep(force: bool = False, verbose: bool = False) -> str | None:
+    """The _rxstep extension next to the library, when the Python headers are installed."""
     import sysconfig
     inc = sysconfig.get_paths().get("include")
     if not inc or not os.path.exists(os.path.join(inc, "Python.h")):
         return None
-    src, out = os.path.join(CSRC, source), pystep_path(name)
+    src, out = os.path.join(CSRC, PYSTEP_SRC), pystep_path()
     if force or _stale(out, src):
         tmp = out + f".tmp{os.getpid()}"
         _run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", inc, "-I", INCLUDE, src, "-o", tmp], verbose)
+        os.replace(tmp, out)
+    return out
+
+
+def build_pyops(force: bool = False, verbose: bool = False) -> str | None:
+    """The _rxops extension next to the library, when the Python, torch and CUDA headers are installed."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return None
+    troot = os.path.dirname(torch.__file__)
+    tinc, inc = os.path.join(troot, "include"), sysconfig.get_paths().get("include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    wanted = [os.path.join(inc or "", "Python.h"), os.path.join(tinc, "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(tinc, "c10", "cuda", "CUDAStream.h"), os.path.join(cuda, "cuda_runtime_api.h")]
+    if not all(os.path.exists(p) for p in wanted):
+        return None
+    src, out = os.path.join(CSRC, PYOPS_SRC), pystep_path("_rxops")
+    if force or _stale(out, src):
+        tmp = out + f".tmp{os.getpid()}"
+        lib = os.path.join(troot, "lib")
+        _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+              "-isystem", inc, "-isystem", tinc, "-isystem", os.path.join(tinc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+              "-I", INCLUDE, src, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+              "-lc10_cuda"], verbose)
         os.replace(tmp, out)
     return out
 

@@ -424,10 +424,10 @@ def test_rope_bad_slots_and_lengths(dev):
 
 
 @gpu
-@pytest.mark.parametrize("in_c", [True, False])
-def test_binding_refuses(dev, in_c, monkeypatch):
+@pytest.mark.parametrize("native", [True, False])
+def test_binding_refuses(dev, native, monkeypatch):
     """The same refusals from the extension and from the Python code that stands in for it."""
-    if not in_c:
+    if not native:
         monkeypatch.setattr(api, "_ops_ext", False)
     d, st = desc_of(BF, 4, 2, 64, 10), i32([0], "cuda")
     q, k = torch.zeros(8, 4, 64, dtype=BF, device="cuda"), torch.zeros(8, 2, 64, dtype=BF, device="cuda")
