@@ -33,7 +33,8 @@
 namespace rx {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TILE = ROPE_THREADS * 4;      // table entries per block (4 per thread)
+constexpr int ROPE_PER = 16;                     // table entries per thread
+constexpr int ROPE_TILE = ROPE_THREADS * ROPE_PER;   // and per block
 constexpr int ROPE_MAX_PAIRS = 64;               // head_dim <= 128
 constexpr int ROPE_MAX_TOKENS = 4;               // tokens per block
 constexpr int ROPE_UNITS = 4;                    // vector pairs in flight per thread
@@ -100,6 +101,13 @@ struct RopeVec<__nv_bfloat16> {
     }
 };
 
+// Where pair i's angle lies in shared memory: the angles that one instruction of a warp reads (the same
+// element of neighbouring vectors) side by side.  PV: pairs of a vector.
+template <int PV>
+__device__ __forceinline__ int rope_slot(int i) {
+    return i % PV * (ROPE_MAX_PAIRS / PV) + i / PV;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int VE = RopeVec<T>::N;          // elements per 16-byte vector
@@ -110,7 +118,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
     pdl_launch_dependents();
     const int64_t table_blocks = (int64_t)p.batch * p.tiles;
     if ((int64_t)blockIdx.x < table_blocks) {
-        kpw_table_tile<ROPE_THREADS>((int)(blockIdx.x / p.tiles), blockIdx.x % p.tiles, p.prefix_slots, p.prefix_indptr,
+        kpw_table_tile<ROPE_THREADS, ROPE_PER>((int)(blockIdx.x / p.tiles), blockIdx.x % p.tiles, p.prefix_slots, p.prefix_indptr,
                                      p.new_slots, p.qo_indptr, p.r2t, p.r2t_stride, p.num_slots, 0, p.total, p.status);
         return;
     }
@@ -157,7 +165,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
             for (int a = threadIdx.x; a < nt * p.pairs; a += ROPE_THREADS) {
                 const int t = a / p.pairs, i = a - t * p.pairs;
                 if (t0 + t >= lo)
-                    cs[t][i] = rope_angle(p.positions[p.axis[i] * p.pos_stride + t0 + t], p.turns[i]);
+                    cs[t][p.interleaved ? rope_slot<VE / 2>(i) : rope_slot<VE>(i)] = rope_angle(p.positions[p.axis[i] * p.pos_stride + t0 + t], p.turns[i]);
             }
             __syncthreads();
         }
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
                 if (p.interleaved) {        // neighbouring channels: both vectors hold whole pairs
 #pragma unroll
                     for (int e = 0; e < VE; e += 2) {
-                        const float2 ca = c[(va[i] * VE + e) / 2], cb = c[(vb[i] * VE + e) / 2];
+                        const float2 ca = c[rope_slot<VE / 2>((va[i] * VE + e) / 2)], cb = c[rope_slot<VE / 2>((vb[i] * VE + e) / 2)];
                         const float a0 = a[e], b0 = b[e];
                         a[e] = a0 * ca.x - a[e + 1] * ca.y;
                         a[e + 1] = a[e + 1] * ca.x + a0 * ca.y;
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
                 } else {
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
-                        const float2 ce = c[va[i] * VE + e];
+                        const float2 ce = c[rope_slot<VE>(va[i] * VE + e)];
                         const float a0 = a[e];
                         a[e] = a0 * ce.x - b[e] * ce.y;
                         b[e] = b[e] * ce.x + a0 * ce.y;

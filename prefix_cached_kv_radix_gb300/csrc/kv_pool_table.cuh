@@ -8,18 +8,17 @@
 
 namespace rx {
 
-// One tile of NT * 4 entries of request b's slot-table row: its matched (prefix) slots, then
+// One tile of NT * PER entries of request b's slot-table row: its matched (prefix) slots, then
 // its new slots, then -1 up to the row's stride.  All loads are issued before the first store
-// (each thread has 4 independent loads in flight).  Bad lengths and slots are reported; a bad
+// (each thread has PER independent loads in flight).  Bad lengths and slots are reported; a bad
 // entry is written as -1.
-template <int NT>
+template <int NT, int PER = 4>
 __device__ __forceinline__ void kpw_table_tile(int b, int64_t tile, const int32_t* __restrict__ prefix_slots,
                                                const int64_t* __restrict__ prefix_indptr,
                                                const int32_t* __restrict__ new_slots,
                                                const int64_t* __restrict__ qo_indptr, int32_t* __restrict__ r2t,
                                                int64_t stride, int64_t num_slots, int64_t t_begin, int64_t t_end,
                                                int32_t* status) {
-    constexpr int PER = 4;
     const int64_t j0 = tile * NT * PER;
     const int64_t p0 = prefix_indptr[b], P = prefix_indptr[b + 1] - p0;
     const int64_t q0 = qo_indptr[b], n = qo_indptr[b + 1] - q0;
