@@ -7,6 +7,8 @@ A step over a batch of requests (each a full prompt whose tail is new):
   a4 prefix_extend_attention (CUDA)   or  a5/a6 decode_attention (CUDA, split-KV + merge)
   a7 insert_batch (host tree)         -> the new tokens become cached
   a8 evict (host tree)                -> LRU leaves freed under memory pressure
+Beside them: rows that still need rotary positions go through write_rope instead of a3, prompts
+without any cached prefix through prompt instead of a4; fork and resize move cached tokens.
 "SGLang: Efficient Execution of Structured Language Model Programs" (RadixAttention) and
 "Prompt Caching" (Ultralytics glossary, "How prompt caching works").  This module only
 strings library calls together and moves the step's small index arrays to the device.
@@ -136,12 +138,13 @@ class PrefixCacheEngine:
         self.device = torch.device(device)
         self.tree = api.RadixTree(num_slots, seed, page_size=page_size)
         self.num_layers = num_layers
-        self.k_pools = torch.empty(num_layers, num_slots, hkv, head_dim, dtype=self.tdtype, device=self.device)
-        self.v_pools = torch.empty_like(self.k_pools)
+        self.poison = poison
+        self._k_store = torch.empty(num_layers, num_slots, hkv, head_dim, dtype=self.tdtype, device=self.device)
+        self._v_store = torch.empty_like(self._k_store)
         if poison:   # unused slots hold NaN so that any stray gather shows up
-            self.k_pools.fill_(float("nan"))
-            self.v_pools.fill_(float("nan"))
-        self.k_pool, self.v_pool = self.k_pools[0], self.v_pools[0]   # layer 0 (single-layer use)
+            self._k_store.fill_(float("nan"))
+            self._v_store.fill_(float("nan"))
+        self._use_slots(num_slots)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.desc = api.make_desc(api.RX_F32 if dtype == "f32" else api.RX_BF16, hq, hkv, head_dim, num_slots,
                                   1.0 / float(np.sqrt(head_dim)))
@@ -185,6 +188,15 @@ class PrefixCacheEngine:
 
     def device_status(self) -> int:
         return int(self.status.item())
+
+    def _use_slots(self, n: int) -> None:
+        """The layers' pools: the first n slots of what is allocated."""
+        self.num_slots = n
+        self.k_pools, self.v_pools = self._k_store[:, :n], self._v_store[:, :n]
+        self.k_pool, self.v_pool = self.k_pools[0], self.v_pools[0]   # layer 0 (single-layer use)
+
+    def _pools(self) -> list:
+        return [p[i] for i in range(self.num_layers) for p in (self.k_pools, self.v_pools)]
 
     # ------------------------------------------------------------------ cached history
     def populate(self, tokens: np.ndarray, k, v) -> int:
@@ -483,3 +495,68 @@ class PrefixCacheEngine:
         library call (rx_step_finish).  Returns the number of slots evicted."""
         return api.rx_step_finish(self.tree.h, plan.tokens, plan.tok_indptr, plan.last_nodes,
                                   self._pin[plan.stage].data_ptr(), plan.layout, evict_tokens)
+
+    # ------------------------------------------------------------------ rotary rows, whole prompts
+    def write_rope(self, plan: StepPlan, dev: dict, rope, positions, q, k_new, v_new, q_out, k_out=None, stream=None,
+                   layer: int = 0) -> None:
+        """a3 for rows whose rotary positions are still to be applied (api.rope_desc): slot table,
+        turned keys and values into `layer`'s pools, turned queries into q_out (may be q), and turned
+        keys into k_out (may be k_new) where prompt() is to read them.  positions: int32 [axes, T]."""
+        api.kv_pool_write_rope(self.desc, rope, plan.batch, dev["prefix_slots"], dev["prefix_indptr"], dev["new_slots"],
+                               dev["qo_indptr"], positions, q, k_new, v_new, q_out, k_out, self.k_pools[layer],
+                               self.v_pools[layer], dev["r2t"].data_ptr(), int(plan.qo_indptr[-1]), self.status,
+                               stream or self._stream.cuda_stream, r2t_stride=dev["r2t"].shape[1])
+
+    def prompt(self, plan: StepPlan, dev: dict, q, k_new, v_new, out, lse=None, stream=None) -> None:
+        """a4 for a step without cached prefixes (ValueError otherwise): each prompt's tokens attend
+        causally to their own, straight from the step's rows."""
+        if plan.layout.total_prefix:
+            raise ValueError("prompt: the plan has cached prefixes; extend() reads those")
+        n = int(plan.qo_indptr[-1])
+        api.prompt_attention(self.desc, plan.batch, q, k_new, v_new, dev["qo_indptr"], out, lse, n, self.status,
+                             stream or self._stream.cuda_stream)
+
+    # ------------------------------------------------------------------ moving cached tokens
+    def fork(self, r2t, parents, keep_lens, kv_lens, tail_slots=None, stream=None):
+        """Slot tables of sequences that continue rows of `r2t` (int32 [rows, stride]): row f keeps the
+        first keep_lens[f] slots of row parents[f], and its later tokens up to kv_lens[f] are copied, in
+        every layer, to slots of its own (tail_slots, or newly allocated ones, which the caller then
+        owns).  Returns (the new table, the tail slots)."""
+        keep, kv = _contig(keep_lens, np.int32), _contig(kv_lens, np.int32)
+        tails = kv.astype(np.int64) - keep
+        if len(keep) != len(kv) or len(parents) != len(kv) or (tails < 0).any():
+            raise ValueError("fork: one parent and two lengths, keep <= kv, for each row")
+        total = int(tails.sum())
+        slots = self.tree.alloc_slots(total) if tail_slots is None else _contig(tail_slots, np.int32)
+        if len(slots) != total:
+            raise ValueError(f"fork: {total} tail slots are needed, {len(slots)} given")
+        st = self._stream if stream is None else stream
+        with torch.cuda.stream(st):
+            out = torch.empty(len(kv), r2t.shape[1], dtype=torch.int32, device=self.device)
+            api.kv_pool_fork(self.desc, self._pools(), self._i32(parents), self._i32(keep), self._i32(kv),
+                             self._i64(np.concatenate([[0], np.cumsum(tails)])), self._i32(slots if total else [0]), r2t, out, total,
+                             self.status, st)
+        return out, slots
+
+    def resize(self, num_slots: int, stream=None) -> int:
+        """Shrink or grow the pools of every layer to num_slots slots with everything cached kept:
+        cached tokens past the new end move to free slots below it (api.radix_resize, kv_pool_copy on
+        the stream).  Memory past the end stays allocated for growing back; growing past what is
+        allocated allocates anew.  Returns the number of tokens moved."""
+        src, dst = self.tree.resize(num_slots)
+        st = self._stream if stream is None else stream
+        with torch.cuda.stream(st):
+            if len(src):
+                api.kv_pool_copy(self.desc, self._pools(), self._i32(src), self._i32(dst), 1, self.status, st)
+            if num_slots > self._k_store.shape[1]:
+                for name in ("_k_store", "_v_store"):
+                    old = getattr(self, name)
+                    new = torch.empty(self.num_layers, num_slots, self.hkv, self.d, dtype=self.tdtype, device=self.device)
+                    if self.poison:
+                        new.fill_(float("nan"))
+                    new[:, :old.shape[1]].copy_(old)
+                    setattr(self, name, new)
+        self._use_slots(num_slots)
+        self.desc.num_slots = num_slots
+        self._io_static = None           # the one-call path's pool addresses are set anew
+        return len(src)
