@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             auto k_next = [&](uint32_t& slot, uint32_t& ph) {
                 if (++slot == NK) slot = 0, ph ^= 1;
             };
-            uint32_t pph0 = 0, pph1 = 0;    // phases of the P barriers, a step each
-            int items0 = 0, items1 = 0;     // items of each Q tile so far
-            bool s0_issued = false, s1_issued = false;   // S of the coming item's first K tile is on its way
+            // by bits, one for each Q tile: phase of its P barriers (a step each), parity of its items so
+            // far, whether it has had any, and whether S of the coming item's first K tile is on its way
+            uint32_t pph = 0, odd = 0, had = 0, issued = 0;
             PtItem nx{};                    // the coming item, where it was there to be read in time
             bool have_nx = false;
             bool ok = true;
@@ -381,19 +381,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 have_nx = false;
                 const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
                 const int nkv = max(n0, n1);
-                if (!s0_issued) {
-                    ok = pt_wait(bar(LY::BAR_Q), items0 & 1, abort_flag) && pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
-                    if (!ok) break;
+#pragma unroll 1
+                for (int t = 0; ok && t < 2; ++t) {
+                    const int nt = t == 0 ? n0 : n1;
+                    if (nt == 0 || ((issued >> t) & 1u)) continue;
+                    ok = pt_wait(bar(LY::BAR_Q + t), (odd >> t) & 1u, abort_flag) && pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
                     tc_fence_after();
-                    issue_s(0, ks, n0 == 1);
+                    if (ok) issue_s(t, ks, nt == 1);
                 }
-                s0_issued = false;
-                if (n1 > 0 && !s1_issued) {
-                    if (!(ok = pt_wait(bar(LY::BAR_Q + 1), items1 & 1, abort_flag))) break;
-                    tc_fence_after();
-                    issue_s(1, ks, n1 == 1);
-                }
-                s1_issued = false;
+                issued = 0;
                 k_next(ks, kph);
                 bool have_v = false;        // the step's V has been seen to be there
                 for (int j = 0; ok && j < nkv; ++j) {
@@ -408,62 +404,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     }
                     if (!have_v && !(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
                     have_v = false;
-                    if (j < n0) {
-                        // the previous item's O_0 has been read out
-                        if (j == 0 && items0 > 0 && !(ok = pt_wait(bar(LY::BAR_OE), (items0 - 1) & 1, abort_flag))) break;
-                        if (!(ok = pt_wait(bar(LY::BAR_P), pph0, abort_flag))) break;
-                        tc_fence_after();
-                        issue_pv(0, vs, 0, j == 0);
-                        if (!(ok = pt_wait(bar(LY::BAR_P + 2), pph0, abort_flag))) break;
-                        tc_fence_after();
-                        issue_pv(0, vs, 1, false);
-                        pph0 ^= 1;
-                        if (j + 1 < n0) {
-                            issue_s(0, ks, j + 2 == n0);
-                        } else {
-                            pt_commit(bar(LY::BAR_OR));   // O_0 of this item complete
-                            // the next item's first scores at once, if all they need is here already:
-                            // their softmax then runs under this item's last products of the other tile
-                            uint32_t ks2 = ks, kph2 = kph;
-                            if (more) k_next(ks2, kph2);
-                            if (have_nx && nx.n >= 0 && ready(bar(LY::BAR_Q), (items0 + 1) & 1) && ready(bar(LY::BAR_KF + ks2), kph2)) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t == 0 ? n0 : n1;
+                        if (j >= nt) continue;
+                        // the previous item's O_t has been read out
+                        if (j == 0 && ((had >> t) & 1u) && !(ok = pt_wait(bar(LY::BAR_OE + t), ((odd >> t) & 1u) ^ 1u, abort_flag))) break;
+#pragma unroll 1
+                        for (int h = 0; ok && h < 2; ++h) {
+                            ok = pt_wait(bar(LY::BAR_P + 2 * h + t), (pph >> t) & 1u, abort_flag);
+                            tc_fence_after();
+                            if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
+                        }
+                        if (!ok) break;
+                        pph ^= 1u << t;
+                        if (more && (t == 1 || j >= n1)) have_v = ready(bar(LY::BAR_VF + vs1), vph1);
+                        // the tile's next scores: of the next step, or of the coming item's first if all they
+                        // need is here already; their softmax then runs under this item's last products
+                        uint32_t kk = ks, kkph = kph;
+                        bool go = j + 1 < nt, last = j + 2 == nt;
+                        if (!go) {
+                            pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
+                            if (t == 0 && more) k_next(kk, kkph);
+                            if (have_nx && nx.n >= 0) {
+                                const int nn = nx.nkv(t, p.tpt);
+                                last = nn == 1;
+                                go = nn > 0 && p.tiles > t && ready(bar(LY::BAR_Q + t), ((odd >> t) & 1u) ^ 1u) &&
+                                     (t == 0 ? ready(bar(LY::BAR_KF + kk), kkph) : (issued & 1u) != 0);
                                 tc_fence_after();
-                                issue_s(0, ks2, nx.nkv(0, p.tpt) == 1);
-                                s0_issued = true;
+                                if (go) issued |= 1u << t;
                             }
                         }
+                        if (go) issue_s(t, kk, last);
                     }
-                    if (j < n1) {
-                        if (j == 0 && items1 > 0 && !(ok = pt_wait(bar(LY::BAR_OE + 1), (items1 - 1) & 1, abort_flag))) break;
-                        if (!(ok = pt_wait(bar(LY::BAR_P + 1), pph1, abort_flag))) break;
-                        tc_fence_after();
-                        issue_pv(1, vs, 0, j == 0);
-                        if (!(ok = pt_wait(bar(LY::BAR_P + 3), pph1, abort_flag))) break;
-                        tc_fence_after();
-                        issue_pv(1, vs, 1, false);
-                        pph1 ^= 1;
-                        have_v = more && ready(bar(LY::BAR_VF + vs1), vph1);
-                        if (more) {
-                            issue_s(1, ks, j + 2 == n1);
-                        } else {
-                            pt_commit(bar(LY::BAR_OR + 1));   // O_1 of this item complete
-                            if (s0_issued) {                  // and the next item's K tile is there
-                                const int nn1 = nx.nkv(1, p.tpt);
-                                if (nn1 > 0 && ready(bar(LY::BAR_Q + 1), (items1 + 1) & 1)) {
-                                    tc_fence_after();
-                                    issue_s(1, ks, nn1 == 1);
-                                    s1_issued = true;
-                                }
-                            }
-                        }
-                    }
+                    if (!ok) break;
                     pt_commit(bar(LY::BAR_E + es));       // this step's V and the next one's K are read
                     es = (es + 1) % LY::NE;
                     if (more) k_next(ks, kph);
                     vs = vs1, vph = vph1;
                 }
-                ++items0;
-                items1 += n1 > 0 ? 1 : 0;
+                odd ^= n1 > 0 ? 3u : 1u;
+                had |= n1 > 0 ? 3u : 1u;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
             }
@@ -731,6 +712,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const uint32_t o_addr = tmem + ((uint32_t)(quarter * 32) << 16) + LY::COL_O0 + t * D;
                 __nv_bfloat16* orow =
                     (__nv_bfloat16*)p.a.out + ((int64_t)it.start + tok) * p.a.out_stride + (int64_t)(g * p.group + hh) * D;
+                // Four neighbouring lanes trade 16-byte pieces so that together they write 64 bytes of one row
+                // at a time: whole sectors, and a quarter of the lines an instruction touches.
+                uint64_t to[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    to[i] = __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)(valid ? orow : nullptr), (lane & ~3) + i);
 #pragma unroll 1
                 for (int cc = 0; cc < D; cc += 32) {
                     float ov[32];
@@ -741,22 +728,30 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(LY::BAR_OE + t));
                     }
-                    if (valid) {
+                    uint32_t w[16];                  // four pieces of 8 columns
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) ov[x] *= inv;
+                    for (int x = 0; x < 16; ++x) w[x] = pack_bf16x2(ov[2 * x] * inv, ov[2 * x + 1] * inv);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            uint4 v;
-                            v.x = pack_bf16x2(ov[x + 0], ov[x + 1]);
-                            v.y = pack_bf16x2(ov[x + 2], ov[x + 3]);
-                            v.z = pack_bf16x2(ov[x + 4], ov[x + 5]);
-                            v.w = pack_bf16x2(ov[x + 6], ov[x + 7]);
-                            *reinterpret_cast<uint4*>(orow + cc + x) = v;
-                        }
-                    }
-                    __syncwarp();                // the whole warp reads the next columns
+                    for (int b = 1; b < 4; b <<= 1)  // piece c of lane l changes places with piece l of lane c
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (!(c & b))
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const bool up = lane & b;
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[4 * c + x] : w[4 * (c ^ b) + x], b);
+                                    if (up) w[4 * c + x] = got;
+                                    else w[4 * (c ^ b) + x] = got;
+                                }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)      // piece lane % 4 of row i of the four
+                        if (to[i])
+                            reinterpret_cast<uint4*>((uintptr_t)to[i] + cc * 2)[lane & 3] =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    __syncwarp();                    // the whole warp reads the next columns
                 }
-                // the non-finite values of the keys this row attends, added to what was just stored
+                // the non-finite values of the keys this row attends, added to what was just stored (by other
+                // lanes: seen after the warp's barrier above)
                 if (any && valid) {
 #pragma unroll 1
                     for (int w = 0; w < PT_CUT * 4; ++w)
