@@ -886,10 +886,11 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     // a scale of zero as the least normal number: masked scores are -inf, and -inf times it has to stay so
     p.scale_log2 = std::max(a.scale * PT_LOG2E, 0x1p-126f);
     const int64_t heads = (int64_t)a.hkv * p.nhb;
-    // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn; one a piece
-    // when there would be fewer such items than SMs.
-    p.tiles = prompt_items(a.total, a.batch, 2 * p.tpt) * heads >= sms ? 2 : 1;
+    // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn (1.4 us a step of
+    // 128 keys); one a piece, whose step is 1 us, while even those are no more than the SMs.
+    p.tiles = prompt_items(a.total, a.batch, p.tpt) * heads > sms ? 2 : 1;
     const int64_t items = prompt_items(a.total, a.batch, p.tiles * p.tpt) * heads;
+    p.a.by_level = prompt_by_level(items, sms, a.batch, 2 * a.total * a.hkv * head_dim * 2);
     p.by_tokens = PromptDiv(p.tiles * p.tpt);
     p.by_heads = PromptDiv((int)heads);
     RX_REQUIRE(items < (1ll << 31), "prompt_attention: too many rows");

@@ -34,6 +34,18 @@ struct PromptDiv {
     __host__ __device__ __forceinline__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> (31 + s)); }
 };
 
+// Whether the items are better taken by tile index, of all sequences together and from the highest
+// down, than sequence by sequence: row tile x has about x tiles of keys, so the longest items come first
+// and the launch ends on the shortest, whatever the order of the sequences (8 ragged f32 prompts 658 ->
+// 510 us, 48 ragged bf16 prompts 125 -> 105 us).  Not where all items run at once anyway, where finding an
+// item among the sequences takes longer than a short item does (250 prompts of 64 tokens: 73 us by
+// sequence, 239 by tile index; 60 of 256: 81 and 78), nor where the keys and values of all sequences
+// are more than the L2 holds beside the rest (of 129 MB): each tile index reads them again (32 prompts
+// of 1024 tokens, 134 MB: 233 and 266 us; one of 16384, 67 MB: 1334 and 1239).
+inline bool prompt_by_level(int64_t items, int resident, int32_t batch, int64_t kv_bytes) {
+    return items > resident && batch <= 64 && kv_bytes <= 80ll << 20;
+}
+
 struct PromptItem {
     int start, n, head, tile;   // first row and rows of the sequence, head, row tile
 };
@@ -46,6 +58,7 @@ struct PromptFinder {
     int w0 = -1;             // first boundary of the window (-1: none loaded)
     int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last
     bool good = false;       // it lies in [0, total]
+    bool unsound = false;    // (by level, where `mine` is the tiles of sequence `lane`) a sequence out of order was seen
 
     __device__ __forceinline__ int load(const PromptParams& p, int b, bool& ok) const {
         const int64_t x = p.indptr[b];
@@ -53,11 +66,64 @@ struct PromptFinder {
         return (int)min(max(x, (int64_t)0), p.total);
     }
 
+    // Item `i` by tile index from the highest down, then sequence, then head.  There are f(x) = sum over the
+    // sequences of max(0, tiles - x) tiles of index x and up; item place q has index x where
+    // f(x + 1) <= q < f(x).  A sequence whose boundaries do not lie in order in [0, total] has no tiles
+    // (item 0 reports it).
+    __device__ __forceinline__ bool find_by_level(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
+                                                  PromptItem& it) {
+        const int lane = threadIdx.x & 31;
+        const int q = heads(i), rounds = (p.batch + 31) >> 5;
+        if (w0 < 0) {                        // the first 32 sequences stay in the lanes
+            w0 = 0;
+            mine = tiles(p, lane, tile_tokens);
+        }
+        // q < f(lo), or lo = -1; q >= f(hi) = f_hi
+        int lo = -1, hi = tile_tokens((int)p.total) + 2, f_hi = 0;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            int f = max(0, mine - mid);
+#pragma unroll 1
+            for (int m = 1; m < rounds; ++m) f += max(0, tiles(p, 32 * m + lane, tile_tokens) - mid);
+            f = (int)__reduce_add_sync(0xffffffffu, (unsigned)f);
+            if (q < f) lo = mid;
+            else hi = mid, f_hi = f;
+        }
+        if (i == 0 && __any_sync(0xffffffffu, unsound) && lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
+        if (lo < 0) return false;
+        int r = q - f_hi;                    // which of the sequences that have a tile `lo`
+#pragma unroll 1
+        for (int m = 0; m < rounds; ++m) {
+            const unsigned has = __ballot_sync(0xffffffffu, (m == 0 ? mine : tiles(p, 32 * m + lane, tile_tokens)) > lo);
+            const bool me = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == r;
+            const unsigned one = __ballot_sync(0xffffffffu, me);
+            if (one) {
+                const int b = 32 * m + __ffs(one) - 1;
+                it.start = (int)p.indptr[b];
+                it.n = (int)(p.indptr[b + 1] - p.indptr[b]);
+                it.tile = lo;
+                it.head = i - q * heads.d;
+                return true;
+            }
+            r -= __popc(has);
+        }
+        return false;
+    }
+
+    // Row tiles of sequence b (0 beyond the batch, and where its boundaries are not sound).
+    __device__ __forceinline__ int tiles(const PromptParams& p, int b, const PromptDiv& tile_tokens) {
+        if (b >= p.batch) return 0;
+        const int64_t s = p.indptr[b], e = p.indptr[b + 1];
+        const bool sound = s >= 0 && e >= s && e <= p.total;
+        unsound |= !sound;
+        return sound ? tile_tokens((int)(e - s) + tile_tokens.d - 1) : 0;
+    }
+
     // Item `i` of the places x heads: within a sequence the heads one after another, and within a
     // head the tiles from the last, which has the most keys, to the first, so that the items that
     // end a launch are short ones.  False for a place left over, and for a sequence whose boundaries
     // do not lie in order in [0, total] (reported).  Every thread of a warp calls it with the same item.
-    __device__ __forceinline__ bool find(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads, PromptItem& it) {
+    __device__ __forceinline__ bool find_by_place(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads, PromptItem& it) {
         const int lane = threadIdx.x & 31;
         const int place = heads(i);      // place-major bound of the sequence: base(b) <= place
         // the last sequence whose places start at or before this one
@@ -95,6 +161,12 @@ struct PromptFinder {
         it.start = s;
         it.n = e - s;
         return (int64_t)it.tile * tile_tokens.d < it.n;
+    }
+
+    __device__ __forceinline__ bool find(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
+                                         PromptItem& it) {
+        return p.by_level ? find_by_level(p, i, tile_tokens, heads, it)
+                                             : find_by_place(p, i, tile_tokens, heads, it);
     }
 };
 

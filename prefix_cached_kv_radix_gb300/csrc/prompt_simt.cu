@@ -272,12 +272,14 @@ static int launch_ps(const PromptParams& p, unsigned grid, cudaStream_t stream) 
     return RX_OK;
 }
 
-int launch_prompt_simt(const PromptParams& p, int head_dim, cudaStream_t stream) {
+int launch_prompt_simt(PromptParams p, int head_dim, cudaStream_t stream) {
     const int64_t items = prompt_items(p.total, p.batch, PS_BM) * p.hq;
     if (items >= (1ll << 31)) {
         set_error("prompt_attention: too many rows");
         return RX_EINVAL;
     }
+    p.by_level = prompt_by_level(items, 152 * (head_dim == 128 ? PsLayout<128>::BLOCKS : PsLayout<64>::BLOCKS), p.batch,
+                                 2 * p.total * p.hkv * head_dim * 4);
     return head_dim == 128 ? launch_ps<128>(p, (unsigned)items, stream) : launch_ps<64>(p, (unsigned)items, stream);
 }
 

@@ -115,9 +115,10 @@ struct PromptParams {
     const int64_t* indptr;
     float* lse;                   // natural log, [total, hq], optional
     float scale;
+    int32_t by_level;             // order of the items
     int32_t* status;
 };
-int launch_prompt_simt(const PromptParams& p, int head_dim, cudaStream_t stream);
+int launch_prompt_simt(PromptParams p, int head_dim, cudaStream_t stream);
 
 // kv_pool_write for the requests of one call whose new tokens are t_begin .. t_end-1 (index
 // arrays absolute: a slice of a step's requests passes its offset pointers).  With stage_bytes
