@@ -56,6 +56,8 @@ struct CopyParams {
 // Item = (pool, page, segment), segment fastest.
 __global__ void __launch_bounds__(MOVE_THREADS) kv_pool_copy_kernel(const __grid_constant__ CopyParams p,
                                                                    const __grid_constant__ PoolList pools) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * MOVE_WARPS;
     for (int64_t it = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5); it < p.items; it += step) {
@@ -101,6 +103,8 @@ __device__ __forceinline__ bool fork_row_ok(const ForkParams& p, int f) {
 // others: one (tail token, pool, segment) per warp and step.
 __global__ void __launch_bounds__(MOVE_THREADS) kv_pool_fork_kernel(const __grid_constant__ ForkParams p,
                                                                    const __grid_constant__ PoolList pools) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t table_blocks = (int64_t)p.rows * p.tiles;
     if ((int64_t)blockIdx.x < table_blocks) {
         const int f = (int)(blockIdx.x / p.tiles);
@@ -212,7 +216,7 @@ extern "C" int kv_pool_copy(const rx_attn_desc* desc, int32_t n_pools, void* con
         const int32_t k = std::min(MOVE_POOLS, n_pools - at);
         for (int32_t i = 0; i < k; ++i) list.p[i] = (uint4*)pools[at + i];
         p.items = n * k * p.segs;
-        kv_pool_copy_kernel<<<(unsigned)move_blocks(p.items), MOVE_THREADS, 0, (cudaStream_t)stream>>>(p, list);
+        launch_pdl(kv_pool_copy_kernel, (unsigned)move_blocks(p.items), MOVE_THREADS, 0, (cudaStream_t)stream, p, list);
     }
     return move_launched("kv_pool_copy");
 }
@@ -258,7 +262,7 @@ extern "C" int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* con
         for (int32_t i = 0; i < p.n_pools; ++i) list.p[i] = (uint4*)pools[at + i];
         p.tiles = at == 0 ? (int32_t)tiles : 0;
         const int64_t blocks = n_rows * (int64_t)p.tiles + move_blocks(total_tail * p.n_pools * p.segs);
-        if (blocks > 0) kv_pool_fork_kernel<<<(unsigned)blocks, MOVE_THREADS, 0, (cudaStream_t)stream>>>(p, list);
+        if (blocks > 0) launch_pdl(kv_pool_fork_kernel, (unsigned)blocks, MOVE_THREADS, 0, (cudaStream_t)stream, p, list);
     }
     return move_launched("kv_pool_fork");
 }

@@ -113,9 +113,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
     constexpr int VE = RopeVec<T>::N;          // elements per 16-byte vector
     constexpr int NU = D / VE / 2;             // vector pairs per head
     __shared__ float2 cs[ROPE_MAX_TOKENS][ROPE_MAX_PAIRS];
-    // a kernel launched after this one with programmatic serialization may start its own set-up;
-    // it waits for this grid before it reads the table or the pools
     pdl_launch_dependents();
+    pdl_wait();
     const int64_t table_blocks = (int64_t)p.batch * p.tiles;
     if ((int64_t)blockIdx.x < table_blocks) {
         kpw_table_tile<ROPE_THREADS, ROPE_PER>((int)(blockIdx.x / p.tiles), blockIdx.x % p.tiles, p.prefix_slots, p.prefix_indptr,
@@ -261,7 +260,7 @@ static int rope_table(const rx_rope_desc* r, int head_dim, RopeParams& p) {
 
 template <typename T, int D>
 static void launch_rope(const RopeParams& p, unsigned grid, cudaStream_t stream) {
-    kv_pool_rope_kernel<T, D><<<grid, ROPE_THREADS, 0, stream>>>(p);
+    launch_pdl(kv_pool_rope_kernel<T, D>, grid, ROPE_THREADS, 0, stream, p);   // an error shows in cudaGetLastError
 }
 
 }  // namespace rx

@@ -271,6 +271,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    pdl_launch_dependents();
+    pdl_wait();                          // what came before has finished; nothing global was touched so far
 
     auto ring_item = [&](int k, PtItem& it) {          // item k of this CTA
         const int4 r = ring[k % PT_RING];
@@ -870,7 +872,7 @@ static int launch_pt(const PromptTcParams& p, unsigned grid, cudaStream_t stream
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    prompt_tc_kernel<D><<<grid, PT_THREADS, PtLayout<D>::ALLOC, stream>>>(p);
+    launch_pdl(prompt_tc_kernel<D>, grid, PT_THREADS, PtLayout<D>::ALLOC, stream, p);   // an error shows in cudaGetLastError
     return RX_OK;
 }
 

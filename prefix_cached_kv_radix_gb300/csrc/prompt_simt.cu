@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(PS_THREADS, PsLayout<D>::BLOCKS)
     using LY = PsLayout<D>;
     constexpr int LD = LY::LD, LDP = LY::LDP, OC = D / 64;   // OC: 4-column groups of a thread
     extern __shared__ __align__(16) float sm[];
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t sb = smem_u32(sm);
     PromptItem it;
     PromptFinder finder;
@@ -268,7 +270,7 @@ static int launch_ps(const PromptParams& p, unsigned grid, cudaStream_t stream) 
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    prompt_simt_kernel<D><<<grid, PS_THREADS, PsLayout<D>::BYTES, stream>>>(p, PromptDiv(PS_BM), PromptDiv(p.hq));
+    launch_pdl(prompt_simt_kernel<D>, grid, PS_THREADS, PsLayout<D>::BYTES, stream, p, PromptDiv(PS_BM), PromptDiv(p.hq));
     return RX_OK;
 }
 
