@@ -5,8 +5,8 @@
 // when the maximum moves.  Bound by the fused multiply-adds (4 head_dim flops per query head, row
 // and key); tensor cores would round the products' inputs, so they are not used for 32-bit rows.
 //
-// One block of 128 threads per (sequence, query head, 64 rows), keys in tiles of 64; two (head_dim
-// 128) or three blocks share an SM, so that one's softmax runs beside another's products.  A thread
+// One block of 128 threads per (sequence, query head, 64 rows), keys in tiles of 64; two
+// blocks share an SM, so that one's softmax runs beside the other's products.  A thread
 // owns 8 rows x 4 keys of the scores and 8 rows x head_dim / 8 columns of the output, both in
 // registers: per 16 bytes it reads from shared memory it does 5 packed (two-wide) multiply-adds in the
 // first product and 8 in the second, so the arithmetic, not shared memory, sets the pace.  P takes the
@@ -45,7 +45,7 @@ struct PsLayout {
     static constexpr int OFF_K = PS_BM * LD;
     static constexpr int OFF_V = OFF_K + NK * K_SIZE;
     static constexpr int BYTES = (OFF_V + PS_BN * D) * 4;
-    static constexpr int BLOCKS = D == 64 ? 3 : 2;         // per SM
+    static constexpr int BLOCKS = 2;                       // per SM
     static_assert(PS_BN * LDP <= K_SIZE, "P takes the place of K");
     static_assert(BLOCKS * (BYTES + 1024) <= 233472, "shared memory of the blocks of an SM");
 };
@@ -120,20 +120,20 @@ __global__ void __launch_bounds__(PS_THREADS, PsLayout<D>::BLOCKS)
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) s2[i][c] = 0ull;
-#pragma unroll 2
+#pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-            ulonglong2 b[4];
+            ulonglong2 a[8], b[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(sm + (ty * 8 + i) * LD + d);
 #pragma unroll
             for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2*>(kt + (tx + 16 * c) * LD + d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sm + (ty * 8 + i) * LD + d);
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    s2[i][c] = f2_fma(a.x, b[c].x, s2[i][c]);
-                    s2[i][c] = f2_fma(a.y, b[c].y, s2[i][c]);
+                    s2[i][c] = f2_fma(a[i].x, b[c].x, s2[i][c]);
+                    s2[i][c] = f2_fma(a[i].y, b[c].y, s2[i][c]);
                 }
-            }
         }
         const bool cut = k0 + PS_BN - 1 > row0;              // a mask or the end of the sequence cuts this tile
         float pr[4][8];
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(PS_THREADS, PsLayout<D>::BLOCKS)
 #pragma unroll 1
             for (int kk = 0; kk < PS_BN; ++kk) pv(kk, true);
         } else {
-#pragma unroll 4
+#pragma unroll 8
             for (int kk = 0; kk < PS_BN; ++kk) pv(kk, false);
         }
         __syncthreads();                                     // P and V are read
