@@ -28,6 +28,15 @@
 //   warps 12-15 the items' output from TMEM, while the others are on the next item
 // While one tile's softmax runs the tensor core works on the other's products.
 //
+// What bounds it: for long prompts the tensor core (one of 16384 tokens, 32/8 heads x 128: 1.24 ms, 1770
+// TFLOP/s, 91 % of the measured cuBLAS burst rate; of 32768: 5.1 ms, 1720; 64/8 heads: 1700): a step of
+// 128 keys takes 2700 clocks, of which its products are 2048.  The issuing warp decides that: with
+// operands the compiler did not know to be warp-uniform the products took 75 clocks each to issue
+// instead of 64 (1254 TFLOP/s), and waits where its queue ran dry cost 500 clocks a step.  For short
+// prompts the passage from one item to the next, about 2 us of which instruction fetch is a part (32
+// prompts of 1024: 1200 TFLOP/s; the code was cut from 112 to 60 KB, which took that case from 391 to
+// 230 us), and HBM (512 prompts of 64 tokens: 118 us for 670 MB, 85 % of the measured copy rate).
+//
 // Rows that a row must not see: a masked score is replaced after the product, so nothing of a
 // hidden key survives, but P V multiplies hidden values by zero, and zero times an infinity or a
 // NaN is not zero.  So in the tiles that the causal mask or the sequence's end cuts, warp 3 clears
@@ -68,7 +77,7 @@ struct PromptTcParams {
     PromptParams a;
     int32_t group;                 // query heads of a kv head
     int32_t hb, nhb;               // heads of a Q tile (at most 128), head blocks of a kv head
-    int32_t tpt, tiles;            // tokens of a Q tile, Q tiles of an item
+    int32_t tpt;                   // tokens of a Q tile
     PromptDiv by_tokens, by_heads; // tokens of an item, heads of a place
     float scale_log2;
     CUtensorMap q_map, k_map, v_map;
@@ -90,7 +99,8 @@ struct PtLayout {
                          BAR_S = BAR_VX + NV, BAR_P = BAR_S + 2, BAR_QE = BAR_P + 4, BAR_OR = BAR_QE + 2,
                          BAR_OE = BAR_OR + 2, BAR_L = BAR_OE + 2, BAR_IF = BAR_L + 2, BAR_IE = BAR_IF + PT_RING,
                          BAR_IC = BAR_IE + PT_RING,   // every cut tile of an item has been cleared
-                         BAR_CLC = BAR_IC + PT_RING, BAR_DONE = BAR_CLC + 1, NBAR = BAR_DONE + 1;
+                         BAR_CLC = BAR_IC + PT_RING, BAR_J = BAR_CLC + 1,   // (SPLIT) the two warpgroups' softmax joined
+                         BAR_DONE = BAR_J + 1, NBAR = BAR_DONE + 1;
     static constexpr int OFF_CLC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // answer of try_cancel
     static constexpr int OFF_RING = OFF_CLC + 16;                       // int4 per entry
     static constexpr int OFF_BAD = OFF_RING + 16 * PT_RING;             // non-finite keys: PT_CUT * 4 words per entry
@@ -217,10 +227,15 @@ __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile 
     return __all_sync(0xffffffffu, ok);
 }
 
-template <int D>
+// SPLIT: an item is one Q tile, and the two softmax warpgroups, S and O take its K/V tiles in turn (even
+// and odd ones) and join at the end: half as many steps, one after another, for calls whose items all
+// run at once.  (One prompt of 409 tokens, 12 heads x 64: 7.3 us, and 7.9 with one K/V tile after
+// another; of 1024 tokens: 10.2 and 11.9.)
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_constant__ PromptTcParams p) {
     using LY = PtLayout<D>;
     constexpr int NK = LY::NK, NV = LY::NV;
+    constexpr int TILES = SPLIT ? 1 : 2;       // Q tiles of an item
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -259,6 +274,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             mbar_init(bar(LY::BAR_IC + i), 1);
         }
         mbar_init(bar(LY::BAR_CLC), 1);
+        mbar_init(bar(LY::BAR_J), 8);
         mbar_init(bar(LY::BAR_DONE), 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 PromptItem w;
                 if (finder.find(p.a, place, p.by_tokens, p.by_heads, w)) {
                     PtItem it;
-                    it.start = w.start, it.n = w.n, it.t0 = w.tile * p.tpt * p.tiles, it.head = w.head;
+                    it.start = w.start, it.n = w.n, it.t0 = w.tile * p.tpt * TILES, it.head = w.head;
                     const int e = k % PT_RING;
                     ok = k < PT_RING || pt_wait(bar(LY::BAR_IE + e), ((k / PT_RING) - 1) & 1, abort_flag);
                     if (ok && lane == 0) {
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         mbar_arrive(bar(LY::BAR_IF + e));
                     }
                     ++k;
-                    const bool two = p.tiles > 1 && it.nkv(1, p.tpt) > 0;
+                    const bool two = TILES > 1 && it.nkv(1, p.tpt) > 0;
                     const int g = it.head / p.nhb, h0 = g * p.group + (it.head - g * p.nhb) * p.hb;
 #pragma unroll 1
                     for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
@@ -357,6 +373,56 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                           IDESC_PV, fresh);
             };
             auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
+            if constexpr (SPLIT) {
+                // K/V tile i of an item goes through S and O of warpgroup i % 2
+                int gt = 0;                         // K/V tiles so far
+                uint32_t pph = 0, odd = 0, had = 0;   // by bits, as below
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    const int e = k % PT_RING;
+                    if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+                    PtItem it;
+                    ring_item(k, it);
+                    if (it.n < 0) break;
+                    const int total = it.nkv(0, p.tpt);
+                    ok = pt_wait(bar(LY::BAR_Q), k & 1, abort_flag);
+#pragma unroll 1
+                    for (int i = -2; ok && i < total; ++i) {
+                        const uint32_t t = i & 1;
+                        if (i >= 0) {
+                            const int u = gt + i;
+                            ok = pt_wait(bar(LY::BAR_VF + u % NV), (u / NV) & 1, abort_flag) &&
+                                 // the previous item's O_t has been read out
+                                 (i > 1 || !((had >> t) & 1u) || pt_wait(bar(LY::BAR_OE + t), ((odd >> t) & 1u) ^ 1u, abort_flag));
+#pragma unroll 1
+                            for (int h = 0; ok && h < 2; ++h) {
+                                ok = pt_wait(bar(LY::BAR_P + 2 * h + t), (pph >> t) & 1u, abort_flag);
+                                tc_fence_after();
+                                if (ok) issue_pv(t, u % NV, h, i < 2 && h == 0);
+                            }
+                            if (!ok) break;
+                            pph ^= 1u << t;
+                        }
+                        if (i + 2 < total) {
+                            const int u = gt + i + 2;
+                            ok = pt_wait(bar(LY::BAR_KF + u % NK), (u / NK) & 1, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            pt_mma_s<D>(tmem + t * PT_BN, qd0, kd0 + (uint32_t)(u % NK) * (uint32_t)(LY::KV_TILE >> 4), IDESC_S);
+                            pt_commit(bar(LY::BAR_S + t));
+                            if (i + 3 == total) pt_commit(bar(LY::BAR_QE));   // Q read for this item
+                        } else if (i >= 0) {
+                            pt_commit(bar(LY::BAR_OR + t));                   // O_t of this item complete
+                        }
+                        if (i >= 0) pt_commit(bar(LY::BAR_E + (gt + i) % LY::NE));
+                    }
+                    gt += total;
+                    odd ^= total > 1 ? 3u : 1u;
+                    had |= total > 1 ? 3u : 1u;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
+                }
+            } else {
             // ring positions: the next K tile to be multiplied by Q, the V tile of the current step, the step's end
             uint32_t ks = 0, kph = 0, vs = 0, vph = 0, es = 0;
             auto k_next = [&](uint32_t& slot, uint32_t& ph) {
@@ -381,7 +447,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 const PtItem it = nx;
                 if (it.n < 0) break;
                 have_nx = false;
-                const int n0 = it.nkv(0, p.tpt), n1 = p.tiles > 1 ? it.nkv(1, p.tpt) : 0;
+                const int n0 = it.nkv(0, p.tpt), n1 = TILES > 1 ? it.nkv(1, p.tpt) : 0;
                 const int nkv = max(n0, n1);
 #pragma unroll 1
                 for (int t = 0; ok && t < 2; ++t) {
@@ -431,7 +497,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                             if (have_nx && nx.n >= 0) {
                                 const int nn = nx.nkv(t, p.tpt);
                                 last = nn == 1;
-                                go = nn > 0 && p.tiles > t && ready(bar(LY::BAR_Q + t), ((odd >> t) & 1u) ^ 1u) &&
+                                go = nn > 0 && ready(bar(LY::BAR_Q + t), ((odd >> t) & 1u) ^ 1u) &&
                                      (t == 0 ? ready(bar(LY::BAR_KF + kk), kkph) : (issued & 1u) != 0);
                                 tc_fence_after();
                                 if (go) issued |= 1u << t;
@@ -449,6 +515,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 had |= n1 > 0 ? 3u : 1u;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
+            }
             }
             pt_commit(bar(LY::BAR_DONE));
             __syncwarp();
@@ -471,7 +538,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 PtItem it;
                 ring_item(k, it);
                 if (it.n < 0) break;
-                const int nkv = max(it.nkv(0, p.tpt), p.tiles > 1 ? it.nkv(1, p.tpt) : 0);
+                const int nkv = max(it.nkv(0, p.tpt), TILES > 1 ? it.nkv(1, p.tpt) : 0);
                 const int g = it.head / p.nhb, cut = it.first_cut();
                 for (int j = 0; j < nkv; ++j) {
                     const int u = gt + j, ks = u % NK, vs = u % NV;
@@ -506,7 +573,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                 PtItem it;
                 ring_item(k, it);
                 if (it.n < 0) break;
-                const int nkv = max(it.nkv(0, p.tpt), p.tiles > 1 ? it.nkv(1, p.tpt) : 0), cut = it.first_cut();
+                const int nkv = max(it.nkv(0, p.tpt), TILES > 1 ? it.nkv(1, p.tpt) : 0), cut = it.first_cut();
                 uint32_t* mask = bad + e * PT_CUT * 4;      // read by the softmax warps before the entry is used again
                 if (lane < PT_CUT * 4) mask[lane] = 0;
                 __syncwarp();
@@ -579,7 +646,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;   // rescaled here, read out by the output warps
         const float sl = p.scale_log2;
         const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
-        int sc = 0, oc = 0;                   // score steps and items of this Q tile so far
+        int sc = 0, oc = 0;                   // score steps, and items (SPLIT: joins), of this Q tile so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const int e = k % PT_RING;
@@ -587,8 +654,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             PtItem it;
             ring_item(k, it);
             if (it.n < 0) break;
-            const int nkv = t < p.tiles ? it.nkv(t, p.tpt) : 0;
-            const int tok = it.t0 + t * p.tpt + row_tok;
+            const int total = it.nkv(0, p.tpt);            // (SPLIT) K/V tiles of both warpgroups
+            const int nkv = SPLIT ? (total + 1 - t) / 2 : it.nkv(t, p.tpt);
+            const int tok = it.t0 + (SPLIT ? 0 : t * p.tpt) + row_tok;
             const int pos = min(tok, it.n - 1);          // attends keys 0..pos
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nkv; ++j) {
@@ -598,7 +666,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
 #pragma unroll
                 for (int c = 0; c < PT_BN; c += 32) tmem_ld32(s_addr + c, s + c);
                 tmem_wait_ld();
-                const int lim = pos - j * PT_BN;   // columns past lim are masked
+                const int lim = pos - (SPLIT ? 2 * j + t : j) * PT_BN;   // columns past lim are masked
                 if (lim < PT_BN - 1) {
 #pragma unroll
                     for (int c = 0; c < PT_BN; c += 32) {
@@ -669,7 +737,35 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             }
             if (!ok) break;
             sc += nkv;
-            if (nkv > 0) {
+            if constexpr (SPLIT) {
+                // Both warpgroups' maximum and sum of each row through the output's factors: first m, then
+                // l 2^(m - M), then the factor 2^(m - M) / L of each one's O.
+                float* const mine = inv_l + t * 128 + r;
+                const float* const other = inv_l + (1 - t) * 128 + r;
+                auto joined = [&]() {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(LY::BAR_J));
+                    const bool got = pt_wait(bar(LY::BAR_J), oc & 1, abort_flag);
+                    ++oc;
+                    return got;
+                };
+                if (k > 0 && !pt_wait(bar(LY::BAR_OE), (k - 1) & 1, abort_flag)) break;   // the last item's have been read
+                *mine = m_ref;
+                if (!joined()) break;
+                const float m = fmaxf(m_ref, *other);
+                const float a = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
+                if (!joined()) break;
+                *mine = l * a;
+                if (!joined()) break;
+                const float sum = l * a + *other;
+                if (!joined()) break;
+                *mine = a / sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(LY::BAR_L + t));
+                const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
+                if (t == 0 && p.a.lse && row_tok < p.tpt && tok < it.n && hh < p.group)
+                    p.a.lse[((int64_t)it.start + tok) * p.a.hq + g * p.group + hh] = (m + log2f(sum)) * PT_LN2;
+            } else if (nkv > 0) {
                 // 1 / l for the output warps, once they have read the last item's
                 if (oc > 0 && !pt_wait(bar(LY::BAR_OE + t), (oc - 1) & 1, abort_flag)) break;
                 oc += 1;
@@ -699,16 +795,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             if (it.n < 0) break;
             const int g = it.head / p.nhb, hh = (it.head - g * p.nhb) * p.hb + row_head;
             const uint32_t* mask = bad + e * PT_CUT * 4;
-            const int nt = p.tiles > 1 && it.nkv(1, p.tpt) > 0 ? 2 : 1;
+            const int nt = TILES > 1 && it.nkv(1, p.tpt) > 0 ? 2 : 1;
+            const bool both = SPLIT && it.nkv(0, p.tpt) > 1;      // O_1 holds the odd K/V tiles' part
 #pragma unroll 1
             for (int t = 0; t < nt; ++t) {
-                ok = pt_wait(bar(LY::BAR_L + t), (ph >> t) & 1, abort_flag) && pt_wait(bar(LY::BAR_OR + t), (ph >> t) & 1, abort_flag) &&
-                     pt_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag);
+                ok = pt_wait(bar(LY::BAR_L + t), SPLIT ? k & 1 : (ph >> t) & 1, abort_flag) &&
+                     pt_wait(bar(LY::BAR_OR + t), (ph >> t) & 1, abort_flag) && pt_wait(bar(LY::BAR_IC + e), (k / PT_RING) & 1, abort_flag);
+                if constexpr (SPLIT)
+                    ok = ok && pt_wait(bar(LY::BAR_L + 1), k & 1, abort_flag) &&
+                         (!both || pt_wait(bar(LY::BAR_OR + 1), (ph >> 1) & 1, abort_flag));
                 if (!ok) break;
-                ph ^= 1u << t;
+                ph ^= both ? 3u : 1u << t;
                 tc_fence_after();
                 const bool any = __any_sync(0xffffffffu, lane < PT_CUT * 4 && mask[lane] != 0);
-                const float inv = inv_l[t * 128 + r];
+                const float inv = inv_l[t * 128 + r], inv1 = SPLIT ? inv_l[128 + r] : 0.f;
                 const int tok = it.t0 + t * p.tpt + row_tok;
                 const bool valid = row_tok < p.tpt && tok < it.n && hh < p.group;
                 const uint32_t o_addr = tmem + ((uint32_t)(quarter * 32) << 16) + LY::COL_O0 + t * D;
@@ -725,14 +825,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     float ov[32];
                     tmem_ld32(o_addr + cc, ov);
                     tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) ov[x] *= inv;
+                    if constexpr (SPLIT) {
+                        if (both) {
+                            float o1[32];
+                            tmem_ld32(o_addr + D + cc, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) ov[x] = fmaf(o1[x], inv1, ov[x]);
+                        }
+                    }
                     if (cc + 32 == D) {          // read: the next item's first product may overwrite it
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(LY::BAR_OE + t));
+                        if (lane == 0) {
+                            if (both) mbar_arrive(bar(LY::BAR_OE + 1));
+                            mbar_arrive(bar(LY::BAR_OE + t));
+                        }
                     }
                     uint32_t w[16];                  // four pieces of 8 columns
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) w[x] = pack_bf16x2(ov[2 * x] * inv, ov[2 * x + 1] * inv);
+                    for (int x = 0; x < 16; ++x) w[x] = pack_bf16x2(ov[2 * x], ov[2 * x + 1]);
 #pragma unroll
                     for (int b = 1; b < 4; b <<= 1)  // piece c of lane l changes places with piece l of lane c
 #pragma unroll
@@ -850,12 +964,12 @@ static int device_sms() {
     return counts[dev];
 }
 
-template <int D>
+template <int D, bool SPLIT>
 static int launch_pt(const PromptTcParams& p, unsigned grid, cudaStream_t stream) {
     static PerDeviceOnce attr;
     const int rc = per_device_once(attr, [] {
         const cudaError_t e =
-            cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PtLayout<D>::ALLOC);
+            cudaFuncSetAttribute(prompt_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PtLayout<D>::ALLOC);
         if (e != cudaSuccess) {
             set_error("prompt_attention: cannot set shared memory size: %s", cudaGetErrorString(e));
             return (int)RX_ECUDA;
@@ -864,7 +978,7 @@ static int launch_pt(const PromptTcParams& p, unsigned grid, cudaStream_t stream
         // must add up to no more than that, or the increasing warps would wait forever
         static_assert(256 * PT_REGS_OTHER + 256 * PT_REGS_SOFTMAX <= PT_THREADS * PT_REGS_LAUNCH, "register split");
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, prompt_tc_kernel<D>) != cudaSuccess || fa.numRegs < (int)PT_REGS_LAUNCH) {
+        if (cudaFuncGetAttributes(&fa, prompt_tc_kernel<D, SPLIT>) != cudaSuccess || fa.numRegs < (int)PT_REGS_LAUNCH) {
             set_error("prompt_attention: kernel built with %d registers per thread; the register split needs %d", fa.numRegs,
                       (int)PT_REGS_LAUNCH);
             return (int)RX_ECUDA;
@@ -872,7 +986,7 @@ static int launch_pt(const PromptTcParams& p, unsigned grid, cudaStream_t stream
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    launch_pdl(prompt_tc_kernel<D>, grid, PT_THREADS, PtLayout<D>::ALLOC, stream, p);   // an error shows in cudaGetLastError
+    launch_pdl(prompt_tc_kernel<D, SPLIT>, grid, PT_THREADS, PtLayout<D>::ALLOC, stream, p);   // an error shows in cudaGetLastError
     return RX_OK;
 }
 
@@ -889,18 +1003,21 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     p.scale_log2 = std::max(a.scale * PT_LOG2E, 0x1p-126f);
     const int64_t heads = (int64_t)a.hkv * p.nhb;
     // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn (1.4 us a step of
-    // 128 keys); one a piece, whose step is 1 us, while even those are no more than the SMs.
-    p.tiles = prompt_items(a.total, a.batch, p.tpt) * heads > sms ? 2 : 1;
-    const int64_t items = prompt_items(a.total, a.batch, p.tiles * p.tpt) * heads;
-    p.a.by_level = prompt_by_level(items, sms, a.batch, 2 * a.total * a.hkv * head_dim * 2);
-    p.by_tokens = PromptDiv(p.tiles * p.tpt);
-    p.by_heads = PromptDiv((int)heads);
+    // 128 keys); one, its K/V tiles split between two softmax warpgroups, while even those items are no
+    // more than the SMs.
+    const bool split = prompt_items(a.total, a.batch, p.tpt) * heads <= sms;
+    const int tokens = split ? p.tpt : 2 * p.tpt;
+    const int64_t items = prompt_items(a.total, a.batch, tokens) * heads;
     RX_REQUIRE(items < (1ll << 31), "prompt_attention: too many rows");
+    p.a.by_level = prompt_by_level(items, sms, a.batch, 2 * a.total * a.hkv * head_dim * 2);
+    p.by_tokens = PromptDiv(tokens);
+    p.by_heads = PromptDiv((int)heads);
     RX_REQUIRE(rows_map(&p.q_map, a.q, a.total, a.hq, head_dim, a.q_stride, p.hb, p.tpt) &&
                    rows_map(&p.k_map, a.k, a.total, a.hkv, head_dim, a.k_stride, 1, PT_BN) &&
                    rows_map(&p.v_map, a.v, a.total, a.hkv, head_dim, a.v_stride, 1, PT_BN),
                "prompt_attention: the driver made no tensor map of these rows");
-    return head_dim == 128 ? launch_pt<128>(p, (unsigned)items, stream) : launch_pt<64>(p, (unsigned)items, stream);
+    if (split) return head_dim == 128 ? launch_pt<128, true>(p, (unsigned)items, stream) : launch_pt<64, true>(p, (unsigned)items, stream);
+    return head_dim == 128 ? launch_pt<128, false>(p, (unsigned)items, stream) : launch_pt<64, false>(p, (unsigned)items, stream);
 }
 
 }  // namespace rx
