@@ -379,8 +379,9 @@ int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, 
  *  - A row's result depends on rows 0..i of its own sequence alone: an infinity or NaN in another
  *    row, or in rows that no sequence has, does not reach it.
  *  - Rows before indptr[0] and from indptr[batch] on are left as they were.
- *  - indptr [batch+1] must not decrease and lie in [0, total] (total <= 2^31-1 rows): a sequence that
- *    does not is RX_DEV_BAD_LENGTH and is skipped.
+ *  - indptr [batch+1] must not decrease and lie in [0, total] (total <= 2^31-1 rows), and a sequence
+ *    has at most 2^26 rows: one that does not keep to this is RX_DEV_BAD_LENGTH and is skipped.  Where
+ *    indptr decreases, rows of other sequences may be left out as well.
  *  - scale is finite and not negative (RX_EINVAL). */
 int prompt_attention(const rx_attn_desc* desc, int32_t batch, const void* d_q, int64_t q_stride,
                      const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride,

@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     }
                     if (!ok) break;
                 }
+                if (lane == 0) PromptFinder::check(p.a, place, p.by_heads);     // while the answer is on its way
                 ok = pt_wait(bar(LY::BAR_CLC), asked & 1, abort_flag);
                 if (!ok) break;
                 ++asked;

@@ -46,6 +46,10 @@ inline bool prompt_by_level(int64_t items, int resident, int32_t batch, int64_t 
     return items > resident && batch <= 64 && kv_bytes <= 80ll << 20;
 }
 
+// The longest sequence: the waits of the bf16 kernel, of which the longest is for one item, give up after 2 s;
+// an item at the end of 2^26 rows takes about 0.7 s.
+constexpr int PROMPT_MAX_ROWS = 1 << 26;
+
 struct PromptItem {
     int start, n, head, tile;   // first row and rows of the sequence, head, row tile
 };
@@ -53,12 +57,24 @@ struct PromptItem {
 // Finds the items' sequences.  A warp keeps 32 consecutive boundaries in its lanes: the items a
 // block takes one after another lie close together, so most are found without a memory access, and
 // the others in two or three rounds of loads.  32-bit arithmetic throughout: rows are below 2^31,
-// and a boundary that is not (the sequence is reported) is clamped.
+// and a boundary that is not is clamped.
 struct PromptFinder {
     int w0 = -1;             // first boundary of the window (-1: none loaded)
-    int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last
+    int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last.  By level: tiles of sequence `lane`
     bool good = false;       // it lies in [0, total]
-    bool unsound = false;    // (by level, where `mine` is the tiles of sequence `lane`) a sequence out of order was seen
+
+    // Whether a sequence's boundaries are in order and in [0, total], and it is not too long.
+    static __device__ __forceinline__ bool sound(const PromptParams& p, int64_t s, int64_t e) {
+        return s >= 0 && e >= s && e <= p.total && e - s <= PROMPT_MAX_ROWS;
+    }
+
+    // Reports sequence b's boundaries on the item that is head 0 of place b: there are more places than
+    // sequences and every item is taken once, so each sequence is looked at, also where boundaries out of
+    // order keep the items from finding it.  One lane of a block calls it, where no one waits for it.
+    static __device__ __forceinline__ void check(const PromptParams& p, int i, const PromptDiv& heads) {
+        const int b = heads(i);
+        if (b < p.batch && i == b * heads.d && !sound(p, p.indptr[b], p.indptr[b + 1])) report(p.status, RX_DEV_BAD_LENGTH);
+    }
 
     __device__ __forceinline__ int load(const PromptParams& p, int b, bool& ok) const {
         const int64_t x = p.indptr[b];
@@ -68,8 +84,7 @@ struct PromptFinder {
 
     // Item `i` by tile index from the highest down, then sequence, then head.  There are f(x) = sum over the
     // sequences of max(0, tiles - x) tiles of index x and up; item place q has index x where
-    // f(x + 1) <= q < f(x).  A sequence whose boundaries do not lie in order in [0, total] has no tiles
-    // (item 0 reports it).
+    // f(x + 1) <= q < f(x).  A sequence that is not sound has no tiles.
     __device__ __forceinline__ bool find_by_level(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
                                                   PromptItem& it) {
         const int lane = threadIdx.x & 31;
@@ -89,7 +104,6 @@ struct PromptFinder {
             if (q < f) lo = mid;
             else hi = mid, f_hi = f;
         }
-        if (i == 0 && __any_sync(0xffffffffu, unsound) && lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
         if (lo < 0) return false;
         int r = q - f_hi;                    // which of the sequences that have a tile `lo`
 #pragma unroll 1
@@ -114,16 +128,14 @@ struct PromptFinder {
     __device__ __forceinline__ int tiles(const PromptParams& p, int b, const PromptDiv& tile_tokens) {
         if (b >= p.batch) return 0;
         const int64_t s = p.indptr[b], e = p.indptr[b + 1];
-        const bool sound = s >= 0 && e >= s && e <= p.total;
-        unsound |= !sound;
-        return sound ? tile_tokens((int)(e - s) + tile_tokens.d - 1) : 0;
+        return sound(p, s, e) ? tile_tokens((int)(e - s) + tile_tokens.d - 1) : 0;
     }
 
     // Item `i` of the places x heads: within a sequence the heads one after another, and within a
     // head the tiles from the last, which has the most keys, to the first, so that the items that
-    // end a launch are short ones.  False for a place left over, and for a sequence whose boundaries
-    // do not lie in order in [0, total] (reported).  Every thread of a warp calls it with the same item.
-    __device__ __forceinline__ bool find_by_place(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads, PromptItem& it) {
+    // end a launch are short ones.  False for a place left over, and for a sequence that is not sound.
+    __device__ __forceinline__ bool find_by_place(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
+                                                  PromptItem& it) {
         const int lane = threadIdx.x & 31;
         const int place = heads(i);      // place-major bound of the sequence: base(b) <= place
         // the last sequence whose places start at or before this one
@@ -147,11 +159,8 @@ struct PromptFinder {
         // beyond the last boundary every lane holds the last: the sequence is the last one
         l = min(l, p.batch - 1 - w0);
         const int b = w0 + l, s = __shfl_sync(0xffffffffu, mine, l), e = __shfl_sync(0xffffffffu, mine, l + 1);
-        const unsigned sound = __ballot_sync(0xffffffffu, good);
-        if (((sound >> l) & 3u) != 3u || e < s) {
-            if (lane == 0) report(p.status, RX_DEV_BAD_LENGTH);
-            return false;
-        }
+        const unsigned in = __ballot_sync(0xffffffffu, good);
+        if (((in >> l) & 3u) != 3u || e < s || e - s > PROMPT_MAX_ROWS) return false;
         const int first = tile_tokens(s);
         const int places = tile_tokens(e) - first + 1;
         const int64_t at = i - (int64_t)(first + b) * heads.d;
@@ -163,10 +172,10 @@ struct PromptFinder {
         return (int64_t)it.tile * tile_tokens.d < it.n;
     }
 
+    // Every thread of a warp calls it with the same item.
     __device__ __forceinline__ bool find(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
                                          PromptItem& it) {
-        return p.by_level ? find_by_level(p, i, tile_tokens, heads, it)
-                                             : find_by_place(p, i, tile_tokens, heads, it);
+        return p.by_level ? find_by_level(p, i, tile_tokens, heads, it) : find_by_place(p, i, tile_tokens, heads, it);
     }
 };
 

@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(PS_THREADS, PsLayout<D>::BLOCKS)
     const uint32_t sb = smem_u32(sm);
     PromptItem it;
     PromptFinder finder;
-    if (!finder.find(p, (int)blockIdx.x, by_rows, by_heads, it)) return;
+    const bool found = finder.find(p, (int)blockIdx.x, by_rows, by_heads, it);
+    if (threadIdx.x == 0) PromptFinder::check(p, (int)blockIdx.x, by_heads);
+    if (!found) return;
     const int h = it.head, g = h / (p.hq / p.hkv);
     const int row0 = it.tile * PS_BM, rows = min(PS_BM, it.n - row0);
     const float* q = (const float*)p.q + (int64_t)(it.start + row0) * p.q_stride + (int64_t)h * D;

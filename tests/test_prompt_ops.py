@@ -646,6 +646,37 @@ def test_prompt_bad_boundaries_are_reported_and_skipped(dev, dt):
 
 @gpu
 @pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,ind,total", [(4, [0, 50, 30, 80], 80), (64, [0, 50, 30, 80], 80), (128, [0, 60, 10, 80], 80),
+                                          (64, [0, 900, 30, 1000], 1000), (16, [0] * 70 + [90, 80, 100], 100), (128, [0, 300, 250, 300, 300], 300)])
+def test_prompt_decreasing_boundaries_are_reported(dev, dt, hq, ind, total):
+    """However few tokens a tile holds, and in either order of the items; rows outside every sequence stay."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    q, k, v = rows_of(gen, total + 40, hq, 1, 64, dt)
+    for at in (0, 20):
+        out = torch.full((total + 40, hq, 64), 7.5, dtype=dt, device="cuda")
+        st = i32([0], "cuda")
+        api.prompt_attention(desc_of(dt, hq, 1, 64), len(ind) - 1, q, k, v, torch.tensor(ind, device="cuda") + at, out, None, total + 40, st)
+        assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+        assert (out[:at] == 7.5).all() and (out[at + total:] == 7.5).all()
+
+
+@gpu
+def test_prompt_too_long_a_sequence_is_reported(dev):
+    """One row more than 2^26 (one head, the same rows as q, k and v: 8.6 GB, and as much for the output)."""
+    n = (1 << 26) + 1
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    x, out = torch.empty(n + 3, 1, 64, dtype=BF, device="cuda"), torch.empty(n + 3, 1, 64, dtype=BF, device="cuda")
+    x[n:] = 1.0
+    out[:100], out[n - 100:] = 7.5, 7.5
+    st = i32([0], "cuda")
+    api.prompt_attention(desc_of(BF, 1, 1, 64), 2, x, x, x, torch.tensor([0, n, n + 3], device="cuda"), out, None, n + 3, st)
+    assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+    assert (out[:100] == 7.5).all() and (out[n - 100:n] == 7.5).all() and (out[n:] == 1.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
 def test_prompt_streams_and_graphs(dev, dt):
     """Calls on several streams at once, and two graphs captured on one stream and replayed on two,
     give the first call's bits."""
