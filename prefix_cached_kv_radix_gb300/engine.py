@@ -531,31 +531,43 @@ class PrefixCacheEngine:
         if len(slots) != total:
             raise ValueError(f"fork: {total} tail slots are needed, {len(slots)} given")
         st = self._stream if stream is None else stream
-        with torch.cuda.stream(st):
-            out = torch.empty(len(kv), r2t.shape[1], dtype=torch.int32, device=self.device)
-            api.kv_pool_fork(self.desc, self._pools(), self._i32(parents), self._i32(keep), self._i32(kv),
-                             self._i64(np.concatenate([[0], np.cumsum(tails)])), self._i32(slots if total else [0]), r2t, out, total,
-                             self.status, st)
+        try:
+            with torch.cuda.stream(st):
+                out = torch.empty(len(kv), r2t.shape[1], dtype=torch.int32, device=self.device)
+                api.kv_pool_fork(self.desc, self._pools(), self._i32(parents), self._i32(keep), self._i32(kv),
+                                 self._i64(np.concatenate([[0], np.cumsum(tails)])), self._i32(slots if total else [0]), r2t, out,
+                                 total, self.status, st)
+        except Exception:                # refused: the slots allocated here go back
+            if tail_slots is None:
+                self.tree.free_slots(slots)
+            raise
         return out, slots
 
     def resize(self, num_slots: int, stream=None) -> int:
         """Shrink or grow the pools of every layer to num_slots slots with everything cached kept:
         cached tokens past the new end move to free slots below it (api.radix_resize, kv_pool_copy on
-        the stream).  Memory past the end stays allocated for growing back; growing past what is
-        allocated allocates anew.  Returns the number of tokens moved."""
-        src, dst = self.tree.resize(num_slots)
+        the stream, after what is on the engine's own and before what comes there).  Memory past the end
+        stays allocated for growing back; growing past what is allocated allocates anew.  Returns the
+        number of tokens moved."""
         st = self._stream if stream is None else stream
+        stores = {}
+        if num_slots > self._k_store.shape[1]:          # first, as it may fail; of the engine's stream, as the old ones
+            with torch.cuda.stream(self._stream):
+                for name in ("_k_store", "_v_store"):
+                    stores[name] = torch.empty(self.num_layers, num_slots, self.hkv, self.d, dtype=self.tdtype, device=self.device)
+        src, dst = self.tree.resize(num_slots)
+        st.wait_stream(self._stream)
         with torch.cuda.stream(st):
             if len(src):
                 api.kv_pool_copy(self.desc, self._pools(), self._i32(src), self._i32(dst), 1, self.status, st)
-            if num_slots > self._k_store.shape[1]:
-                for name in ("_k_store", "_v_store"):
-                    old = getattr(self, name)
-                    new = torch.empty(self.num_layers, num_slots, self.hkv, self.d, dtype=self.tdtype, device=self.device)
-                    if self.poison:
-                        new.fill_(float("nan"))
-                    new[:, :old.shape[1]].copy_(old)
-                    setattr(self, name, new)
+            for name, new in stores.items():
+                old = getattr(self, name)
+                if self.poison:
+                    new.fill_(float("nan"))
+                new[:, :old.shape[1]].copy_(old)
+        self._stream.wait_stream(st)
+        for name, new in stores.items():
+            setattr(self, name, new)
         self._use_slots(num_slots)
         self.desc.num_slots = num_slots
         self._io_static = None           # the one-call path's pool addresses are set anew

@@ -185,3 +185,40 @@ def test_one_call_step_after_resize():
             want, _ = oracle_rows(w, b)
             compare(out[qo[b]:qo[b + 1]].float().cpu().numpy(), want, f"{slots} slots, request {b}")
         eng.tree.check()
+
+
+def test_resize_on_another_stream_is_in_order():
+    """What the engine's stream has written is moved, and what comes there next sees it moved, also where
+    the memory of the old pools is used again at once."""
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    n, slots = 3000, 20000
+    eng = PrefixCacheEngine("bf16", 8, 8, 128, slots, 3)
+    toks = np.arange(n, dtype=np.int32)
+    k, v = (torch.randn(n, 8, 128, device="cuda").bfloat16() for _ in range(2))
+    eng.populate(toks, k, v)
+    a, b = torch.randn(8192, 8192, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for size in (40000, 6000, 70000):
+        with torch.cuda.stream(b):
+            for _ in range(4):
+                a @ a                                  # a busy stream
+        eng.resize(size, stream=b)
+        junk = [torch.full((slots, 8, 128), 9.0, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+        sl, m, _ = eng.tree.match_prefix(toks)
+        at = torch.tensor(sl, device="cuda").long()
+        assert m == n and torch.equal(eng.k_pool[at], k) and torch.equal(eng.v_pool[at], v)
+        del junk
+    assert eng.device_status() == 0
+
+
+def test_refused_fork_gives_its_slots_back():
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    eng = PrefixCacheEngine("f32", 2, 2, 64, 64, 3)
+    free = eng.tree.stats()["free_slots"]
+    with pytest.raises(ValueError):
+        eng.fork(torch.zeros(1, 8, device="cuda"), [0], [2], [5])          # not a table of slots
+    assert eng.tree.stats()["free_slots"] == free
+    with pytest.raises(ValueError):
+        eng.fork(torch.zeros(1, 8, dtype=torch.int32, device="cuda"), [0], [6], [5])
+    assert eng.tree.stats()["free_slots"] == free
+    eng.tree.check()
