@@ -307,8 +307,9 @@ typedef struct {
 /* kv_pool_write for rows whose rotary positions are still to be applied: turns the new keys on
  * their way into the pool, copies the new values, turns the queries, and builds the slot table,
  * in one launch (decode steps of one token per request and whole prompts alike).
- * The batch, slot lists, pools, table and their errors are those of kv_pool_write; d_req_to_token
- * NULL makes no table, and d_new_slots NULL writes no pool (then no table either): only rows are
+ * The batch, slot lists, pools, table and their errors are those of kv_pool_write; d_prefix_slots may
+ * be NULL where nothing is matched (a request that has matched slots is then RX_DEV_BAD_LENGTH),
+ * d_req_to_token NULL makes no table, and d_new_slots NULL writes no pool (then no table either): only rows are
  * turned.  Rows are [T, hq | hkv, head_dim] with the heads of a row contiguous and `stride` elements
  * between rows, so that they can be parts of one projection's output; strides and addresses are
  * multiples of 16 bytes.  d_positions: int32 [n_axes, pos_stride], entry (a, t) the position of row
@@ -382,7 +383,7 @@ int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, 
  *  - indptr [batch+1] must not decrease and lie in [0, total] (total <= 2^31-1 rows), and a sequence
  *    has at most 2^26 rows: one that does not keep to this is RX_DEV_BAD_LENGTH and is skipped.  Where
  *    indptr decreases, rows of other sequences may be left out as well.
- *  - scale is finite and not negative (RX_EINVAL). */
+ *  - scale is finite, as scale log2(e) in float is, and not negative (RX_EINVAL). */
 int prompt_attention(const rx_attn_desc* desc, int32_t batch, const void* d_q, int64_t q_stride,
                      const void* d_k, int64_t k_stride, const void* d_v, int64_t v_stride,
                      const int64_t* d_indptr, void* d_out, int64_t out_stride, float* d_lse, int64_t total,

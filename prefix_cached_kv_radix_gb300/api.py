@@ -647,7 +647,7 @@ def decode_attention_noalloc(desc, batch, q, req_to_token, kv_lens, k_pool, v_po
 
 
 # ---------------------------------------------------------------------------- rows, pages, prompts
-_NBYTES = {RX_F32: 4, RX_BF16: 2}
+_FLOATS = {RX_F32: "torch.float32", RX_BF16: "torch.bfloat16"}
 _INTS = {"torch.int32": 4, "torch.int64": 8}
 _ops_ext = None
 
@@ -678,7 +678,7 @@ def _rows(name, t, heads: int, desc, total: int):
         return None, 0
     d = desc.head_dim
     shape, stride = t.shape, t.stride()
-    if not t.is_cuda or t.element_size() != _NBYTES[desc.dtype] or not t.is_floating_point():
+    if not t.is_cuda or str(t.dtype) != _FLOATS[desc.dtype]:
         raise ValueError(f"{name}: not rows of the descriptor's type on a CUDA device")
     if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < total or stride[2] != 1 or \
             (heads > 1 and stride[1] != d):
@@ -708,7 +708,7 @@ def _here(*tensors):
 def _pool_list(desc, pools):
     n = desc.num_slots * desc.hkv * desc.head_dim
     for p in pools:
-        if not p.is_cuda or not p.is_contiguous() or p.numel() != n or p.element_size() != _NBYTES[desc.dtype]:
+        if not p.is_cuda or not p.is_contiguous() or p.numel() != n or str(p.dtype) != _FLOATS[desc.dtype]:
             raise ValueError("pools: want contiguous [num_slots, hkv, head_dim] of the descriptor's type on a CUDA device")
     return (ctypes.c_void_p * max(len(pools), 1))(*[p.data_ptr() for p in pools])
 
@@ -756,7 +756,8 @@ def kv_pool_write_rope(desc, rope, batch, prefix_slots, prefix_indptr, new_slots
     stride = 0
     if req_to_token is not None:
         stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride
-    _here(k_new, positions, qo_indptr, k_pool, q, status)
+    _here(prefix_slots, prefix_indptr, new_slots, qo_indptr, positions, q, k_new, v_new, q_out, k_out, k_pool, v_pool, req_to_token,
+          status)
     _check("kv_pool_write_rope", load().kv_pool_write_rope(
         ctypes.byref(desc), ctypes.byref(rope), batch, _ints("prefix_slots", prefix_slots, 4, 0),
         _ints("prefix_indptr", prefix_indptr, 8, batch + 1), _ints("new_slots", new_slots, 4, total_new),
@@ -789,8 +790,10 @@ def kv_pool_fork(desc, pools, parents, keep_lens, kv_lens, tail_indptr, tail_slo
     if ext is not None:
         return _check("kv_pool_fork", ext.kv_pool_fork(ctypes.addressof(desc), pools, parents, keep_lens, kv_lens, tail_indptr,
                                                        tail_slots, r2t_in, r2t_out, total_tail, status, _stream_of(stream)))
+    if r2t_in.dim() != 2 or r2t_out.dim() != 2:
+        raise ValueError("r2t_in, r2t_out: want [rows, stride]")
     n = r2t_out.shape[0]
-    _here(parents, r2t_in, r2t_out, status, *pools)
+    _here(parents, keep_lens, kv_lens, tail_indptr, tail_slots, r2t_in, r2t_out, status, *pools)
     _check("kv_pool_fork", load().kv_pool_fork(
         ctypes.byref(desc), len(pools), _pool_list(desc, pools), n, _ints("parents", parents, 4, n),
         _ints("keep_lens", keep_lens, 4, n), _ints("kv_lens", kv_lens, 4, n), _ints("tail_indptr", tail_indptr, 8, n + 1),
@@ -809,9 +812,10 @@ def prompt_attention(desc, batch, q, k, v, indptr, out, lse, total, status, stre
     ka, ks = _rows("k", k, desc.hkv, desc, total)
     va, vs = _rows("v", v, desc.hkv, desc, total)
     oa, os_ = _rows("out", out, desc.hq, desc, total)
-    if lse is not None and (not lse.is_contiguous() or lse.numel() < total * desc.hq or lse.element_size() != 4):
-        raise ValueError(f"lse: want contiguous float32 [{total}, {desc.hq}]")
-    _here(q, k, v, out, indptr, status)
+    if lse is not None and (not lse.is_cuda or not lse.is_contiguous() or lse.numel() < total * desc.hq or
+                            str(lse.dtype) != "torch.float32"):
+        raise ValueError(f"lse: want contiguous float32 [{total}, {desc.hq}] on a CUDA device")
+    _here(q, k, v, out, lse, indptr, status)
     _check("prompt_attention", load().prompt_attention(
         ctypes.byref(desc), batch, qa, qs, ka, ks, va, vs, _ints("indptr", indptr, 8, batch + 1), oa, os_,
         None if lse is None else lse.data_ptr(), total, _ints("status", status, 4, 1), _stream(stream)))

@@ -8,7 +8,7 @@
 //
 // Both are bound by HBM: each byte is read once and written once, and nothing is computed.  A warp
 // moves a segment of up to MOVE_SEG 16-byte vectors of one page in one pool, all its loads in
-// flight before its first store (4 KB a warp, 64 warps an SM: more than the latency of HBM times
+// flight before its first store (4 KB a warp, 32 warps an SM: more than the latency of HBM times
 // its rate needs), so the rows' order in the pool does not matter as long as a row is some hundred
 // bytes.  The pool addresses travel as a kernel argument, so one launch moves a token's rows of
 // every layer.  Measured: 3001 pages of 16 tokens in 4 layers (8 kv heads x 128, bf16), 1.57 GB read and
@@ -188,8 +188,8 @@ static int move_launched(const char* fn) {
     return RX_OK;
 }
 
-// Blocks of a grid-stride launch over `items` warps' work: all of it at once up to eight blocks an
-// SM, the most that are resident.
+// Blocks of a grid-stride launch over `items` warps' work: a block for each eight, up to eight blocks an
+// SM, twice what is resident, so that SMs that finish early take from the second half.
 static int64_t move_blocks(int64_t items) { return std::min<int64_t>((items + MOVE_WARPS - 1) / MOVE_WARPS, 152 * 8); }
 
 }  // namespace rx

@@ -10,8 +10,8 @@ namespace rx {
 
 // One tile of NT * PER entries of request b's slot-table row: its matched (prefix) slots, then
 // its new slots, then -1 up to the row's stride.  All loads are issued before the first store
-// (each thread has PER independent loads in flight).  Bad lengths and slots are reported; a bad
-// entry is written as -1.
+// (each thread has PER independent loads in flight).  Bad lengths (matched slots without a list of
+// them are one) and slots are reported; a bad entry is written as -1.
 template <int NT, int PER = 4>
 __device__ __forceinline__ void kpw_table_tile(int b, int64_t tile, const int32_t* __restrict__ prefix_slots,
                                                const int64_t* __restrict__ prefix_indptr,
@@ -23,7 +23,7 @@ __device__ __forceinline__ void kpw_table_tile(int b, int64_t tile, const int32_
     const int64_t p0 = prefix_indptr[b], P = prefix_indptr[b + 1] - p0;
     const int64_t q0 = qo_indptr[b], n = qo_indptr[b + 1] - q0;
     int32_t* row = r2t + (int64_t)b * stride;
-    const bool bad_len = P < 0 || n < 0 || P + n > stride || q0 < t_begin || q0 + n > t_end;
+    const bool bad_len = P < 0 || n < 0 || P + n > stride || q0 < t_begin || q0 + n > t_end || (P > 0 && !prefix_slots);
     if (bad_len && j0 == 0 && threadIdx.x == 0) report(status, RX_DEV_BAD_LENGTH);
     int32_t s[PER];
 #pragma unroll

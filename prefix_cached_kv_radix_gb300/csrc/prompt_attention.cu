@@ -424,99 +424,99 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
                 }
             } else {
-            // ring positions: the next K tile to be multiplied by Q, the V tile of the current step, the step's end
-            uint32_t ks = 0, kph = 0, vs = 0, vph = 0, es = 0;
-            auto k_next = [&](uint32_t& slot, uint32_t& ph) {
-                if (++slot == NK) slot = 0, ph ^= 1;
-            };
-            // by bits, one for each Q tile: phase of its P barriers (a step each), parity of its items so
-            // far, whether it has had any, and whether S of the coming item's first K tile is on its way
-            uint32_t pph = 0, odd = 0, had = 0, issued = 0;
-            PtItem nx{};                    // the coming item, where it was there to be read in time
-            bool have_nx = false;
-            bool ok = true;
-            // The tensor core works off what is issued in order and with some 400 clocks of it in its
-            // queue; what this warp does between two groups of products has to fit into that.  So the
-            // waits for K and V, which are long there, stand where the queue is full, and a step's end is
-            // committed once for the K and the V tile that it frees.
-            for (int k = 0; ok; ++k) {
-                const int e = k % PT_RING;
-                if (!have_nx) {
-                    if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
-                    ring_item(k, nx);
-                }
-                const PtItem it = nx;
-                if (it.n < 0) break;
-                have_nx = false;
-                const int n0 = it.nkv(0, p.tpt), n1 = TILES > 1 ? it.nkv(1, p.tpt) : 0;
-                const int nkv = max(n0, n1);
-#pragma unroll 1
-                for (int t = 0; ok && t < 2; ++t) {
-                    const int nt = t == 0 ? n0 : n1;
-                    if (nt == 0 || ((issued >> t) & 1u)) continue;
-                    ok = pt_wait(bar(LY::BAR_Q + t), (odd >> t) & 1u, abort_flag) && pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
-                    tc_fence_after();
-                    if (ok) issue_s(t, ks, nt == 1);
-                }
-                issued = 0;
-                k_next(ks, kph);
-                bool have_v = false;        // the step's V has been seen to be there
-                for (int j = 0; ok && j < nkv; ++j) {
-                    const bool more = j + 1 < nkv;
-                    uint32_t vs1 = vs + 1, vph1 = vph;
-                    if (vs1 == NV) vs1 = 0, vph1 ^= 1;
-                    if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) break;
-                    if (j + 1 == n0) {                        // the coming item, for its first scores
-                        const int e2 = (k + 1) % PT_RING;
-                        have_nx = ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1);
-                        if (have_nx) ring_item(k + 1, nx);
+                // ring positions: the next K tile to be multiplied by Q, the V tile of the current step, the step's end
+                uint32_t ks = 0, kph = 0, vs = 0, vph = 0, es = 0;
+                auto k_next = [&](uint32_t& slot, uint32_t& ph) {
+                    if (++slot == NK) slot = 0, ph ^= 1;
+                };
+                // by bits, one for each Q tile: phase of its P barriers (a step each), parity of its items so
+                // far, whether it has had any, and whether S of the coming item's first K tile is on its way
+                uint32_t pph = 0, odd = 0, had = 0, issued = 0;
+                PtItem nx{};                    // the coming item, where it was there to be read in time
+                bool have_nx = false;
+                bool ok = true;
+                // The tensor core works off what is issued in order and with some 400 clocks of it in its
+                // queue; what this warp does between two groups of products has to fit into that.  So the
+                // waits for K and V, which are long there, stand where the queue is full, and a step's end is
+                // committed once for the K and the V tile that it frees.
+                for (int k = 0; ok; ++k) {
+                    const int e = k % PT_RING;
+                    if (!have_nx) {
+                        if (!pt_wait(bar(LY::BAR_IF + e), (k / PT_RING) & 1, abort_flag)) break;
+                        ring_item(k, nx);
                     }
-                    if (!have_v && !(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
-                    have_v = false;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t == 0 ? n0 : n1;
-                        if (j >= nt) continue;
-                        // the previous item's O_t has been read out
-                        if (j == 0 && ((had >> t) & 1u) && !(ok = pt_wait(bar(LY::BAR_OE + t), ((odd >> t) & 1u) ^ 1u, abort_flag))) break;
+                    const PtItem it = nx;
+                    if (it.n < 0) break;
+                    have_nx = false;
+                    const int n0 = it.nkv(0, p.tpt), n1 = TILES > 1 ? it.nkv(1, p.tpt) : 0;
+                    const int nkv = max(n0, n1);
 #pragma unroll 1
-                        for (int h = 0; ok && h < 2; ++h) {
-                            ok = pt_wait(bar(LY::BAR_P + 2 * h + t), (pph >> t) & 1u, abort_flag);
-                            tc_fence_after();
-                            if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
+                    for (int t = 0; ok && t < 2; ++t) {
+                        const int nt = t == 0 ? n0 : n1;
+                        if (nt == 0 || ((issued >> t) & 1u)) continue;
+                        ok = pt_wait(bar(LY::BAR_Q + t), (odd >> t) & 1u, abort_flag) && pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag);
+                        tc_fence_after();
+                        if (ok) issue_s(t, ks, nt == 1);
+                    }
+                    issued = 0;
+                    k_next(ks, kph);
+                    bool have_v = false;        // the step's V has been seen to be there
+                    for (int j = 0; ok && j < nkv; ++j) {
+                        const bool more = j + 1 < nkv;
+                        uint32_t vs1 = vs + 1, vph1 = vph;
+                        if (vs1 == NV) vs1 = 0, vph1 ^= 1;
+                        if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), kph, abort_flag))) break;
+                        if (j + 1 == n0) {                        // the coming item, for its first scores
+                            const int e2 = (k + 1) % PT_RING;
+                            have_nx = ready(bar(LY::BAR_IF + e2), ((k + 1) / PT_RING) & 1);
+                            if (have_nx) ring_item(k + 1, nx);
+                        }
+                        if (!have_v && !(ok = pt_wait(bar(LY::BAR_VF + vs), vph, abort_flag))) break;
+                        have_v = false;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int nt = t == 0 ? n0 : n1;
+                            if (j >= nt) continue;
+                            // the previous item's O_t has been read out
+                            if (j == 0 && ((had >> t) & 1u) && !(ok = pt_wait(bar(LY::BAR_OE + t), ((odd >> t) & 1u) ^ 1u, abort_flag))) break;
+#pragma unroll 1
+                            for (int h = 0; ok && h < 2; ++h) {
+                                ok = pt_wait(bar(LY::BAR_P + 2 * h + t), (pph >> t) & 1u, abort_flag);
+                                tc_fence_after();
+                                if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
+                            }
+                            if (!ok) break;
+                            pph ^= 1u << t;
+                            if (more && (t == 1 || j >= n1)) have_v = ready(bar(LY::BAR_VF + vs1), vph1);
+                            // the tile's next scores: of the next step, or of the coming item's first if all they
+                            // need is here already; their softmax then runs under this item's last products
+                            uint32_t kk = ks, kkph = kph;
+                            bool go = j + 1 < nt, last = j + 2 == nt;
+                            if (!go) {
+                                pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
+                                if (t == 0 && more) k_next(kk, kkph);
+                                if (have_nx && nx.n >= 0) {
+                                    const int nn = nx.nkv(t, p.tpt);
+                                    last = nn == 1;
+                                    go = nn > 0 && ready(bar(LY::BAR_Q + t), ((odd >> t) & 1u) ^ 1u) &&
+                                         (t == 0 ? ready(bar(LY::BAR_KF + kk), kkph) : (issued & 1u) != 0);
+                                    tc_fence_after();
+                                    if (go) issued |= 1u << t;
+                                }
+                            }
+                            if (go) issue_s(t, kk, last);
                         }
                         if (!ok) break;
-                        pph ^= 1u << t;
-                        if (more && (t == 1 || j >= n1)) have_v = ready(bar(LY::BAR_VF + vs1), vph1);
-                        // the tile's next scores: of the next step, or of the coming item's first if all they
-                        // need is here already; their softmax then runs under this item's last products
-                        uint32_t kk = ks, kkph = kph;
-                        bool go = j + 1 < nt, last = j + 2 == nt;
-                        if (!go) {
-                            pt_commit(bar(LY::BAR_OR + t));   // O_t of this item complete
-                            if (t == 0 && more) k_next(kk, kkph);
-                            if (have_nx && nx.n >= 0) {
-                                const int nn = nx.nkv(t, p.tpt);
-                                last = nn == 1;
-                                go = nn > 0 && ready(bar(LY::BAR_Q + t), ((odd >> t) & 1u) ^ 1u) &&
-                                     (t == 0 ? ready(bar(LY::BAR_KF + kk), kkph) : (issued & 1u) != 0);
-                                tc_fence_after();
-                                if (go) issued |= 1u << t;
-                            }
-                        }
-                        if (go) issue_s(t, kk, last);
+                        pt_commit(bar(LY::BAR_E + es));       // this step's V and the next one's K are read
+                        es = (es + 1) % LY::NE;
+                        if (more) k_next(ks, kph);
+                        vs = vs1, vph = vph1;
                     }
-                    if (!ok) break;
-                    pt_commit(bar(LY::BAR_E + es));       // this step's V and the next one's K are read
-                    es = (es + 1) % LY::NE;
-                    if (more) k_next(ks, kph);
-                    vs = vs1, vph = vph1;
+                    odd ^= n1 > 0 ? 3u : 1u;
+                    had |= n1 > 0 ? 3u : 1u;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
                 }
-                odd ^= n1 > 0 ? 3u : 1u;
-                had |= n1 > 0 ? 3u : 1u;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
-            }
             }
             pt_commit(bar(LY::BAR_DONE));
             __syncwarp();
@@ -1033,7 +1033,7 @@ extern "C" int prompt_attention(const rx_attn_desc* desc, int32_t batch, const v
     RX_REQUIRE(desc->dtype == RX_F32 || desc->dtype == RX_BF16, "prompt_attention: unknown dtype %d", desc->dtype);
     RX_REQUIRE(desc->hq > 0 && desc->hkv > 0 && desc->hq <= 65536 && desc->hq % desc->hkv == 0, "prompt_attention: bad head counts");
     RX_REQUIRE(desc->head_dim == 64 || desc->head_dim == 128, "prompt_attention: head_dim must be 64 or 128");
-    RX_REQUIRE(std::isfinite(desc->scale) && desc->scale >= 0.f, "prompt_attention: scale must be finite and not negative");
+    RX_REQUIRE(std::isfinite(desc->scale * PT_LOG2E) && desc->scale >= 0.f, "prompt_attention: scale must be finite and not negative");
     if (batch == 0 || total == 0) return RX_OK;
     RX_REQUIRE(d_q && d_k && d_v && d_indptr && d_out, "prompt_attention: null device pointer");
     const int64_t elt = desc->dtype == RX_F32 ? 4 : 2, D = desc->head_dim;

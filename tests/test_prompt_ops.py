@@ -54,7 +54,7 @@ def test_prompt_attention_refuses():
                dict(out=None), dict(q=A + 8), dict(k=A + 2), dict(qs=255), dict(ks=127), dict(ks=64), dict(os_=248),
                dict(vs=132), dict(desc=desc_of(BF, 4, 3, 64)), dict(desc=desc_of(BF, 4, 0, 64)), dict(desc=desc_of(BF, 4, 2, 96)),
                dict(desc=desc_of(BF, 4, 2, 64, scale=-1.0)), dict(desc=desc_of(BF, 4, 2, 64, scale=math.inf)),
-               dict(desc=desc_of(BF, 4, 2, 64, scale=math.nan)), dict(desc=api.make_desc(7, 4, 2, 64, 4, 1.0))):
+               dict(desc=desc_of(BF, 4, 2, 64, scale=math.nan)), dict(desc=desc_of(BF, 4, 2, 64, scale=3e38)), dict(desc=api.make_desc(7, 4, 2, 64, 4, 1.0))):
         call(**kw)
 
 
@@ -424,6 +424,21 @@ def test_rope_bad_slots_and_lengths(dev):
 
 
 @gpu
+def test_rope_without_a_prefix_list(dev):
+    """No list of matched slots: fine for requests without any, a bad length for the others."""
+    gen = torch.Generator("cuda").manual_seed(12)
+    c = rope_case(gen, BF, 2, 2, 64, [4, 3, 5], [0, 0, 0], torch.arange(12, device="cuda")[None])
+    kp, vp = (torch.zeros(c["num"], 2, 64, dtype=BF, device="cuda") for _ in range(2))
+    for pi, want in (([0, 0, 0, 0], api.RX_DEV_OK), ([0, 0, 2, 2], api.RX_DEV_BAD_LENGTH)):
+        r2t, st = torch.empty(3, 9, dtype=torch.int32, device="cuda"), i32([0], "cuda")
+        api.kv_pool_write_rope(desc_of(BF, 2, 2, 64, c["num"]), api.rope_desc(32), 3, None, torch.tensor(pi, device="cuda"), c["ns"],
+                               c["qi"], c["pos"], None, c["k"], c["v"], None, None, kp, vp, r2t, 12, st)
+        ns = c["ns"].tolist()
+        mid = ns[4:7] + [-1] * 6 if want == api.RX_DEV_OK else [-1] * 9
+        assert int(st.item()) == want and r2t.tolist() == [ns[:4] + [-1] * 5, mid, ns[7:] + [-1] * 4]
+
+
+@gpu
 @pytest.mark.parametrize("native", [True, False])
 def test_binding_refuses(dev, native, monkeypatch):
     """The same refusals from the extension and from the Python code that stands in for it."""
@@ -445,6 +460,28 @@ def test_binding_refuses(dev, native, monkeypatch):
     with pytest.raises(ValueError):
         api.kv_pool_write_rope(d, api.rope_desc(32), 1, None, None, None, ip, torch.zeros(2, 8, dtype=torch.int32, device="cuda"), q, k,
                                None, q, k, None, None, None, 8, st)
+
+
+@gpu
+@pytest.mark.parametrize("native", [True, False])
+def test_binding_refuses_other_types_and_places(dev, native, monkeypatch):
+    """Types of the same size as the right ones, and buffers on the host."""
+    if not native:
+        monkeypatch.setattr(api, "_ops_ext", False)
+    d, st, ip = desc_of(BF, 4, 2, 64, 10), i32([0], "cuda"), torch.tensor([0, 8], device="cuda")
+    q, k = torch.zeros(8, 4, 64, dtype=BF, device="cuda"), torch.zeros(8, 2, 64, dtype=BF, device="cuda")
+    lse = torch.zeros(8, 4, device="cuda")
+    for bad in (dict(q=q.half()), dict(out=q.half()), dict(lse=lse.cpu()), dict(lse=lse.int()), dict(ip=ip.double()), dict(st=st.float())):
+        a = dict(dict(q=q, out=torch.empty_like(q), ip=ip, lse=lse, st=st), **bad)
+        with pytest.raises(ValueError):
+            api.prompt_attention(d, 1, a["q"], k, k, a["ip"], a["out"], a["lse"], 8, a["st"])
+    pool, one = torch.zeros(10, 2, 64, dtype=BF, device="cuda"), i32([1], "cuda")
+    for bad in (pool.half(), pool.cpu(), pool.short(), pool.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            api.kv_pool_copy(d, [pool, bad], one, one, 1, st)
+    for bad in (one, one.cpu()[None], one.float()[None]):
+        with pytest.raises(ValueError):
+            api.kv_pool_fork(d, [pool], one, one, one, ip, one, one[None], bad, 0, st)
 
 
 @gpu
@@ -673,6 +710,104 @@ def test_prompt_too_long_a_sequence_is_reported(dev):
     api.prompt_attention(desc_of(BF, 1, 1, 64), 2, x, x, x, torch.tensor([0, n, n + 3], device="cuda"), out, None, n + 3, st)
     assert int(st.item()) == api.RX_DEV_BAD_LENGTH
     assert (out[:100] == 7.5).all() and (out[n - 100:n] == 7.5).all() and (out[n:] == 1.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_prompt_small_calls_beside_a_long_one(dev, dt):
+    """Small calls on other streams while a long one holds every SM, and as it leaves them one by one: blocks
+    take the work of those that have not begun, so that one may have several items of a small call."""
+    gen = torch.Generator("cuda").manual_seed(8)
+    desc, st = desc_of(dt, 4, 2, 64), i32([0], "cuda")
+    small = [rows_of(gen, sum(lens), 4, 2, 64, dt) + (lens, indptr(lens, "cuda")) for lens in ([513], [1, 200, 0, 64, 300], [30] * 20)]
+    want = [run_prompt(q, k, v, lens, desc)[0] for q, k, v, lens, _ in small]
+    n = 12000 if dt == BF else 5000
+    lq, lk, lv = rows_of(gen, n, 16, 2, 64, dt)
+    ldesc, lip = desc_of(dt, 16, 2, 64), indptr([n], "cuda")
+    long_out = torch.empty(n, 16, 64, dtype=dt, device="cuda")
+    streams, outs = [torch.cuda.Stream() for _ in range(5)], []
+    torch.cuda.synchronize()
+    for r in range(6):
+        with torch.cuda.stream(streams[0]):
+            api.prompt_attention(ldesc, 1, lq, lk, lv, lip, long_out, None, n, st)
+        for i in range(12):
+            q, k, v, lens, ip = small[i % 3]
+            with torch.cuda.stream(streams[1 + i % 4]):
+                o = torch.full((q.shape[0], 4, 64), 7.5, dtype=dt, device="cuda")
+                api.prompt_attention(desc, len(lens), q, k, v, ip, o, None, q.shape[0], st)
+                outs.append((i % 3, o))
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for i, o in outs:
+        assert torch.equal(o, want[i])
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("n", [90, 2500])
+def test_chain_of_calls_without_waits(dev, dt, n):
+    """Each operator reads what the one before it wrote, in eager order, and twice as a captured graph:
+    turned in place, attended, the pool's rows moved, forked, attended again through the forked table."""
+    gen = torch.Generator("cuda").manual_seed(n)
+    hq, hkv, d = 4, 2, 64
+    c = rope_case(gen, dt, hq, hkv, d, [n], [0], torch.arange(n, device="cuda")[None], slots_extra=2 * n)
+    num, T = c["num"], n
+    desc, rope, st = desc_of(dt, hq, hkv, d, num), api.rope_desc(32), i32([0], "cuda")
+    free = torch.tensor(sorted(set(range(num)) - set(c["ns"].tolist())), dtype=torch.int32, device="cuda")
+    dst, tail = free[:n].contiguous(), free[n:2 * n].contiguous()
+    x0, x = c["x"], torch.empty_like(c["x"])
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:hq + 2 * hkv]
+    pools = [torch.empty(num, hkv, d, dtype=dt, device="cuda") for _ in range(2)]
+    r2t, moved = torch.empty(1, n, dtype=torch.int32, device="cuda"), dst[None].contiguous()
+    fork, out, dec = torch.empty(1, n, dtype=torch.int32, device="cuda"), torch.empty(n, hq, d, dtype=dt, device="cuda"), torch.empty(1, hq, d, dtype=dt, device="cuda")
+    zero, kvl, ti = i32([0], "cuda"), i32([n], "cuda"), indptr([n], "cuda")
+    ws = torch.empty(max(api.decode_workspace_bytes(desc, 1, n), 256), dtype=torch.uint8, device="cuda")
+
+    def run():
+        x.copy_(x0)
+        api.kv_pool_write_rope(desc, rope, 1, None, c["pi"], c["ns"], c["qi"], c["pos"], q, k, v, q, k, *pools, r2t, T, st)
+        api.prompt_attention(desc, 1, q, k, v, c["qi"], out, None, T, st)
+        api.kv_pool_copy(desc, pools, c["ns"], dst, 1, st)
+        api.kv_pool_fork(desc, pools, zero, zero, kvl, ti, tail, moved, fork, n, st)
+        api.decode_attention(desc, 1, out[n - 1:], fork, kvl, *pools, dec, None, n, ws, st)
+        api.kv_pool_write_rope(desc, rope, 1, None, None, None, c["qi"], c["pos"], q, k, None, q, k, None, None, None, T, st)
+
+    def wipe():
+        for t in (x, *pools, out, dec):
+            t.fill_(math.nan)
+        r2t.fill_(-7), fork.fill_(-7)
+
+    def take():
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        return [t.clone() for t in (q, k, out, dec, fork, r2t)] + [p[i.long()] for p in pools for i in (c["ns"], dst, tail)]
+    wipe()
+    run()
+    got = take()
+    assert torch.equal(got[6], got[7]) and torch.equal(got[6], got[8]) and torch.equal(got[4][0], tail)
+    turned = [torch.empty(n, h, d, dtype=dt, device="cuda") for h in (hq, hkv)]
+    api.kv_pool_write_rope(desc, rope, 1, None, None, None, c["qi"], c["pos"], x0[:, :hq], x0[:, hq:hq + hkv], None, *turned, None, None,
+                           None, T, st)
+    torch.cuda.synchronize()
+    want, _, to, _ = attention(*turned, v, [n], desc.scale)
+    close(out, want, to, "out")
+    for r in range(3):
+        wipe()
+        run()
+        for a, b in zip(got, take()):
+            assert torch.equal(a, b)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        run()
+        run()
+    for r in range(3):
+        wipe()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+            g.replay()
+        for a, b in zip(got, take()):
+            assert torch.equal(a, b)
 
 
 @gpu
