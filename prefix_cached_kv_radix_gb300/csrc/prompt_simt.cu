@@ -21,7 +21,7 @@
 //
 // Measured, against 79 TFLOP/s of the multiply-add pipe: 8 ragged prompts of up to 2001 tokens, 16/4 heads x
 // 64, 0.43 ms (49; with pairs of channels instead of rows 0.48), four of 4096 tokens 54, one of 8192 tokens, 16/4
-// heads x 128, 58.  Small calls are one block's chain of tiles: one of 300 tokens 23 us.
+// heads x 128, 58.  Small calls are one block's chain of tiles: one of 300 tokens, 12 heads x 64, 23 us.
 //
 // A value row that a row may not see enters none of its sums, so an infinity or a NaN there (a later
 // token, the next sequence's row) stays where it is.
@@ -40,6 +40,7 @@ namespace rx {
 constexpr int PS_BM = 64, PS_BN = 64;
 constexpr float PS_LOG2E = 1.4426950408889634f;
 constexpr float PS_LN2 = 0.6931471805599453f;
+constexpr int PS_ALONE = 120000;   // bytes of shared memory with which a block has an SM to itself
 
 template <int D, int TX_>
 struct PsLayout {
@@ -292,11 +293,12 @@ __global__ void __launch_bounds__(PsLayout<D, TX>::THREADS, PsLayout<D, TX>::BLO
 }
 
 template <int D, int TX>
-static int launch_ps(const PromptParams& p, unsigned grid, cudaStream_t stream) {
+static int launch_ps(const PromptParams& p, unsigned grid, bool alone, cudaStream_t stream) {
     using LY = PsLayout<D, TX>;
+    constexpr int MORE = std::max(LY::BYTES, PS_ALONE);
     static PerDeviceOnce attr;
     const int rc = per_device_once(attr, [] {
-        const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<D, TX>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::BYTES);
+        const cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<D, TX>, cudaFuncAttributeMaxDynamicSharedMemorySize, MORE);
         if (e != cudaSuccess) {
             set_error("prompt_attention: cannot set shared memory size: %s", cudaGetErrorString(e));
             return (int)RX_ECUDA;
@@ -304,7 +306,7 @@ static int launch_ps(const PromptParams& p, unsigned grid, cudaStream_t stream) 
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    launch_pdl(prompt_simt_kernel<D, TX>, grid, LY::THREADS, LY::BYTES, stream, p, PromptDiv(PS_BM), PromptDiv(p.hq));
+    launch_pdl(prompt_simt_kernel<D, TX>, grid, LY::THREADS, alone ? MORE : LY::BYTES, stream, p, PromptDiv(PS_BM), PromptDiv(p.hq));
     return RX_OK;
 }
 
@@ -319,10 +321,17 @@ int launch_prompt_simt(PromptParams p, int head_dim, cudaStream_t stream) {
     // heads x 64, TX 8 and 16: one of 7680 tokens 1653 and 1717 us, of 5120 875 and 786, of 300 40 and 23; 20 of
     // 500 187 and 198, 100 of 200 325 and 311.  With head_dim 128 its output would not fit the registers.)
     const bool wide = head_dim == 64 && items > 2 * 152 * PsLayout<64, 8>::BLOCKS && p.total >= 256ll * p.batch;
-    p.by_level = prompt_by_level(items, 152 * (wide ? PsLayout<64, 8>::BLOCKS : PsLayout<64, 16>::BLOCKS), p.batch,
+    // One block an SM, the longest first, for calls of up to a few items an SM: two on one SM would each take
+    // nearly twice as long beside SMs that are idle (or soon are).  Not for short sequences, whose items are
+    // alike.  (12 heads x 64, one block and two: 640 tokens 41 and 53 us, 1280 76 and 124, 1920 155 and 183,
+    // 2560 261 and 240; 10 of 64 9.1 and 12.0, 18 of 64 16 and 12.  16 heads x 128: 300 37 and 41, 1280 158 and
+    // 224, 1920 346 and 327.)
+    const bool alone = items <= 152 || (items <= 152 * 5 / 2 && p.total >= 256ll * p.batch);
+    p.by_level = prompt_by_level(items, 152 * (alone ? 1 : wide ? PsLayout<64, 8>::BLOCKS : PsLayout<64, 16>::BLOCKS), p.batch,
                                  2 * p.total * p.hkv * head_dim * 4);
-    if (head_dim == 128) return launch_ps<128, 16>(p, (unsigned)items, stream);
-    return wide ? launch_ps<64, 8>(p, (unsigned)items, stream) : launch_ps<64, 16>(p, (unsigned)items, stream);
+    const unsigned grid = (unsigned)items;
+    if (head_dim == 128) return launch_ps<128, 16>(p, grid, alone, stream);
+    return wide ? launch_ps<64, 8>(p, grid, alone, stream) : launch_ps<64, 16>(p, grid, alone, stream);
 }
 
 }  // namespace rx

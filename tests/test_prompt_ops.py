@@ -583,6 +583,25 @@ def test_prompt_long(dev, dt, hq, hkv, d, n):
 
 @gpu
 @pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("lens", [[2100, 1, 0, 1437, 640, 900], [700] * 9, [5120]])
+@pytest.mark.parametrize("bad", [0.0, math.inf, math.nan])
+def test_prompt_many_long_items(dev, dt, lens, bad):
+    """Calls of more items than run at once, whose sequences are long (f32 then takes larger register tiles),
+    with values that are not finite here and there, rows in front and behind, and one scale of zero."""
+    gen = torch.Generator("cuda").manual_seed(len(lens))
+    n = sum(lens)
+    q, k, v = rows_of(gen, n + 70, 16, 4, 64, dt, wide=1)
+    for x in (q, k, v):
+        x[:30] = math.nan
+        x[30 + n:] = math.nan
+    if bad:
+        for at in (0, 63, 64, 699, 701, n // 2, n - 1):
+            v[30 + at, at % 4, at % 64] = bad
+    check_prompt(q, k, v, lens, desc_of(dt, 16, 4, 64, scale=None if bad or len(lens) > 1 else 0.0), start=30)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
 def test_prompt_leaves_other_rows(dev, dt):
     """Rows before the first and behind the last sequence, NaN inside: neither read nor written."""
     gen = torch.Generator("cuda").manual_seed(1)
