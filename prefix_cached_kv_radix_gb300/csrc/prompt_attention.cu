@@ -29,7 +29,7 @@
 // While one tile's softmax runs the tensor core works on the other's products.
 //
 // What bounds it: for long prompts the tensor core (one of 16384 tokens, 32/8 heads x 128: 1.24 ms, 1770
-// TFLOP/s, 91 % of the measured cuBLAS burst rate; of 32768: 5.1 ms, 1720; 64/8 heads: 1700): a step of
+// TFLOP/s, 91 % of the measured cuBLAS burst rate; of 32768: 5.1 to 5.2 ms, 1700; 64/8 heads: 1700): a step of
 // 128 keys takes 2700 clocks, of which its products are 2048.  The issuing warp decides that: with
 // operands the compiler did not know to be warp-uniform the products took 75 clocks each to issue
 // instead of 64 (1254 TFLOP/s), and waits where its queue ran dry cost 500 clocks a step.  For short
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                     }
                     if (!ok) break;
                 }
-                if (lane == 0) PromptFinder::check(p.a, place, p.by_heads);     // while the answer is on its way
+                if (lane == 0) PromptFinder::check(p.a, place);     // while the answer is on its way
                 ok = pt_wait(bar(LY::BAR_CLC), asked & 1, abort_flag);
                 if (!ok) break;
                 ++asked;

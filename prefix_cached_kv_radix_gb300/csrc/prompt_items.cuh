@@ -68,12 +68,11 @@ struct PromptFinder {
         return s >= 0 && e >= s && e <= p.total && e - s <= PROMPT_MAX_ROWS;
     }
 
-    // Reports sequence b's boundaries on the item that is head 0 of place b: there are more places than
-    // sequences and every item is taken once, so each sequence is looked at, also where boundaries out of
-    // order keep the items from finding it.  One lane of a block calls it, where no one waits for it.
-    static __device__ __forceinline__ void check(const PromptParams& p, int i, const PromptDiv& heads) {
-        const int b = heads(i);
-        if (b < p.batch && i == b * heads.d && !sound(p, p.indptr[b], p.indptr[b + 1])) report(p.status, RX_DEV_BAD_LENGTH);
+    // Reports sequence i's boundaries on item i: there are no fewer items than sequences and every item is
+    // taken once, so each sequence is looked at, also where boundaries out of order keep its items from
+    // finding it.  One lane of a block calls it, where no one waits for it.
+    static __device__ __forceinline__ void check(const PromptParams& p, int i) {
+        if (i < p.batch && !sound(p, p.indptr[i], p.indptr[i + 1])) report(p.status, RX_DEV_BAD_LENGTH);
     }
 
     __device__ __forceinline__ int load(const PromptParams& p, int b, bool& ok) const {

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(PsLayout<D, TX>::THREADS, PsLayout<D, TX>::BLO
     PromptItem it;
     PromptFinder finder;
     if (!finder.find(p, (int)blockIdx.x, by_rows, by_heads, it)) {
-        if (threadIdx.x == 0) PromptFinder::check(p, (int)blockIdx.x, by_heads);
+        if (threadIdx.x == 0) PromptFinder::check(p, (int)blockIdx.x);
         return;
     }
     const int h = it.head, g = h / (p.hq / p.hkv);
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(PsLayout<D, TX>::THREADS, PsLayout<D, TX>::BLO
             to[0] = x[i].x, to[LDQ] = x[i].y, to[2 * LDQ] = x[i].z, to[3 * LDQ] = x[i].w;
         }
     }
-    if (threadIdx.x == 0) PromptFinder::check(p, (int)blockIdx.x, by_heads);    // under the first loads
+    if (threadIdx.x == 0) PromptFinder::check(p, (int)blockIdx.x);    // under the first loads
     float m[8], l[8];                                        // row maximum times sl; this thread's part of the sum
     uint64_t o[4][OC * 4];                                   // rows 2i and 2i + 1 of a column
 #pragma unroll

@@ -870,3 +870,62 @@ def test_prompt_streams_and_graphs(dev, dt):
     for _, o, want in graphs:
         assert torch.equal(o, want)
     assert int(st.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
+def test_branches_that_fork_and_join(dev, dt):
+    """Two streams joined by events, eager and as a graph of two branches: a call that depends on kernels of
+    both waits for both, though each call's set-up may begin before the one in front of it has ended."""
+    gen = torch.Generator("cuda").manual_seed(13)
+    hq, hkv, d, n = 8, 2, 128, 3000
+    c = rope_case(gen, dt, hq, hkv, d, [n], [0], torch.arange(n, device="cuda")[None], slots_extra=2 * n)
+    desc, rope, st = desc_of(dt, hq, hkv, d, c["num"]), api.rope_desc(64), i32([0], "cuda")
+    free = torch.tensor(sorted(set(range(c["num"])) - set(c["ns"].tolist())), dtype=torch.int32, device="cuda")
+    one, two = free[:n].contiguous(), free[n:2 * n].contiguous()
+    pools = [torch.empty(c["num"], hkv, d, dtype=dt, device="cuda") for _ in range(2)]
+    q, k = torch.empty(n, hq, d, dtype=dt, device="cuda"), torch.empty(n, hkv, d, dtype=dt, device="cuda")
+    out = torch.empty_like(q)
+    fork, zero, kvl, ti = torch.empty(1, n, dtype=torch.int32, device="cuda"), i32([0], "cuda"), i32([n], "cuda"), indptr([n], "cuda")
+    moved = one[None].contiguous()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def run():                                              # on stream a
+        api.kv_pool_write_rope(desc, rope, 1, None, c["pi"], c["ns"], c["qi"], c["pos"], c["q"], c["k"], c["v"], q, k, *pools, None, n, st)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            api.prompt_attention(desc, 1, q, k, c["v"], c["qi"], out, None, n, st)
+        api.kv_pool_copy(desc, pools, c["ns"], one, 1, st)
+        a.wait_stream(b)
+        # reads what the copy moved, overwrites (in place) what the other branch read
+        api.kv_pool_fork(desc, pools, zero, zero, kvl, ti, two, moved, fork, n, st)
+        api.kv_pool_write_rope(desc, rope, 1, None, None, None, c["qi"], c["pos"], q, k, None, q, k, None, None, None, n, st)
+
+    def wipe():
+        for t in (*pools, q, k, out):
+            t.fill_(math.nan)
+        torch.cuda.synchronize()
+
+    def take():
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        return [t.clone() for t in (q, k, out, fork)] + [p[i.long()] for p in pools for i in (c["ns"], one, two)]
+    wipe()
+    with torch.cuda.stream(a):
+        run()
+    got = take()
+    turned = [torch.empty_like(q), torch.empty_like(k)]
+    api.kv_pool_write_rope(desc, rope, 1, None, None, None, c["qi"], c["pos"], c["q"], c["k"], None, *turned, None, None, None, n, st)
+    torch.cuda.synchronize()
+    want, _, to, _ = attention(*turned, c["v"], [n], desc.scale)
+    close(got[2], want, to, "out")
+    assert torch.equal(got[4], got[5]) and torch.equal(got[4], got[6]) and torch.equal(got[4], turned[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=a):
+        run()
+    for r in range(6):
+        wipe()
+        with torch.cuda.stream(a):
+            g.replay() if r % 2 else run()
+        for x, y in zip(got, take()):
+            assert torch.equal(x, y)
