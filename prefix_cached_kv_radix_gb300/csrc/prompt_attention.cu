@@ -16,13 +16,14 @@
 // items of those that have not been launched (clusterlaunchcontrol.try_cancel), so the assignment
 // is dynamic without a counter in memory: launches on several streams and replays of captured
 // graphs share nothing.  Roles (512 threads):
-//   warp 0      takes and decodes the items, hands them on through a ring in shared memory, and
-//               loads their Q tiles as the buffers come free
+//   warp 0      decodes the items taken, hands them on through a ring in shared memory, and loads their
+//               Q tiles as the buffers come free
 //   warp 1      issues the tcgen05.mma: per K/V tile j and Q tile t
 //               O_t += P_t(j) V(j) in two halves of 64 keys as P comes in (P from TMEM), then at
 //               once S_t(j+1) = Q_t K(j+1)^T over the columns P was read from, or the next item's
 //               first scores
-//   warp 2      loads K and V tiles into rings of their own, on into the next items
+//   warp 2      loads K and V tiles into rings of their own, on into the next items, and asks for the next
+//               item when it loads an item's last but one tile
 //   warp 3      TMEM; clears what must not enter a sum (below)
 //   warps 4-7, 8-11   softmax of Q tile 0 and 1, a row per thread
 //   warps 12-15 the items' output from TMEM, while the others are on the next item
@@ -66,6 +67,7 @@ constexpr int PT_BN = 128;         // keys per K/V tile
 constexpr int PT_THREADS = 512;
 constexpr int PT_RING = 4;         // items in flight between the roles
 constexpr int PT_CONSUMERS = 15;   // MMA warp, K/V warp, clearing warp, eight softmax warps, four output warps
+constexpr int PT_LEAD = 2;         // K/V tiles of an item still to be loaded when its successor is asked for
 constexpr int PT_CUT = 3;          // K/V tiles of an item that a mask or the sequence's end can cut
 // 2 * 128 * 80 + 2 * 128 * 176 = 512 * 128
 constexpr uint32_t PT_REGS_SOFTMAX = 176, PT_REGS_OTHER = 80, PT_REGS_LAUNCH = 128;
@@ -296,6 +298,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         it.t0 = __shfl_sync(0xffffffffu, r.z, 0), it.head = __shfl_sync(0xffffffffu, r.w, 0);
     };
 
+    // Asks for a block that has not been launched.  The K/V warp does when it comes to an item's last tiles:
+    // asked for as soon as there was room for them, the first few items of each block were shared out at the
+    // launch's beginning, whoever was done first (one of 2000 tokens, 32/8 heads x 128: 27 us, and 35; of 4096: 86
+    // and 92; eight prompts of 64 tokens an SM alike).  Warp 0 does where its place has no item.
+    auto ask = [&]() {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar(LY::BAR_CLC), 16);
+            clc_try_cancel(base + LY::OFF_CLC, bar(LY::BAR_CLC));
+        }
+    };
+
     if (warp < 4) {
         regs_decrease<PT_REGS_OTHER>();
         if (warp == 0) {
@@ -305,11 +318,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
             int k = 0, use0 = 0, use1 = 0, asked = 0;
             bool ok = true;
             for (;;) {
-                // the next block's place, asked for while this one's item is handed on
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(LY::BAR_CLC), 16);
-                    clc_try_cancel(base + LY::OFF_CLC, bar(LY::BAR_CLC));
-                }
                 PromptItem w;
                 if (finder.find(p.a, place, p.by_tokens, p.by_heads, w)) {
                     PtItem it;
@@ -339,6 +347,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         }
                     }
                     if (!ok) break;
+                } else {
+                    ask();
                 }
                 if (lane == 0) PromptFinder::check(p.a, place);     // while the answer is on its way
                 ok = pt_wait(bar(LY::BAR_CLC), asked & 1, abort_flag);
@@ -558,6 +568,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
                         __syncwarp();
                     }
                     if (!ok) break;
+                    if (j == max(nkv - PT_LEAD, 0)) ask();
                 }
                 gt += nkv;
                 __syncwarp();
