@@ -230,8 +230,7 @@ __device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile 
 }
 
 // SPLIT: an item is one Q tile, and the two softmax warpgroups, S and O take its K/V tiles in turn (even
-// and odd ones) and join at the end: half as many steps, one after another, for calls whose items all
-// run at once.  (One prompt of 409 tokens, 12 heads x 64: 7.3 us, and 7.9 with one K/V tile after
+// and odd ones) and join at the end: half as many steps, one after another, for calls of few items.  (One prompt of 409 tokens, 12 heads x 64: 7.3 us, and 7.9 with one K/V tile after
 // another; of 1024 tokens: 10.2 and 11.9.)
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_constant__ PromptTcParams p) {
@@ -1016,8 +1015,11 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     const int64_t heads = (int64_t)a.hkv * p.nhb;
     // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn (1.4 us a step of
     // 128 keys); one, its K/V tiles split between two softmax warpgroups, while even those items are no
-    // more than the SMs.
-    const bool split = prompt_items(a.total, a.batch, p.tpt) * heads <= sms;
+    // more than the SMs, or two an SM if the sequences are long.  (12 heads x 64, one Q tile and two: 2000 tokens
+    // 15.2 and 22.4 us, 3000 22.6 and 31.2; 12 of 128 6.7 and 6.2; at four an SM 5000 tokens 49.7 and 48.4.
+    // 32/8 heads x 128: 700 tokens 12.4 and 14.0, 1100 16.7 and 18.2; 6 of 100 9.4 and 7.9.)
+    const int64_t one = prompt_items(a.total, a.batch, p.tpt) * heads;
+    const bool split = one <= sms || (one <= 2 * sms && a.total >= 512ll * a.batch);
     const int tokens = split ? p.tpt : 2 * p.tpt;
     const int64_t items = prompt_items(a.total, a.batch, tokens) * heads;
     RX_REQUIRE(items < (1ll << 31), "prompt_attention: too many rows");

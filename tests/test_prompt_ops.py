@@ -602,6 +602,24 @@ def test_prompt_many_long_items(dev, dt, lens, bad):
 
 @gpu
 @pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,hkv,d,lens", [(12, 12, 64, [2500]), (16, 2, 128, [1300, 1, 0, 850]), (14, 2, 64, [640, 1700, 129]),
+                                           (4, 4, 128, [5000]), (8, 8, 128, [1025, 2047])])
+@pytest.mark.parametrize("bad", [0.0, math.inf, math.nan])
+def test_prompt_one_or_two_items_an_sm(dev, dt, hq, hkv, d, lens, bad):
+    """Calls of a few items an SM, long ones and short ones among them, whose blocks take more than one."""
+    gen = torch.Generator("cuda").manual_seed(hq)
+    n = sum(lens)
+    q, k, v = rows_of(gen, n + 5, hq, hkv, d, dt)
+    for x in (q, k, v):
+        x[n:] = math.nan
+    if bad:
+        for at in (0, 127, 128, n // 3, n - 1):
+            v[at, at % hkv, at % d] = bad
+    check_prompt(q, k, v, lens, desc_of(dt, hq, hkv, d))
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
 def test_prompt_leaves_other_rows(dev, dt):
     """Rows before the first and behind the last sequence, NaN inside: neither read nor written."""
     gen = torch.Generator("cuda").manual_seed(1)
