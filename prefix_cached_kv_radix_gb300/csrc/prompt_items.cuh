@@ -42,8 +42,9 @@ struct PromptDiv {
 // sequence, 239 by tile index; 60 of 256: 81 and 78), nor where the keys and values of all sequences
 // are more than the L2 holds beside the rest (of 129 MB): each tile index reads them again (32 prompts
 // of 1024 tokens, 134 MB: 233 and 266 us; one of 16384, 67 MB: 1334 and 1239).
+constexpr int PROMPT_LEVEL_SEQS = 64;    // two a lane
 inline bool prompt_by_level(int64_t items, int resident, int32_t batch, int64_t kv_bytes) {
-    return items > resident && batch <= 64 && kv_bytes <= 80ll << 20;
+    return items > resident && batch <= PROMPT_LEVEL_SEQS && kv_bytes <= 80ll << 20;
 }
 
 // The longest sequence: the waits of the bf16 kernel, of which the longest is for one item, give up after 2 s;
@@ -60,7 +61,8 @@ struct PromptItem {
 // and a boundary that is not is clamped.
 struct PromptFinder {
     int w0 = -1;             // first boundary of the window (-1: none loaded)
-    int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last.  By level: tiles of sequence `lane`
+    int mine = 0;            // boundary w0 + lane, clamped; beyond the last one: the last.  By level: tiles of sequence `lane`,
+    int more = 0;            // and of sequence 32 + lane
     bool good = false;       // it lies in [0, total]
 
     // Whether a sequence's boundaries are in order and in [0, total], and it is not too long.
@@ -87,27 +89,25 @@ struct PromptFinder {
     __device__ __forceinline__ bool find_by_level(const PromptParams& p, int i, const PromptDiv& tile_tokens, const PromptDiv& heads,
                                                   PromptItem& it) {
         const int lane = threadIdx.x & 31;
-        const int q = heads(i), rounds = (p.batch + 31) >> 5;
-        if (w0 < 0) {                        // the first 32 sequences stay in the lanes
+        const int q = heads(i);
+        if (w0 < 0) {
             w0 = 0;
             mine = tiles(p, lane, tile_tokens);
+            more = tiles(p, 32 + lane, tile_tokens);
         }
         // q < f(lo), or lo = -1; q >= f(hi) = f_hi
         int lo = -1, hi = tile_tokens((int)p.total) + 2, f_hi = 0;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            int f = max(0, mine - mid);
-#pragma unroll 1
-            for (int m = 1; m < rounds; ++m) f += max(0, tiles(p, 32 * m + lane, tile_tokens) - mid);
-            f = (int)__reduce_add_sync(0xffffffffu, (unsigned)f);
+            const int f = (int)__reduce_add_sync(0xffffffffu, (unsigned)(max(0, mine - mid) + max(0, more - mid)));
             if (q < f) lo = mid;
             else hi = mid, f_hi = f;
         }
         if (lo < 0) return false;
         int r = q - f_hi;                    // which of the sequences that have a tile `lo`
 #pragma unroll 1
-        for (int m = 0; m < rounds; ++m) {
-            const unsigned has = __ballot_sync(0xffffffffu, (m == 0 ? mine : tiles(p, 32 * m + lane, tile_tokens)) > lo);
+        for (int m = 0; m < PROMPT_LEVEL_SEQS / 32; ++m) {
+            const unsigned has = __ballot_sync(0xffffffffu, (m == 0 ? mine : more) > lo);
             const bool me = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == r;
             const unsigned one = __ballot_sync(0xffffffffu, me);
             if (one) {
