@@ -36,12 +36,13 @@ struct PromptDiv {
 
 // Whether the items are better taken by tile index, of all sequences together and from the highest
 // down, than sequence by sequence: row tile x has about x tiles of keys, so the longest items come first
-// and the launch ends on the shortest, whatever the order of the sequences (8 ragged f32 prompts 658 ->
-// 510 us, 48 ragged bf16 prompts 125 -> 105 us).  Not where all items run at once anyway, where finding an
-// item among the sequences takes longer than a short item does (250 prompts of 64 tokens: 73 us by
-// sequence, 239 by tile index; 60 of 256: 81 and 78), nor where the keys and values of all sequences
-// are more than the L2 holds beside the rest (of 129 MB): each tile index reads them again (32 prompts
-// of 1024 tokens, 134 MB: 233 and 266 us; one of 16384, 67 MB: 1334 and 1239).
+// and the launch ends on the shortest, whatever the order of the sequences (bf16, by sequence and by tile
+// index: 48 ragged prompts 111 and 102 us, one of 2000 37 and 27, 12 heads x 64 and one of 16384 453 and
+// 394; 8 ragged f32 prompts 658 and 510).  Not where all items run at once anyway, nor with more sequences
+// than a warp's lanes hold at two each (searched in memory, 250 prompts of 64 tokens took 239 us and not 73),
+// nor where the keys and values of all sequences are more than the L2 holds beside the rest (of 129 MB):
+// each tile index reads them again (32 prompts of 1024 tokens, 134 MB: 222 and 258 us; at 67 MB both are
+// alike: one of 16384 1245 and 1275, four of 4096 338 and 330).
 constexpr int PROMPT_LEVEL_SEQS = 64;    // two a lane
 inline bool prompt_by_level(int64_t items, int resident, int32_t batch, int64_t kv_bytes) {
     return items > resident && batch <= PROMPT_LEVEL_SEQS && kv_bytes <= 80ll << 20;
