@@ -35,7 +35,7 @@
 // operands the compiler did not know to be warp-uniform the products took 75 clocks each to issue
 // instead of 64 (1254 TFLOP/s), and waits where its queue ran dry cost 500 clocks a step.  For short
 // prompts the passage from one item to the next, about 2 us of which instruction fetch is a part (32
-// prompts of 1024: 1200 TFLOP/s; the code was cut from 112 to 60 KB, which took that case from 391 to
+// prompts of 1024: 1230 TFLOP/s; the code was cut from 112 to 60 KB, which took that case from 391 to
 // 230 us), and HBM (512 prompts of 64 tokens: 118 us for 670 MB, 85 % of the measured copy rate).
 //
 // Rows that a row must not see: a masked score is replaced after the product, so nothing of a
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
     // Asks for a block that has not been launched.  The K/V warp does when it comes to an item's last tiles:
     // asked for as soon as there was room for them, the first few items of each block were shared out at the
     // launch's beginning, whoever was done first (one of 2000 tokens, 32/8 heads x 128: 27 us, and 35; of 4096: 86
-    // and 92; eight prompts of 64 tokens an SM alike).  Warp 0 does where its place has no item.
+    // and 92; 250 prompts of 64 tokens alike).  Warp 0 does where its place has no item.
     auto ask = [&]() {
         if (lane == 0) {
             mbar_arrive_expect_tx(bar(LY::BAR_CLC), 16);
