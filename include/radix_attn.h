@@ -318,7 +318,8 @@ typedef struct {
  *    d_k_out, optional: the turned keys as rows too (needed where no pool is written), likewise in
  *    place or apart.  Otherwise no output may overlap an input.
  *  - Rows before qo_indptr[0] and from qo_indptr[batch] on (a padded batch) are left as they were;
- *    qo_indptr[batch] > total_new is RX_DEV_BAD_LENGTH, and the rows up to total_new are done.
+ *    qo_indptr[batch] > total_new is RX_DEV_BAD_LENGTH, and the rows up to total_new are done;
+ *    qo_indptr[0] < 0 or qo_indptr[batch] < qo_indptr[0] is RX_DEV_BAD_LENGTH too.
  *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, that row's pool entries are not written.
  *  - Two rows with the same slot: that slot holds parts of either.
  * Angles are exact but for the rounding of the frequency to double (2^-52 of the angle) and of the

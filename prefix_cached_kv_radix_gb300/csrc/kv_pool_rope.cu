@@ -126,12 +126,13 @@ __global__ void __launch_bounds__(ROPE_THREADS) kv_pool_rope_kernel(const __grid
     }
     const int64_t block = blockIdx.x - table_blocks;
     // rows of the batch only: what lies before its first and behind its last request is left alone
-    const int64_t lo = max(p.qo_indptr[0], (int64_t)0), end = p.qo_indptr[p.batch];
-    const int64_t hi = min(end, p.total);
-    if (block == 0 && threadIdx.x == 0 && (end > p.total || p.qo_indptr[0] < 0)) report(p.status, RX_DEV_BAD_LENGTH);
+    const int64_t first = p.qo_indptr[0], end = p.qo_indptr[p.batch];
+    const int64_t lo = max(first, (int64_t)0), hi = min(end, p.total);
+    if (block == 0 && threadIdx.x == 0 && (end > p.total || first < 0 || end < first)) report(p.status, RX_DEV_BAD_LENGTH);
     const int64_t t0 = block * p.tokens;
-    const int nt = (int)min((int64_t)p.tokens, hi - t0);
-    if (nt <= 0 || t0 + nt <= lo) return;
+    if (t0 >= hi) return;                                         // in 64 bits: `end` may be any number
+    const int nt = (int)min((int64_t)p.tokens, hi - t0);          // hi - t0 is in [1, total]
+    if (t0 + nt <= lo) return;
     const int qu = p.q ? p.hq * NU : 0;                           // units of a token's queries,
     const int ku = p.hkv * NU;                                    // of its keys, and of its values
     const int per = qu + ku + (p.new_slots ? ku : 0);

@@ -23,7 +23,9 @@ __device__ __forceinline__ void kpw_table_tile(int b, int64_t tile, const int32_
     const int64_t p0 = prefix_indptr[b], P = prefix_indptr[b + 1] - p0;
     const int64_t q0 = qo_indptr[b], n = qo_indptr[b + 1] - q0;
     int32_t* row = r2t + (int64_t)b * stride;
-    const bool bad_len = P < 0 || n < 0 || P + n > stride || q0 < t_begin || q0 + n > t_end || (P > 0 && !prefix_slots);
+    // without sums: boundaries may be any numbers, and one that wrapped would pass
+    const bool bad_len = P < 0 || n < 0 || P > stride || n > stride - P || q0 < t_begin || q0 > t_end || n > t_end - q0 ||
+                         (P > 0 && !prefix_slots);
     if (bad_len && j0 == 0 && threadIdx.x == 0) report(status, RX_DEV_BAD_LENGTH);
     int32_t s[PER];
 #pragma unroll

@@ -424,6 +424,27 @@ def test_rope_bad_slots_and_lengths(dev):
 
 
 @gpu
+@pytest.mark.parametrize("table", [True, False])
+@pytest.mark.parametrize("ends", [(0, -1), (0, -2 ** 32 + 1000), (5, -2 ** 32 + 2 ** 20), (0, -2 ** 62), (20, 3), (-2 ** 40, -2 ** 32 + 30),
+                                  (2 ** 63 - 2, -2 ** 63 + 1)])
+def test_rope_boundaries_far_below_zero(dev, table, ends):
+    """Boundaries that 32 bits would take for others, or whose sums wrap: reported, and no row, slot or table
+    entry of the bad request is touched."""
+    gen = torch.Generator("cuda").manual_seed(14)
+    c = rope_case(gen, BF, 2, 2, 64, [40], [0], torch.arange(40, device="cuda")[None])
+    kp, vp = (torch.full((c["num"], 2, 64), 7.5, dtype=BF, device="cuda") for _ in range(2))
+    qo, ko = (torch.full((40, 2, 64), 7.5, dtype=BF, device="cuda") for _ in range(2))
+    r2t, st = torch.full((1, 48), 99, dtype=torch.int32, device="cuda"), i32([0], "cuda")
+    api.kv_pool_write_rope(desc_of(BF, 2, 2, 64, c["num"]), api.rope_desc(32), 1, c["ps"], c["pi"], c["ns"],
+                           torch.tensor(ends, dtype=torch.int64, device="cuda"), c["pos"], c["q"], c["k"], c["v"], qo, ko, kp, vp,
+                           r2t if table else None, 40, st)
+    assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+    for x in (kp, vp, qo, ko):
+        assert (x == 7.5).all()
+    assert (r2t == (-1 if table else 99)).all()
+
+
+@gpu
 def test_rope_without_a_prefix_list(dev):
     """No list of matched slots: fine for requests without any, a bad length for the others."""
     gen = torch.Generator("cuda").manual_seed(12)
