@@ -15,7 +15,7 @@ strings library calls together and moves the step's small index arrays to the de
 """
 from __future__ import annotations
 
-
+import contextlib
 import ctypes
 
 import numpy as np
@@ -517,11 +517,32 @@ class PrefixCacheEngine:
                              stream or self._stream.cuda_stream)
 
     # ------------------------------------------------------------------ moving cached tokens
+    def _torch_stream(self, stream):
+        """The torch stream of a `stream` argument: a torch stream, an address, or None (the engine's own)."""
+        if not stream:
+            return self._stream
+        return torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+
+    @contextlib.contextmanager
+    def _in_order(self, st):
+        """Work on `st`, the current stream inside, that follows what is on the engine's stream and that what
+        comes there follows: rows being written are read whole, and slots that were freed and handed out
+        again are not overwritten while an earlier kernel reads them."""
+        if st != self._stream:
+            st.wait_stream(self._stream)
+        try:
+            with torch.cuda.stream(st):
+                yield
+        finally:
+            if st != self._stream:
+                self._stream.wait_stream(st)
+
     def fork(self, r2t, parents, keep_lens, kv_lens, tail_slots=None, stream=None):
         """Slot tables of sequences that continue rows of `r2t` (int32 [rows, stride]): row f keeps the
         first keep_lens[f] slots of row parents[f], and its later tokens up to kv_lens[f] are copied, in
         every layer, to slots of its own (tail_slots, or newly allocated ones, which the caller then
-        owns).  Returns (the new table, the tail slots)."""
+        owns).  Runs on `stream` after what is on the engine's own stream and before what comes there.
+        Returns (the new table, the tail slots)."""
         keep, kv = _contig(keep_lens, np.int32), _contig(kv_lens, np.int32)
         tails = kv.astype(np.int64) - keep
         if len(keep) != len(kv) or len(parents) != len(kv) or (tails < 0).any():
@@ -530,13 +551,15 @@ class PrefixCacheEngine:
         slots = self.tree.alloc_slots(total) if tail_slots is None else _contig(tail_slots, np.int32)
         if len(slots) != total:
             raise ValueError(f"fork: {total} tail slots are needed, {len(slots)} given")
-        st = self._stream if stream is None else stream
+        st = self._torch_stream(stream)
         try:
-            with torch.cuda.stream(st):
+            with torch.cuda.stream(self._stream):    # the table is the engine's stream's, as its other buffers are
                 out = torch.empty(len(kv), r2t.shape[1], dtype=torch.int32, device=self.device)
+            with self._in_order(st):
                 api.kv_pool_fork(self.desc, self._pools(), self._i32(parents), self._i32(keep), self._i32(kv),
                                  self._i64(np.concatenate([[0], np.cumsum(tails)])), self._i32(slots if total else [0]), r2t, out,
                                  total, self.status, st)
+                r2t.record_stream(st)    # the caller may let go of its table
         except Exception:                # refused: the slots allocated here go back
             if tail_slots is None:
                 self.tree.free_slots(slots)

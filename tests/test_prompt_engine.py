@@ -211,6 +211,46 @@ def test_resize_on_another_stream_is_in_order():
     assert eng.device_status() == 0
 
 
+@pytest.mark.parametrize("own", [False, True])
+def test_fork_on_another_stream_is_in_order(own):
+    """Rows and table that the engine's stream is still writing are forked whole, and what comes on the engine's
+    stream next (the table read, the parents' rows overwritten, the given-back slots written again) comes after
+    the fork; `own`: on the engine's stream itself.  The stream is given as such and as an address."""
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    n, keep = 2000, 16
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        eng = PrefixCacheEngine("bf16", 8, 8, 128, 3 * n, 3, num_layers=2)
+        a = torch.randn(8192, 8192, device="cuda")
+        rows = torch.randn(2, 2, n, 8, 128, device="cuda").bfloat16()
+    other = s if own else torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (other, other.cuda_stream):
+        at = eng.tree.alloc_slots(n)
+        idx = torch.tensor(at, device="cuda").long()
+        with torch.cuda.stream(s):
+            table = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+            rows.neg_()
+            for _ in range(6):
+                a @ a                                      # a busy stream, then the parent's rows and table on it
+            eng.k_pools[:, idx], eng.v_pools[:, idx] = rows[0], rows[1]
+            table[0] = idx.int()
+        got, tail = eng.fork(table, [0], [keep], [n], stream=handle)
+        with torch.cuda.stream(s):
+            del table
+            junk = torch.full((1, n), -5, dtype=torch.int32, device="cuda")
+            eng.k_pools[:, idx[keep:]], eng.v_pools[:, idx[keep:]] = math.nan, math.nan
+            seen = got.clone()
+            copies = torch.stack([eng.k_pools[:, seen[0].long()], eng.v_pools[:, seen[0].long()]])
+            eng.k_pools[:, torch.tensor(tail, device="cuda").long()] = math.nan
+            eng.tree.free_slots(tail)
+            eng.tree.free_slots(at)
+        torch.cuda.synchronize()
+        assert seen[0].tolist() == at[:keep].tolist() + tail.tolist()
+        assert torch.equal(copies, rows) and (junk == -5).all()
+    assert eng.device_status() == 0
+
+
 def test_refused_fork_gives_its_slots_back():
     from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
     eng = PrefixCacheEngine("f32", 2, 2, 64, 64, 3)
