@@ -570,28 +570,41 @@ class PrefixCacheEngine:
         """Shrink or grow the pools of every layer to num_slots slots with everything cached kept:
         cached tokens past the new end move to free slots below it (api.radix_resize, kv_pool_copy on
         the stream, after what is on the engine's own and before what comes there).  Memory past the end
-        stays allocated for growing back; growing past what is allocated allocates anew.  Returns the
-        number of tokens moved."""
-        st = self._stream if stream is None else stream
+        stays allocated for growing back; growing past what is allocated allocates anew.  Where it fails, it
+        has changed nothing (should the device fail the copy itself, the pools have the new size and
+        all that is not pinned is evicted).  Returns the number of tokens moved."""
+        st, pools = self._torch_stream(stream), self._pools()
+        movable = min(self.tree.stats()["cached_tokens"], max(self.num_slots - num_slots, 0))
         stores = {}
-        if num_slots > self._k_store.shape[1]:          # first, as it may fail; of the engine's stream, as the old ones
-            with torch.cuda.stream(self._stream):
+        # What may fail comes before the tree names the new slots: the memory, the copy's checks, and its
+        # launch, as one of slot 0 to itself, which changes nothing.
+        if num_slots > self._k_store.shape[1]:
+            with torch.cuda.stream(self._stream):       # of the engine's stream, as the old ones
                 for name in ("_k_store", "_v_store"):
                     stores[name] = torch.empty(self.num_layers, num_slots, self.hkv, self.d, dtype=self.tdtype, device=self.device)
-        src, dst = self.tree.resize(num_slots)
-        st.wait_stream(self._stream)
-        with torch.cuda.stream(st):
-            if len(src):
-                api.kv_pool_copy(self.desc, self._pools(), self._i32(src), self._i32(dst), 1, self.status, st)
+        with self._in_order(st):
             for name, new in stores.items():
                 old = getattr(self, name)
                 if self.poison:
                     new.fill_(float("nan"))
                 new[:, :old.shape[1]].copy_(old)
-        self._stream.wait_stream(st)
-        for name, new in stores.items():
-            setattr(self, name, new)
-        self._use_slots(num_slots)
-        self.desc.num_slots = num_slots
-        self._io_static = None           # the one-call path's pool addresses are set anew
-        return len(src)
+            if movable:
+                ids = torch.zeros(2, movable, dtype=torch.int32, device=self.device)
+                api.kv_pool_copy(self.desc, pools, ids[0, :1], ids[1, :1], 1, self.status, st)
+            src, dst = self.tree.resize(num_slots)
+            n = len(src)
+            try:
+                if n:
+                    for row, slots in zip(ids, (src, dst)):
+                        row[:n].copy_(torch.from_numpy(slots))
+                    api.kv_pool_copy(self.desc, pools, ids[0, :n], ids[1, :n], 1, self.status, st)
+            except Exception:            # the rows are not where the tree says: what is not pinned, all that moved, goes
+                self.tree.evict_count(self.tree.stats()["cached_tokens"])
+                raise
+            finally:
+                for name, new in stores.items():
+                    setattr(self, name, new)
+                self._use_slots(num_slots)
+                self.desc.num_slots = num_slots
+                self._io_static = None   # the one-call path's pool addresses are set anew
+        return n

@@ -251,6 +251,61 @@ def test_fork_on_another_stream_is_in_order(own):
     assert eng.device_status() == 0
 
 
+@pytest.mark.parametrize("failing", ["memory", "first copy", "second copy", "growing", "slots held"])
+def test_failed_resize_is_consistent(failing, monkeypatch):
+    """A resize that fails leaves tree, pools and descriptor of one size, and every match names rows that are
+    there: nothing has changed, or, where the copy of the moved rows itself fails, they are no longer cached."""
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    eng = PrefixCacheEngine("bf16", 2, 2, 64, 256, 3, num_layers=2)
+    toks, n = np.arange(90, dtype=np.int32), 90
+    kv = [[torch.randn(n, 2, 64, device="cuda").bfloat16() for _ in range(2)] for _ in range(2)]
+    eng.populate(toks, *kv)
+    before, stats = eng.tree.match_prefix(toks)[0].tolist(), eng.tree.stats()
+    assert max(before) >= 120
+    calls, copy, held = [], api.kv_pool_copy, None
+
+    def fails(*a):
+        calls.append(a)
+        if len(calls) == (2 if failing == "second copy" else 1):
+            raise api.RxError("kv_pool_copy", api.RX_ECUDA, "planted")
+        return copy(*a)
+
+    def none_left(*a, **kw):
+        raise torch.OutOfMemoryError("planted")
+    with monkeypatch.context() as m:
+        if failing == "slots held":
+            held = eng.tree.alloc_slots(eng.tree.stats()["free_slots"])
+            stats = eng.tree.stats()
+        elif failing in ("memory", "growing"):
+            for f in ("empty", "zeros", "from_numpy"):
+                m.setattr(torch, f, none_left)
+        else:
+            m.setattr(api, "kv_pool_copy", fails)
+        with pytest.raises((api.RxError, torch.OutOfMemoryError)):
+            eng.resize(300 if failing == "growing" else 120)
+    if held is not None:
+        eng.tree.free_slots(held)
+        stats = eng.tree.stats()
+    size = 120 if failing == "second copy" else 256
+    assert eng.num_slots == eng.desc.num_slots == eng.k_pools.shape[1] == eng.v_pools.shape[1] == eng.tree.stats()["num_slots"] == size
+    eng.tree.check()
+    slots, m, _ = eng.tree.match_prefix(toks)
+    if failing == "second copy":
+        assert m == 0 and eng.tree.stats()["free_slots"] == 120
+        eng.populate(toks, *kv)                            # and it serves on
+        slots = eng.tree.match_prefix(toks)[0]
+    else:
+        assert slots.tolist() == before
+        for key in ("cached_tokens", "free_slots"):
+            assert eng.tree.stats()[key] == stats[key]
+        assert eng.resize(120) > 0
+        slots = eng.tree.match_prefix(toks)[0]
+    at = torch.tensor(slots, device="cuda").long()
+    for i in range(2):
+        assert torch.equal(eng.k_pools[i][at], kv[0][i]) and torch.equal(eng.v_pools[i][at], kv[1][i])
+    assert eng.device_status() == 0
+
+
 def test_refused_fork_gives_its_slots_back():
     from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
     eng = PrefixCacheEngine("f32", 2, 2, 64, 64, 3)
