@@ -358,7 +358,8 @@ int kv_pool_copy(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, 
  * pools as for kv_pool_copy; n_pools may be 0 (tables only).  total_tail (host) >=
  * d_tail_indptr[n_rows].  Tail slots are named once each and hold no row that is read.
  *  - A parent or length that does not fit the tables or the tail list: RX_DEV_BAD_LENGTH, that row
- *    becomes -1 and its rows are not copied.
+ *    becomes -1 and its rows are not copied.  The others are made, also where offsets in
+ *    d_tail_indptr decrease.
  *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, -1 in the table, that row is not copied. */
 int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, int32_t n_rows,
                  const int32_t* d_parents, const int32_t* d_keep_lens, const int32_t* d_kv_lens,

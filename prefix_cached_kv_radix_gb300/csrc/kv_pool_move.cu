@@ -101,6 +101,23 @@ __device__ __forceinline__ bool fork_row_ok(const ForkParams& p, int f) {
            a >= 0 && b <= p.total_tail && b - a == len - keep;
 }
 
+// Whether no tail offset is below the one before it, by a warp.
+__device__ __noinline__ int offsets_ordered(const ForkParams& p, int lane) {
+    bool down = false;
+    for (int f = lane; f < p.rows; f += 32) down |= p.tail_indptr[f + 1] < p.tail_indptr[f];
+    return !__any_sync(0xffffffffu, down);
+}
+
+// The first row that can be made and that tail token i is of, by a warp; -1: none.
+__device__ __noinline__ int row_of_token(const ForkParams& p, int64_t i, int lane) {
+    for (int f0 = 0; f0 < p.rows; f0 += 32) {
+        const int f = f0 + lane;
+        const unsigned m = __ballot_sync(0xffffffffu, f < p.rows && p.tail_indptr[f] <= i && i < p.tail_indptr[f + 1] && fork_row_ok(p, f));
+        if (m) return f0 + __ffs(m) - 1;
+    }
+    return -1;
+}
+
 // Blocks [0, rows * tiles): the output table, one tile of FORK_TILE entries of a row each.  The
 // others: one (tail token, pool, segment) per warp and step.
 __global__ void __launch_bounds__(MOVE_THREADS) kv_pool_fork_kernel(const __grid_constant__ ForkParams p,
@@ -136,6 +153,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) kv_pool_fork_kernel(const __grid
     const int lane = threadIdx.x & 31;
     const int64_t step = (gridDim.x - table_blocks) * MOVE_WARPS;
     const int64_t items = p.total_tail * p.n_pools * p.segs;
+    int ordered = -1;                                      // whether the tail offsets nowhere decrease (-1: not looked at)
     for (int64_t it = (blockIdx.x - table_blocks) * MOVE_WARPS + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t q = it / p.segs, seg = it - q * p.segs;
         const int64_t i = q / p.n_pools;                   // tail token, of the last row that starts at or before it
@@ -149,8 +167,13 @@ __global__ void __launch_bounds__(MOVE_THREADS) kv_pool_fork_kernel(const __grid
             lo += last * w;
             hi = min(hi, lo + w);
         }
-        const int f = lo;
-        if (i < p.tail_indptr[f] || i >= p.tail_indptr[f + 1] || !fork_row_ok(p, f)) continue;   // no row's, or a bad row (reported above)
+        int f = lo;
+        if (i < p.tail_indptr[f] || i >= p.tail_indptr[f + 1] || !fork_row_ok(p, f)) {
+            // No row's token, or a bad row's (reported above), or the search was led astray by offsets that
+            // decrease at some bad row: then each row is looked at, so that a good one gets its copies.
+            if (ordered < 0) ordered = offsets_ordered(p, lane);
+            if (ordered || (f = row_of_token(p, i, lane)) < 0) continue;
+        }
         const int64_t j = p.keep[f] + (i - p.tail_indptr[f]);
         const int32_t s = p.r2t_in[(int64_t)p.parents[f] * p.in_stride + j], d = p.tail_slots[i];
         if (s < 0 || s >= p.num_slots || d < 0 || d >= p.num_slots) {

@@ -316,6 +316,48 @@ def test_fork_bad_rows(dev):
     assert int(st.item()) == api.RX_DEV_BAD_SLOT and torch.equal(x, want)
 
 
+@gpu
+@pytest.mark.parametrize("rows", [5, 70, 2000])
+def test_fork_offsets_that_decrease(dev, rows):
+    """Offsets that fall back at bad rows: every good row has its table and its copies all the same, and tail
+    tokens of bad rows and behind the last are left alone."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    rng = np.random.default_rng(rows)
+    tail_of = [int(x) for x in rng.integers(0, 4, rows)]
+    bad = sorted({3, *(int(x) for x in rng.integers(1, rows - 1, rows // 20))})
+    ti, at = [0], 0
+    for f in range(rows):                                  # a bad row's end is anywhere, the next good one goes on behind it
+        ti.append(at + tail_of[f])
+        at = ti[-1]
+    for f in bad:
+        ti[f + 1] = int(rng.integers(-3, ti[f] + 1)) if f != 3 else 0
+    # the row after a bad one starts at the offset that is out of place: it is bad too unless that happens to fit
+    keep = [int(x) for x in rng.integers(0, 5, rows)]
+    lens = [k + t for k, t in zip(keep, tail_of)]
+    par = [f % 2 for f in range(rows)]
+    total, num = at + 7, at + 7 + 40
+    good = [ti[f] >= 0 and ti[f + 1] <= total and ti[f + 1] - ti[f] == tail_of[f] for f in range(rows)]
+    owner = {}
+    for f in range(rows):
+        for i in range(ti[f], ti[f + 1]) if good[f] else ():
+            assert i not in owner                          # the case names each slot once
+            owner[i] = f
+    assert not all(good) and any(a > b for a, b in zip(ti, ti[1:]))
+    x, lst = some_pools(gen, 3, num, 2, 64, BF)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").reshape(2, 10)
+    tails = torch.arange(40, 40 + total, dtype=torch.int32, device="cuda")
+    out, st, want = torch.full((rows, 11), 99, dtype=torch.int32, device="cuda"), i32([0], "cuda"), x.clone()
+    api.kv_pool_fork(desc_of(BF, 2, 2, 64, num), lst, i32(par, "cuda"), i32(keep, "cuda"), i32(lens, "cuda"), torch.tensor(ti, device="cuda"), tails,
+                     table, out, total, st)
+    assert int(st.item()) == api.RX_DEV_BAD_LENGTH
+    for f, row in enumerate(out.tolist()):
+        mine = [10 * par[f] + j for j in range(keep[f])] + [40 + i for i in range(ti[f], ti[f + 1])] if good[f] else []
+        assert row == mine + [-1] * (11 - len(mine)), f
+    for i, f in owner.items():
+        want[:, 40 + i] = x[:, 10 * par[f] + keep[f] + i - ti[f]]
+    assert torch.equal(x, want)
+
+
 # ============================================================================ kv_pool_write_rope
 def rope_case(gen, dt, hq, hkv, d, new, pre, axes_pos, slots_extra=9, wide=1):
     T, P = sum(new), sum(pre)
