@@ -255,9 +255,12 @@ static int rope_table(const rx_rope_desc* r, int head_dim, RopeParams& p) {
         if (r->cyclic) a = (a + 1) % r->n_axes;
         const double w = r->inv_freq ? r->inv_freq[i] : std::pow(r->base, -2.0 * i / r->rot_dim);
         RX_REQUIRE(std::isfinite(w), "kv_pool_write_rope: frequency %d is not finite", i);
-        double f = w / 6.283185307179586476925287;        // turns per position; whole turns do not matter
+        // Turns per position; whole turns do not matter.  Of the magnitude, the sign by the integers' wrap:
+        // 1 - f would round a small f away.
+        double f = std::fabs(w) / 6.283185307179586476925287;
         f -= std::floor(f);
-        p.turns[i] = f < 1.0 ? (uint64_t)std::ldexp(f, 64) : 0;
+        const uint64_t turn = (uint64_t)std::ldexp(f, 64);
+        p.turns[i] = w < 0 ? 0 - turn : turn;
     }
     return RX_OK;
 }

@@ -444,6 +444,29 @@ def test_rope_in_place_alone_and_padded(dev, dt, T):
 
 
 @gpu
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("scale", [2.0 ** -54, 2.0 ** -40, 1e-6, 0.3, 50.0])
+def test_rope_negative_frequencies(dev, dt, scale):
+    """Each frequency and its negative at positions next to both ends of 32 bits: the angle's stated error,
+    2^-52 of it and 2^-25 turn, in either sign.  Rows of ones and zeros show cosine and sine alone: to the
+    angle's error come the sine's or cosine's own (2 EPS32 of a value up to 1, and the rounding to the type)."""
+    freq = np.array([-0.99, 0.99, -0.5, 0.5, -1.51, 1.51, -1.0, 1.0]) * 2 * math.pi * scale
+    pos = torch.tensor([[2 ** 31 - 1, 2 ** 31 - 2, -2 ** 31, -2 ** 31 + 1, 1 << 30, 12345, -1, 0]], dtype=torch.int32, device="cuda")
+    n = pos.shape[1]
+    k = torch.zeros(n, 1, 64, dtype=dt, device="cuda")
+    k[:, :, :8] = 1
+    out, st = torch.empty_like(k), i32([0], "cuda")
+    api.kv_pool_write_rope(desc_of(dt, 1, 1, 64), api.rope_desc(8, inv_freq=freq), 1, None, None, None, torch.tensor([0, n], device="cuda"),
+                           pos, None, k, None, None, out, None, None, None, n, st)
+    ang = pos[0].double()[:, None] * torch.tensor(freq, device="cuda")
+    half = 2.0 ** -8 if dt == BF else 2.0 ** -24
+    tol = 2 * math.pi * 2.0 ** -25 + ang.abs() * 2.0 ** -50        # 2^-52 here, and the product's and the frequency's there
+    for got, want in ((out[:, 0, :8].double(), ang.cos()), (out[:, 0, 8:16].double(), ang.sin())):
+        assert ((got - want).abs() <= tol + want.abs() * (half + 2 * 2.0 ** -24) + 1e-40).all()
+    assert int(st.item()) == 0
+
+
+@gpu
 def test_rope_bad_slots_and_lengths(dev):
     gen = torch.Generator("cuda").manual_seed(8)
     c = rope_case(gen, BF, 2, 2, 64, [40], [0], torch.arange(40, device="cuda")[None])
