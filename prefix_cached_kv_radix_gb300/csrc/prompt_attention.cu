@@ -655,7 +655,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + t * PT_BN;   // scores, then P over them
         const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;   // rescaled here, read out by the output warps
-        const float sl = p.scale_log2;
+        // A scale of zero as the least number above it: masked scores are -inf, and -inf times it has to stay
+        // so.  Scores are below 2^128: it moves none by more than 2^-21.
+        const float sl = fmaxf(p.scale_log2, 0x1p-149f);
         const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
         int sc = 0, oc = 0;                   // score steps, and items (SPLIT: joins), of this Q tile so far
         bool ok = true;
@@ -1010,8 +1012,7 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     p.hb = std::min(p.group, 128);
     p.nhb = (p.group + p.hb - 1) / p.hb;
     p.tpt = 128 / p.hb;
-    // a scale of zero as the least normal number: masked scores are -inf, and -inf times it has to stay so
-    p.scale_log2 = std::max(a.scale * PT_LOG2E, 0x1p-126f);
+    p.scale_log2 = a.scale * PT_LOG2E;
     const int64_t heads = (int64_t)a.hkv * p.nhb;
     // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn (1.4 us a step of
     // 128 keys); one, its K/V tiles split between two softmax warpgroups, while even those items are no

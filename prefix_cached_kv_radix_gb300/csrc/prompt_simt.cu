@@ -97,8 +97,9 @@ __global__ void __launch_bounds__(PsLayout<D, TX>::THREADS, PsLayout<D, TX>::BLO
     const int keys = row0 + rows;                            // keys the block needs
     const int nkv = (keys + PS_BN - 1) / PS_BN;
     const int ty = threadIdx.x / TX, tx = threadIdx.x % TX;  // rows ty*8.., keys tx + TX c, columns (tx + TX c)*4
-    // a scale of zero as the least normal number: masked scores are -inf, and -inf times it has to stay so
-    const float sl = fmaxf(p.scale * PS_LOG2E, 0x1p-126f);
+    // A scale of zero as the least number above it: masked scores are -inf, and -inf times it has to stay so.
+    // Scores are below 2^128: it moves none by more than 2^-21.
+    const float sl = fmaxf(p.scale * PS_LOG2E, 0x1p-149f);
     auto load_k = [&](int j) {
         ps_load<D, LD, THREADS>(sb + (LY::OFF_K + j % LY::NK * LY::K_SIZE) * 4, k + (int64_t)(j * PS_BN) * p.k_stride, p.k_stride,
                                 PS_BN, keys - j * PS_BN);

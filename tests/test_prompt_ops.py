@@ -764,6 +764,18 @@ def test_prompt_growing_and_extreme_scores(dev, dt):
 
 @gpu
 @pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("hq,hkv,d,lens", [(2, 2, 64, [300]), (4, 1, 128, [1, 70, 0, 2, 129]), (16, 4, 64, [700] * 9)])
+@pytest.mark.parametrize("scale", [0.0, 1e-39, 2.0 ** -126])
+def test_prompt_scale_of_nearly_nothing(dev, dt, hq, hkv, d, lens, scale):
+    """Products of up to 1e37 by a scale of zero are zero: each row is the mean of the values up to it; and
+    scales near and below the least normal number."""
+    gen = torch.Generator("cuda").manual_seed(d)
+    q, k, v = rows_of(gen, sum(lens), hq, hkv, d, F)
+    check_prompt((q * 1e18).to(dt), (k * 1e18).to(dt), v.to(dt), lens, desc_of(dt, hq, hkv, d, scale=scale))
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
 def test_prompt_far_rows(dev, dt):
     """Element offsets past 2^32: 5000 rows, a million elements apart."""
     n, gap = 5000, 1 << 20
