@@ -21,7 +21,7 @@
 #include "radix_attn.h"
 #include "rx_common.h"
 #include "rx_device.cuh"
-#include "rx_kernels.h"
+#include "rx_launch.h"
 
 namespace rx {
 

@@ -60,6 +60,7 @@
 #include "rx_common.h"
 #include "rx_device.cuh"
 #include "rx_kernels.h"
+#include "rx_launch.h"
 
 namespace rx {
 
@@ -205,6 +206,19 @@ __device__ __forceinline__ void pt_commit(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------- waits
+// Whether an mbarrier phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // A whole warp's bounded wait (2 s) on an mbarrier phase; on time-out it sets *abort, which ends
 // every role's waits and is reported once, at the end.  As short as can be: there are some thirty
 // waits in the kernel, and an item of a short sequence runs every role's code once, so that

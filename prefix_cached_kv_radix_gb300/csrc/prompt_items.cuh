@@ -1,14 +1,32 @@
-// The work items of prompt_attention: row tiles of the packed sequences, found from the sequence
-// boundaries on the device.
+// The arguments of prompt_attention's kernels, and their work items: row tiles of the packed
+// sequences, found from the sequence boundaries on the device.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "radix_attn.h"
 #include "rx_device.cuh"
-#include "rx_kernels.h"
 
 namespace rx {
+
+// Causal attention over packed prompts (prompt_attention): sequence b's rows are
+// indptr[b] .. indptr[b+1]-1 of q, k, v and out, strides in elements between rows.
+struct PromptParams {
+    int32_t batch, hq, hkv;
+    int64_t total;                // rows of the buffers
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int64_t* indptr;
+    float* lse;                   // natural log, [total, hq], optional
+    float scale;
+    int32_t by_level;             // order of the items
+    int32_t* status;
+};
+int launch_prompt_simt(PromptParams p, int head_dim, cudaStream_t stream);
 
 // A sequence [s, e) gets the tile places from floor(s / R) + b to floor(e / R) + b, b its number
 // and R the tokens of a tile: enough for ceil((e - s) / R) tiles (at most one place is left over),

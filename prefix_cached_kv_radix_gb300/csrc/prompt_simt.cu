@@ -34,6 +34,7 @@
 #include "rx_common.h"
 #include "rx_device.cuh"
 #include "rx_kernels.h"
+#include "rx_launch.h"
 
 namespace rx {
 

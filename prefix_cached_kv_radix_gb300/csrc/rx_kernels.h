@@ -5,7 +5,6 @@
 #include <stdint.h>
 
 #include <mutex>
-#include <utility>
 
 #include "radix_attn.h"
 
@@ -32,25 +31,6 @@ int per_device_once(PerDeviceOnce& o, F&& f) {
     const int rc = f();
     if (rc == RX_OK) o.done |= 1ull << dev;
     return rc;
-}
-
-// Launches with programmatic serialization: the grid may be set up while the last blocks of the kernel
-// before it in the stream run, once all of those have started.  Every thread of such a kernel calls
-// pdl_wait before it touches global memory or leaves, so that the kernel has finished only when all
-// before it have.
-template <class... P, class... A>
-cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // Generic CUDA-core causal attention (one warp per row and head).
@@ -122,23 +102,6 @@ struct SmallExtendArgs {
 };
 int launch_extend_small(const SmallExtendArgs& a, cudaStream_t stream);
 
-// Causal attention over packed prompts (prompt_attention): sequence b's rows are
-// indptr[b] .. indptr[b+1]-1 of q, k, v and out, strides in elements between rows.
-struct PromptParams {
-    int32_t batch, hq, hkv;
-    int64_t total;                // rows of the buffers
-    const void* q;
-    const void* k;
-    const void* v;
-    void* out;
-    int64_t q_stride, k_stride, v_stride, out_stride;
-    const int64_t* indptr;
-    float* lse;                   // natural log, [total, hq], optional
-    float scale;
-    int32_t by_level;             // order of the items
-    int32_t* status;
-};
-int launch_prompt_simt(PromptParams p, int head_dim, cudaStream_t stream);
 
 // kv_pool_write for the requests of one call whose new tokens are t_begin .. t_end-1 (index
 // arrays absolute: a slice of a step's requests passes its offset pointers).  With stage_bytes
