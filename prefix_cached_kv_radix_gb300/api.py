@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import numpy as np
 
@@ -469,7 +470,8 @@ def rx_step_run(args) -> int:
 
 
 def _load_ext(name: str):
-    """A CPython extension built next to the library, or False where it was not built."""
+    """A CPython extension built next to the library, or False where it was not built or does not load
+    (built against another Python or torch)."""
     from .build import pystep_path
     path = pystep_path(name)
     if not os.path.exists(path):
@@ -478,8 +480,12 @@ def _load_ext(name: str):
     import importlib.util
     loader = importlib.machinery.ExtensionFileLoader(name, path)
     spec = importlib.util.spec_from_file_location(name, path, loader=loader)
-    m = importlib.util.module_from_spec(spec)
-    loader.exec_module(m)
+    try:
+        m = importlib.util.module_from_spec(spec)
+        loader.exec_module(m)
+    except ImportError as e:
+        warnings.warn(f"{name} does not load; the binding's Python code makes its calls.  {e}")
+        return False
     return m
 
 
@@ -654,12 +660,16 @@ _ops_ext = None
 
 def ops_ext():
     """The _rxops extension (the checks and marshalling of the operators below in C++), bound to the
-    loaded library; None when it was not built (the Python code below then
-    makes the same checks and the same calls)."""
+    loaded library; None when it was not built, or not for this torch (the Python code below then makes the
+    same checks and the same calls)."""
     global _ops_ext
     if _ops_ext is None:
-        import torch  # noqa: F401  (the extension links to it)
+        import torch                     # the extension links to it
         ext = _load_ext("_rxops")
+        made_for = getattr(ext, "torch_version", None)
+        if ext and made_for != str(torch.__version__):
+            warnings.warn(f"_rxops was built for torch {made_for}, not {torch.__version__}; the Python code makes its calls")
+            ext = False
         if ext:
             ext.bind({n: ctypes.cast(getattr(load(), n), ctypes.c_void_p).value
                       for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention")})

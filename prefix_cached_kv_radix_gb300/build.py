@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -58,6 +59,13 @@ def _stale(obj: str, src: str) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(p) > t for p in [src, *_headers(), __file__])
+
+
+def _text(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def _run(cmd, verbose):
@@ -125,7 +133,8 @@ def build_pystep(force: bool = False, verbose: bool = False) -> str | None:
 
 
 def build_pyops(force: bool = False, verbose: bool = False) -> str | None:
-    """The _rxops extension next to the library, when the Python, torch and CUDA headers are installed."""
+    """The _rxops extension next to the library, when the Python, torch and CUDA headers are installed and
+    it compiles against them (with a warning and None otherwise: api.py does the same in Python)."""
     import sysconfig
     try:
         import torch
@@ -139,14 +148,26 @@ def build_pyops(force: bool = False, verbose: bool = False) -> str | None:
     if not all(os.path.exists(p) for p in wanted):
         return None
     src, out = os.path.join(CSRC, PYOPS_SRC), pystep_path("_rxops")
-    if force or _stale(out, src):
+    version = str(torch.__version__)
+    made_for = os.path.join(OUT_DIR, "_rxops.torch")      # the torch version whose tensors it reads
+    if force or _stale(out, src) or _text(made_for) != version:
         tmp = out + f".tmp{os.getpid()}"
         lib = os.path.join(troot, "lib")
-        _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-              "-isystem", inc, "-isystem", tinc, "-isystem", os.path.join(tinc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-              "-I", INCLUDE, src, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-              "-lc10_cuda"], verbose)
+        try:
+            _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                  f'-DRX_TORCH_VERSION="{version}"',
+                  "-isystem", inc, "-isystem", tinc, "-isystem", os.path.join(tinc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+                  "-I", INCLUDE, src, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+                  "-lc10_cuda"], verbose)
+        except (RuntimeError, OSError) as e:
+            for f in (out, made_for, tmp):                # one of other sources or another torch is no stand-in
+                if os.path.exists(f):
+                    os.remove(f)
+            warnings.warn(f"_rxops does not compile against torch {version}; the binding's Python code makes its calls.\n{e}")
+            return None
         os.replace(tmp, out)
+        with open(made_for, "w") as f:
+            f.write(version)
     return out
 
 

@@ -277,4 +277,12 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_rxops", "Marshalling of the r
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rxops() { return PyModule_Create(&module_def); }
+// torch_version: the torch it was compiled for, whose tensors alone it may read
+PyMODINIT_FUNC PyInit__rxops() {
+    PyObject* m = PyModule_Create(&module_def);
+    if (m && PyModule_AddStringConstant(m, "torch_version", RX_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
