@@ -639,11 +639,11 @@ const char* rx_version(void);
  * off, a call pays one relaxed atomic load.  Process-wide; returns the previous setting. */
 int rx_set_tracing(int on);
 
-/* Self-test of the bounded waits inside the kernels: one CTA waits on an mbarrier that no
- * thread arrives at; after limit_ns (clamped to [1 us, 100 ms]) the wait gives up and sets
- * *d_status (device int32, caller-owned) to RX_DEV_TIMEOUT unless it already holds a code, and
- * the kernel ends.  The device stays usable.  Asynchronous on `stream`; RX_ECUDA if the launch
- * fails. */
+/* Self-test of the bounded waits inside the kernels: one CTA waits on mbarriers that no
+ * thread arrives at, with each of the kernels' two kinds of wait; after limit_ns (clamped to [1 us,
+ * 100 ms]) each gives up, and if both do *d_status (device int32, caller-owned) becomes
+ * RX_DEV_TIMEOUT unless it already holds a code, and the kernel ends.  The device stays usable.
+ * Asynchronous on `stream`; RX_ECUDA if the launch fails. */
 int rx_wait_selftest(int32_t* d_status, uint64_t limit_ns, void* stream);
 
 #ifdef __cplusplus

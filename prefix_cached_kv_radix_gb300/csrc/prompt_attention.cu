@@ -56,6 +56,7 @@
 #include <cmath>
 
 #include "prompt_items.cuh"
+#include "prompt_wait.cuh"
 #include "radix_attn.h"
 #include "rx_common.h"
 #include "rx_device.cuh"
@@ -203,44 +204,6 @@ __device__ __forceinline__ void pt_commit(uint32_t bar) {
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
-}
-
-// ---------------------------------------------------------------- waits
-// Whether an mbarrier phase has completed, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// A whole warp's bounded wait (2 s) on an mbarrier phase; on time-out it sets *abort, which ends
-// every role's waits and is reported once, at the end.  As short as can be: there are some thirty
-// waits in the kernel, and an item of a short sequence runs every role's code once, so that
-// fetching instructions is much of its time.
-__device__ __forceinline__ bool pt_wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
-    auto now = [] {
-        uint32_t t;
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-        return t;
-    };
-    const uint32_t t0 = now();
-    bool ok;
-    do ok = mbar_try_wait(bar, parity);
-    while (!ok && !*abort && now() - t0 < 2000000000u);
-    if (!ok) *abort = 1;
-    return ok;
-}
-
-__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    bool ok = mbar_try_wait(bar, parity);     // up to 100 us by itself
-    if (!ok) ok = pt_wait_on(bar, parity, abort);
-    return __all_sync(0xffffffffu, ok);
 }
 
 // SPLIT: an item is one Q tile, and the two softmax warpgroups, S and O take its K/V tiles in turn (even
