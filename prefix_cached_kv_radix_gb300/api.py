@@ -715,12 +715,16 @@ def _here(*tensors):
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
+def _pool(desc, name, p):
+    """Address of a KV pool: contiguous [num_slots, hkv, head_dim] of the descriptor's type."""
+    if p is None or not p.is_cuda or not p.is_contiguous() or p.numel() != desc.num_slots * desc.hkv * desc.head_dim or \
+            str(p.dtype) != _FLOATS[desc.dtype]:
+        raise ValueError(f"{name}: want contiguous [num_slots, hkv, head_dim] of the descriptor's type on a CUDA device")
+    return p.data_ptr()
+
+
 def _pool_list(desc, pools):
-    n = desc.num_slots * desc.hkv * desc.head_dim
-    for p in pools:
-        if not p.is_cuda or not p.is_contiguous() or p.numel() != n or str(p.dtype) != _FLOATS[desc.dtype]:
-            raise ValueError("pools: want contiguous [num_slots, hkv, head_dim] of the descriptor's type on a CUDA device")
-    return (ctypes.c_void_p * max(len(pools), 1))(*[p.data_ptr() for p in pools])
+    return (ctypes.c_void_p * max(len(pools), 1))(*[_pool(desc, "pools", p) for p in pools])
 
 
 def rope_desc(sections, base: float = 10000.0, cyclic: bool = False, interleaved: bool = False, inv_freq=None) -> rx_rope_desc:
@@ -758,11 +762,7 @@ def kv_pool_write_rope(desc, rope, batch, prefix_slots, prefix_indptr, new_slots
     xa, xs = _rows("k_out", k_out, desc.hkv, desc, total_new)
     if positions.dim() != 2 or positions.shape[0] != rope.n_axes or positions.shape[1] < total_new:
         raise ValueError(f"positions: want [{rope.n_axes}, {total_new}]")
-    pool_rows = desc.num_slots if new_slots is not None else 0
-    kp, _ = _rows("k_pool", k_pool, desc.hkv, desc, pool_rows)
-    vp, _ = _rows("v_pool", v_pool, desc.hkv, desc, pool_rows)
-    if any(x is not None and not x.is_contiguous() for x in (k_pool, v_pool)):
-        raise ValueError("pools: not contiguous")
+    kp, vp = (None, None) if new_slots is None else (_pool(desc, "k_pool", k_pool), _pool(desc, "v_pool", v_pool))
     stride = 0
     if req_to_token is not None:
         stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride

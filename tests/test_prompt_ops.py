@@ -571,6 +571,27 @@ def test_binding_refuses_other_types_and_places(dev, native, monkeypatch):
 
 
 @gpu
+@pytest.mark.parametrize("native", [True, False])
+def test_binding_refuses_pools_of_another_size(dev, native, monkeypatch):
+    """A rotary write's pools have the descriptor's slots, no fewer and no more, as those of the row movers."""
+    if not native:
+        monkeypatch.setattr(api, "_ops_ext", False)
+    d, st, ip = desc_of(BF, 4, 2, 64, 10), i32([0], "cuda"), torch.tensor([0, 1], device="cuda")
+    k, pos, slot = torch.ones(1, 2, 64, dtype=BF, device="cuda"), i32([[0]], "cuda"), i32([4], "cuda")
+    pool = [torch.zeros(n, 2, 64, dtype=BF, device="cuda") for n in (10, 9, 11)]
+
+    def write(kp, vp, slots=slot):
+        api.kv_pool_write_rope(d, api.rope_desc(32), 1, None, None, slots, ip, pos, None, k, k, None, None if slots is not None else k.clone(),
+                               kp, vp, None, 1, st)
+    for kp, vp in ((pool[1], pool[0]), (pool[2], pool[0]), (pool[0], pool[2]), (pool[0], None), (pool[0].float(), pool[0])):
+        with pytest.raises(ValueError):
+            write(kp, vp)
+    write(pool[1], None, slots=None)                       # no pool is written: none is looked at
+    write(pool[0], pool[0].clone())
+    assert int(st.item()) == 0 and pool[0].ne(0).any(dim=2).any(dim=1).nonzero().flatten().tolist() == [4]
+
+
+@gpu
 def test_binding_in_python_makes_the_same_calls(dev, monkeypatch):
     """Every operator through the extension and through the Python code: the same results."""
     gen = torch.Generator("cuda").manual_seed(11)
