@@ -377,10 +377,13 @@ int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, 
  * and its own stride in elements between rows (multiples of 16 bytes, as the addresses are); d_lse:
  * optional [total, hq] float32 natural-log log-sum-exp.  d_out overlaps no input.
  * bf16 runs on tcgen05 tensor cores (sm_103a), f32 on CUDA cores in 32-bit arithmetic; softmax
- * statistics and sums are 32-bit.  No workspace; calls on several streams, or captured into graphs
+ * statistics and sums are 32-bit.  bf16 rounds the probabilities to bf16 for their product with V (before
+ * they are divided by their 32-bit sum; at most 2^-8 of each, as prefix_extend_attention does).  No workspace; calls on several streams, or captured into graphs
  * that run at once, share nothing.
  *  - A row's result depends on rows 0..i of its own sequence alone: an infinity or NaN in another
- *    row, or in rows that no sequence has, does not reach it.
+ *    row, or in rows that no sequence has, does not reach it.  One in a value row that it attends makes
+ *    that channel of it not finite: as the value is, or, where the key's probability is too small
+ *    for 32 bits, NaN (zero times an infinity); which of the two it is there is not specified.
  *  - Rows before indptr[0] and from indptr[batch] on are left as they were.
  *  - indptr [batch+1] must not decrease and lie in [0, total] (total <= 2^31-1 rows), and a sequence
  *    has at most 2^26 rows: one that does not keep to this is RX_DEV_BAD_LENGTH and is skipped.  Where

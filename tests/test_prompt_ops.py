@@ -764,6 +764,34 @@ def test_prompt_non_finite_values_stay_in_their_place(dev, dt, hq, hkv, d, bad):
 
 @gpu
 @pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_prompt_non_finite_values_of_vanishing_weight(dev, dt, d, bad):
+    """A value that is not finite under a score so low that its probability is 0 in 32 bits, in tiles that the
+    mask cuts for some rows and not for others: that channel of the rows that attend it is not finite
+    (which of infinity and NaN is left open), and everything else is as if the value were finite."""
+    gen = torch.Generator("cuda").manual_seed(15)
+    n = 600
+    for at in (3, 200, 300, 599):
+        q, k, v = (x.contiguous() for x in rows_of(gen, n, 2, 1, d, dt))
+        q = q.abs() + 0.5
+        k[at] = -1000.0                                     # scores of -500 sqrt(d) and below, beside others of a few
+        desc = desc_of(dt, 2, 1, d)
+        clean, _, st = run_prompt(q, k, v, [n], desc)
+        want, wl, to, tl = attention(q, k, v, [n], desc.scale)
+        assert st == 0
+        close(clean, want, to, "clean")
+        v[at, 0, 5] = bad
+        out, lse, st = run_prompt(q, k, v, [n], desc)
+        close(lse, wl, tl, "lse")
+        rest = torch.ones_like(out, dtype=torch.bool)
+        rest[at:, :, 5] = False
+        assert st == 0 and torch.equal(out[rest], clean[rest])
+        assert not torch.isfinite(out[at:, :, 5].float()).any()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, BF])
 def test_prompt_growing_and_extreme_scores(dev, dt):
     """Scores whose maximum keeps growing (the running maximum moves at every tile), one that falls,
     the type's lowest values as keys, and a scale of zero."""
