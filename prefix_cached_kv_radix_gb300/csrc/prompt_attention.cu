@@ -54,6 +54,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "prompt_items.cuh"
 #include "prompt_wait.cuh"
@@ -632,9 +633,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_tc_kernel(const __grid_c
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + t * PT_BN;   // scores, then P over them
         const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;   // rescaled here, read out by the output warps
-        // A scale of zero as the least number above it: masked scores are -inf, and -inf times it has to stay
-        // so.  Scores are below 2^128: it moves none by more than 2^-21.
-        const float sl = fmaxf(p.scale_log2, 0x1p-149f);
+        const float sl = p.scale_log2;
         const int row_tok = r / p.hb, row_head = r - row_tok * p.hb;
         int sc = 0, oc = 0;                   // score steps, and items (SPLIT: joins), of this Q tile so far
         bool ok = true;
@@ -989,7 +988,14 @@ static int launch_prompt_tc(const PromptParams& a, int head_dim, cudaStream_t st
     p.hb = std::min(p.group, 128);
     p.nhb = (p.group + p.hb - 1) / p.hb;
     p.tpt = 128 / p.hb;
-    p.scale_log2 = a.scale * PT_LOG2E;
+    // A scale of zero as the least number above it: masked scores are -inf, and -inf times it has to stay so.
+    // Scores are below 2^128: it moves none by more than 2^-21.  By its bits, as the calling thread may have
+    // the processor take numbers this small for zero.
+    const float sl = a.scale * PT_LOG2E;
+    int32_t bits;
+    std::memcpy(&bits, &sl, sizeof bits);
+    bits = std::max(bits, 1);            // -0 has the sign bit
+    std::memcpy(&p.scale_log2, &bits, sizeof bits);
     const int64_t heads = (int64_t)a.hkv * p.nhb;
     // Two Q tiles an item share its K/V tiles and keep the tensor core busy in turn (1.4 us a step of
     // 128 keys); one, its K/V tiles split between two softmax warpgroups, while even those items are no

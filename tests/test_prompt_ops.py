@@ -820,6 +820,13 @@ def test_prompt_scale_of_nearly_nothing(dev, dt, hq, hkv, d, lens, scale):
     scales near and below the least normal number."""
     gen = torch.Generator("cuda").manual_seed(d)
     q, k, v = rows_of(gen, sum(lens), hq, hkv, d, F)
+    if scale == 0:
+        flushes = torch.set_flush_denormal(True)           # the host's setting does not matter, nor does zero's sign
+        try:
+            runs = [run_prompt(q.to(dt), k.to(dt), v.to(dt), lens, desc_of(dt, hq, hkv, d, scale=z))[0] for z in (0.0, -0.0)]
+        finally:
+            torch.set_flush_denormal(False)
+        assert torch.isfinite(runs[0].float()).all() and torch.equal(*runs), flushes
     check_prompt((q * 1e18).to(dt), (k * 1e18).to(dt), v.to(dt), lens, desc_of(dt, hq, hkv, d, scale=scale))
 
 
