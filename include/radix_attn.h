@@ -378,8 +378,8 @@ int kv_pool_fork(const rx_attn_desc* desc, int32_t n_pools, void* const* pools, 
  * optional [total, hq] float32 natural-log log-sum-exp.  d_out overlaps no input.
  * bf16 runs on tcgen05 tensor cores (sm_103a), f32 on CUDA cores in 32-bit arithmetic; softmax
  * statistics and sums are 32-bit.  bf16 rounds the probabilities to bf16 for their product with V (before
- * they are divided by their 32-bit sum; at most 2^-8 of each, as prefix_extend_attention does).  No workspace; calls on several streams, or captured into graphs
- * that run at once, share nothing.
+ * they are divided by their 32-bit sum; by at most 2^-8 of each, as prefix_extend_attention does).
+ * No workspace; calls on several streams, or captured into graphs that run at once, share nothing.
  *  - A row's result depends on rows 0..i of its own sequence alone: an infinity or NaN in another
  *    row, or in rows that no sequence has, does not reach it.  One in a value row that it attends makes
  *    that channel of it not finite: as the value is, or, where the key's probability is too small
@@ -636,8 +636,8 @@ const char* rx_version(void);
 
 /* Tracing (the pages have no counterpart; a profiling aid): on != 0 puts an NVTX range named
  * after the entry point around every call that does work (the tree operations, the step
- * runtime's plan/launch/finish/prefetch/stage wait, kv_pool_write and the attention calls), so
- * that a profiler's timeline shows the library's host and GPU work per call.  Off by default;
+ * runtime's plan/launch/finish/prefetch/stage wait, the pool writes, copies and forks, and the
+ * attention calls), so that a profiler's timeline shows the library's host and GPU work per call.  Off by default;
  * RX_NVTX=1 in the environment when the library is loaded turns it on from the start.  While
  * off, a call pays one relaxed atomic load.  Process-wide; returns the previous setting. */
 int rx_set_tracing(int on);

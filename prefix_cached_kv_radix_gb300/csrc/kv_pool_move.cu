@@ -12,7 +12,7 @@
 // its rate needs), so the rows' order in the pool does not matter as long as a row is some hundred
 // bytes.  The pool addresses travel as a kernel argument, so one launch moves a token's rows of
 // every layer.  Measured: 3001 pages of 16 tokens in 4 layers (8 kv heads x 128, bf16), 1.57 GB read and
-// written, 239 us, 6.6 TB/s (98 % of the measured copy rate); 64 forked rows with 10,000 copied tokens of
+// written, 240 us, 6.56 TB/s (97 % of the measured copy rate); 64 forked rows with 10,000 copied tokens of
 // 2 layers in f32 48 us, 7.2 TB/s (part of it from the L2); 700 slots of 2 layers 2.8 us, the launch.
 #include <cuda_runtime.h>
 

@@ -29,14 +29,17 @@
 //   warps 12-15 the items' output from TMEM, while the others are on the next item
 // While one tile's softmax runs the tensor core works on the other's products.
 //
-// What bounds it: for long prompts the tensor core (one of 16384 tokens, 32/8 heads x 128: 1.24 ms, 1770
-// TFLOP/s, 91 % of the measured cuBLAS burst rate; of 32768: 5.1 to 5.2 ms, 1700; 64/8 heads: 1700): a step of
-// 128 keys takes 2700 clocks, of which its products are 2048.  The issuing warp decides that: with
-// operands the compiler did not know to be warp-uniform the products took 75 clocks each to issue
-// instead of 64 (1254 TFLOP/s), and waits where its queue ran dry cost 500 clocks a step.  For short
-// prompts the passage from one item to the next, about 2 us of which instruction fetch is a part (32
-// prompts of 1024: 1230 TFLOP/s; the code was cut from 112 to 60 KB, which took that case from 391 to
-// 230 us), and HBM (512 prompts of 64 tokens: 118 us for 670 MB, 85 % of the measured copy rate).
+// What bounds it: for long prompts of 128-wide heads the tensor core (32/8 heads, one of 16384 tokens: 1.24
+// to 1.37 ms from card to card, 1600 to 1770 TFLOP/s of 1950 measured for a burst and 1706 sustained; of 32768:
+// 5.0 to 5.3 ms, 1660 to 1760): a step of 128 keys takes 2700 clocks, of which its products are 2048.  The
+// issuing warp decides that: issued by one thread under `if (lane == 0)` the products took 75 clocks each
+// instead of 64 (1254 TFLOP/s), and waits where its queue ran dry cost 500 clocks a step.  For 64-wide heads
+// the softmax warps' own chain: a step takes about 2450 clocks, of which tensor core and exponentials are
+// 1024 each, neither pipe busy for more than 45 % (four prompts of 4096 tokens, 12 heads: 106 us, twice the
+// burst rate's time).  For short prompts the passage from one item to the next, 2 to 3 us of which
+// instruction fetch is a part (32 prompts of 1024: 234 to 242 us, 1150 to 1180 TFLOP/s; the code was cut from
+// 112 to 60 KB, which took that case from 391 to 230 us; 200 prompts of 64 tokens, 12 heads x 64: 51 us), and
+// HBM (512 prompts of 64 tokens: 120 us for 670 MB, 82 % of the measured copy rate).
 //
 // Rows that a row must not see: a masked score is replaced after the product, so nothing of a
 // hidden key survives, but P V multiplies hidden values by zero, and zero times an infinity or a

@@ -54,13 +54,14 @@ struct PromptDiv {
 
 // Whether the items are better taken by tile index, of all sequences together and from the highest
 // down, than sequence by sequence: row tile x has about x tiles of keys, so the longest items come first
-// and the launch ends on the shortest, whatever the order of the sequences (bf16, by sequence and by tile
-// index: 48 ragged prompts 111 and 102 us, one of 2000 37 and 27, 12 heads x 64 and one of 16384 453 and
-// 394; 8 ragged f32 prompts 658 and 510).  Not where all items run at once anyway, nor with more sequences
-// than a warp's lanes hold at two each (searched in memory, 250 prompts of 64 tokens took 239 us and not 73),
-// nor where the keys and values of all sequences are more than the L2 holds beside the rest (of 129 MB):
-// each tile index reads them again (32 prompts of 1024 tokens, 134 MB: 222 and 258 us; at 67 MB both are
-// alike: one of 16384 1245 and 1275, four of 4096 338 and 330).
+// and the launch ends on the shortest, whatever the order of the sequences (by sequence and by tile index,
+// on rows that change from call to call: 48 ragged bf16 prompts 113 and 106 us; 12 heads x 64, one of 2000
+// tokens 18.8 and 16.0, four of 4096 126 and 107, one of 16384 431 and 375; 8 ragged f32 prompts 622 and
+// 425).  Not where all items run at once anyway, nor with more sequences than a warp's lanes hold at two each
+// (searched in memory, 250 prompts of 64 tokens took 239 us and not 73), nor where the keys and values of all
+// sequences are more than the L2 holds beside the rest (of 129 MB): each tile index reads them again (32
+// prompts of 1024 tokens, 134 MB, the same rows in each call: 222 and 258 us; at 67 MB, 32/8 heads x 128, both are
+// alike: one of 16384 1332 and 1335, four of 4096 370 and 369).
 constexpr int PROMPT_LEVEL_SEQS = 64;    // two a lane
 inline bool prompt_by_level(int64_t items, int resident, int32_t batch, int64_t kv_bytes) {
     return items > resident && batch <= PROMPT_LEVEL_SEQS && kv_bytes <= 80ll << 20;
