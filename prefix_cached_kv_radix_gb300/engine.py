@@ -501,7 +501,8 @@ class PrefixCacheEngine:
                    layer: int = 0) -> None:
         """a3 for rows whose rotary positions are still to be applied (api.rope_desc): slot table,
         turned keys and values into `layer`'s pools, turned queries into q_out (may be q), and turned
-        keys into k_out (may be k_new) where prompt() is to read them.  positions: int32 [axes, T]."""
+        keys into k_out (may be k_new) where prompt() is to read them.  positions: int32 [axes, T].  On another
+        stream than the engine's the caller orders the two, as for every call of a step."""
         api.kv_pool_write_rope(self.desc, rope, plan.batch, dev["prefix_slots"], dev["prefix_indptr"], dev["new_slots"],
                                dev["qo_indptr"], positions, q, k_new, v_new, q_out, k_out, self.k_pools[layer],
                                self.v_pools[layer], dev["r2t"].data_ptr(), int(plan.qo_indptr[-1]), self.status,
@@ -560,7 +561,7 @@ class PrefixCacheEngine:
                                  self._i64(np.concatenate([[0], np.cumsum(tails)])), self._i32(slots if total else [0]), r2t, out,
                                  total, self.status, st)
                 r2t.record_stream(st)    # the caller may let go of its table
-        except Exception:                # refused: the slots allocated here go back
+        except BaseException:            # refused or interrupted: the slots allocated here go back
             if tail_slots is None:
                 self.tree.free_slots(slots)
             raise
@@ -598,7 +599,7 @@ class PrefixCacheEngine:
                     for row, slots in zip(ids, (src, dst)):
                         row[:n].copy_(torch.from_numpy(slots))
                     api.kv_pool_copy(self.desc, pools, ids[0, :n], ids[1, :n], 1, self.status, st)
-            except Exception:            # the rows are not where the tree says: what is not pinned, all that moved, goes
+            except BaseException:        # the rows are not where the tree says: what is not pinned, all that moved, goes
                 self.tree.evict_count(self.tree.stats()["cached_tokens"])
                 raise
             finally:

@@ -317,3 +317,33 @@ def test_refused_fork_gives_its_slots_back():
         eng.fork(torch.zeros(1, 8, dtype=torch.int32, device="cuda"), [0], [6], [5])
     assert eng.tree.stats()["free_slots"] == free
     eng.tree.check()
+
+
+@pytest.mark.parametrize("op", ["resize", "fork"])
+def test_interrupted_move_is_consistent(op, monkeypatch):
+    """Ctrl-C in the midst of a resize or a fork: no match names rows that were not moved, no slot is lost."""
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    eng = PrefixCacheEngine("f32", 2, 2, 64, 256, 3)
+    toks = np.arange(90, dtype=np.int32)
+    eng.populate(toks, *(torch.randn(90, 2, 64, device="cuda") for _ in range(2)))
+    assert max(eng.tree.match_prefix(toks)[0]) >= 120
+    free, left, copy = eng.tree.stats()["free_slots"], [1], api.kv_pool_copy
+
+    def interrupted(*a):
+        if op == "fork" or not left:
+            raise KeyboardInterrupt
+        left.pop()
+        return copy(*a)
+    with monkeypatch.context() as m:
+        m.setattr(api, "kv_pool_copy", interrupted)
+        m.setattr(api, "kv_pool_fork", interrupted)
+        with pytest.raises(KeyboardInterrupt):
+            if op == "resize":
+                eng.resize(120)
+            else:
+                eng.fork(torch.zeros(1, 8, dtype=torch.int32, device="cuda"), [0], [2], [5])
+    eng.tree.check()
+    size = 120 if op == "resize" else 256
+    assert eng.num_slots == eng.desc.num_slots == eng.k_pools.shape[1] == eng.tree.stats()["num_slots"] == size
+    assert eng.tree.match_prefix(toks)[1] == (0 if op == "resize" else 90)
+    assert eng.tree.stats()["free_slots"] == (120 if op == "resize" else free)
