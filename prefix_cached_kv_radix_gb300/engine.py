@@ -522,7 +522,11 @@ class PrefixCacheEngine:
         """The torch stream of a `stream` argument: a torch stream, an address, or None (the engine's own)."""
         if not stream:
             return self._stream
-        return torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+        if not isinstance(stream, int):
+            return stream
+        if not 0 < stream < 1 << 64:     # torch would cut it
+            raise ValueError(f"stream: {stream} is no address")
+        return torch.cuda.ExternalStream(stream, self.device)
 
     @contextlib.contextmanager
     def _in_order(self, st):
@@ -548,11 +552,10 @@ class PrefixCacheEngine:
         tails = kv.astype(np.int64) - keep
         if len(keep) != len(kv) or len(parents) != len(kv) or (tails < 0).any():
             raise ValueError("fork: one parent and two lengths, keep <= kv, for each row")
-        total = int(tails.sum())
+        total, st = int(tails.sum()), self._torch_stream(stream)
         slots = self.tree.alloc_slots(total) if tail_slots is None else _contig(tail_slots, np.int32)
         if len(slots) != total:
             raise ValueError(f"fork: {total} tail slots are needed, {len(slots)} given")
-        st = self._torch_stream(stream)
         try:
             with torch.cuda.stream(self._stream):    # the table is the engine's stream's, as its other buffers are
                 out = torch.empty(len(kv), r2t.shape[1], dtype=torch.int32, device=self.device)

@@ -347,3 +347,19 @@ def test_interrupted_move_is_consistent(op, monkeypatch):
     assert eng.num_slots == eng.desc.num_slots == eng.k_pools.shape[1] == eng.tree.stats()["num_slots"] == size
     assert eng.tree.match_prefix(toks)[1] == (0 if op == "resize" else 90)
     assert eng.tree.stats()["free_slots"] == (120 if op == "resize" else free)
+
+
+@pytest.mark.parametrize("stream", ["no stream", 1 << 70])
+def test_moves_on_what_is_no_stream_change_nothing(stream):
+    from prefix_cached_kv_radix_gb300.engine import PrefixCacheEngine
+    eng = PrefixCacheEngine("f32", 2, 2, 64, 64, 3)
+    eng.populate(np.arange(20, dtype=np.int32), *(torch.randn(20, 2, 64, device="cuda") for _ in range(2)))
+    before = eng.tree.stats()
+    for call in (lambda: eng.fork(torch.zeros(1, 8, dtype=torch.int32, device="cuda"), [0], [2], [5], stream=stream),
+                 lambda: eng.resize(30, stream=stream), lambda: eng.resize(90, stream=stream)):
+        with pytest.raises(Exception):
+            call()
+        after = eng.tree.stats()
+        assert all(after[k] == before[k] for k in ("free_slots", "num_slots", "cached_tokens"))
+        assert eng.num_slots == eng.desc.num_slots == eng.k_pools.shape[1] == 64
+        eng.tree.check()
