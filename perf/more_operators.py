@@ -126,9 +126,9 @@ def _scales_of(x, code):
     fits, for e4m3 a power of two (so that neither the quotients nor the values read back are rounded)."""
     top = x.float().abs().amax(-1)
     if code == "int8":
-        s = (top / 127.0).clamp(min=2.0 ** -126)
+        s = (top.double() / 127.0).float().clamp(min=2.0 ** -126)
     else:
-        part, power = torch.frexp(top.double() / 448.0)
+        part, power = torch.frexp(top.double() / torch.full_like(top, 448.0))      # a number 448 would be taken as its reciprocal
         power = torch.where(top > 0, power - (part == 0.5).to(power.dtype), -126).clamp(-126, 127)
         s = ((power + 127) << 23).view(torch.float32)        # 2 ** power
     return torch.where(torch.isfinite(top), s, math.nan)
