@@ -494,6 +494,86 @@ int decode_attention_noalloc(const rx_attn_desc* desc, int32_t batch,
                              void* d_out, float* d_lse, int32_t max_kv_len,
                              int32_t* d_status, void* stream);
 
+/* ------------------------------------------------------------------ pools held in 8 bits
+ * A pool of 8-bit codes takes half the memory of a bf16 pool and half the time to read: twice the
+ * tokens stay cached, and decode attention, bound by HBM, runs at about twice the speed.  A value is its code times the scale
+ * of its block of slots and kv head:
+ *   K[slot, g, i] = k_pool[slot, g, i] * scales[slot / block, g, 0]
+ *   V[slot, g, i] = v_pool[slot, g, i] * scales[slot / block, g, 1]
+ * Pools: [num_slots, hkv, head_dim] bytes, int8 codes or e4m3 codes (4 exponent bits, 3 mantissa bits,
+ * no infinities), 16-byte aligned; scales: [ceil(num_slots / block), hkv, 2] float32, 8-byte aligned.
+ *  - block 1, fixed 0: kv_pool_write_q8 computes the scales, one per written token, head and pool.  A
+ *    cached token then has the same value whoever shares it and whatever is written beside it.
+ *  - fixed 1: the scales are the caller's (calibrated), for blocks of any power of two of slots
+ *    (pages; or 2^30: one scale a head), and the write only reads them.  They are finite, positive
+ *    normal numbers; codes and results for others are not specified.
+ * desc->dtype is the type of the rows: bf16 or f32. */
+enum rx_q8_format { RX_Q8_INT8 = 0, RX_Q8_E4M3 = 1 };
+typedef struct {
+    int32_t format;     /* rx_q8_format of both pools */
+    int32_t block;      /* slots per scale, a power of two up to 2^30 */
+    int32_t fixed;      /* 0: computed by the write (block 1 only); 1: given */
+} rx_q8_desc;
+
+/* kv_pool_write into 8-bit pools, in one launch: the new tokens' rows quantised into their slots, their scales (fixed 0),
+ * and the slot table.  The batch, slot lists, table and their errors are those of kv_pool_write_rope:
+ * d_prefix_slots may be NULL where nothing is matched, d_req_to_token NULL makes no table, rows before
+ * qo_indptr[0] and from qo_indptr[batch] on (a padded batch) are not written.  d_k_new, d_v_new: rows [T, hkv,
+ * head_dim] of desc->dtype with the heads of a row contiguous and their own stride in elements between
+ * rows; strides and addresses are multiples of 16 bytes.
+ *  - code = x / scale (the real quotient), rounded to the nearest code, ties to even, and cut to
+ *    [-127, 127] or [-448, 448].
+ *  - Computed scales, from a = max |x| of the row: int8 a / 127 rounded to float32, e4m3 the smallest
+ *    power of two not below a / 448 (then x / scale is exact, and values read back are exact in bf16 too);
+ *    2^-126 at least.  A row with an infinity or NaN gets the scale NaN and codes 0: it reads as NaN.
+ *  - With fixed scales a NaN becomes int8 code 0, or the e4m3 NaN.
+ *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, that row is not written.  Two rows with the same slot: that
+ *    slot holds parts of either. */
+int kv_pool_write_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const int32_t* d_prefix_slots,
+                     const int64_t* d_prefix_indptr, const int32_t* d_new_slots, const int64_t* d_qo_indptr,
+                     const void* d_k_new, int64_t k_stride, const void* d_v_new, int64_t v_stride,
+                     void* d_k_pool, void* d_v_pool, float* d_scales, int32_t* d_req_to_token, int64_t r2t_stride,
+                     int64_t total_new, int32_t* d_status, void* stream);
+
+/* The cached rows of n slots as rows of desc->dtype again: d_k_out[i] = K[d_slots[i]], d_v_out[i] =
+ * V[d_slots[i]], [n, hkv, head_dim] with strides as above; either may be NULL.  code * scale in 32 bits, rounded
+ * to desc->dtype.  A slot may be named more than once.  A slot outside [0, num_slots): RX_DEV_BAD_SLOT,
+ * that row is left as it was. */
+int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int64_t n, const int32_t* d_slots, const void* d_k_pool,
+                    const void* d_v_pool, const float* d_scales, void* d_k_out, int64_t k_stride, void* d_v_out, int64_t v_stride,
+                    int32_t* d_status, void* stream);
+
+/* decode_attention over 8-bit pools: arguments, layouts and errors are its, but for what is said here.
+ *  - Codes go into the products as they are, scales in 32 bits; sums and softmax statistics are 32-bit.
+ *    desc->dtype f32 gives 32-bit results, on the tensor cores as well (queries and weighted probabilities in two 16-bit
+ *    parts each); bf16 rounds the weighted probabilities to 11 bits.
+ *  - A request of length 0 (a padded batch) gives a row of zeros and a log-sum-exp of -infinity.
+ *  - A key at a slot outside [0, num_slots) is reported and left out.
+ *  - groups: as for decode_attention; used for bf16 rows (f32 rows read each request's own keys, with the same result).
+ *    Members of a group are given once each.
+ *  - d_workspace: >= decode_q8_workspace_bytes(...) bytes, 256-byte aligned.  Calls that may overlap (other streams, graphs that
+ *    run at once) need workspaces of their own.  Any ratio hq / hkv; any number of requests up to 2^31 / (hq * chunks). */
+int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
+                        const int32_t* d_req_to_token, int64_t r2t_stride, const int32_t* d_kv_lens,
+                        const rx_shared_groups* groups, const void* d_k_pool, const void* d_v_pool, const float* d_scales,
+                        void* d_out, float* d_lse, int32_t max_kv_len, void* d_workspace, size_t ws_bytes,
+                        int32_t* d_status, void* stream);
+size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_kv_len, const rx_shared_groups* groups);
+
+/* prefix_extend_attention over 8-bit pools (the new tokens' own rows are in the pools too, written by
+ * kv_pool_write_q8, and are read from there): arguments, layouts and errors are its, without groups.
+ *  - A key at a slot outside [0, num_slots) is reported and left out; a row that is left no key is
+ *    zeros, its log-sum-exp -infinity.
+ *  - Rows before qo_indptr[0] and from qo_indptr[batch] on are left as they were.
+ *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request; it decides how far few rows over long
+ *    contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned). */
+int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
+                               const int64_t* d_qo_indptr, const int32_t* d_prefix_lens, const int32_t* d_req_to_token,
+                               int64_t r2t_stride, const void* d_k_pool, const void* d_v_pool, const float* d_scales,
+                               void* d_out, float* d_lse, int32_t max_qo_len, int32_t max_kv_len, void* d_workspace,
+                               size_t ws_bytes, int32_t* d_status, void* stream);
+size_t extend_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_qo_len, int32_t max_kv_len);
+
 /* ------------------------------------------------------------------ one-call step launch
  * Everything of a planned step that follows rx_step_plan, in one call: the staging buffer
  * (h_stage) to its device copy (io->d_stage) -- for at most 1 MiB of device-row step, by

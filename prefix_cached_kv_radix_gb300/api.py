@@ -21,6 +21,7 @@ RX_DEV_OK, RX_DEV_BAD_SLOT, RX_DEV_BAD_LENGTH, RX_DEV_TIMEOUT = 0, 1, 2, 3
 RX_F32, RX_BF16 = 0, 1
 RX_DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20   # include/radix_attn.h
 RX_ROPE_MAX_AXES = 4
+RX_Q8_INT8, RX_Q8_E4M3 = 0, 1
 
 EXPORTS = ("radix_create", "radix_destroy", "match_prefix", "match_prefix_len", "match_prefix_len_batch", "radix_set_page_size",
            "radix_lock", "radix_unlock", "alloc_slots",
@@ -31,6 +32,8 @@ EXPORTS = ("radix_create", "radix_destroy", "match_prefix", "match_prefix_len", 
            "kv_pool_write", "prefix_extend_attention", "extend_workspace_bytes", "decode_workspace_bytes",
            "decode_attention",
            "decode_attention_noalloc", "kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention", "radix_resize",
+           "kv_pool_write_q8", "kv_pool_read_q8", "decode_attention_q8", "decode_q8_workspace_bytes",
+           "prefix_extend_attention_q8", "extend_q8_workspace_bytes",
            "rx_last_error", "rx_version", "rx_wait_selftest", "rx_set_tracing")
 
 
@@ -49,6 +52,10 @@ class rx_rope_desc(ctypes.Structure):
     _fields_ = [("n_axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("sections", ctypes.c_int32 * RX_ROPE_MAX_AXES),
                 ("cyclic", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("base", ctypes.c_double),
                 ("inv_freq", ctypes.c_void_p)]
+
+
+class rx_q8_desc(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("block", ctypes.c_int32), ("fixed", ctypes.c_int32)]
 
 
 class rx_stats(ctypes.Structure):
@@ -154,6 +161,12 @@ def load(path: str = LIB_PATH):
         "kv_pool_copy": (ctypes.c_int, [P, I32, P, I64, I64, P, P, P, P]),
         "kv_pool_fork": (ctypes.c_int, [P, I32, P, I32, P, P, P, P, P, P, I32, I64, P, I64, I64, P, P]),
         "prompt_attention": (ctypes.c_int, [P, I32, P, I64, P, I64, P, I64, P, P, I64, P, I64, P, P]),
+        "kv_pool_write_q8": (ctypes.c_int, [P, P, I32, P, P, P, P, P, I64, P, I64, P, P, P, P, I64, I64, P, P]),
+        "kv_pool_read_q8": (ctypes.c_int, [P, P, I64, P, P, P, P, P, I64, P, I64, P, P]),
+        "decode_attention_q8": (ctypes.c_int, [P, P, I32, P, P, I64, P, P, P, P, P, P, P, I32, P, SZ, P, P]),
+        "decode_q8_workspace_bytes": (SZ, [P, I32, I32, P]),
+        "prefix_extend_attention_q8": (ctypes.c_int, [P, P, I32, P, P, P, P, I64, P, P, P, P, P, I32, I32, P, SZ, P, P]),
+        "extend_q8_workspace_bytes": (SZ, [P, I32, I32, I32]),
         "radix_resize": (ctypes.c_int, [P, I64, P, P, I64, P]),
         "rx_last_error": (ctypes.c_char_p, []),
         "rx_version": (ctypes.c_char_p, []),
@@ -672,7 +685,8 @@ def ops_ext():
             ext = False
         if ext:
             ext.bind({n: ctypes.cast(getattr(load(), n), ctypes.c_void_p).value
-                      for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention")})
+                      for n in ("kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention", "kv_pool_write_q8",
+                                "kv_pool_read_q8", "decode_attention_q8", "prefix_extend_attention_q8")})
         _ops_ext = ext
     return _ops_ext or None
 
@@ -829,3 +843,142 @@ def prompt_attention(desc, batch, q, k, v, indptr, out, lse, total, status, stre
     _check("prompt_attention", load().prompt_attention(
         ctypes.byref(desc), batch, qa, qs, ka, ks, va, vs, _ints("indptr", indptr, 8, batch + 1), oa, os_,
         None if lse is None else lse.data_ptr(), total, _ints("status", status, 4, 1), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- pools held in 8 bits
+_CODES = {RX_Q8_INT8: "torch.int8", RX_Q8_E4M3: "torch.float8_e4m3fn"}
+
+
+def q8_desc(format: int, block: int = 1, fixed: bool = False) -> rx_q8_desc:
+    """Pools of 8-bit codes: RX_Q8_INT8 or RX_Q8_E4M3, and their scales -- one for each token and head, computed by
+    the write, or (fixed) the caller's, one for each `block` slots and head.  See include/radix_attn.h."""
+    return rx_q8_desc(format, block, int(fixed))
+
+
+def _codes(desc, q8, name, p):
+    """Address of a pool of codes: contiguous [num_slots, hkv, head_dim] of the format's type (or uint8)."""
+    if p is None:
+        return None
+    if not p.is_cuda or not p.is_contiguous() or p.numel() != desc.num_slots * desc.hkv * desc.head_dim or \
+            str(p.dtype) not in (_CODES.get(q8.format), "torch.uint8"):
+        raise ValueError(f"{name}: want contiguous [num_slots, hkv, head_dim] of {_CODES.get(q8.format)} on a CUDA device")
+    return p.data_ptr()
+
+
+def _floats(name, t, count):
+    """Address of `count` or more contiguous float32 (None -> NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous() or t.numel() < count or str(t.dtype) != "torch.float32":
+        raise ValueError(f"{name}: want {count} contiguous float32 on a CUDA device")
+    return t.data_ptr()
+
+
+def _scales(desc, q8, t):
+    block = max(q8.block, 1)
+    return _floats("scales", t, -(-desc.num_slots // block) * desc.hkv * 2)
+
+
+def _whole_rows(name, t, desc, rows):
+    """Address of contiguous rows [>= rows, hq, head_dim] of the descriptor's type."""
+    if not t.is_cuda or not t.is_contiguous() or str(t.dtype) != _FLOATS[desc.dtype] or t.dim() != 3 or \
+            t.shape[1] != desc.hq or t.shape[2] != desc.head_dim or t.shape[0] < rows:
+        raise ValueError(f"{name}: want contiguous [{rows}, {desc.hq}, {desc.head_dim}] of the descriptor's type on a CUDA device")
+    return t.data_ptr()
+
+
+def _room(workspace):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def kv_pool_write_q8(desc, q8, batch, prefix_slots, prefix_indptr, new_slots, qo_indptr, k_new, v_new, k_pool, v_pool, scales,
+                     req_to_token, total_new, status, stream=None, r2t_stride=None) -> None:
+    """kv_pool_write into pools of 8-bit codes (q8_desc): rows quantised into their slots, their scales (unless
+    fixed) into scales [blocks, hkv, 2], and the slot table (None: none made).  Rows may be parts of wider ones."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("kv_pool_write_q8", ext.kv_pool_write_q8(
+            ctypes.addressof(desc), ctypes.addressof(q8), batch, prefix_slots, prefix_indptr, new_slots, qo_indptr, k_new, v_new,
+            k_pool, v_pool, scales, req_to_token, total_new, status, r2t_stride, _stream_of(stream)))
+    ka, ks = _rows("k_new", k_new, desc.hkv, desc, total_new)
+    va, vs = _rows("v_new", v_new, desc.hkv, desc, total_new)
+    stride = 0
+    if req_to_token is not None:
+        stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride
+    _here(prefix_slots, prefix_indptr, new_slots, qo_indptr, k_new, v_new, k_pool, v_pool, scales, req_to_token, status)
+    _check("kv_pool_write_q8", load().kv_pool_write_q8(
+        ctypes.byref(desc), ctypes.byref(q8), batch, _ints("prefix_slots", prefix_slots, 4, 0),
+        _ints("prefix_indptr", prefix_indptr, 8, batch + 1), _ints("new_slots", new_slots, 4, total_new),
+        _ints("qo_indptr", qo_indptr, 8, batch + 1), ka, ks, va, vs, _codes(desc, q8, "k_pool", k_pool),
+        _codes(desc, q8, "v_pool", v_pool), _scales(desc, q8, scales), _ints("req_to_token", req_to_token, 4, batch * stride),
+        stride, total_new, _ints("status", status, 4, 1), _stream(stream)))
+
+
+def kv_pool_read_q8(desc, q8, slots, k_pool, v_pool, scales, k_out, v_out, status, stream=None) -> None:
+    """Rows of 8-bit pools as numbers again: k_out[i], v_out[i] (either may be None) = the K and V rows of slots[i],
+    in the descriptor's type.  Rows may be parts of wider ones."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("kv_pool_read_q8", ext.kv_pool_read_q8(ctypes.addressof(desc), ctypes.addressof(q8), slots, k_pool, v_pool, scales,
+                                                             k_out, v_out, status, _stream_of(stream)))
+    n = slots.numel()
+    ka, ks = _rows("k_out", k_out, desc.hkv, desc, n)
+    va, vs = _rows("v_out", v_out, desc.hkv, desc, n)
+    _here(slots, k_pool, v_pool, scales, k_out, v_out, status)
+    _check("kv_pool_read_q8", load().kv_pool_read_q8(
+        ctypes.byref(desc), ctypes.byref(q8), n, _ints("slots", slots, 4, n), _codes(desc, q8, "k_pool", k_pool),
+        _codes(desc, q8, "v_pool", v_pool), _scales(desc, q8, scales), ka, ks, va, vs, _ints("status", status, 4, 1),
+        _stream(stream)))
+
+
+def decode_q8_workspace_bytes(desc, batch, max_kv_len, groups=None) -> int:
+    return int(load().decode_q8_workspace_bytes(ctypes.byref(desc), batch, max_kv_len,
+                                                ctypes.byref(groups) if groups is not None else None))
+
+
+def extend_q8_workspace_bytes(desc, batch, max_qo_len, max_kv_len) -> int:
+    return int(load().extend_q8_workspace_bytes(ctypes.byref(desc), batch, max_qo_len, max_kv_len))
+
+
+def decode_attention_q8(desc, q8, batch, q, req_to_token, kv_lens, k_pool, v_pool, scales, out, lse, max_kv_len, workspace,
+                        status, groups=None, stream=None, r2t_stride=None) -> None:
+    """decode_attention over pools of 8-bit codes.  req_to_token: [batch, stride], or an address with r2t_stride."""
+    ext = ops_ext()
+    if ext is not None:
+        return _check("decode_attention_q8", ext.decode_attention_q8(
+            ctypes.addressof(desc), ctypes.addressof(q8), batch, q, req_to_token, kv_lens,
+            None if groups is None else ctypes.addressof(groups), k_pool, v_pool, scales, out, lse, max_kv_len, workspace, status,
+            r2t_stride, _stream_of(stream)))
+    stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride
+    wa, wb = _room(workspace)
+    _here(q, req_to_token, kv_lens, k_pool, v_pool, scales, out, lse, workspace, status)
+    _check("decode_attention_q8", load().decode_attention_q8(
+        ctypes.byref(desc), ctypes.byref(q8), batch, _whole_rows("q", q, desc, batch),
+        _ints("req_to_token", req_to_token, 4, batch * stride), stride, _ints("kv_lens", kv_lens, 4, batch),
+        ctypes.byref(groups) if groups is not None else None, _codes(desc, q8, "k_pool", k_pool), _codes(desc, q8, "v_pool", v_pool),
+        _scales(desc, q8, scales), _whole_rows("out", out, desc, batch), _floats("lse", lse, batch * desc.hq), max_kv_len, wa, wb,
+        _ints("status", status, 4, 1), _stream(stream)))
+
+
+def prefix_extend_attention_q8(desc, q8, batch, q, qo_indptr, prefix_lens, req_to_token, k_pool, v_pool, scales, out, lse,
+                               max_qo_len, workspace, status, max_kv_len=None, stream=None, r2t_stride=None) -> None:
+    """prefix_extend_attention over pools of 8-bit codes.  max_kv_len: the most keys any request has (default: what a row
+    of the slot table holds)."""
+    stride = req_to_token.shape[1] if r2t_stride is None else r2t_stride
+    longest = stride if max_kv_len is None else max_kv_len
+    ext = ops_ext()
+    if ext is not None:
+        return _check("prefix_extend_attention_q8", ext.prefix_extend_attention_q8(
+            ctypes.addressof(desc), ctypes.addressof(q8), batch, q, qo_indptr, prefix_lens, req_to_token, k_pool, v_pool, scales, out,
+            lse, max_qo_len, longest, workspace, status, stride, _stream_of(stream)))
+    wa, wb = _room(workspace)
+    _here(q, qo_indptr, prefix_lens, req_to_token, k_pool, v_pool, scales, out, lse, workspace, status)
+    rows = q.shape[0] if q.dim() else 0
+    _check("prefix_extend_attention_q8", load().prefix_extend_attention_q8(
+        ctypes.byref(desc), ctypes.byref(q8), batch, _whole_rows("q", q, desc, 0), _ints("qo_indptr", qo_indptr, 8, batch + 1),
+        _ints("prefix_lens", prefix_lens, 4, batch), _ints("req_to_token", req_to_token, 4, batch * stride), stride,
+        _codes(desc, q8, "k_pool", k_pool), _codes(desc, q8, "v_pool", v_pool), _scales(desc, q8, scales),
+        _whole_rows("out", out, desc, rows), _floats("lse", lse, rows * desc.hq), max_qo_len, longest, wa, wb,
+        _ints("status", status, 4, 1), _stream(stream)))

@@ -1,6 +1,6 @@
-// _rxops: the argument checks and marshalling of the row, page and prompt operators as a Python
-// extension: what the binding's Python code does for kv_pool_write_rope, kv_pool_copy,
-// kv_pool_fork and prompt_attention, with the same checks and the same library calls, in a
+// _rxops: the argument checks and marshalling of the row, page and prompt operators and of those over 8-bit
+// pools as a Python extension: what the binding's Python code does for kv_pool_write_rope, kv_pool_copy,
+// kv_pool_fork, prompt_attention and the _q8 calls, with the same checks and the same library calls, in a
 // fraction of the time.  (A decode step's rotary write takes 3 us on the GPU; its 20 arguments cost
 // 22 us in the interpreter, 9 us through the tensors' Python methods from C, and 4 us from the
 // tensors' C++ fields here.)  No arithmetic of the operators happens here.
@@ -29,6 +29,10 @@ decltype(&kv_pool_write_rope) g_rope;
 decltype(&kv_pool_copy) g_copy;
 decltype(&kv_pool_fork) g_fork;
 decltype(&prompt_attention) g_prompt;
+decltype(&kv_pool_write_q8) g_write_q8;
+decltype(&kv_pool_read_q8) g_read_q8;
+decltype(&decode_attention_q8) g_decode_q8;
+decltype(&prefix_extend_attention_q8) g_extend_q8;
 
 // A Python exception is set.
 struct Raised {};
@@ -110,6 +114,43 @@ struct Call {
         if (!t.is_contiguous() || t.numel() != d->num_slots * d->hkv * d->head_dim)
             bad(std::string(name) + ": want contiguous [" + std::to_string(d->num_slots) + ", " + std::to_string(d->hkv) + ", " +
                 std::to_string(d->head_dim) + "]");
+        return t.data_ptr();
+    }
+
+    // a pool of 8-bit codes: contiguous [num_slots, hkv, head_dim] of the format's type, or of bytes
+    void* codes(const char* name, PyObject* o, const rx_q8_desc* q8) const {
+        if (o == Py_None) return nullptr;
+        const at::ScalarType want = q8->format == RX_Q8_E4M3 ? at::kFloat8_e4m3fn : at::kChar;
+        const bool bytes = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kByte;
+        const at::Tensor& t = tensor(name, o, bytes ? at::kByte : want);
+        if (!t.is_contiguous() || t.numel() != d->num_slots * d->hkv * d->head_dim)
+            bad(std::string(name) + ": want contiguous [" + std::to_string(d->num_slots) + ", " + std::to_string(d->hkv) + ", " +
+                std::to_string(d->head_dim) + "]");
+        return t.data_ptr();
+    }
+    float* scales(PyObject* o, const rx_q8_desc* q8) const {
+        const int64_t block = q8->block > 0 ? q8->block : 1;
+        return array<float>("scales", o, at::kFloat, (d->num_slots + block - 1) / block * d->hkv * 2);
+    }
+
+    // contiguous rows [>= n, hq, head_dim] of the descriptor's type
+    void* whole_rows(const char* name, PyObject* o, int64_t n, int64_t* have = nullptr) const {
+        const at::Tensor& t = tensor(name, o, type());
+        if (t.dim() != 3 || !t.is_contiguous() || t.size(0) < n || t.size(1) != d->hq || t.size(2) != d->head_dim)
+            bad(std::string(name) + ": want contiguous [" + std::to_string(n) + ", " + std::to_string(d->hq) + ", " +
+                std::to_string(d->head_dim) + "]");
+        if (have) *have = t.size(0);
+        return t.data_ptr();
+    }
+
+    // a workspace of any type, and its size
+    void* room(PyObject* o, size_t& bytes) const {
+        bytes = 0;
+        if (o == Py_None) return nullptr;
+        if (!THPVariable_Check(o)) bad("workspace: want a tensor");
+        const at::Tensor& t = tensor("workspace", o, THPVariable_Unpack(o).scalar_type());
+        if (!t.is_contiguous()) bad("workspace: want a contiguous tensor");
+        bytes = (size_t)t.nbytes();
         return t.data_ptr();
     }
 
@@ -245,10 +286,105 @@ PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+PyObject* py_write_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 17, g_write_q8 != nullptr, [&] {
+        const Call c(a[0], a[16]);
+        const auto* q8 = as_ptr<const rx_q8_desc>(a[1]);
+        const int32_t batch = as_i32(a[2]);
+        const int64_t total = as_i64(a[13]);
+        int64_t ks, vs, ts = 0, unused;
+        void* k = c.rows("k_new", a[7], c.d->hkv, total, ks);
+        void* v = c.rows("v_new", a[8], c.d->hkv, total, vs);
+        void* kp = c.codes("k_pool", a[9], q8);
+        void* vp = c.codes("v_pool", a[10], q8);
+        float* sc = c.scales(a[11], q8);
+        if (a[15] != Py_None) ts = as_i64(a[15]);
+        else if (a[12] != Py_None) c.table("req_to_token", a[12], unused, ts);
+        int32_t* rt = c.i32("req_to_token", a[12], batch * ts);
+        const int32_t* ps = c.i32("prefix_slots", a[3], 0);
+        const int64_t* pi = c.i64("prefix_indptr", a[4], batch + 1ll);
+        const int32_t* ns = c.i32("new_slots", a[5], total);
+        const int64_t* qi = c.i64("qo_indptr", a[6], batch + 1ll);
+        int32_t* st = c.i32("status", a[14], 1);
+        Unlocked u;
+        return g_write_q8(c.d, q8, batch, ps, pi, ns, qi, k, ks, v, vs, kp, vp, sc, rt, ts, total, st, c.stream);
+    });
+}
+
+PyObject* py_read_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, g_read_q8 != nullptr, [&] {
+        const Call c(a[0], a[9]);
+        const auto* q8 = as_ptr<const rx_q8_desc>(a[1]);
+        const at::Tensor& slots = c.tensor("slots", a[2], at::kInt);
+        const int64_t count = slots.numel();
+        const int32_t* sl = c.i32("slots", a[2], count);
+        void* kp = c.codes("k_pool", a[3], q8);
+        void* vp = c.codes("v_pool", a[4], q8);
+        const float* sc = c.scales(a[5], q8);
+        int64_t ks, vs;
+        void* k = c.rows("k_out", a[6], c.d->hkv, count, ks);
+        void* v = c.rows("v_out", a[7], c.d->hkv, count, vs);
+        int32_t* st = c.i32("status", a[8], 1);
+        Unlocked u;
+        return g_read_q8(c.d, q8, count, sl, kp, vp, sc, k, ks, v, vs, st, c.stream);
+    });
+}
+
+PyObject* py_decode_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 17, g_decode_q8 != nullptr, [&] {
+        const Call c(a[0], a[16]);
+        const auto* q8 = as_ptr<const rx_q8_desc>(a[1]);
+        const int32_t batch = as_i32(a[2]), longest = as_i32(a[12]);
+        int64_t ts = 0, unused;
+        if (a[15] != Py_None) ts = as_i64(a[15]);
+        else c.table("req_to_token", a[4], unused, ts);
+        const void* q = c.whole_rows("q", a[3], batch);
+        const int32_t* rt = c.i32("req_to_token", a[4], batch * ts);
+        const int32_t* len = c.i32("kv_lens", a[5], batch);
+        const auto* grp = a[6] == Py_None ? nullptr : as_ptr<const rx_shared_groups>(a[6]);
+        const void* kp = c.codes("k_pool", a[7], q8);
+        const void* vp = c.codes("v_pool", a[8], q8);
+        const float* sc = c.scales(a[9], q8);
+        void* out = c.whole_rows("out", a[10], batch);
+        float* lse = c.array<float>("lse", a[11], at::kFloat, (int64_t)batch * c.d->hq);
+        size_t bytes;
+        void* ws = c.room(a[13], bytes);
+        int32_t* st = c.i32("status", a[14], 1);
+        Unlocked u;
+        return g_decode_q8(c.d, q8, batch, q, rt, ts, len, grp, kp, vp, sc, out, lse, longest, ws, bytes, st, c.stream);
+    });
+}
+
+PyObject* py_extend_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 18, g_extend_q8 != nullptr, [&] {
+        const Call c(a[0], a[17]);
+        const auto* q8 = as_ptr<const rx_q8_desc>(a[1]);
+        const int32_t batch = as_i32(a[2]), rows = as_i32(a[12]), longest = as_i32(a[13]);
+        const int64_t ts = as_i64(a[16]);
+        int64_t have;
+        const void* q = c.whole_rows("q", a[3], 0, &have);
+        const int64_t* qi = c.i64("qo_indptr", a[4], batch + 1ll);
+        const int32_t* pl = c.i32("prefix_lens", a[5], batch);
+        const int32_t* rt = c.i32("req_to_token", a[6], batch * ts);
+        const void* kp = c.codes("k_pool", a[7], q8);
+        const void* vp = c.codes("v_pool", a[8], q8);
+        const float* sc = c.scales(a[9], q8);
+        void* out = c.whole_rows("out", a[10], have);
+        float* lse = c.array<float>("lse", a[11], at::kFloat, have * c.d->hq);
+        size_t bytes;
+        void* ws = c.room(a[14], bytes);
+        int32_t* st = c.i32("status", a[15], 1);
+        Unlocked u;
+        return g_extend_q8(c.d, q8, batch, q, qi, pl, rt, ts, kp, vp, sc, out, lse, rows, longest, ws, bytes, st, c.stream);
+    });
+}
+
 PyObject* py_bind(PyObject*, PyObject* m) {
-    void* f[4];
-    const char* names[4] = {"kv_pool_write_rope", "kv_pool_copy", "kv_pool_fork", "prompt_attention"};
-    for (int i = 0; i < 4; ++i) {
+    constexpr int N = 8;
+    void* f[N];
+    const char* names[N] = {"kv_pool_write_rope", "kv_pool_copy",    "kv_pool_fork",        "prompt_attention",
+                            "kv_pool_write_q8",   "kv_pool_read_q8", "decode_attention_q8", "prefix_extend_attention_q8"};
+    for (int i = 0; i < N; ++i) {
         PyObject* o = PyMapping_GetItemString(m, names[i]);
         if (!o) return nullptr;
         f[i] = PyLong_AsVoidPtr(o);
@@ -262,6 +398,10 @@ PyObject* py_bind(PyObject*, PyObject* m) {
     g_copy = (decltype(g_copy))f[1];
     g_fork = (decltype(g_fork))f[2];
     g_prompt = (decltype(g_prompt))f[3];
+    g_write_q8 = (decltype(g_write_q8))f[4];
+    g_read_q8 = (decltype(g_read_q8))f[5];
+    g_decode_q8 = (decltype(g_decode_q8))f[6];
+    g_extend_q8 = (decltype(g_extend_q8))f[7];
     Py_RETURN_NONE;
 }
 
@@ -270,6 +410,10 @@ PyMethodDef methods[] = {{"bind", py_bind, METH_O, "Bind the library's functions
                          {"kv_pool_copy", (PyCFunction)(void (*)())py_copy, METH_FASTCALL, ""},
                          {"kv_pool_fork", (PyCFunction)(void (*)())py_fork, METH_FASTCALL, ""},
                          {"prompt_attention", (PyCFunction)(void (*)())py_prompt, METH_FASTCALL, ""},
+                         {"kv_pool_write_q8", (PyCFunction)(void (*)())py_write_q8, METH_FASTCALL, ""},
+                         {"kv_pool_read_q8", (PyCFunction)(void (*)())py_read_q8, METH_FASTCALL, ""},
+                         {"decode_attention_q8", (PyCFunction)(void (*)())py_decode_q8, METH_FASTCALL, ""},
+                         {"prefix_extend_attention_q8", (PyCFunction)(void (*)())py_extend_q8, METH_FASTCALL, ""},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_rxops", "Marshalling of the row, page and prompt operators.", -1, methods,

@@ -1,0 +1,771 @@
+"""KV pools held in 8 bits: rows quantised and read back, decode and extend attention over codes, against plain
+64-bit definitions.
+
+The pages have no 8-bit cache; these stand beside kv_pool_write and the attention entry points.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from prefix_cached_kv_radix_gb300 import api
+
+api.load()
+gpu = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+INT8, E4M3 = api.RX_Q8_INT8, api.RX_Q8_E4M3
+TYPE = {INT8: torch.int8, E4M3: torch.float8_e4m3fn}
+TOP = {INT8: 127.0, E4M3: 448.0}
+A = 0x1000        # stands for an aligned device address in calls that are refused before any launch
+
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda")
+
+
+def desc_of(dt, hq, hkv, d, slots=64, scale=None):
+    return api.make_desc(api.RX_F32 if dt == F else api.RX_BF16, hq, hkv, d, slots, 1 / math.sqrt(d) if scale is None else scale)
+
+
+def i32(v, dev):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=dev)
+
+
+def i64(v, dev):
+    return torch.tensor(np.asarray(v), dtype=torch.int64, device=dev)
+
+
+def indptr(lens, dev, start=0):
+    return i64(np.concatenate([[0], np.cumsum(lens)]) + start, dev)
+
+
+# ============================================================================ definitions, in 64 bits
+def scales_of(x, fmt):
+    """The write's scales of rows x [..., d]."""
+    a = x.double().abs().amax(-1)
+    if fmt == INT8:
+        s = (a / 127.0).float().double().clamp(min=2.0 ** -126)
+    else:
+        s = torch.full_like(a, 2.0 ** -126)
+        for e in range(-126, 121):                # the first power of two that is large enough
+            s = torch.where(448.0 * s < a, torch.full_like(a, 2.0 ** (e + 1)), s)
+    return torch.where(a.isfinite(), s, torch.full_like(a, math.nan))
+
+
+def codes_of(x, s, fmt):
+    y = x.double() / s.double()[..., None]
+    if fmt == INT8:
+        return torch.where(y.isnan(), torch.zeros_like(y), y).clamp(-127, 127).round()
+    y = torch.where(s.isnan()[..., None], torch.zeros_like(y), y).clamp(-448, 448)
+    power = torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))).long() - 3
+    step = ((power + 1023) << 52).view(torch.float64)        # 2 ** power, exactly
+    return (y / step).round() * step
+
+
+def as_codes(values, fmt):
+    return values.to(torch.int8) if fmt == INT8 else values.float().to(torch.float8_e4m3fn)
+
+
+def bytes_of(t):
+    return t.view(torch.uint8)
+
+
+class Cache:
+    """Pools of codes with every slot filled, made here and not by the write."""
+
+    def __init__(self, dev, fmt, slots, hkv, d, block=1, seed=0, size=1.0):
+        g = torch.Generator(device=dev).manual_seed(seed)
+        self.q8, self.fmt, self.block = api.q8_desc(fmt, block, block > 1), fmt, block
+        x = torch.randn(2, slots, hkv, d, generator=g, device=dev) * size
+        x *= torch.randn(2, slots, 1, 1, generator=g, device=dev).exp()
+        blocks = -(-slots // block)
+        if block == 1:
+            self.scales = scales_of(x, fmt).permute(1, 2, 0).float().contiguous()
+        else:
+            self.scales = (1 + torch.rand(blocks, hkv, 2, generator=g, device=dev)) * (4 * size / TOP[fmt])
+        per_slot = self.scales[torch.arange(slots, device=dev) // block]
+        self.k, self.v = (as_codes(codes_of(x[j], per_slot[:, :, j], fmt), fmt) for j in range(2))
+
+    def values(self, slots):
+        s = self.scales[slots.long() // self.block].double()
+        k, v = (bytes_of(p)[slots.long()].view(p.dtype).double() for p in (self.k, self.v))
+        return k * s[..., :1], v * s[..., 1:]
+
+
+def attend(q, k, v, scale, first):
+    """Rows q [n, hq, d], row i over keys 0 .. first + i of k, v [len, hkv, d], in 64 bits.  Returns the rows, their
+    log-sum-exp, sum_j p_j |v_j|, a bound of the 32-bit sums' error of a score, the largest p_j |v_ji| of a row times its
+    keys, and the largest |v_ji| times its keys."""
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    q = q.double().view(n, hkv, hq // hkv, d)
+    seen = torch.arange(k.shape[0], device=q.device)[None, :] <= first + torch.arange(n, device=q.device)[:, None]
+    if k.shape[0] == 0 or n == 0:
+        z = torch.zeros(n, hq, d, dtype=torch.float64, device=q.device)
+        return z, torch.full((n, hq), -math.inf, dtype=torch.float64, device=q.device), z, z[..., 0], z[..., 0], z[..., 0]
+    s = torch.einsum("nhgd,khd->nhgk", q, k) * scale
+    s = s.masked_fill(~seen[:, None, None, :], -math.inf)
+    mag = torch.einsum("nhgd,khd->nhgk", q.abs(), k.abs()) * scale
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse.clamp(min=-1e300)[..., None])
+    o, a = torch.einsum("nhgk,khd->nhgd", p, v), torch.einsum("nhgk,khd->nhgd", p, v.abs())
+    # d products summed in 32 bits with a few roundings of the scaled score after them
+    err = (d + 8) * 2.0 ** -23 * mag.masked_fill(~seen[:, None, None, :], 0).amax(-1)
+    top = v.abs().amax(-1).t()[None, :, None, :]
+    weighed = (p * top).masked_fill(~seen[:, None, None, :], 0).amax(-1) * k.shape[0]
+    largest = top.expand(p.shape).masked_fill(~seen[:, None, None, :], 0).amax(-1) * k.shape[0]
+    return tuple(t.reshape(n, hq, *t.shape[3:]) for t in (o, lse, a, err, weighed, largest))
+
+
+def agree(out, lse, want, dt):
+    """out is off by its own rounding, the rounding of the weighted probabilities (bf16 rows: 2^-8 of each at most) and
+    the scores' 32-bit errors, which change a probability by that much of itself, twice (its own and the sum's).  A weighted
+    probability p_j vs_j held in 16 bits with 5 of exponent next to the row's largest has steps of 2^-24 of that at least,
+    half of one times a code at most (two such parts, the second 2^-11 as large: 2^-35); the largest code of a
+    row here is at least half the largest there is.  And p_j below 2^-126 is zero in 32 bits."""
+    o, z, a, err, weighed, largest = want
+    half, part, step = (2.0 ** -8, 2.0 ** -8, 2.0 ** -24) if dt == BF else (2.0 ** -24, 2.0 ** -20, 2.0 ** -35)
+    tol = half * o.abs() + (part + 2 * err[..., None] + 2.0 ** -19) * a * (1 + half)
+    tol += (weighed * step + largest * 2.0 ** -126)[..., None] + 1e-30
+    bad = (out.double() - o).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((out.double() - o).abs() / tol).max()))
+    if lse is not None:
+        empty = z.isinf()
+        assert torch.equal(lse.double()[empty], z[empty])
+        gap = (lse.double() - z).abs()[~empty]
+        assert (gap <= err[~empty] + 2.0 ** -18 * (1 + z.abs()[~empty])).all(), float(gap.max())
+
+
+# ============================================================================ refusals (CPU)
+def refused(fn, *args):
+    rc = getattr(api.load(), fn)(*args)
+    assert rc == api.RX_EINVAL, (fn, rc)
+    assert fn in api.load().rx_last_error().decode()
+
+
+BAD_CACHES = (api.rx_q8_desc(2, 1, 0), api.rx_q8_desc(-1, 1, 0), api.rx_q8_desc(0, 0, 1), api.rx_q8_desc(0, 3, 1),
+              api.rx_q8_desc(0, 2, 0), api.rx_q8_desc(0, -4, 1), api.rx_q8_desc(0, 1, 2), api.rx_q8_desc(0, -(1 << 31), 1))
+BAD_SHAPES = (desc_of(BF, 4, 0, 64), desc_of(BF, 4, 2, 96), desc_of(BF, 4, 2, 64, slots=0), desc_of(BF, 4, 2, 64, slots=1 << 31),
+              api.make_desc(7, 4, 2, 64, 4, 1.0))
+BAD_HEADS = (desc_of(BF, 4, 3, 64), desc_of(BF, 0, 2, 64), desc_of(BF, -4, 2, 64))
+
+
+def test_write_q8_refuses():
+    def call(desc=None, q8=None, batch=1, ind=A, pi=A, ns=A, k=A, ks=128, v=A, vs=128, kp=A, vp=A, sc=A, r2t=A, stride=8, total=4):
+        refused("kv_pool_write_q8", ctypes.byref(desc or desc_of(BF, 4, 2, 64)), ctypes.byref(q8 or api.q8_desc(INT8)), batch, A, pi,
+                ns, ind, k, ks, v, vs, kp, vp, sc, r2t, stride, total, None, None)
+    for bad in BAD_CACHES:
+        call(q8=bad)
+    for bad in BAD_SHAPES:
+        call(desc=bad)
+    for kw in (dict(batch=-1), dict(total=-1), dict(total=1 << 31), dict(stride=-1), dict(ind=None), dict(pi=None), dict(ns=None),
+               dict(k=None), dict(v=None), dict(kp=None), dict(vp=None), dict(sc=None), dict(k=A + 8), dict(v=A + 2), dict(ks=120),
+               dict(vs=130), dict(kp=A + 8), dict(vp=A + 1), dict(sc=A + 4)):
+        call(**kw)
+
+
+def test_read_q8_refuses():
+    def call(desc=None, q8=None, n=4, sl=A, kp=A, vp=A, sc=A, k=A, ks=128, v=A, vs=128):
+        refused("kv_pool_read_q8", ctypes.byref(desc or desc_of(BF, 4, 2, 64)), ctypes.byref(q8 or api.q8_desc(INT8)), n, sl, kp, vp, sc,
+                k, ks, v, vs, None, None)
+    for bad in BAD_CACHES:
+        call(q8=bad)
+    for bad in BAD_SHAPES:
+        call(desc=bad)
+    for kw in (dict(n=-1), dict(n=1 << 31), dict(sl=None), dict(kp=None), dict(vp=None), dict(sc=None), dict(k=A + 8), dict(v=A + 2),
+               dict(ks=120), dict(vs=130), dict(kp=A + 8), dict(sc=A + 4)):
+        call(**kw)
+
+
+def test_decode_q8_refuses():
+    def call(desc=None, q8=None, batch=1, q=A, r2t=A, stride=8, lens=A, kp=A, vp=A, sc=A, out=A, longest=8, ws=A, nbytes=1 << 40):
+        refused("decode_attention_q8", ctypes.byref(desc or desc_of(BF, 4, 2, 64)), ctypes.byref(q8 or api.q8_desc(INT8)), batch, q, r2t,
+                stride, lens, None, kp, vp, sc, out, None, longest, ws, nbytes, None, None)
+    for bad in BAD_CACHES:
+        call(q8=bad)
+    for bad in BAD_SHAPES + BAD_HEADS:
+        call(desc=bad)
+    for kw in (dict(batch=-1), dict(stride=-1), dict(longest=-1), dict(q=None), dict(r2t=None), dict(lens=None), dict(kp=None),
+               dict(vp=None), dict(sc=None), dict(out=None), dict(q=A + 8), dict(out=A + 4), dict(kp=A + 8), dict(sc=A + 4)):
+        call(**kw)
+
+
+def test_extend_q8_refuses():
+    def call(desc=None, q8=None, batch=1, q=A, ind=A, pre=A, r2t=A, stride=8, kp=A, vp=A, sc=A, out=A, rows=4, longest=8, ws=A,
+             nbytes=1 << 40):
+        refused("prefix_extend_attention_q8", ctypes.byref(desc or desc_of(BF, 4, 2, 64)), ctypes.byref(q8 or api.q8_desc(INT8)), batch,
+                q, ind, pre, r2t, stride, kp, vp, sc, out, None, rows, longest, ws, nbytes, None, None)
+    for bad in BAD_CACHES:
+        call(q8=bad)
+    for bad in BAD_SHAPES + BAD_HEADS:
+        call(desc=bad)
+    for kw in (dict(batch=-1), dict(stride=-1), dict(longest=-1), dict(rows=-1), dict(q=None), dict(ind=None), dict(pre=None),
+               dict(r2t=None), dict(kp=None), dict(vp=None), dict(sc=None), dict(out=None), dict(q=A + 8), dict(out=A + 4),
+               dict(vp=A + 8), dict(sc=A + 4)):
+        call(**kw)
+
+
+def test_nothing_to_do_is_no_error():
+    """No requests, no rows, no slots: fine, without a device."""
+    d, c = desc_of(BF, 4, 2, 64), api.q8_desc(E4M3)
+    lib, by = api.load(), ctypes.byref
+    assert lib.kv_pool_write_q8(by(d), by(c), 0, *[None] * 5, 0, None, 0, None, None, None, None, 0, 0, None, None) == api.RX_OK
+    assert lib.kv_pool_read_q8(by(d), by(c), 0, None, None, None, None, None, 0, None, 0, None, None) == api.RX_OK
+    assert lib.decode_attention_q8(by(d), by(c), 0, None, None, 0, None, None, None, None, None, None, None, 0, None, 0, None,
+                                   None) == api.RX_OK
+    assert lib.prefix_extend_attention_q8(by(d), by(c), 1, None, None, None, None, 0, None, None, None, None, None, 0, 0, None, 0,
+                                          None, None) == api.RX_OK
+
+
+# ============================================================================ writing
+def special_rows(x, fmt):
+    """Rows whose scales and codes are on a border: zeros, the smallest and largest numbers, halves between codes,
+    largest values that a power of two times 448 just holds or just does not."""
+    n = x.shape[0]
+    big = 3e38
+    rows = [torch.zeros_like(x[0, 0]), torch.full_like(x[0, 0], big), torch.full_like(x[0, 0], -big)]
+    d = x.shape[-1]
+    ramp = torch.arange(d, device=x.device, dtype=torch.float32)
+    rows.append((ramp - d // 2 + 0.5).clamp(-126.5, 126.5).index_fill(0, i64([0], x.device), 127.0).to(x.dtype))  # scale 1: halves
+    rows.append((ramp * 2.0 ** -9).index_fill(0, i64([1], x.device), 448.0).to(x.dtype))      # e4m3's smallest steps
+    rows.append((ramp * 2.0 ** -10).index_fill(0, i64([1], x.device), 448.0).to(x.dtype))     # and halves of them
+    for top in (448.0 * 2 ** 5, 450.0, 1.75 * 2 ** -20, 1.7578125 * 2 ** -20, 1e-37, 2.0 ** -126, 2.0 ** -133):
+        rows.append((torch.randn(d, device=x.device).clamp(-1, 1) * top).index_fill(0, i64([3], x.device), top).to(x.dtype))
+    for j, r in enumerate(rows[:n]):
+        x[j, 0] = r
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hkv,d,block,strided", [(1, 64, 1, False), (3, 128, 1, True), (12, 64, 1, True), (8, 128, 1, False),
+                                                 (2, 64, 4, True), (5, 128, 64, False), (2, 128, 1 << 30, False)])
+def test_write_q8(dev, fmt, dt, hkv, d, block, strided):
+    torch.manual_seed(hkv * d + block)
+    lens, pre = [1, 0, 37, 5, 200], [0, 3, 17, 0, 900]
+    n, slots, lead = sum(lens), 2600, 2
+    total = n + lead + 3                         # two rows before the batch, three behind it
+    wide = special_rows(torch.randn(total, 3 * hkv if strided else hkv, d, device=dev).to(dt), fmt)
+    x = special_rows(torch.randn(total, hkv, d, device=dev).to(dt), fmt)
+    k, v = (wide[:, hkv:2 * hkv], wide[:, :hkv]) if strided else (x, wide)
+    ids = torch.randperm(slots, device=dev).to(torch.int32)
+    new, old = ids[:total].contiguous(), ids[total:total + sum(pre)].contiguous()
+    c = api.q8_desc(fmt, block, block > 1)
+    kp, vp = (torch.full((slots, hkv, d), 0x55, dtype=torch.uint8, device=dev) for _ in range(2))
+    blocks = -(-slots // block)
+    if block > 1:
+        scales = (0.25 + torch.rand(blocks, hkv, 2, device=dev)) * (3.0 / TOP[fmt])
+        scales[0, 0] = 1.0                       # halves between codes
+    else:
+        scales = torch.full((blocks, hkv, 2), 7.0, device=dev)
+    was = scales.clone()
+    r2t = torch.full((len(lens), 1104), 99, dtype=torch.int32, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    desc = desc_of(dt, hkv, hkv, d, slots)
+    api.kv_pool_write_q8(desc, c, len(lens), old, indptr(pre, dev), new, indptr(lens, dev, lead), k, v, kp.view(TYPE[fmt]),
+                         vp.view(TYPE[fmt]), scales, r2t, total, st)
+    assert int(st) == 0
+    rows = slice(lead, lead + n)
+    at = new[rows].long()
+    for j, (name, y, pool) in enumerate((("k", k, kp), ("v", v, vp))):
+        s = was[at // block, :, j].double() if block > 1 else scales_of(y[rows], fmt)
+        if block == 1:
+            assert torch.equal(scales[at, :, j].double().nan_to_num(-1), s.nan_to_num(-1)), name
+        want = bytes_of(as_codes(codes_of(y[rows], s, fmt), fmt))
+        got = pool[at]
+        zero = (want & 0x7f) == 0                # a code of -0 is a zero as well
+        assert torch.equal(torch.where(zero, want & 0x7f, want), torch.where(zero, got & 0x7f, got)), name
+        rest = torch.ones(slots, dtype=torch.bool, device=dev)
+        rest[at] = False
+        assert (pool[rest] == 0x55).all()
+    if block > 1:
+        assert torch.equal(scales, was)
+    else:
+        assert (scales[rest] == 7.0).all()
+    qo, po = np.concatenate([[0], np.cumsum(lens)]) + lead, np.concatenate([[0], np.cumsum(pre)])
+    for b in range(len(lens)):
+        want = torch.cat([old[po[b]:po[b + 1]], new[qo[b]:qo[b + 1]]])
+        assert torch.equal(r2t[b, :len(want)], want) and (r2t[b, len(want):] == -1).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_write_q8_not_finite(dev, fmt, dt):
+    """An infinity or a NaN: that token, head and pool reads as NaN; its neighbours are what they are."""
+    x = torch.randn(4, 3, 64, device=dev).to(dt)
+    y = x.clone()
+    y[1, 2, 63], y[2, 0, 5], y[3, 1, 0] = math.inf, math.nan, -math.inf
+    c, desc = api.q8_desc(fmt), desc_of(dt, 3, 3, 64, 8)
+    pools = [torch.zeros(8, 3, 64, dtype=torch.int8, device=dev).view(TYPE[fmt]) for _ in range(2)]
+    scales, st = torch.zeros(8, 3, 2, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    new = i32([6, 1, 3, 0], dev)
+    api.kv_pool_write_q8(desc, c, 1, None, i64([0, 0], dev), new, i64([0, 4], dev), y, x, *pools, scales, None, 4, st)
+    out = [torch.empty_like(x) for _ in range(2)]
+    api.kv_pool_read_q8(desc, c, new, *pools, scales, *out, st)
+    assert int(st) == 0
+    bad = torch.zeros(4, 3, dtype=torch.bool, device=dev)
+    bad[1, 2] = bad[2, 0] = bad[3, 1] = True
+    assert out[0][bad].isnan().all() and out[0][~bad].isfinite().all() and out[1].isfinite().all()
+    assert (bytes_of(pools[0])[new.long()][bad] == 0).all()
+    if fmt == E4M3:                              # a step is at most an eighth of the value, or 2^-9 of the scale
+        gap = (out[1].double() - x.double()).abs()
+        assert (gap <= x.double().abs() / 16 + scales[new.long(), :, 1:].double() * 2.0 ** -10).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+def test_write_q8_fixed_takes_any_value(dev, fmt):
+    """Given scales: values past the largest code are cut to it; a NaN is the format's."""
+    x = torch.tensor([math.inf, -math.inf, math.nan, 1e38, -1e38, 1.0, -1.0, 0.0] * 8, device=dev).view(1, 1, 64)
+    c, desc = api.q8_desc(fmt, 2, True), desc_of(F, 1, 1, 64, 2)
+    pools = [torch.zeros(2, 1, 64, dtype=torch.int8, device=dev).view(TYPE[fmt]) for _ in range(2)]
+    scales, st = torch.full((1, 1, 2), 0.5, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    api.kv_pool_write_q8(desc, c, 1, None, None, i32([1], dev), i64([0, 1], dev), x, x, *pools, scales, None, 1, st)
+    t = TOP[fmt]
+    want = torch.tensor([t, -t, 0.0 if fmt == INT8 else math.nan, t, -t, 2.0, -2.0, 0.0] * 8, device=dev)
+    for p in pools:
+        assert torch.equal(p[1, 0].float().nan_to_num(7.0), want.nan_to_num(7.0))
+        assert (bytes_of(p)[0] == 0).all()
+
+
+@gpu
+def test_write_q8_bad_slots_and_lengths(dev):
+    """A bad slot leaves its row out and the others in; a batch longer than its rows is reported."""
+    x = torch.randn(4, 2, 64, device=dev)
+    c, desc = api.q8_desc(INT8), desc_of(F, 2, 2, 64, 8)
+    for new, qo, code, written in (([1, 8, 2, -1], [0, 4], api.RX_DEV_BAD_SLOT, [1, 2]),
+                                   ([1, 4, 2, 3], [0, 9], api.RX_DEV_BAD_LENGTH, [1, 4, 2, 3]),
+                                   ([1, 4, 2, 3], [-2, 2], api.RX_DEV_BAD_LENGTH, [1, 4]),
+                                   ([1, 4, 2, 3], [3, 1], api.RX_DEV_BAD_LENGTH, [])):
+        pools = [torch.zeros(8, 2, 64, dtype=torch.int8, device=dev) for _ in range(2)]
+        scales, st = torch.zeros(8, 2, 2, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+        api.kv_pool_write_q8(desc, c, 1, None, i64([0, 0], dev), i32(new, dev), i64(qo, dev), x, x, *pools, scales, None, 4, st)
+        assert int(st) == code
+        touched = (scales != 0).flatten(1).any(1).nonzero().flatten().tolist()
+        assert sorted(touched) == sorted(written)
+
+
+# ============================================================================ reading
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hkv,d,block,n", [(1, 64, 1, 1), (3, 128, 1, 77), (12, 64, 16, 700), (8, 128, 1, 1025), (2, 64, 1 << 30, 9)])
+def test_read_q8(dev, fmt, dt, hkv, d, block, n):
+    slots = n + 13
+    cache = Cache(dev, fmt, slots, hkv, d, block, seed=n)
+    if fmt == INT8:
+        cache.k[0, 0, 0] = -128                  # a code that the write does not make
+    else:
+        bytes_of(cache.k)[0, 0, 0] = 0x7f        # e4m3's NaN
+    at = torch.randint(0, slots, (n,), device=dev, dtype=torch.int32)
+    at[0] = 0
+    wide = torch.full((n, 2 * hkv + 1, d), 3.0, dtype=dt, device=dev)
+    k, v = wide[:, :hkv], wide[:, hkv + 1:]
+    desc, st = desc_of(dt, hkv, hkv, d, slots), torch.zeros(1, dtype=torch.int32, device=dev)
+    api.kv_pool_read_q8(desc, cache.q8, at, cache.k, cache.v, cache.scales, k, v, st)
+    assert int(st) == 0
+    s = cache.scales[at.long() // block]
+    for j, (got, pool) in enumerate(((k, cache.k), (v, cache.v))):
+        want = (bytes_of(pool)[at.long()].view(pool.dtype).float() * s[:, :, j:j + 1]).to(dt)
+        assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+    assert (wide[:, hkv] == 3.0).all()
+    only = torch.empty(n, hkv, d, dtype=dt, device=dev)
+    api.kv_pool_read_q8(desc, cache.q8, at, None, cache.v, cache.scales, None, only, st)
+    assert torch.equal(only, v)
+    at[n // 2] = slots
+    only.fill_(5.0)
+    api.kv_pool_read_q8(desc, cache.q8, at, cache.k, None, cache.scales, only, None, st)
+    assert int(st) == api.RX_DEV_BAD_SLOT
+    keep = torch.arange(n, device=dev) != n // 2
+    assert (only[~keep] == 5.0).all() and torch.equal(only[keep].nan_to_num(7.0), k[keep].nan_to_num(7.0))
+
+
+# ============================================================================ decode
+def table_of(lens, stride, slots, dev, seed=0):
+    """Slot tables of requests that share nothing; unused entries -1.  Returns it and the slots in use."""
+    ids = torch.randperm(slots, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+    t, at = torch.full((max(len(lens), 1), stride), -1, dtype=torch.int32), 0
+    for b, n in enumerate(lens):
+        t[b, :n] = ids[at:at + n]
+        at += n
+    return t.to(dev), ids[:at].long().to(dev)
+
+
+def decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=None, scale=None, q=None, longest=None):
+    b = len(lens)
+    desc = desc_of(dt, hq, hkv, d, cache.k.shape[0], scale)
+    if q is None:
+        q = torch.randn(b, hq, d, generator=torch.Generator(device=dev).manual_seed(b + hq), device=dev).to(dt)
+    out, lse = torch.full_like(q, 9.0), torch.full((b, hq), 9.0, device=dev)
+    longest = max(max(lens), 1) if longest is None else longest
+    nbytes = api.decode_q8_workspace_bytes(desc, b, longest, groups)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    api.decode_attention_q8(desc, cache.q8, b, q, r2t, i32(lens, dev), cache.k, cache.v, cache.scales, out, lse, longest, ws, st,
+                            groups=groups)
+    return q, out, lse, int(st)
+
+
+def poison(cache, used):
+    """Every slot that is not in use holds NaN: a scale of NaN (block 1)."""
+    if cache.block == 1:
+        rest = torch.ones(cache.k.shape[0], dtype=torch.bool, device=used.device)
+        rest[used] = False
+        cache.scales[rest] = math.nan
+
+
+HEADS = [(4, 4, 64), (12, 12, 64), (8, 2, 128), (6, 2, 64), (16, 2, 128), (7, 1, 128), (12, 1, 64), (32, 2, 128)]
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_decode_q8(dev, fmt, dt, hq, hkv, d):
+    lens = [1, 0, 2, 15, 16, 17, 63, 64, 65, 129, 300, 1, 777]
+    slots = sum(lens) + 40
+    r2t, used = table_of(lens, 784, slots, dev)
+    cache = Cache(dev, fmt, slots, hkv, d, seed=hq)
+    poison(cache, used)
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t)
+    assert st == 0
+    for b, n in enumerate(lens):
+        k, v = cache.values(r2t[b, :n])
+        agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), dt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("lens,block", [([5000], 1), ([20011, 3], 64), ([1025, 1024, 1023, 2049], 16), ([70001], 1 << 30)])
+def test_decode_q8_long(dev, fmt, dt, lens, block):
+    hq, hkv, d = 8, 2, 128
+    slots = sum(lens) + 5
+    r2t, used = table_of(lens, (max(lens) + 7) // 8 * 8, slots, dev)
+    cache = Cache(dev, fmt, slots, hkv, d, block, seed=1)
+    poison(cache, used)
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t)
+    assert st == 0
+    for b, n in enumerate(lens):
+        k, v = cache.values(r2t[b, :n])
+        agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), dt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_decode_q8_scales_far_apart(dev, fmt, dt):
+    """Value rows of very different sizes, zeros among them, keys that say much and nothing: the sums keep what
+    is attended, whatever the sizes of the rest."""
+    hq, hkv, d, n = 8, 2, 64, 200
+    cache = Cache(dev, fmt, n, hkv, d, seed=3)
+    r2t = torch.arange(n, dtype=torch.int32, device=dev)[None]
+    cache.scales[:, :, 1] *= (torch.randn(n, hkv, device=dev) * 12).exp2()
+    cache.scales[3, :, 1], cache.scales[5, :, 1] = 1e30, 2.0 ** -126
+    bytes_of(cache.v)[7] = 0
+    cache.scales[7, :, 1] = 2.0 ** -126
+    cache.scales[9, :, 0], cache.scales[7, :, 0] = 0.0, 4.0
+    for size in (0.1, 1.0, 30.0):
+        q = (torch.randn(1, hq, d, device=dev) * size).to(dt)
+        q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, [n], r2t, q=q)
+        k, v = cache.values(r2t[0])
+        agree(out, lse, attend(q, k, v, 1 / math.sqrt(d), n - 1), dt)
+        far = cache.scales.clone()               # all but an unattended huge row
+        cache.scales[3, :, 1] = 1.0
+        q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, [n], r2t, q=q)
+        k, v = cache.values(r2t[0])
+        agree(out, lse, attend(q, k, v, 1 / math.sqrt(d), n - 1), dt)
+        cache.scales.copy_(far)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+def test_decode_q8_queries_far_apart(dev, dt):
+    """Queries from far below to far above one in a batch, zeros among them."""
+    hq, hkv, d = 4, 2, 128
+    lens = [33] * 8
+    r2t, _ = table_of(lens, 40, 300, dev)
+    cache = Cache(dev, INT8, 300, hkv, d, seed=5)
+    q = torch.randn(8, hq, d, device=dev)
+    q *= torch.tensor([1e-38, 1e-20, 1e-6, 1.0, 100.0, 1e4, 0.0, 1.0], device=dev)[:, None, None]
+    q[7, 0, 1:] = 0.0
+    q[7, 1, ::2] *= 1e-5
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t, q=q.to(dt))
+    assert st == 0
+    for b in range(8):
+        k, v = cache.values(r2t[b, :33])
+        agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), 32), dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+def test_decode_q8_bad_slots_and_lengths(dev, dt):
+    """Keys at bad slots are left out; requests with bad lengths are left as they were."""
+    hq, hkv, d = 8, 2, 64
+    lens = [40, 3, 70, 20, 5, 9]
+    r2t, _ = table_of(lens, 72, 200, dev)
+    cache = Cache(dev, E4M3, 200, hkv, d, seed=2)
+    r2t[0, 7], r2t[0, 39], r2t[1, :3] = -1, 200, -5
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t)
+    assert st == api.RX_DEV_BAD_SLOT
+    for b, n in enumerate(lens):
+        ok = r2t[b, :n]
+        ok = ok[(ok >= 0) & (ok < 200)]
+        k, v = cache.values(ok)
+        agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), len(ok) - 1), dt)
+    for wrong, longest in ((-1, 70), (73, 100), (71, 70)):
+        q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, [40, wrong, 5], r2t[[0, 1, 4]].contiguous(), longest=longest)
+        assert st in (api.RX_DEV_BAD_LENGTH, api.RX_DEV_BAD_SLOT)
+        assert (out[1] == 9.0).all() and (lse[1] == 9.0).all() and (out[2] != 9.0).any()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_decode_q8_groups(dev, fmt, dt):
+    """Requests that share leading slots give what they give alone."""
+    hq, hkv, d = 8, 2, 128
+    lens = [300, 411, 301, 90, 640, 300, 17]
+    slots = 3000
+    r2t, _ = table_of(lens, 648, slots, dev)
+    r2t[[1, 2, 5], :300] = r2t[0, :300].clone()
+    r2t[4, :77] = r2t[3, :77].clone()
+    cache = Cache(dev, fmt, slots, hkv, d, seed=4)
+    g = api.shared_groups_struct(2, 4, i32([0, 4, 6], dev), i32([0, 1, 2, 5, 4, 3], dev), i32([300, 77], dev), 300)
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=g)
+    assert st == 0
+    for b, n in enumerate(lens):
+        k, v = cache.values(r2t[b, :n])
+        agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), dt)
+
+
+# ============================================================================ extend
+def extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t, scale=None, lead=0, longest=None, q=None):
+    n = sum(lens)
+    desc = desc_of(dt, hq, hkv, d, cache.k.shape[0], scale)
+    if q is None:
+        q = torch.randn(lead + n + 2, hq, d, generator=torch.Generator(device=dev).manual_seed(n + hq), device=dev).to(dt)
+    out, lse = torch.full_like(q, 9.0), torch.full((q.shape[0], hq), 9.0, device=dev)
+    longest = r2t.shape[1] if longest is None else longest
+    nbytes = api.extend_q8_workspace_bytes(desc, len(lens), max(lens), longest)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    api.prefix_extend_attention_q8(desc, cache.q8, len(lens), q, indptr(lens, dev, lead), i32(pre, dev), r2t, cache.k, cache.v,
+                                   cache.scales, out, lse, max(lens), ws, st, max_kv_len=longest)
+    assert (out[:lead] == 9.0).all() and (out[lead + n:] == 9.0).all() and (lse[lead + n:] == 9.0).all()
+    return q, out, lse, int(st)
+
+
+def extend_agrees(cache, dt, d, lens, pre, r2t, q, out, lse, lead=0):
+    at = lead
+    for b, (n, p) in enumerate(zip(lens, pre)):
+        k, v = cache.values(r2t[b, :n + p])
+        agree(out[at:at + n], lse[at:at + n], attend(q[at:at + n], k, v, 1 / math.sqrt(d), p), dt)
+        at += n
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_extend_q8(dev, fmt, dt, hq, hkv, d):
+    lens, pre = [1, 3, 0, 17, 64, 129, 5, 2], [0, 0, 50, 100, 31, 127, 700, 128]
+    total = [a + b for a, b in zip(lens, pre)]
+    slots = sum(total) + 33
+    r2t, used = table_of(total, 712, slots, dev)
+    cache = Cache(dev, fmt, slots, hkv, d, seed=hq)
+    poison(cache, used)
+    q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t, lead=3)
+    assert st == 0
+    extend_agrees(cache, dt, d, lens, pre, r2t, q, out, lse, lead=3)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("lens,pre,block", [([1], [9000], 1), ([7], [20000], 16), ([300], [1500], 1), ([2, 33], [4000, 130], 64),
+                                            ([513], [0], 1 << 30)])
+def test_extend_q8_long(dev, fmt, dt, lens, pre, block):
+    hq, hkv, d = 8, 2, 128
+    total = [a + b for a, b in zip(lens, pre)]
+    slots = sum(total) + 33
+    r2t, used = table_of(total, (max(total) + 7) // 8 * 8, slots, dev)
+    cache = Cache(dev, fmt, slots, hkv, d, block, seed=7)
+    poison(cache, used)
+    q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t)
+    assert st == 0
+    extend_agrees(cache, dt, d, lens, pre, r2t, q, out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_extend_q8_later_rows_do_not_reach_earlier_ones(dev, fmt, dt):
+    """A new token whose key or value is not finite: the rows before it are what they are without it."""
+    hq, hkv, d = 8, 2, 64
+    r2t, _ = table_of([200], 200, 210, dev)
+    cache = Cache(dev, fmt, 210, hkv, d, seed=9)
+    cache.scales[r2t[0, 150].long()] = math.nan
+    cache.scales[r2t[0, 180].long()] = math.inf
+    q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, [150], [50], r2t)
+    assert st == 0 and out[:100].isfinite().all() and out[100:150].isnan().all()
+    k, v = cache.values(r2t[0, :150])
+    agree(out[:100], lse[:100], attend(q[:100], k, v, 1 / math.sqrt(d), 50), dt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_extend_q8_scales_far_apart(dev, fmt, dt):
+    hq, hkv, d, n = 4, 2, 64, 140
+    cache = Cache(dev, fmt, 300, hkv, d, seed=3)
+    r2t, _ = table_of([290], 296, 300, dev)
+    cache.scales[:, :, 1] *= (torch.randn(300, hkv, device=dev) * 12).exp2()
+    cache.scales[r2t[0, 3].long(), :, 1] = 1e30
+    bytes_of(cache.v)[r2t[0, 7].long()] = 0
+    cache.scales[r2t[0, 7].long(), :, 1] = 2.0 ** -126
+    cache.scales[r2t[0, 200].long(), :, 0] = 0.0
+    q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, [n], [150], r2t)
+    assert st == 0
+    extend_agrees(cache, dt, d, [n], [150], r2t, q, out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+def test_extend_q8_bad_slots_and_lengths(dev, dt):
+    hq, hkv, d = 8, 2, 64
+    lens, pre = [20, 3, 40], [30, 0, 130]
+    r2t, _ = table_of([50, 3, 170], 176, 300, dev)
+    cache = Cache(dev, INT8, 300, hkv, d, seed=2)
+    r2t[0, 7], r2t[0, 49], r2t[1, 0], r2t[2, 131] = -1, 300, 1 << 30, -7
+    q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t)
+    assert st == api.RX_DEV_BAD_SLOT
+    at = 0
+    for b, (n, p) in enumerate(zip(lens, pre)):
+        for i in range(n):
+            ok = r2t[b, :p + i + 1]
+            ok = ok[(ok >= 0) & (ok < 300)]
+            k, v = cache.values(ok)
+            agree(out[at:at + 1], lse[at:at + 1], attend(q[at:at + 1], k, v, 1 / math.sqrt(d), len(ok) - 1), dt)
+            at += 1
+    good, _ = table_of([50, 3, 170], 176, 300, dev)
+    for pre, longest in (([30, -1, 130], 176), ([30, 175, 130], 176), ([30, 100, 130], 102)):
+        q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, good, longest=longest)
+        assert st == api.RX_DEV_BAD_LENGTH
+        assert (out[20:23] == 9.0).all()
+        extend_agrees(cache, dt, d, [20], [30], good, q, out, lse)
+
+
+# ============================================================================ together
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("captured", [False, True])
+def test_serving_steps_q8(dev, fmt, dt, captured):
+    """Prompts written and extended, then tokens decoded one by one, as a serving loop runs them; eager and as a
+    captured graph whose inputs change between replays; on a stream of its own."""
+    hq, hkv, d, slots, b = 8, 2, 64, 600, 3
+    torch.manual_seed(11)
+    cache = Cache(dev, fmt, slots, hkv, d, seed=1)
+    ids = torch.randperm(slots, device=dev).to(torch.int32)
+    lens = [60, 1, 130]
+    stride = 144
+    desc, c = desc_of(dt, hq, hkv, d, slots), cache.q8
+    r2t = torch.full((b, stride), -1, dtype=torch.int32, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    n = sum(lens)
+    x = torch.randn(n, hq + 2 * hkv, d, device=dev).to(dt)
+    q, k, v = x[:, :hq].contiguous(), x[:, hq:hq + hkv], x[:, hq + hkv:]
+    out, lse = torch.empty_like(q), torch.empty(n, hq, device=dev)
+    ew = torch.empty(max(api.extend_q8_workspace_bytes(desc, b, 130, stride), 1), dtype=torch.uint8, device=dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        api.kv_pool_write_q8(desc, c, b, None, i64([0] * 4, dev), ids[:n].contiguous(), indptr(lens, dev), k, v, cache.k, cache.v,
+                             cache.scales, r2t, n, st)
+        api.prefix_extend_attention_q8(desc, c, b, q, indptr(lens, dev), i32([0] * 3, dev), r2t, cache.k, cache.v, cache.scales, out,
+                                       lse, 130, ew, st)
+    side.synchronize()
+    extend_agrees(cache, dt, d, lens, [0] * 3, r2t, q, out, lse)
+    # the prompts' values are what was written
+    at = ids[:n].long()
+    want = codes_of(v, scales_of(v, fmt), fmt) * scales_of(v, fmt)[..., None]
+    assert torch.equal(cache.values(at)[1], want)
+
+    steps = 4
+    kv_lens, qd = i32(lens, dev), torch.empty(b, hq, d, dtype=dt, device=dev)
+    kn, vn = (torch.empty(b, hkv, d, dtype=dt, device=dev) for _ in range(2))
+    new, old, oi = (torch.zeros(b, dtype=torch.int32, device=dev), torch.zeros(stride * b, dtype=torch.int32, device=dev),
+                    torch.zeros(b + 1, dtype=torch.int64, device=dev))
+    od, ld = torch.empty_like(qd), torch.empty(b, hq, device=dev)
+    longest = max(lens) + steps
+    dw = torch.empty(max(api.decode_q8_workspace_bytes(desc, b, longest), 1), dtype=torch.uint8, device=dev)
+    qi = indptr([1] * b, dev)
+
+    def step():
+        api.kv_pool_write_q8(desc, c, b, old, oi, new, qi, kn, vn, cache.k, cache.v, cache.scales, r2t, b, st)
+        api.decode_attention_q8(desc, c, b, qd, r2t, kv_lens, cache.k, cache.v, cache.scales, od, ld, longest, dw, st)
+
+    graph = None
+    tables = [r2t[i, :m].clone() for i, m in enumerate(lens)]
+    for t in range(steps):
+        fresh = ids[n + t * b:n + (t + 1) * b]
+        oi.copy_(indptr([len(x) for x in tables], dev))
+        old[:int(oi[-1])] = torch.cat(tables)
+        tables = [torch.cat([x, fresh[i:i + 1]]) for i, x in enumerate(tables)]
+        new.copy_(fresh)
+        for y in (qd, kn, vn):
+            y.copy_(torch.randn(y.shape, device=dev).to(dt))
+        kv_lens.copy_(i32([len(x) for x in tables], dev))
+        if captured:
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    step()
+            graph.replay()
+        else:
+            step()
+        assert int(st) == 0
+        for i, x in enumerate(tables):
+            kk, vv = cache.values(x)
+            agree(od[i:i + 1], ld[i:i + 1], attend(qd[i:i + 1], kk, vv, 1 / math.sqrt(d), len(x) - 1), dt)
+
+
+@gpu
+def test_binding_refuses(dev):
+    """Wrong types, sizes and devices are refused by the extension and by the Python code alike."""
+    hq, hkv, d, slots = 4, 2, 64, 32
+    cache = Cache(dev, INT8, slots, hkv, d)
+    desc, st = desc_of(BF, hq, hkv, d, slots), torch.zeros(1, dtype=torch.int32, device=dev)
+    r2t, _ = table_of([5, 9], 16, slots, dev)
+    q = torch.zeros(2, hq, d, dtype=BF, device=dev)
+    good = dict(q=q, r2t=r2t, lens=i32([5, 9], dev), k=cache.k, v=cache.v, s=cache.scales, out=q.clone(), st=st)
+    ext = api.ops_ext()
+    assert ext is not None
+    try:
+        for use in (ext, False):
+            api._ops_ext = use
+            for name, wrong in (("q", q.float()), ("q", q[:1]), ("q", q.cpu()), ("q", q.transpose(1, 2)), ("r2t", r2t.long()),
+                                ("lens", i64([5, 9], dev)), ("k", cache.k.view(torch.float8_e4m3fn)), ("v", cache.v[:5]),
+                                ("s", cache.scales[:5]), ("s", cache.scales.double()), ("out", q[:1]), ("st", st.long())):
+                a = dict(good, **{name: wrong})
+                with pytest.raises(ValueError):
+                    api.decode_attention_q8(desc, cache.q8, 2, a["q"], a["r2t"], a["lens"], a["k"], a["v"], a["s"], a["out"], None, 9,
+                                            torch.empty(1 << 20, dtype=torch.uint8, device=dev), a["st"])
+            rows = torch.zeros(3, hkv, d, dtype=BF, device=dev)
+            for name, wrong in (("k", rows.float()), ("k", rows[:2]), ("k", rows.cpu()), ("s", cache.scales[1:])):
+                a = dict(dict(k=rows, s=cache.scales), **{name: wrong})
+                with pytest.raises(ValueError):
+                    api.kv_pool_write_q8(desc, cache.q8, 1, None, i64([0, 0], dev), i32([1, 2, 3], dev), i64([0, 3], dev), a["k"], rows,
+                                         cache.k, cache.v, a["s"], None, 3, st)
+                with pytest.raises(ValueError):
+                    api.kv_pool_read_q8(desc, cache.q8, i32([1, 2, 3], dev), cache.k, cache.v, a["s"], a["k"], rows, st)
+    finally:
+        api._ops_ext = ext
