@@ -1,0 +1,72 @@
+// The entry points of attention over 8-bit pools: argument checks, and which kernel takes a call.
+#include "kv_q8.cuh"
+#include "radix_attn.h"
+#include "rx_common.h"
+#include "rx_q8.h"
+
+using namespace rx;
+
+static int attention_q8_check(const char* fn, const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, int64_t r2t_stride,
+                              int32_t max_qo_len, int32_t max_kv_len) {
+    const int rc = q8_check(fn, desc, q8, true);
+    if (rc != RX_OK) return rc;
+    RX_REQUIRE(batch >= 0 && max_qo_len >= 0 && max_kv_len >= 0 && r2t_stride >= 0, "%s: bad arguments", fn);
+    return RX_OK;
+}
+
+static int attention_q8_pointers(const char* fn, const RowsQ8Args& a) {
+    RX_REQUIRE(a.q && a.r2t && a.k_pool && a.v_pool && a.scales && a.out && (a.kv_lens || (a.qo_indptr && a.prefix_lens)),
+               "%s: null device pointer", fn);
+    for (const void* x : {a.q, (const void*)a.k_pool, (const void*)a.v_pool, (const void*)a.out})
+        RX_REQUIRE(((uintptr_t)x & 15) == 0, "%s: rows and pools must be 16-byte aligned", fn);
+    RX_REQUIRE(((uintptr_t)a.scales & 7) == 0, "%s: scales must be 8-byte aligned", fn);
+    return RX_OK;
+}
+
+static bool workspace_shape(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
+    return d && batch > 0 && max_qo_len > 0 && max_kv_len >= 0 && d->hkv > 0 && d->hq > 0 && d->hq % d->hkv == 0 && d->head_dim > 0;
+}
+
+extern "C" size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_kv_len,
+                                            const rx_shared_groups* groups) {
+    if (!workspace_shape(desc, batch, 1, max_kv_len)) return 0;
+    return rows_q8_plan(desc, batch, 1, max_kv_len).bytes;
+}
+
+extern "C" size_t extend_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
+    if (!workspace_shape(desc, batch, max_qo_len, max_kv_len)) return 0;
+    return rows_q8_plan(desc, batch, max_qo_len, max_kv_len).bytes;
+}
+
+extern "C" int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
+                                   const int32_t* d_req_to_token, int64_t r2t_stride, const int32_t* d_kv_lens,
+                                   const rx_shared_groups* groups, const void* d_k_pool, const void* d_v_pool, const float* d_scales,
+                                   void* d_out, float* d_lse, int32_t max_kv_len, void* d_workspace, size_t ws_bytes,
+                                   int32_t* d_status, void* stream) {
+    static const char* fn = "decode_attention_q8";
+    RX_TRACE("decode_attention_q8");
+    int rc = attention_q8_check(fn, desc, q8, batch, r2t_stride, 1, max_kv_len);
+    if (rc != RX_OK || batch == 0) return rc;
+    RX_REQUIRE(d_kv_lens, "%s: null device pointer", fn);
+    const RowsQ8Args a{d_q,  nullptr, nullptr, d_kv_lens, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool, (const uint8_t*)d_v_pool,
+                       (const float2*)d_scales, d_out, d_lse, batch, 1, max_kv_len, d_status};
+    rc = attention_q8_pointers(fn, a);
+    if (rc != RX_OK) return rc;
+    return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
+                                          const int64_t* d_qo_indptr, const int32_t* d_prefix_lens, const int32_t* d_req_to_token,
+                                          int64_t r2t_stride, const void* d_k_pool, const void* d_v_pool, const float* d_scales,
+                                          void* d_out, float* d_lse, int32_t max_qo_len, int32_t max_kv_len, void* d_workspace,
+                                          size_t ws_bytes, int32_t* d_status, void* stream) {
+    static const char* fn = "prefix_extend_attention_q8";
+    RX_TRACE("prefix_extend_attention_q8");
+    int rc = attention_q8_check(fn, desc, q8, batch, r2t_stride, max_qo_len, max_kv_len);
+    if (rc != RX_OK || batch == 0 || max_qo_len == 0) return rc;
+    const RowsQ8Args a{d_q,  d_qo_indptr, d_prefix_lens, nullptr, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool,
+                       (const uint8_t*)d_v_pool, (const float2*)d_scales, d_out, d_lse, batch, max_qo_len, max_kv_len, d_status};
+    rc = attention_q8_pointers(fn, a);
+    if (rc != RX_OK) return rc;
+    return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
+}

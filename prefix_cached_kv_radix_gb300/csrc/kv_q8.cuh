@@ -64,4 +64,27 @@ __device__ __forceinline__ void q8_to_f32(uint32_t w, float* f) {
     }
 }
 
+// Four codes as two pairs of f16, exact: bytes (0, 1) and (2, 3), or, TRANSPOSED, (0, 2) and (1, 3) -- the codes of two keys at
+// one channel each, where the word holds two neighbouring channels of two keys.
+template <int FMT, bool TRANSPOSED>
+__device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+    if (FMT == RX_Q8_INT8) {
+        // the code plus 128 as the last bits of 1024, and 1152 taken off
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t x = __byte_perm(u, 0x64646464u, TRANSPOSED ? 0x4240 : 0x4140);
+        const uint32_t y = __byte_perm(u, 0x64646464u, TRANSPOSED ? 0x4341 : 0x4342);
+        const uint32_t off = 0x64806480u;                   // 1152, twice
+        const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&off));
+        const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&off));
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    } else {
+        if (TRANSPOSED) w = __byte_perm(w, 0, 0x3120);
+        const __half2_raw p = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+        const __half2_raw q = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    }
+}
+
 }  // namespace rx

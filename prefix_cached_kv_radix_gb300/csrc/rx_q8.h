@@ -1,0 +1,40 @@
+// Internal launch interfaces of the attention over 8-bit pools.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv_q8.cuh"
+#include "radix_attn.h"
+#include "rx_kernels.h"
+
+namespace rx {
+
+// What both entry points hand on.  kv_lens non-null selects decode (one token a request, max_qo_len 1).
+struct RowsQ8Args {
+    const void* q;
+    const int64_t* qo_indptr;
+    const int32_t* prefix_lens;
+    const int32_t* kv_lens;
+    const int32_t* r2t;
+    int64_t stride;
+    const uint8_t* k_pool;
+    const uint8_t* v_pool;
+    const float2* scales;
+    void* out;
+    float* lse;
+    int32_t batch, max_qo_len, max_kv_len;
+    int32_t* status;
+};
+
+// How rows_q8.cu splits a call, and the workspace it needs (0 where no row's keys are split).
+struct RowsPlan {
+    int nt, chunk;
+    int64_t tiles, chunks;
+    size_t o_bytes, bytes;
+};
+RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len);
+int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,
+                   cudaStream_t stream);
+
+}  // namespace rx
