@@ -526,7 +526,8 @@ typedef struct {
  *  - Computed scales, from a = max |x| of the row: int8 a / 127 rounded to float32, e4m3 the smallest
  *    power of two not below a / 448 (then x / scale is exact, and values read back are exact in bf16 too);
  *    2^-126 at least.  A row with an infinity or NaN gets the scale NaN and codes 0: it reads as NaN.
- *  - With fixed scales a NaN becomes int8 code 0, or the e4m3 NaN.
+ *  - With fixed scales a NaN becomes code 0.  (e4m3's own NaNs, 0x7f and 0xff, are never written; what attention makes of
+ *    them is not specified.)
  *  - A slot outside [0, num_slots): RX_DEV_BAD_SLOT, that row is not written.  Two rows with the same slot: that
  *    slot holds parts of either. */
 int kv_pool_write_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const int32_t* d_prefix_slots,

@@ -27,6 +27,11 @@ static bool workspace_shape(const rx_attn_desc* d, int32_t batch, int32_t max_qo
     return d && batch > 0 && max_qo_len > 0 && max_kv_len >= 0 && d->hkv > 0 && d->hq > 0 && d->hq % d->hkv == 0 && d->head_dim > 0;
 }
 
+// bf16 rows that fill a tile of 128 at least in part go to the tcgen05 kernel; f32 rows keep 32-bit results on mma.sync.
+static bool many_rows(const rx_attn_desc* d, int32_t max_qo_len) {
+    return d->dtype == RX_BF16 && (int64_t)max_qo_len * (d->hq / d->hkv) > ROWS_Q8_MOST;
+}
+
 extern "C" size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_kv_len,
                                             const rx_shared_groups* groups) {
     if (!workspace_shape(desc, batch, 1, max_kv_len)) return 0;
@@ -35,6 +40,7 @@ extern "C" size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t ba
 
 extern "C" size_t extend_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
     if (!workspace_shape(desc, batch, max_qo_len, max_kv_len)) return 0;
+    if (many_rows(desc, max_qo_len)) return extend_q8_bytes(desc);
     return rows_q8_plan(desc, batch, max_qo_len, max_kv_len).bytes;
 }
 
@@ -68,5 +74,6 @@ extern "C" int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_
                        (const uint8_t*)d_v_pool, (const float2*)d_scales, d_out, d_lse, batch, max_qo_len, max_kv_len, d_status};
     rc = attention_q8_pointers(fn, a);
     if (rc != RX_OK) return rc;
+    if (many_rows(desc, max_qo_len)) return extend_q8_launch(a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
     return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
 }

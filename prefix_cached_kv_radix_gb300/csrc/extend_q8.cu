@@ -1,0 +1,932 @@
+// Extend attention over 8-bit pools on tcgen05 tensor cores: prompts of many new tokens (bf16 rows).
+//
+// Row i of request b attends keys 0 .. P_b + i, codes kc, vc with scales ks, vs:
+//   x_j = scale log2(e) ks_j (q . kc_j),  P_j = 2^(x_j - m),  l += P_j,  O += bf16(P_j vs_j) vc_j,  o = O / l,
+// m the row's running reference (moved when the maximum grows by more than 2^8).  Codes are exact in bf16, so the products
+// are those of bf16 rows and the scales stay in 32 bits; P_j vs_j is rounded to bf16 for the tensor core (at
+// most 2^-8 of it, as the bf16 kernel rounds P_j), l sums the unrounded P_j, o is rounded once.
+//
+// A work item is a request's kv head and 256 packed rows (row = token * G + query head of the group) in two Q tiles that share
+// each K/V tile of 128 keys.  What is shared out is not items but the K/V tiles of all items, one after
+// another: CTA i of 152 takes the i-th equal part of them, so that long and short requests, and few rows over a long
+// context, fill the GPU alike without a counter in memory.  An item that a border cuts is finished from normalised
+// parts in the workspace by a second kernel.  (Borders close to an item's end move there.)  Roles (512 threads):
+//   warp 0       items in order, handed on through a ring in shared memory, and their Q tiles
+//   warp 1       issues the tcgen05.mma: O_t += P_t(j) V(j) in two halves, then at once S_t(j+1) = Q_t K(j+1)^T
+//   warps 2, 3, 12-15  K/V tiles: codes by 16-byte loads through the slot table, a tile ahead in registers, widened to
+//                bf16 and stored in the 128B-swizzled layout that tcgen05 reads; the keys' scales beside the V tile
+//   warps 4-7, 8-11  softmax of Q tile 0 and 1, a row per thread, and the item's output
+// TMEM columns: S0/P0 [0,128) S1/P1 [128,256) O0 [256,256+D) O1 after.  Every wait is bounded; on time-out the kernel
+// records RX_DEV_TIMEOUT, waits for its copies, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "kv_q8.cuh"
+#include "prompt_wait.cuh"
+#include "radix_attn.h"
+#include "rx_common.h"
+#include "rx_device.cuh"
+#include "rx_launch.h"
+#include "rx_q8.h"
+#include "tc_issue.cuh"
+
+namespace rx {
+
+constexpr int EQ_BN = 128;             // keys per K/V tile
+constexpr int EQ_THREADS = 512;
+constexpr int EQ_ROWS = 256;           // packed rows of an item
+constexpr int EQ_CTAS = 152;
+constexpr int EQ_RING = 4;             // items in flight between the roles
+constexpr int EQ_CONSUMERS = 15;       // MMA warp, six converter warps, eight softmax warps
+constexpr int EQ_CONV = 192;           // converter threads
+constexpr uint32_t EQ_REGS_SOFTMAX = 168, EQ_REGS_OTHER = 88, EQ_REGS_LAUNCH = 128;   // 2*128*88 + 2*128*168 = 512*128
+constexpr float EQ_LOG2E = 1.4426950408889634f, EQ_LN2 = 0.6931471805599453f;
+constexpr float EQ_RESCALE = 8.0f;     // log2 units
+
+struct ExtendQ8Params {
+    const __nv_bfloat16* q;
+    const int64_t* qo_indptr;
+    const int32_t* prefix_lens;
+    const int32_t* r2t;
+    int64_t stride, num_slots;
+    Q8Pools pools;
+    __nv_bfloat16* out;
+    float* lse;
+    int32_t batch, hq, hkv, group;
+    int32_t max_qo_len, max_kv_len;
+    float scale_log2;
+    int32_t* status;
+    float* part_o;                     // [CTAs][2][EQ_ROWS][D], normalised
+    float* part_lse;                   // [CTAs][2][EQ_ROWS], base 2
+    int4* meta;                        // [CTAs][2]: request (-1: no part), kv head, first row, whether the item ends here
+    int32_t q_map_ok;
+    CUtensorMap q_map;
+};
+
+template <int D>
+struct EqLayout {
+    static constexpr int NK = D == 128 ? 2 : 4;    // K ring depth
+    static constexpr int NV = D == 128 ? 2 : 4;    // V ring depth
+    static constexpr int Q_TILE = 128 * D * 2;
+    static constexpr int KV_TILE = EQ_BN * D * 2;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
+    static constexpr int OFF_V = OFF_K + NK * KV_TILE;
+    static constexpr int OFF_KS = OFF_V + NV * KV_TILE;              // [NV][128] K scales times scale log2(e)
+    static constexpr int OFF_VS = OFF_KS + NV * EQ_BN * 4;           // [NV][128] V scales, -1 for no key
+    static constexpr int OFF_FLAG = OFF_VS + NV * EQ_BN * 4;         // [NV] int4: some key of the tile is at a bad slot
+    static constexpr int OFF_RING = OFF_FLAG + NV * 16;              // 3 int4 an entry
+    static constexpr int OFF_SCAN = OFF_RING + EQ_RING * 48;         // int64 per warp, and four results
+    static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
+    static constexpr int BAR_Q = 0, BAR_KF = 1, BAR_KE = BAR_KF + NK, BAR_VF = BAR_KE + NK, BAR_VE = BAR_VF + NV, BAR_S = BAR_VE + NV,
+                         BAR_P = BAR_S + 2, BAR_QE = BAR_P + 4, BAR_OR = BAR_QE + 2, BAR_IF = BAR_OR + 2, BAR_IE = BAR_IF + EQ_RING,
+                         BAR_DONE = BAR_IE + EQ_RING, NBAR = BAR_DONE + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;              // TMEM address, abort flag
+    static constexpr int ALLOC = OFF_MISC + 8 + 1024;                // room to align the base to 1024 B
+    static constexpr uint32_t TMEM_COLS = 512, COL_O0 = 256;
+    static constexpr int CPR = D / 16;                               // 16-byte chunks of a row's codes
+    static constexpr int NX = (EQ_BN * CPR + EQ_CONV - 1) / EQ_CONV; // chunks per converter thread, tile and pool
+    static_assert(ALLOC <= 232448, "shared memory budget");
+};
+
+// A piece of an item: K/V tiles j0 .. j1 - 1 of its rows.
+struct EqItem {
+    int b, g, row0, ntiles, n, before, j0, j1, kv_end, whole, slot;
+    int64_t q0;
+};
+
+// A request's rows and keys; n = 0 where there is none to do.
+__device__ __forceinline__ void eq_request(const ExtendQ8Params& p, int b, bool tell, int64_t& q0, int& n, int& before) {
+    q0 = p.qo_indptr[b];
+    const int64_t m = p.qo_indptr[b + 1] - q0, P = p.prefix_lens[b];
+    n = (int)m, before = (int)P;
+    if (q0 >= 0 && m >= 0 && m <= p.max_qo_len && P >= 0 && P + m <= p.stride && P + m <= p.max_kv_len) return;
+    if (tell && m != 0) report(p.status, RX_DEV_BAD_LENGTH);
+    n = 0;
+}
+
+// K/V tiles of the item that starts at packed row `row0`.
+__device__ __forceinline__ int eq_tiles(int row0, int rows, int G, int before) {
+    return (before + (min(row0 + EQ_ROWS, rows) - 1) / G) / EQ_BN + 1;
+}
+
+// K/V tiles of all of a request's items, for one kv head.
+__device__ __forceinline__ int64_t eq_units(const ExtendQ8Params& p, int b, bool tell) {
+    int64_t q0, sum = 0;
+    int n, before;
+    eq_request(p, b, tell, q0, n, before);
+    const int rows = n * p.group;
+    for (int r = 0; r < rows; r += EQ_ROWS) sum += eq_tiles(r, rows, p.group, before);
+    return sum;
+}
+
+// Where unit `at` of request b's (of `units` a kv head) lies: kv head, first row and K/V tile of the item.
+__device__ __forceinline__ void eq_locate(const ExtendQ8Params& p, int b, int64_t units, int64_t at, int& g, int& row0, int& j, int& tiles) {
+    int64_t q0;
+    int n, before;
+    eq_request(p, b, false, q0, n, before);
+    g = (int)(at / units);
+    int64_t left = at - g * units;
+    for (row0 = 0;; row0 += EQ_ROWS) {
+        tiles = eq_tiles(row0, n * p.group, p.group, before);
+        if (left < tiles) break;
+        left -= tiles;
+    }
+    j = (int)left;
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_constant__ ExtendQ8Params p) {
+    using LY = EqLayout<D>;
+    constexpr int NK = LY::NK, NV = LY::NV, CPR = LY::CPR, NX = LY::NX;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t bar0 = base + LY::OFF_BAR;
+    auto bar = [&](int i) { return bar0 + (uint32_t)(8 * i); };
+    volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(gbase + LY::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + LY::OFF_MISC + 4);
+    int4* ring = reinterpret_cast<int4*>(gbase + LY::OFF_RING);
+    int64_t* scan = reinterpret_cast<int64_t*>(gbase + LY::OFF_SCAN);
+    // from a shuffle, so that the compiler knows it the same for the whole warp
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int G = p.group;
+
+    if (tid == 0) {
+        mbar_init(bar(LY::BAR_Q), 32 + 1);   // warp 0's lanes, and lane 0's expect-tx arrival
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(bar(LY::BAR_KF + i), EQ_CONV / 32);
+            mbar_init(bar(LY::BAR_KE + i), 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(bar(LY::BAR_VF + i), EQ_CONV / 32);
+            mbar_init(bar(LY::BAR_VE + i), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(LY::BAR_S + t), 1);
+            mbar_init(bar(LY::BAR_P + t), 4);          // one arrival per softmax warp, keys 0-63
+            mbar_init(bar(LY::BAR_P + 2 + t), 4);      // keys 64-127
+            mbar_init(bar(LY::BAR_QE + t), 1);         // Q buffer t read by its item's last S
+            mbar_init(bar(LY::BAR_OR + t), 1);         // O_t of an item complete
+        }
+        for (int i = 0; i < EQ_RING; ++i) {
+            mbar_init(bar(LY::BAR_IF + i), 1);
+            mbar_init(bar(LY::BAR_IE + i), EQ_CONSUMERS);
+        }
+        mbar_init(bar(LY::BAR_DONE), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + LY::OFF_MISC, LY::TMEM_COLS);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();                          // what came before has finished; nothing global was touched so far
+
+    // ---------------------------------------------------------------- this CTA's part of the units
+    // scan[16], scan[17]: the first unit of this part and of the next; scan[18], scan[19]: the request of the first, and the
+    // units before that request
+    {
+        auto warp_sum = [&](int64_t v) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            return v;
+        };
+        int64_t v = 0, mine = 0;         // this thread's request's units (of the last round), and those of all its requests
+        for (int b = tid; b < p.batch; b += EQ_THREADS) {
+            v = eq_units(p, b, blockIdx.x == 0) * p.hkv;
+            mine += v;
+        }
+        mine = warp_sum(mine);
+        if (lane == 0) scan[warp] = mine;
+        if (tid < 4) scan[16 + tid] = 0;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < EQ_THREADS / 32; ++w) total += scan[w];
+        // at least two tiles a CTA; borders within a sixteenth of a part of an item's ends move there
+        const int64_t parts = max(min((int64_t)gridDim.x, total / 2), (int64_t)1);
+        const int64_t near = 1 + total / parts / 16;
+        const int64_t want[2] = {min((int64_t)blockIdx.x, parts) * total / parts, min((int64_t)blockIdx.x + 1, parts) * total / parts};
+        int64_t before = 0;              // units of the rounds so far
+        for (int b0 = 0; b0 < p.batch; b0 += EQ_THREADS) {
+            const int b = b0 + tid;
+            if (p.batch > EQ_THREADS) v = b < p.batch ? eq_units(p, b, false) * p.hkv : 0;
+            else if (b >= p.batch) v = 0;
+            int64_t inc = v;             // inclusive scan
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            __syncthreads();             // the sums of the round before are read
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            int64_t at = before + inc - v;
+            for (int w = 0; w < warp; ++w) at += scan[w];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (want[e] >= at && want[e] < at + v) {
+                    int g, row0, j, tiles;
+                    eq_locate(p, b, v / p.hkv, want[e] - at, g, row0, j, tiles);
+                    const int64_t to = want[e] + (j < near ? -j : tiles - j < near ? tiles - j : 0);
+                    scan[16 + e] = to;
+                    if (e == 0) scan[18] = b, scan[19] = at;
+                }
+            for (int w = 0; w < EQ_THREADS / 32; ++w) before += scan[w];
+        }
+        if (tid == 0) {                  // past the last unit
+            if (want[0] >= total) scan[16] = total;
+            if (want[1] >= total) scan[17] = total;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // The k-th item of this CTA, for a whole warp; false at the end.  The entry is free once every warp has read it.
+    auto take = [&](int k, EqItem& it) -> bool {
+        const int e = k % EQ_RING;
+        if (!pt_wait(bar(LY::BAR_IF + e), (k / EQ_RING) & 1, abort_flag)) return false;
+        const int4 a = ring[3 * e], c = ring[3 * e + 1], d = ring[3 * e + 2];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
+        auto u = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        it.b = u(a.x), it.g = u(a.y), it.row0 = u(a.z), it.ntiles = u(a.w);
+        it.n = u(c.x), it.before = u(c.y), it.j0 = u(c.z), it.j1 = u(c.w);
+        it.kv_end = u(d.x), it.q0 = ((int64_t)u(d.w) << 32) | (uint32_t)u(d.z);
+        const int f = u(d.y);
+        it.whole = f & 1, it.slot = f >> 1;
+        return it.b >= 0;
+    };
+
+    if (warp < 4 || warp >= 12) {
+        regs_decrease<EQ_REGS_OTHER>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ items and Q
+            const uint32_t qs = base + LY::OFF_Q;
+            int64_t cur = scan[16];
+            const int64_t end = scan[17];
+            int b = (int)scan[18], g = 0, row0 = 0, j = 0, tiles = 0, n = 0, before = 0, k = 0;
+            int64_t q0 = 0;
+            int quse0 = 0, quse1 = 0;    // items so far that used Q buffer 0 / 1
+            int4 told[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};
+            bool ok = true;
+            if (cur < end) {
+                // the border may have moved past the end of its request
+                int64_t units = eq_units(p, b, false), at = cur - scan[19];
+                while (at >= units * p.hkv) {
+                    at -= units * p.hkv;
+                    units = eq_units(p, ++b, false);
+                }
+                eq_locate(p, b, units, at, g, row0, j, tiles);
+                eq_request(p, b, false, q0, n, before);
+            }
+            while (ok && cur < end) {
+                const int rows = n * G, j1 = (int)min((int64_t)tiles, j + (end - cur));
+                const int ntiles = rows - row0 > 128 ? 2 : 1;
+                const bool whole = j == 0 && j1 == tiles;
+                const int slot = j == 0 ? 1 : 0;
+                if (!whole) told[slot] = make_int4(b, g, row0, j1 == tiles ? 1 : 0);
+                const int e = k % EQ_RING;
+                if (k >= EQ_RING && !(ok = pt_wait(bar(LY::BAR_IE + e), ((k / EQ_RING) - 1) & 1, abort_flag))) break;
+                if (lane == 0) {
+                    ring[3 * e] = make_int4(b, g, row0, ntiles);
+                    ring[3 * e + 1] = make_int4(n, before, j, j1);
+                    ring[3 * e + 2] = make_int4(before + (min(row0 + EQ_ROWS, rows) - 1) / G + 1, (whole ? 1 : 0) | (slot << 1),
+                                                (int)(uint32_t)q0, (int)(q0 >> 32));
+                    mbar_arrive(bar(LY::BAR_IF + e));
+                }
+                ++k;
+                if (quse0 > 0 && !(ok = pt_wait(bar(LY::BAR_QE), (quse0 - 1) & 1, abort_flag))) break;
+                if (ntiles > 1 && quse1 > 0 && !(ok = pt_wait(bar(LY::BAR_QE + 1), (quse1 - 1) & 1, abort_flag))) break;
+                quse0 += 1;
+                quse1 += ntiles > 1 ? 1 : 0;
+                // full 128-row tiles by TMA, one box per 64 columns; a ragged one row by row, two lanes a row, the rows
+                // past the end like the last
+                const int full = p.q_map_ok && q0 + n <= INT32_MAX ? min(ntiles, (rows - row0) >> 7) : 0;
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar(LY::BAR_Q), (uint32_t)(full * LY::Q_TILE));
+                    for (int t = 0; t < full; ++t)
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(qs + (uint32_t)(t * LY::Q_TILE + h * 128 * 128), &p.q_map, h * 64, g * G,
+                                        (int)q0 + row0 / G + t * (128 / G), bar(LY::BAR_Q));
+                }
+                for (int rr = full * 128 + (lane >> 1); rr < ntiles * 128; rr += 16) {
+                    const int t = rr >> 7, r = rr & 127, R = min(row0 + rr, rows - 1);
+                    const __nv_bfloat16* src = p.q + ((q0 + R / G) * p.hq + g * G + R % G) * D;
+                    const uint32_t to = qs + (uint32_t)(t * LY::Q_TILE + r * 128);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int c = 2 * i + (lane & 1);
+                        cp_async_16(to + (uint32_t)((c >> 3) * 128 * 128 + (((c & 7) ^ (r & 7)) << 4)), src + c * 8, 16);
+                    }
+                }
+                cp_async_arrive_noinc(bar(LY::BAR_Q));
+                // on to the next item: row tile, kv head, request
+                cur += j1 - j;
+                if (cur >= end) break;
+                j = 0;
+                row0 += EQ_ROWS;
+                if (row0 >= rows) {
+                    row0 = 0;
+                    if (++g == p.hkv) {
+                        g = 0;
+                        do eq_request(p, ++b, false, q0, n, before);
+                        while (n == 0);
+                    }
+                }
+                tiles = eq_tiles(row0, n * G, G, before);
+            }
+            if (ok) {
+                const int e = k % EQ_RING;
+                if (k < EQ_RING || pt_wait(bar(LY::BAR_IE + e), ((k / EQ_RING) - 1) & 1, abort_flag)) {
+                    if (lane == 0) {
+                        ring[3 * e] = make_int4(-1, 0, 0, 0);
+                        mbar_arrive(bar(LY::BAR_IF + e));
+                    }
+                }
+            }
+            if (lane < 2) p.meta[blockIdx.x * 2 + lane] = lane == 0 ? told[0] : told[1];
+            cp_async_wait_all();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            constexpr uint32_t IDESC_S = idesc_bf16_f32(128, EQ_BN, 0, 0);
+            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
+            const uint32_t qd0 = (uint32_t)sdesc_sw128(base + LY::OFF_Q, 16, 1024);
+            const uint32_t kd0 = (uint32_t)sdesc_sw128(base + LY::OFF_K, 16, 1024);
+            const uint32_t vd0 = (uint32_t)sdesc_sw128(base + LY::OFF_V, EQ_BN * 128, 1024);
+            auto issue_s = [&](int t, int ks) {
+                pt_mma_s<D>(tmem + t * EQ_BN, qd0 + (uint32_t)t * (uint32_t)(LY::Q_TILE >> 4), kd0 + (uint32_t)ks * (uint32_t)(LY::KV_TILE >> 4),
+                            IDESC_S);
+                pt_commit(bar(LY::BAR_S + t));
+            };
+            auto issue_pv = [&](int t, int vs, int h, bool fresh) {      // keys 64 h .. 64 h + 63
+                pt_mma_pv(tmem + LY::COL_O0 + t * D, tmem + t * EQ_BN + h * 32,
+                          vd0 + (uint32_t)vs * (uint32_t)(LY::KV_TILE >> 4) + (uint32_t)h * (uint32_t)(64 * 128 >> 4), IDESC_PV, fresh);
+            };
+            int gt = 0, ic = 0, sc0 = 0, sc1 = 0;    // K/V tiles, items and score steps of Q tile 0 / 1 so far
+            bool ok = true;
+            EqItem it;
+            for (int k = 0; ok && take(k, it); ++k) {
+                const int nt = it.ntiles, nkv = it.j1 - it.j0;
+                ok = pt_wait(bar(LY::BAR_Q), ic & 1, abort_flag) && pt_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag);
+                ic += 1;
+                if (!ok) break;
+                fence_proxy_async_smem();            // rows that warp 0 copied
+                tc_fence_after();
+                for (int t = 0; t < nt; ++t) {
+                    issue_s(t, gt % NK);
+                    if (nkv == 1) pt_commit(bar(LY::BAR_QE + t));
+                }
+                pt_commit(bar(LY::BAR_KE + gt % NK));
+                for (int j = 0; ok && j < nkv; ++j) {
+                    const int u = gt + j, vs = u % NV, ks = (u + 1) % NK;
+                    const bool more = j + 1 < nkv;
+                    if (!(ok = pt_wait(bar(LY::BAR_VF + vs), (u / NV) & 1, abort_flag))) break;
+                    if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), ((u + 1) / NK) & 1, abort_flag))) break;
+                    for (int t = 0; t < nt; ++t) {
+                        const int ph = ((t == 0 ? sc0 : sc1) + j) & 1;
+                        for (int h = 0; ok && h < 2; ++h) {
+                            ok = pt_wait(bar(LY::BAR_P + 2 * h + t), ph, abort_flag);
+                            tc_fence_after();
+                            if (ok) issue_pv(t, vs, h, j == 0 && h == 0);
+                        }
+                        if (!ok) break;
+                        if (t == nt - 1) pt_commit(bar(LY::BAR_VE + vs));
+                        if (more) {
+                            issue_s(t, ks);
+                            if (j + 2 == nkv) pt_commit(bar(LY::BAR_QE + t));
+                        } else {
+                            pt_commit(bar(LY::BAR_OR + t));
+                        }
+                    }
+                    if (ok && more) pt_commit(bar(LY::BAR_KE + ks));
+                }
+                sc0 += nkv;
+                sc1 += nt > 1 ? nkv : 0;
+                gt += nkv;
+            }
+            pt_commit(bar(LY::BAR_DONE));
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ K/V tiles
+            const int lt = warp < 4 ? tid - 64 : tid - 384 + 64;
+            const int c = lt % CPR, key0 = lt / CPR;         // this thread's chunk of every key row it handles
+            constexpr int STEP = EQ_CONV / CPR;              // keys from one of its rows to the next
+            static_assert(EQ_CONV % CPR == 0, "one chunk per thread");
+            const uint32_t nslots = (uint32_t)p.num_slots;
+            const uint32_t pitch = (uint32_t)(p.hkv * D);
+            // The tile whose codes are loaded next, and its slots: one tile ahead of the one being stored.
+            EqItem it;
+            int k = 0, j = 0;
+            bool have = take(0, it);
+            if (have) j = it.j0;
+            const int32_t* slots = nullptr;
+            const uint8_t *kb = nullptr, *vb = nullptr;
+            const float2* sb = nullptr;
+            int32_t sl[NX], ss = -1;
+            auto begin = [&]() {
+                slots = p.r2t + (int64_t)it.b * p.stride;
+                kb = p.pools.k + (size_t)it.g * D + c * 16;
+                vb = p.pools.v + (size_t)it.g * D + c * 16;
+                sb = p.pools.scales + it.g;
+            };
+            auto load_slots = [&]() {
+                const int left = it.kv_end - j * EQ_BN;      // keys of this tile and after it
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int key = key0 + x * STEP;
+                    sl[x] = key < EQ_BN && key < left ? slots[j * EQ_BN + key] : -2;     // -2: no key
+                }
+                ss = lt < EQ_BN && lt < left ? slots[j * EQ_BN + lt] : -2;
+            };
+            auto next = [&]() {
+                if (++j == it.j1) {
+                    have = take(++k, it);
+                    if (!have) return;
+                    j = it.j0;
+                    begin();
+                }
+                load_slots();
+            };
+            uint4 kr[NX], vr[NX];
+            float2 sc = make_float2(0.f, 0.f);
+            int32_t kept = -2;                               // ss of the tile in the registers
+            auto load_codes = [&](uint4* r, const uint8_t* from) {
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    r[x] = make_uint4(0, 0, 0, 0);
+                    if ((uint32_t)sl[x] < nslots) r[x] = *reinterpret_cast<const uint4*>(from + (size_t)(uint32_t)sl[x] * pitch);
+                }
+            };
+            auto load_scale = [&]() {
+                kept = ss;
+                sc = make_float2(1.f, -1.f);                 // no key
+                if ((uint32_t)ss < nslots) sc = sb[(int64_t)(ss >> p.pools.shift) * p.hkv];
+                else if (ss != -2) report(p.status, RX_DEV_BAD_SLOT);
+            };
+            auto store = [&](const uint4* r, uint32_t buf) {
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int key = key0 + x * STEP;
+                    if (key >= EQ_BN) continue;
+                    uint32_t w[8];
+                    q8_to_bf16<FMT>(r[x].x, w[0], w[1]);
+                    q8_to_bf16<FMT>(r[x].y, w[2], w[3]);
+                    q8_to_bf16<FMT>(r[x].z, w[4], w[5]);
+                    q8_to_bf16<FMT>(r[x].w, w[6], w[7]);
+                    // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half; the lanes of the halves take
+                    // them in opposite order, so that eight lanes fill eight different pieces of 128 bytes
+                    const uint32_t row = buf + (uint32_t)((c >> 2) * EQ_BN * 128 + key * 128);
+                    const int swap = c >> 2, cc = (2 * c) & 7;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int hh = h ^ swap;
+                        const uint32_t to = row + (uint32_t)(((cc + hh) ^ (key & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hh ? w[4] : w[0]), "r"(hh ? w[5] : w[1]),
+                                     "r"(hh ? w[6] : w[2]), "r"(hh ? w[7] : w[3])
+                                     : "memory");
+                    }
+                }
+            };
+            auto publish = [&](uint32_t full) {
+                fence_proxy_async_smem();                    // stored before the tensor core reads
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            };
+            bool cur = have;                                 // a tile is in the registers
+            if (have) {
+                begin();
+                load_slots();
+                load_codes(kr, kb);
+                load_codes(vr, vb);
+                load_scale();
+                next();
+            }
+            for (int u = 0; cur; ++u) {
+                const int ks = u % NK, vs = u % NV;
+                if (u >= NK && !pt_wait(bar(LY::BAR_KE + ks), ((u / NK) - 1) & 1, abort_flag)) break;
+                store(kr, base + LY::OFF_K + ks * LY::KV_TILE);
+                publish(bar(LY::BAR_KF + ks));
+                if (have) load_codes(kr, kb);
+                if (u >= NV && !pt_wait(bar(LY::BAR_VE + vs), ((u / NV) - 1) & 1, abort_flag)) break;
+                store(vr, base + LY::OFF_V + vs * LY::KV_TILE);
+                if (lt < EQ_BN) {
+                    reinterpret_cast<float*>(gbase + LY::OFF_KS)[vs * EQ_BN + lt] = sc.x * p.scale_log2;
+                    reinterpret_cast<float*>(gbase + LY::OFF_VS)[vs * EQ_BN + lt] = sc.y;
+                    const bool bad = __any_sync(0xffffffffu, kept != -2 && (uint32_t)kept >= nslots);
+                    if (lane == 0) reinterpret_cast<int*>(gbase + LY::OFF_FLAG)[vs * 4 + lt / 32] = bad ? 1 : 0;
+                }
+                publish(bar(LY::BAR_VF + vs));
+                cur = have;
+                if (have) {
+                    load_codes(vr, vb);
+                    load_scale();
+                    next();
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax warpgroups
+        regs_increase<EQ_REGS_SOFTMAX>();
+        const int t = (warp >> 2) - 1, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + t * EQ_BN;   // scores, then weights over them
+        const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;
+        int gt = 0, sc = 0, oc = 0;           // K/V tiles of all items, and score steps and items of this Q tile so far
+        bool ok = true;
+        EqItem it;
+        for (int k = 0; ok && take(k, it); ++k) {
+            const int nkv = it.j1 - it.j0;
+            if (t >= it.ntiles) {
+                gt += nkv;
+                continue;
+            }
+            const int R = it.row0 + t * 128 + r, rows = it.n * G;
+            const int pos = it.before + min(R, rows - 1) / G - it.j0 * EQ_BN;      // sees keys 0 .. pos of this piece
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < nkv; ++j, ++gt) {
+                const int vs = gt % NV;
+                if (!(ok = pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag))) break;
+                if (!(ok = pt_wait(bar(LY::BAR_VF + vs), (gt / NV) & 1, abort_flag))) break;     // the scales
+                tc_fence_after();
+                const float* kscale = reinterpret_cast<const float*>(gbase + LY::OFF_KS) + vs * EQ_BN;
+                const float* vscale = reinterpret_cast<const float*>(gbase + LY::OFF_VS) + vs * EQ_BN;
+                const int4 flag = *reinterpret_cast<const int4*>(gbase + LY::OFF_FLAG + vs * 16);
+                const int lim = pos - j * EQ_BN;      // columns past lim are hidden
+                float alpha = 1.f;
+                bool moved = false;
+                auto refer = [&](float mx) {          // the reference after scores up to mx
+                    float m_new = m_ref;
+                    if (m_ref == -INFINITY || mx > m_ref + EQ_RESCALE) m_new = fmaxf(m_ref, mx);
+                    alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+                    moved = j > 0 && __any_sync(0xffffffffu, m_new != m_ref);
+                    l *= alpha;
+                    m_ref = m_new;
+                    return m_new == -INFINITY ? 0.f : m_new;
+                };
+                auto rescale = [&]() {
+                    // PV_t(j-1) has completed (S_t(j) was issued after it and is complete), and PV_t(j) waits for
+                    // the arrivals below.  Rare: rolled.
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 32) {
+                        float ov[32];
+                        tmem_ld32(o_addr + cc, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        tmem_st32(o_addr + cc, ov);
+                    }
+                };
+                auto publish = [&](int h) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(LY::BAR_P + 2 * h + t));
+                };
+                if (__any_sync(0xffffffffu, lim < EQ_BN - 1) || (flag.x | flag.y | flag.z | flag.w)) {
+                    // Tiles that the causal limit cuts, or with keys at bad slots: what is hidden is taken out by
+                    // selection, scores and weights alike (a hidden key's scales may be anything).  Rolled.
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < EQ_BN; c0 += 32) {
+                        float v[32];
+                        tmem_ld32(s_addr + c0, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            v[e] = c0 + e > lim || vscale[c0 + e] == -1.f ? -INFINITY : v[e] * kscale[c0 + e];
+                            mx = fmaxf(mx, v[e]);
+                        }
+                        tmem_st32(s_addr + c0, v);
+                    }
+                    tmem_wait_st();
+                    const float ref = refer(mx);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < EQ_BN; c0 += 32) {     // group c0's weights go to columns already read
+                        float v[32];
+                        uint32_t pk[16];
+                        tmem_ld32(s_addr + c0, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float e0 = fast_exp2(v[e] - ref), e1 = fast_exp2(v[e + 1] - ref);
+                            l += e0 + e1;
+                            pk[e >> 1] = pack_bf16x2(v[e] == -INFINITY ? 0.f : e0 * vscale[c0 + e],
+                                                     v[e + 1] == -INFINITY ? 0.f : e1 * vscale[c0 + e + 1]);
+                        }
+                        tmem_st16u(s_addr + c0 / 2, pk);
+                    }
+                    if (moved) rescale();
+                    publish(0);
+                    publish(1);
+                    continue;
+                }
+                float s[EQ_BN];
+#pragma unroll
+                for (int c = 0; c < EQ_BN; c += 32) tmem_ld32(s_addr + c, s + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < EQ_BN; c += 4) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(kscale + c);
+                    f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f.x), s[c], s[c + 1]);
+                    f2_unpack(f2_mul(f2_pack(s[c + 2], s[c + 3]), f.y), s[c + 2], s[c + 3]);
+                }
+                float mx8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx8[i] = s[i];
+#pragma unroll
+                for (int c = 8; c + 16 <= EQ_BN; c += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], s[EQ_BN - 8 + i]);
+                const float ref = refer(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                const uint64_t nm2 = f2_pack(-ref, -ref);
+                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+                // weights in two halves of 64 keys (32 columns), each published as soon as it is stored
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[EQ_BN / 4];
+#pragma unroll
+                    for (int cc = 0; cc < EQ_BN / 2; cc += 4) {
+                        const int c = h * (EQ_BN / 2) + cc;
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(vscale + c);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x0, x1;
+                            f2_unpack(f2_add(f2_pack(s[c + 2 * i], s[c + 2 * i + 1]), nm2), x0, x1);
+                            const uint64_t e2 = f2_pack(fast_exp2(x0), fast_exp2(x1));
+                            acc2[((c >> 1) + i) & 3] = f2_add(acc2[((c >> 1) + i) & 3], e2);
+                            f2_unpack(f2_mul(e2, i ? f.y : f.x), x0, x1);
+                            pk[(cc >> 1) + i] = pack_bf16x2(x0, x1);
+                        }
+                    }
+                    tmem_st32u(s_addr + h * 32, pk);
+                    if (h == 0 && moved) rescale();
+                    publish(h);
+                }
+                float ra, rb;
+                f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), ra, rb);
+                l += ra + rb;
+            }
+            if (!ok) break;
+            sc += nkv;
+            // O_t is complete once its last PV has been; the next item's first PV, which overwrites it, waits for weights
+            // that this warpgroup publishes after these reads
+            if (!(ok = pt_wait(bar(LY::BAR_OR + t), oc & 1, abort_flag))) break;
+            oc += 1;
+            tc_fence_after();
+            const bool valid = R < rows;
+            const int tok = min(R, rows - 1) / G, h = it.g * G + min(R, rows - 1) % G;
+            const int64_t at = (it.q0 + tok) * p.hq + h;
+            const float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : m_ref + log2f(l);      // no key: zeros
+            const int64_t part = ((int64_t)blockIdx.x * 2 + it.slot) * EQ_ROWS + t * 128 + r;
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 32) {
+                float ov[32];
+                tmem_ld32(o_addr + cc, ov);
+                tmem_wait_ld();
+                if (valid && it.whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(p.out + at * D + cc + e) =
+                            make_uint4(pack_bf16x2(ov[e] * inv, ov[e + 1] * inv), pack_bf16x2(ov[e + 2] * inv, ov[e + 3] * inv),
+                                       pack_bf16x2(ov[e + 4] * inv, ov[e + 5] * inv), pack_bf16x2(ov[e + 6] * inv, ov[e + 7] * inv));
+                } else if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(p.part_o + part * D + cc + e) =
+                            make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
+                }
+                __syncwarp();                    // the whole warp reads the next columns
+            }
+            if (valid && it.whole && p.lse) p.lse[at] = lse * EQ_LN2;
+            if (valid && !it.whole) p.part_lse[part] = lse;
+            __syncwarp();
+            tc_fence_before();
+        }
+    }
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // copies may still be on their way to shared memory: wait out the time that any of them takes
+        if (tid == 0) report(p.status, RX_DEV_TIMEOUT);
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 10000000ull) __nanosleep(1000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        // every MMA this CTA issued has completed before TMEM is released; this wait does not stop on the abort flag
+        volatile int no_abort = 0;
+        warp_wait(bar(LY::BAR_DONE), 0, &no_abort, p.status, 500000000ull);
+        tmem_dealloc(tmem, LY::TMEM_COLS);
+    }
+}
+
+// The parts of an item that starts in CTA blockIdx.x and goes on in later ones: 32 of its rows a block, 8 a warp.
+template <int D>
+__global__ void __launch_bounds__(128) extend_q8_merge_kernel(const __grid_constant__ ExtendQ8Params p) {
+    __shared__ int list[EQ_CTAS];
+    __shared__ int count;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int4 item = p.meta[blockIdx.x * 2 + 1];
+    if (item.x < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t q0;
+    int n, before;
+    eq_request(p, item.x, false, q0, n, before);
+    const int rows = n * p.group, r0 = blockIdx.y * 32;
+    if (item.z + r0 >= rows) return;
+    if (warp == 0) {
+        int parts = 1;
+        if (lane == 0) list[0] = blockIdx.x * 2 + 1;
+        bool done = false;
+        for (int c0 = blockIdx.x + 1; c0 < (int)gridDim.x && !done; c0 += 32) {
+            const int c = c0 + lane;
+            const int4 m = c < (int)gridDim.x ? p.meta[c * 2] : make_int4(-1, 0, 0, 0);
+            const unsigned ends = __ballot_sync(0xffffffffu, m.x >= 0 && m.w);
+            const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;      // to the part that ends the item
+            const unsigned is = __ballot_sync(0xffffffffu, m.x >= 0) & upto;
+            if ((is >> lane) & 1u) list[parts + __popc(is & ((1u << lane) - 1u))] = c * 2;
+            parts += __popc(is);
+            done = ends != 0;
+        }
+        if (lane == 0) count = parts;
+    }
+    __syncthreads();
+    const int parts = count;
+    constexpr int E = D / 32;
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + warp * 8 + i, R = item.z + r;
+        if (R >= rows) return;
+        float M = -INFINITY;
+        for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[(int64_t)list[s] * EQ_ROWS + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float acc[E], W = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const int64_t at = (int64_t)list[s] * EQ_ROWS + r;
+            const float w = exp2f(p.part_lse[at] - ref);
+            W += w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += w * p.part_o[at * D + lane * E + e];
+        }
+        const float inv = W == 0.f ? 0.f : 1.f / W;
+        const int64_t at = (q0 + R / p.group) * p.hq + item.y * p.group + R % p.group;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (p.lse && lane == 0) p.lse[at] = W == 0.f ? -INFINITY : (M + log2f(W)) * EQ_LN2;
+    }
+}
+
+// The current device must be an sm_103: checked once per device.
+static int eq_device() {
+    static PerDeviceOnce checked;
+    return per_device_once(checked, [] {
+        int dev = 0, major = 0, minor = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+            set_error("prefix_extend_attention_q8: cannot query the device");
+            return (int)RX_ECUDA;
+        }
+        if (major != 10 || minor != 3) {
+            set_error("prefix_extend_attention_q8: the tcgen05 kernel needs an sm_103 (GB300) device");
+            return (int)RX_EDEVICE;
+        }
+        return (int)RX_OK;
+    });
+}
+
+// Tensor map of q as [rows][hq][D] bf16, boxes of a 128-row tile's 64 columns: G heads of 128 / G tokens.  The rows are found through
+// qo_indptr, so the host knows no tighter bound than the coordinates'; the kernel addresses only full tiles of a request's rows.
+static bool eq_rows_map(CUtensorMap* m, const void* q, int hq, int D, int G) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    if (!enc || 128 % G != 0) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)hq, (cuuint64_t)INT32_MAX};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)hq * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t extend_q8_bytes(const rx_attn_desc* d) {
+    const size_t rows = (size_t)EQ_CTAS * 2 * EQ_ROWS;
+    return rows * d->head_dim * sizeof(float) + rows * sizeof(float) + (size_t)EQ_CTAS * 2 * sizeof(int4);
+}
+
+template <int D, int FMT>
+static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
+    static PerDeviceOnce attr;
+    constexpr int smem = EqLayout<D>::ALLOC;
+    const int rc = per_device_once(attr, [&] {
+        const cudaError_t e = cudaFuncSetAttribute(extend_q8_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) {
+            set_error("prefix_extend_attention_q8: cannot set shared memory size: %s", cudaGetErrorString(e));
+            return (int)RX_ECUDA;
+        }
+        // the warpgroups share out the registers the block is launched with: fewer, and they would wait forever
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, extend_q8_kernel<D, FMT>) != cudaSuccess || fa.numRegs < (int)EQ_REGS_LAUNCH) {
+            set_error("prefix_extend_attention_q8: kernel built with %d registers per thread; the register split needs %d", fa.numRegs,
+                      (int)EQ_REGS_LAUNCH);
+            return (int)RX_ECUDA;
+        }
+        return (int)RX_OK;
+    });
+    if (rc != RX_OK) return rc;
+    cudaError_t e = launch_pdl(extend_q8_kernel<D, FMT>, EQ_CTAS, EQ_THREADS, smem, s, p);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(EQ_CTAS, EQ_ROWS / 32);
+        cfg.blockDim = dim3(128);
+        cfg.stream = s;
+        cudaLaunchAttribute pdl[1];
+        pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        pdl[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = pdl;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, extend_q8_merge_kernel<D>, p);
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        set_error("prefix_extend_attention_q8: launch failed: %s", cudaGetErrorString(e));
+        return RX_ECUDA;
+    }
+    return RX_OK;
+}
+
+int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    const int dc = eq_device();
+    if (dc != RX_OK) return dc;
+    const size_t need = extend_q8_bytes(d);
+    RX_REQUIRE(ws && ws_bytes >= need && ((uintptr_t)ws & 255) == 0,
+               "prefix_extend_attention_q8: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", need, ws_bytes);
+    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - EQ_ROWS, "prefix_extend_attention_q8: too many rows in a request");
+    ExtendQ8Params p{};
+    p.q = (const __nv_bfloat16*)a.q;
+    p.qo_indptr = a.qo_indptr;
+    p.prefix_lens = a.prefix_lens;
+    p.r2t = a.r2t;
+    p.stride = a.stride;
+    p.num_slots = d->num_slots;
+    p.pools = {a.k_pool, a.v_pool, a.scales, q8_shift(q8)};
+    p.out = (__nv_bfloat16*)a.out;
+    p.lse = a.lse;
+    p.batch = a.batch;
+    p.hq = d->hq;
+    p.hkv = d->hkv;
+    p.group = d->hq / d->hkv;
+    p.max_qo_len = a.max_qo_len;
+    p.max_kv_len = a.max_kv_len;
+    p.scale_log2 = d->scale * EQ_LOG2E;
+    p.status = a.status;
+    const size_t rows = (size_t)EQ_CTAS * 2 * EQ_ROWS;
+    p.part_o = (float*)ws;
+    p.part_lse = p.part_o + rows * d->head_dim;
+    p.meta = (int4*)(p.part_lse + rows);
+    p.q_map_ok = eq_rows_map(&p.q_map, a.q, d->hq, d->head_dim, p.group) ? 1 : 0;
+    if (d->head_dim == 128)
+        return q8->format == RX_Q8_INT8 ? launch_extend<128, RX_Q8_INT8>(p, stream) : launch_extend<128, RX_Q8_E4M3>(p, stream);
+    return q8->format == RX_Q8_INT8 ? launch_extend<64, RX_Q8_INT8>(p, stream) : launch_extend<64, RX_Q8_E4M3>(p, stream);
+}
+
+}  // namespace rx

@@ -125,6 +125,7 @@ __device__ __forceinline__ uint2 codes_e4m3(const float* x, float s, float inv) 
     for (int i = 0; i < 8; ++i) {
         y[i] = x[i] * inv;
         if (FIXED) {
+            if (y[i] != y[i]) y[i] = 0.f;          // a NaN
             // Steps of e4m3 at y: an eighth of its power of two, 2^-9 at least.  Next to the middle between two
             // codes the exact difference decides, by moving y off that middle.
             const int e = min(max((int)((__float_as_uint(y[i]) >> 23) & 0xffu), 121), 136) - 3;

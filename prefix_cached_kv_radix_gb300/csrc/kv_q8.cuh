@@ -87,4 +87,29 @@ __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t& a, uint32_t& b) 
     }
 }
 
+// Four codes as two pairs of bf16, exact.
+template <int FMT>
+__device__ __forceinline__ void q8_to_bf16(uint32_t w, uint32_t& a, uint32_t& b) {
+    const uint32_t low = w & 0x7f7f7f7fu, top = w & 0x80808080u;
+    if (FMT == RX_Q8_INT8) {
+        // 128 + the code's low seven bits, less 128 or, where its top bit is set, 256
+        const uint32_t x = __byte_perm(low, 0x43434343u, 0x4140), y = __byte_perm(low, 0x43434343u, 0x4342);
+        const uint32_t u = __byte_perm(top, 0x43434343u, 0x4140), v = __byte_perm(top, 0x43434343u, 0x4342);
+        const __nv_bfloat162 p = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&u));
+        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&v));
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    } else {
+        // exponent and mantissa at bf16's places make 2^-120 of the value (the smallest ones bf16 numbers below
+        // 2^-126, which the product takes as they are); 0x7f, e4m3's NaN, which no computed code is, reads as 480
+        const uint32_t x = __byte_perm(low, 0, 0x4140) * 16 + __byte_perm(top, 0, 0x1404);
+        const uint32_t y = __byte_perm(low, 0, 0x4342) * 16 + __byte_perm(top, 0, 0x3424);
+        const uint32_t scale = 0x7b807b80u;                  // 2^120, twice
+        const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&scale));
+        const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&scale));
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    }
+}
+
 }  // namespace rx
