@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 ok = pt_wait(bar(LY::BAR_Q), ic & 1, abort_flag) && pt_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag);
                 ic += 1;
                 if (!ok) break;
-                fence_proxy_async_smem();            // rows that warp 0 copied
+                fence_proxy_async_smem();            // rows and codes that other warps stored, before the tensor core reads them
                 tc_fence_after();
                 for (int t = 0; t < nt; ++t) {
                     issue_s(t, gt % NK);
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     const bool more = j + 1 < nkv;
                     if (!(ok = pt_wait(bar(LY::BAR_VF + vs), (u / NV) & 1, abort_flag))) break;
                     if (more && !(ok = pt_wait(bar(LY::BAR_KF + ks), ((u + 1) / NK) & 1, abort_flag))) break;
+                    fence_proxy_async_smem();
                     for (int t = 0; t < nt; ++t) {
                         const int ph = ((t == 0 ? sc0 : sc1) + j) & 1;
                         for (int h = 0; ok && h < 2; ++h) {
@@ -434,9 +435,12 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
         } else {
             // ------------------------------------------------------------ K/V tiles
             const int lt = warp < 4 ? tid - 64 : tid - 384 + 64;
-            const int c = lt % CPR, key0 = lt / CPR;         // this thread's chunk of every key row it handles
+            // This thread's 16-byte chunk of every key row it handles: 8 lanes have 4 chunks of a 64-channel half of two
+            // neighbouring keys, whose pieces lie in different banks.
+            const int c = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
+            const int key0 = (lt >> 5) * (32 / CPR) + (D == 128 ? ((lane >> 3) & 2) + ((lane >> 2) & 1) : lane >> 2);
             constexpr int STEP = EQ_CONV / CPR;              // keys from one of its rows to the next
-            static_assert(EQ_CONV % CPR == 0, "one chunk per thread");
+            static_assert(EQ_CONV % CPR == 0 && STEP % 8 == 0, "one chunk and one swizzle per thread");
             const uint32_t nslots = (uint32_t)p.num_slots;
             const uint32_t pitch = (uint32_t)(p.hkv * D);
             // The tile whose codes are loaded next, and its slots: one tile ahead of the one being stored.
@@ -498,22 +502,16 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     q8_to_bf16<FMT>(r[x].y, w[2], w[3]);
                     q8_to_bf16<FMT>(r[x].z, w[4], w[5]);
                     q8_to_bf16<FMT>(r[x].w, w[6], w[7]);
-                    // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half; the lanes of the halves take
-                    // them in opposite order, so that eight lanes fill eight different pieces of 128 bytes
-                    const uint32_t row = buf + (uint32_t)((c >> 2) * EQ_BN * 128 + key * 128);
-                    const int swap = c >> 2, cc = (2 * c) & 7;
+                    // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half
+                    const uint32_t row = buf + (uint32_t)((c >> 2) * EQ_BN * 128 + key0 * 128 + x * STEP * 128);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int hh = h ^ swap;
-                        const uint32_t to = row + (uint32_t)(((cc + hh) ^ (key & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hh ? w[4] : w[0]), "r"(hh ? w[5] : w[1]),
-                                     "r"(hh ? w[6] : w[2]), "r"(hh ? w[7] : w[3])
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((((2 * c) & 7) + h) ^ (key0 & 7)) * 16),
+                                     "r"(w[4 * h]), "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
                                      : "memory");
-                    }
                 }
             };
             auto publish = [&](uint32_t full) {
-                fence_proxy_async_smem();                    // stored before the tensor core reads
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
             };
