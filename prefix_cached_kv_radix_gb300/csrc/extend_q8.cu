@@ -78,7 +78,7 @@ struct EqLayout {
     static constexpr int OFF_V = OFF_K + NK * KV_TILE;
     static constexpr int OFF_KS = OFF_V + NV * KV_TILE;              // [NV][128] K scales times scale log2(e)
     static constexpr int OFF_VS = OFF_KS + NV * EQ_BN * 4;           // [NV][128] V scales, -1 for no key
-    static constexpr int OFF_FLAG = OFF_VS + NV * EQ_BN * 4;         // [NV] int4: some key of the tile is at a bad slot
+    static constexpr int OFF_FLAG = OFF_VS + NV * EQ_BN * 4;         // [NV] int4: some key of the tile is at a bad slot or has a scale that is not finite
     static constexpr int OFF_RING = OFF_FLAG + NV * 16;              // 3 int4 an entry
     static constexpr int OFF_SCAN = OFF_RING + EQ_RING * 48;         // int64 per warp, and four results
     static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
@@ -145,11 +145,56 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return d;
 }
 
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
+// Scores and weights of a warp's 32 rows as the tensor core's own fragments have them: lane l holds, of rows l / 4
+// (+ 8) of each 16, columns 2 (l % 4), + 1 of every 8 (16x256b), and of the packed weights column l % 4 of
+// every 4 (16x128b).  So a lane needs the scales of a quarter of the keys, for four rows.
+__device__ __forceinline__ void tmem_ld_scores(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_weights(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_scores8(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 "
+        "{%0,%1,%2,%3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_scores8(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_weights4(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1,%2};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1])
         : "memory");
 }
 
@@ -535,7 +580,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 if (lt < EQ_BN) {
                     reinterpret_cast<float*>(gbase + LY::OFF_KS)[vs * EQ_BN + lt] = sc.x * p.scale_log2;
                     reinterpret_cast<float*>(gbase + LY::OFF_VS)[vs * EQ_BN + lt] = sc.y;
-                    const bool bad = __any_sync(0xffffffffu, kept != -2 && (uint32_t)kept >= nslots);
+                    const bool bad = __any_sync(0xffffffffu, (kept != -2 && (uint32_t)kept >= nslots) || !isfinite(sc.x) || !isfinite(sc.y));
                     if (lane == 0) reinterpret_cast<int*>(gbase + LY::OFF_FLAG)[vs * 4 + lt / 32] = bad ? 1 : 0;
                 }
                 publish(bar(LY::BAR_VF + vs));
@@ -550,52 +595,73 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
     } else {
         // ------------------------------------------------------------ softmax warpgroups
         regs_increase<EQ_REGS_SOFTMAX>();
-        const int t = (warp >> 2) - 1, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const int t = (warp >> 2) - 1, quarter = warp & 3, r8 = lane >> 2, t4 = lane & 3;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16, half = 16u << 16;
         const uint32_t s_addr = tmem + lane_base + t * EQ_BN;   // scores, then weights over them
         const uint32_t o_addr = tmem + lane_base + LY::COL_O0 + t * D;
         int gt = 0, sc = 0, oc = 0;           // K/V tiles of all items, and score steps and items of this Q tile so far
         bool ok = true;
         EqItem it;
+        // of four values, one for each row 8 i + r8 and the same in the row's four lanes: row `lane`'s
+        auto of_row = [&](const float* v) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float y = __shfl_sync(0xffffffffu, v[i], 4 * (lane & 7));
+                if (lane >> 3 == i) x = y;
+            }
+            return x;
+        };
         for (int k = 0; ok && take(k, it); ++k) {
             const int nkv = it.j1 - it.j0;
             if (t >= it.ntiles) {
                 gt += nkv;
                 continue;
             }
-            const int R = it.row0 + t * 128 + r, rows = it.n * G;
-            const int pos = it.before + min(R, rows - 1) / G - it.j0 * EQ_BN;      // sees keys 0 .. pos of this piece
-            float m_ref = -INFINITY, l = 0.f;
+            const int rows = it.n * G, first = it.row0 + t * 128 + quarter * 32;      // the warp's first row
+            int lim[4];                          // row 8 i + r8 sees columns 0 .. lim[i] of the coming tile
+            float m_ref[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lim[i] = it.before + min(first + 8 * i + r8, rows - 1) / G - it.j0 * EQ_BN;
+                m_ref[i] = -INFINITY, l[i] = 0.f;
+            }
             for (int j = 0; j < nkv; ++j, ++gt) {
                 const int vs = gt % NV;
                 if (!(ok = pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag))) break;
                 if (!(ok = pt_wait(bar(LY::BAR_VF + vs), (gt / NV) & 1, abort_flag))) break;     // the scales
                 tc_fence_after();
-                const float* kscale = reinterpret_cast<const float*>(gbase + LY::OFF_KS) + vs * EQ_BN;
-                const float* vscale = reinterpret_cast<const float*>(gbase + LY::OFF_VS) + vs * EQ_BN;
+                const float* kscale = reinterpret_cast<const float*>(gbase + LY::OFF_KS) + vs * EQ_BN + 2 * t4;
+                const float* vscale = reinterpret_cast<const float*>(gbase + LY::OFF_VS) + vs * EQ_BN + 2 * t4;
                 const int4 flag = *reinterpret_cast<const int4*>(gbase + LY::OFF_FLAG + vs * 16);
-                const int lim = pos - j * EQ_BN;      // columns past lim are hidden
-                float alpha = 1.f;
+                float alpha[4], ref[4];
                 bool moved = false;
-                auto refer = [&](float mx) {          // the reference after scores up to mx
-                    float m_new = m_ref;
-                    if (m_ref == -INFINITY || mx > m_ref + EQ_RESCALE) m_new = fmaxf(m_ref, mx);
-                    alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
-                    moved = j > 0 && __any_sync(0xffffffffu, m_new != m_ref);
-                    l *= alpha;
-                    m_ref = m_new;
-                    return m_new == -INFINITY ? 0.f : m_new;
+                auto refer = [&](float* mx) {    // the rows' references after scores up to mx in this lane
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                        float m_new = m_ref[i];
+                        if (m_ref[i] == -INFINITY || mx[i] > m_ref[i] + EQ_RESCALE) m_new = fmaxf(m_ref[i], mx[i]);
+                        alpha[i] = m_ref[i] == -INFINITY ? 0.f : fast_exp2(m_ref[i] - m_new);
+                        moved |= m_new != m_ref[i];
+                        l[i] *= alpha[i];
+                        m_ref[i] = m_new;
+                        ref[i] = m_new == -INFINITY ? 0.f : m_new;
+                    }
+                    moved = j > 0 && __any_sync(0xffffffffu, moved);
                 };
                 auto rescale = [&]() {
                     // PV_t(j-1) has completed (S_t(j) was issued after it and is complete), and PV_t(j) waits for
                     // the arrivals below.  Rare: rolled.
+                    const float a = of_row(alpha);
 #pragma unroll 1
                     for (int cc = 0; cc < D; cc += 32) {
                         float ov[32];
                         tmem_ld32(o_addr + cc, ov);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        for (int e = 0; e < 32; ++e) ov[e] *= a;
                         tmem_st32(o_addr + cc, ov);
                     }
                 };
@@ -605,91 +671,118 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(LY::BAR_P + 2 * h + t));
                 };
-                if (__any_sync(0xffffffffu, lim < EQ_BN - 1) || (flag.x | flag.y | flag.z | flag.w)) {
-                    // Tiles that the causal limit cuts, or with keys at bad slots: what is hidden is taken out by
-                    // selection, scores and weights alike (a hidden key's scales may be anything).  Rolled.
-                    float mx = -INFINITY;
+                if (flag.x | flag.y | flag.z | flag.w) {
+                    // Tiles with a key at a bad slot, or with scales that are not finite, which must not reach rows that do
+                    // not see the key: scores and weights are taken out by selection.  Rolled, eight columns a turn.
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c0 = 0; c0 < EQ_BN; c0 += 32) {
-                        float v[32];
-                        tmem_ld32(s_addr + c0, v);
+                    for (int c0 = 0; c0 < EQ_BN; c0 += 8) {
+                        float v[8];
+                        tmem_ld_scores8(s_addr + c0, v);
+                        tmem_ld_scores8(s_addr + half + c0, v + 4);
                         tmem_wait_ld();
+                        const float2 f = *reinterpret_cast<const float2*>(kscale + c0), w = *reinterpret_cast<const float2*>(vscale + c0);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            v[e] = c0 + e > lim || vscale[c0 + e] == -1.f ? -INFINITY : v[e] * kscale[c0 + e];
-                            mx = fmaxf(mx, v[e]);
+                        for (int x = 0; x < 8; ++x) {
+                            const bool out = c0 + 2 * t4 + (x & 1) > lim[x >> 1] || (x & 1 ? w.y : w.x) == -1.f;
+                            v[x] = out ? -INFINITY : v[x] * (x & 1 ? f.y : f.x);
+                            mx[x >> 1] = fmaxf(mx[x >> 1], v[x]);
                         }
-                        tmem_st32(s_addr + c0, v);
+                        tmem_st_scores8(s_addr + c0, reinterpret_cast<const uint32_t*>(v));
+                        tmem_st_scores8(s_addr + half + c0, reinterpret_cast<const uint32_t*>(v + 4));
                     }
                     tmem_wait_st();
-                    const float ref = refer(mx);
+                    refer(mx);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < EQ_BN; c0 += 32) {     // group c0's weights go to columns already read
-                        float v[32];
-                        uint32_t pk[16];
-                        tmem_ld32(s_addr + c0, v);
+                    for (int c0 = 0; c0 < EQ_BN; c0 += 8) {     // these columns' weights go to columns already read
+                        float v[8];
+                        uint32_t pk[4];
+                        tmem_ld_scores8(s_addr + c0, v);
+                        tmem_ld_scores8(s_addr + half + c0, v + 4);
                         tmem_wait_ld();
+                        const float2 w = *reinterpret_cast<const float2*>(vscale + c0);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float e0 = fast_exp2(v[e] - ref), e1 = fast_exp2(v[e + 1] - ref);
-                            l += e0 + e1;
-                            pk[e >> 1] = pack_bf16x2(v[e] == -INFINITY ? 0.f : e0 * vscale[c0 + e],
-                                                     v[e + 1] == -INFINITY ? 0.f : e1 * vscale[c0 + e + 1]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float e0 = fast_exp2(v[2 * i] - ref[i]), e1 = fast_exp2(v[2 * i + 1] - ref[i]);
+                            l[i] += e0 + e1;
+                            pk[i] = pack_bf16x2(v[2 * i] == -INFINITY ? 0.f : e0 * w.x, v[2 * i + 1] == -INFINITY ? 0.f : e1 * w.y);
                         }
-                        tmem_st16u(s_addr + c0 / 2, pk);
+                        tmem_st_weights4(s_addr + c0 / 2, pk);
+                        tmem_st_weights4(s_addr + half + c0 / 2, pk + 2);
                     }
                     if (moved) rescale();
                     publish(0);
                     publish(1);
-                    continue;
-                }
-                float s[EQ_BN];
+                } else {
+                    float s[2][64];              // [16 rows][columns 8 i + 2 t4, + 1 of row r8, then of row r8 + 8]
+                    tmem_ld_scores(s_addr, s[0]);
+                    tmem_ld_scores(s_addr + half, s[1]);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < EQ_BN; c += 32) tmem_ld32(s_addr + c, s + c);
-                tmem_wait_ld();
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t f = *reinterpret_cast<const uint64_t*>(kscale + 8 * i);
 #pragma unroll
-                for (int c = 0; c < EQ_BN; c += 4) {
-                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(kscale + c);
-                    f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f.x), s[c], s[c + 1]);
-                    f2_unpack(f2_mul(f2_pack(s[c + 2], s[c + 3]), f.y), s[c + 2], s[c + 3]);
-                }
-                float mx8[8];
+                        for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx8[i] = s[i];
-#pragma unroll
-                for (int c = 8; c + 16 <= EQ_BN; c += 16)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx8[i] = fmax3(mx8[i], s[c + i], s[c + 8 + i]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], s[EQ_BN - 8 + i]);
-                const float ref = refer(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-                const uint64_t nm2 = f2_pack(-ref, -ref);
-                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-                // weights in two halves of 64 keys (32 columns), each published as soon as it is stored
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[EQ_BN / 4];
-#pragma unroll
-                    for (int cc = 0; cc < EQ_BN / 2; cc += 4) {
-                        const int c = h * (EQ_BN / 2) + cc;
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(vscale + c);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x0, x1;
-                            f2_unpack(f2_add(f2_pack(s[c + 2 * i], s[c + 2 * i + 1]), nm2), x0, x1);
-                            const uint64_t e2 = f2_pack(fast_exp2(x0), fast_exp2(x1));
-                            acc2[((c >> 1) + i) & 3] = f2_add(acc2[((c >> 1) + i) & 3], e2);
-                            f2_unpack(f2_mul(e2, i ? f.y : f.x), x0, x1);
-                            pk[(cc >> 1) + i] = pack_bf16x2(x0, x1);
-                        }
+                            for (int x = 0; x < 4; x += 2)
+                                f2_unpack(f2_mul(f2_pack(s[a][4 * i + x], s[a][4 * i + x + 1]), f), s[a][4 * i + x], s[a][4 * i + x + 1]);
                     }
-                    tmem_st32u(s_addr + h * 32, pk);
-                    if (h == 0 && moved) rescale();
-                    publish(h);
+                    if (__any_sync(0xffffffffu, lim[0] < EQ_BN - 1)) {       // the causal limit cuts this tile (rows' limits ascend)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (8 * i + 2 * t4 + (x & 1) > lim[x >> 1]) s[x >> 2][4 * i + (x & 3)] = -INFINITY;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float* v = s[q >> 1] + 2 * (q & 1);
+                        float a = v[0], b = v[4], c = v[8], d = v[12];
+                        a = fmaxf(a, v[1]), b = fmaxf(b, v[5]), c = fmaxf(c, v[9]), d = fmaxf(d, v[13]);
+#pragma unroll
+                        for (int i = 4; i < 16; i += 4) {
+                            a = fmax3(a, v[4 * i], v[4 * i + 1]);
+                            b = fmax3(b, v[4 * i + 4], v[4 * i + 5]);
+                            c = fmax3(c, v[4 * i + 8], v[4 * i + 9]);
+                            d = fmax3(d, v[4 * i + 12], v[4 * i + 13]);
+                        }
+                        mx[q] = fmaxf(fmax3(a, b, c), d);
+                    }
+                    refer(mx);
+                    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+                    // weights in two halves of 64 keys (32 columns), each published as soon as it is stored
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[2][16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint64_t f = *reinterpret_cast<const uint64_t*>(vscale + 64 * h + 8 * i);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float* v = s[q >> 1] + 32 * h + 4 * i + 2 * (q & 1);
+                                float x0, x1;
+                                f2_unpack(f2_add(f2_pack(v[0], v[1]), f2_pack(-ref[q], -ref[q])), x0, x1);
+                                const uint64_t e2 = f2_pack(fast_exp2(x0), fast_exp2(x1));
+                                acc2[q] = f2_add(acc2[q], e2);
+                                f2_unpack(f2_mul(e2, f), x0, x1);
+                                pk[q >> 1][2 * i + (q & 1)] = pack_bf16x2(x0, x1);
+                            }
+                        }
+                        tmem_st_weights(s_addr + h * 32, pk[0]);
+                        tmem_st_weights(s_addr + half + h * 32, pk[1]);
+                        if (h == 0 && moved) rescale();
+                        publish(h);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float ra, rb;
+                        f2_unpack(acc2[q], ra, rb);
+                        l[q] += ra + rb;
+                    }
                 }
-                float ra, rb;
-                f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), ra, rb);
-                l += ra + rb;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lim[i] -= EQ_BN;
             }
             if (!ok) break;
             sc += nkv;
@@ -698,10 +791,17 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             if (!(ok = pt_wait(bar(LY::BAR_OR + t), oc & 1, abort_flag))) break;
             oc += 1;
             tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            }
+            const float sum = of_row(l), top = of_row(m_ref);
+            const int r = quarter * 32 + lane, R = first + lane;
             const bool valid = R < rows;
             const int tok = min(R, rows - 1) / G, h = it.g * G + min(R, rows - 1) % G;
             const int64_t at = (it.q0 + tok) * p.hq + h;
-            const float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : m_ref + log2f(l);      // no key: zeros
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, lse = sum == 0.f ? -INFINITY : top + log2f(sum);      // no key: zeros
             const int64_t part = ((int64_t)blockIdx.x * 2 + it.slot) * EQ_ROWS + t * 128 + r;
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 32) {
