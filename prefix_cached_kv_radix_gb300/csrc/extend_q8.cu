@@ -81,15 +81,16 @@ struct EqLayout {
     static constexpr int OFF_FLAG = OFF_VS + NV * EQ_BN * 4;         // [NV] int4: some key of the tile is at a bad slot or has a scale that is not finite
     static constexpr int OFF_RING = OFF_FLAG + NV * 16;              // 3 int4 an entry
     static constexpr int OFF_SCAN = OFF_RING + EQ_RING * 48;         // int64 per warp, and four results
-    static constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
+    static constexpr int CPR = D / 16;                               // 16-byte chunks of a row's codes
+    static constexpr int NX = (EQ_BN * CPR + EQ_CONV - 1) / EQ_CONV; // chunks per converter thread, tile and pool
+    static constexpr int OFF_CODES = OFF_SCAN + 20 * 8;              // [NX][EQ_CONV] 16-byte chunks of the coming K tile's codes
+    static constexpr int OFF_BAR = OFF_CODES + NX * EQ_CONV * 16;
     static constexpr int BAR_Q = 0, BAR_KF = 1, BAR_KE = BAR_KF + NK, BAR_VF = BAR_KE + NK, BAR_VE = BAR_VF + NV, BAR_S = BAR_VE + NV,
                          BAR_P = BAR_S + 2, BAR_QE = BAR_P + 4, BAR_OR = BAR_QE + 2, BAR_IF = BAR_OR + 2, BAR_IE = BAR_IF + EQ_RING,
                          BAR_DONE = BAR_IE + EQ_RING, NBAR = BAR_DONE + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;              // TMEM address, abort flag
     static constexpr int ALLOC = OFF_MISC + 8 + 1024;                // room to align the base to 1024 B
     static constexpr uint32_t TMEM_COLS = 512, COL_O0 = 256;
-    static constexpr int CPR = D / 16;                               // 16-byte chunks of a row's codes
-    static constexpr int NX = (EQ_BN * CPR + EQ_CONV - 1) / EQ_CONV; // chunks per converter thread, tile and pool
     static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
@@ -521,15 +522,20 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 }
                 load_slots();
             };
-            uint4 kr[NX], vr[NX];
+            // The coming K tile's codes travel to shared memory, to where the thread that widens them reads them; the coming
+            // V tile's to registers (both in registers, some were spilled and waited for at once: 720 TFLOP/s).
+            // Each chunk's place is filled again as soon as its codes are stored, so a load has a whole tile's time.
+            const uint32_t codes = base + LY::OFF_CODES + lt * 16;
+            uint4 vr[NX];
             float2 sc = make_float2(0.f, 0.f);
-            int32_t kept = -2;                               // ss of the tile in the registers
-            auto load_codes = [&](uint4* r, const uint8_t* from) {
-#pragma unroll
-                for (int x = 0; x < NX; ++x) {
-                    r[x] = make_uint4(0, 0, 0, 0);
-                    if ((uint32_t)sl[x] < nslots) r[x] = *reinterpret_cast<const uint4*>(from + (size_t)(uint32_t)sl[x] * pitch);
-                }
+            int32_t kept = -2;                               // ss of the V tile in the registers
+            auto fetch_k = [&](int x) {
+                const bool in = (uint32_t)sl[x] < nslots;
+                cp_async_16(codes + x * EQ_CONV * 16, kb + (size_t)(in ? (uint32_t)sl[x] : 0u) * pitch, in ? 16u : 0u);
+            };
+            auto fetch_v = [&](int x) {
+                vr[x] = make_uint4(0, 0, 0, 0);
+                if ((uint32_t)sl[x] < nslots) vr[x] = *reinterpret_cast<const uint4*>(vb + (size_t)(uint32_t)sl[x] * pitch);
             };
             auto load_scale = [&]() {
                 kept = ss;
@@ -537,60 +543,75 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 if ((uint32_t)ss < nslots) sc = sb[(int64_t)(ss >> p.pools.shift) * p.hkv];
                 else if (ss != -2) report(p.status, RX_DEV_BAD_SLOT);
             };
-            auto store = [&](const uint4* r, uint32_t buf) {
+            // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half
+            const uint32_t piece = (uint32_t)((c >> 2) * EQ_BN * 128 + key0 * 128 + ((2 * c) & 7) * 16) ^ (uint32_t)((key0 & 7) * 16);
+            auto store = [&](const uint4& r, int x, uint32_t buf) {
+                uint32_t w[8];
+                q8_to_bf16<FMT>(r.x, w[0], w[1]);
+                q8_to_bf16<FMT>(r.y, w[2], w[3]);
+                q8_to_bf16<FMT>(r.z, w[4], w[5]);
+                q8_to_bf16<FMT>(r.w, w[6], w[7]);
 #pragma unroll
-                for (int x = 0; x < NX; ++x) {
-                    const int key = key0 + x * STEP;
-                    if (key >= EQ_BN) continue;
-                    uint32_t w[8];
-                    q8_to_bf16<FMT>(r[x].x, w[0], w[1]);
-                    q8_to_bf16<FMT>(r[x].y, w[2], w[3]);
-                    q8_to_bf16<FMT>(r[x].z, w[4], w[5]);
-                    q8_to_bf16<FMT>(r[x].w, w[6], w[7]);
-                    // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half
-                    const uint32_t row = buf + (uint32_t)((c >> 2) * EQ_BN * 128 + key0 * 128 + x * STEP * 128);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((((2 * c) & 7) + h) ^ (key0 & 7)) * 16),
-                                     "r"(w[4 * h]), "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
-                                     : "memory");
-                }
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + x * STEP * 128 + (h ? piece ^ 16u : piece)),
+                                 "r"(w[4 * h]), "r"(w[4 * h + 1]), "r"(w[4 * h + 2]), "r"(w[4 * h + 3])
+                                 : "memory");
             };
             auto publish = [&](uint32_t full) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);
             };
-            bool cur = have;                                 // a tile is in the registers
+            bool cur = have;                                 // a tile's codes are on their way
             if (have) {
                 begin();
                 load_slots();
-                load_codes(kr, kb);
-                load_codes(vr, vb);
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    fetch_k(x);
+                    fetch_v(x);
+                }
+                cp_async_commit();
                 load_scale();
                 next();
             }
             for (int u = 0; cur; ++u) {
                 const int ks = u % NK, vs = u % NV;
                 if (u >= NK && !pt_wait(bar(LY::BAR_KE + ks), ((u / NK) - 1) & 1, abort_flag)) break;
-                store(kr, base + LY::OFF_K + ks * LY::KV_TILE);
+                cp_async_wait<0>();
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+                    if (key0 + x * STEP < EQ_BN) {
+                        uint4 r;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                                     : "r"(codes + x * EQ_CONV * 16)
+                                     : "memory");
+                        store(r, x, base + LY::OFF_K + ks * LY::KV_TILE);
+                        if (have) fetch_k(x);
+                    }
+                cp_async_commit();
                 publish(bar(LY::BAR_KF + ks));
-                if (have) load_codes(kr, kb);
                 if (u >= NV && !pt_wait(bar(LY::BAR_VE + vs), ((u / NV) - 1) & 1, abort_flag)) break;
-                store(vr, base + LY::OFF_V + vs * LY::KV_TILE);
                 if (lt < EQ_BN) {
                     reinterpret_cast<float*>(gbase + LY::OFF_KS)[vs * EQ_BN + lt] = sc.x * p.scale_log2;
                     reinterpret_cast<float*>(gbase + LY::OFF_VS)[vs * EQ_BN + lt] = sc.y;
                     const bool bad = __any_sync(0xffffffffu, (kept != -2 && (uint32_t)kept >= nslots) || !isfinite(sc.x) || !isfinite(sc.y));
                     if (lane == 0) reinterpret_cast<int*>(gbase + LY::OFF_FLAG)[vs * 4 + lt / 32] = bad ? 1 : 0;
                 }
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+                    if (key0 + x * STEP < EQ_BN) {
+                        store(vr[x], x, base + LY::OFF_V + vs * LY::KV_TILE);
+                        if (have) fetch_v(x);
+                    }
                 publish(bar(LY::BAR_VF + vs));
                 cur = have;
                 if (have) {
-                    load_codes(vr, vb);
                     load_scale();
                     next();
                 }
             }
+            cp_async_wait_all();
         }
     } else {
         // ------------------------------------------------------------ softmax warpgroups
