@@ -32,6 +32,7 @@
 #include "rx_device.cuh"
 #include "rx_launch.h"
 #include "rx_q8.h"
+#include "share_out.cuh"
 #include "tc_issue.cuh"
 
 namespace rx {
@@ -250,62 +251,14 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
     pdl_wait();                          // what came before has finished; nothing global was touched so far
 
     // ---------------------------------------------------------------- this CTA's part of the units
-    // scan[16], scan[17]: the first unit of this part and of the next; scan[18], scan[19]: the request of the first, and the
-    // units before that request
-    {
-        auto warp_sum = [&](int64_t v) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            return v;
-        };
-        int64_t v = 0, mine = 0;         // this thread's request's units (of the last round), and those of all its requests
-        for (int b = tid; b < p.batch; b += EQ_THREADS) {
-            v = eq_units(p, b, blockIdx.x == 0) * p.hkv;
-            mine += v;
-        }
-        mine = warp_sum(mine);
-        if (lane == 0) scan[warp] = mine;
-        if (tid < 4) scan[16 + tid] = 0;
-        __syncthreads();
-        int64_t total = 0;
-#pragma unroll
-        for (int w = 0; w < EQ_THREADS / 32; ++w) total += scan[w];
-        // at least two tiles a CTA; borders within a sixteenth of a part of an item's ends move there
-        const int64_t parts = max(min((int64_t)gridDim.x, total / 2), (int64_t)1);
-        const int64_t near = 1 + total / parts / 16;
-        const int64_t want[2] = {min((int64_t)blockIdx.x, parts) * total / parts, min((int64_t)blockIdx.x + 1, parts) * total / parts};
-        int64_t before = 0;              // units of the rounds so far
-        for (int b0 = 0; b0 < p.batch; b0 += EQ_THREADS) {
-            const int b = b0 + tid;
-            if (p.batch > EQ_THREADS) v = b < p.batch ? eq_units(p, b, false) * p.hkv : 0;
-            else if (b >= p.batch) v = 0;
-            int64_t inc = v;             // inclusive scan
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += x;
-            }
-            __syncthreads();             // the sums of the round before are read
-            if (lane == 31) scan[warp] = inc;
-            __syncthreads();
-            int64_t at = before + inc - v;
-            for (int w = 0; w < warp; ++w) at += scan[w];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (want[e] >= at && want[e] < at + v) {
-                    int g, row0, j, tiles;
-                    eq_locate(p, b, v / p.hkv, want[e] - at, g, row0, j, tiles);
-                    const int64_t to = want[e] + (j < near ? -j : tiles - j < near ? tiles - j : 0);
-                    scan[16 + e] = to;
-                    if (e == 0) scan[18] = b, scan[19] = at;
-                }
-            for (int w = 0; w < EQ_THREADS / 32; ++w) before += scan[w];
-        }
-        if (tid == 0) {                  // past the last unit
-            if (want[0] >= total) scan[16] = total;
-            if (want[1] >= total) scan[17] = total;
-        }
-    }
+    // at least two tiles a CTA; borders close to an item's ends move there
+    share_out<EQ_THREADS>(
+        p.batch, 2, scan, scan + 16, [&](int b, bool tell) { return eq_units(p, b, tell) * p.hkv; },
+        [&](int b, int64_t at, int64_t near) {
+            int g, row0, j, tiles;
+            eq_locate(p, b, eq_units(p, b, false), at, g, row0, j, tiles);
+            return at + (j < near ? -j : tiles - j < near ? tiles - j : 0);
+        });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -342,7 +295,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             if (cur < end) {
                 // the border may have moved past the end of its request
                 int64_t units = eq_units(p, b, false), at = cur - scan[19];
-                while (at >= units * p.hkv) {
+                while (b + 1 < p.batch && at >= units * p.hkv) {
                     at -= units * p.hkv;
                     units = eq_units(p, ++b, false);
                 }
@@ -400,8 +353,9 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     row0 = 0;
                     if (++g == p.hkv) {
                         g = 0;
-                        do eq_request(p, ++b, false, q0, n, before);
-                        while (n == 0);
+                        do n = 0;
+                        while (++b < p.batch && (eq_request(p, b, false, q0, n, before), n == 0));
+                        if (n == 0) break;
                     }
                 }
                 tiles = eq_tiles(row0, n * G, G, before);
@@ -867,66 +821,29 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
     }
 }
 
-// The parts of an item that starts in CTA blockIdx.x and goes on in later ones: 32 of its rows a block, 8 a warp.
+// Rows from their parts: blockIdx.x the begun and not ended item, four rows a block, a warp each.
 template <int D>
 __global__ void __launch_bounds__(128) extend_q8_merge_kernel(const __grid_constant__ ExtendQ8Params p) {
+    constexpr int E = D / 32;
     __shared__ int list[EQ_CTAS];
-    __shared__ int count;
+    __shared__ uint32_t room[EQ_CTAS];
     pdl_launch_dependents();
     pdl_wait();
-    const int4 item = p.meta[blockIdx.x * 2 + 1];
-    if (item.x < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int count = parts_of<EQ_CTAS>(p.meta, blockIdx.x, EQ_CTAS, list, room);
+    if (count == 0) return;
+    const int4 item = p.meta[list[0]];
     int64_t q0;
     int n, before;
     eq_request(p, item.x, false, q0, n, before);
-    const int rows = n * p.group, r0 = blockIdx.y * 32;
-    if (item.z + r0 >= rows) return;
-    if (warp == 0) {
-        int parts = 1;
-        if (lane == 0) list[0] = blockIdx.x * 2 + 1;
-        bool done = false;
-        for (int c0 = blockIdx.x + 1; c0 < (int)gridDim.x && !done; c0 += 32) {
-            const int c = c0 + lane;
-            const int4 m = c < (int)gridDim.x ? p.meta[c * 2] : make_int4(-1, 0, 0, 0);
-            const unsigned ends = __ballot_sync(0xffffffffu, m.x >= 0 && m.w);
-            const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;      // to the part that ends the item
-            const unsigned is = __ballot_sync(0xffffffffu, m.x >= 0) & upto;
-            if ((is >> lane) & 1u) list[parts + __popc(is & ((1u << lane) - 1u))] = c * 2;
-            parts += __popc(is);
-            done = ends != 0;
-        }
-        if (lane == 0) count = parts;
-    }
-    __syncthreads();
-    const int parts = count;
-    constexpr int E = D / 32;
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + warp * 8 + i, R = item.z + r;
-        if (R >= rows) return;
-        float M = -INFINITY;
-        for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_lse[(int64_t)list[s] * EQ_ROWS + r]);
+    const int r = blockIdx.y * 4 + warp, R = item.z + r;
+    if (R >= n * p.group) return;
+    float acc[E];
+    const float lse = merge_few<D>(list, count, p.part_o, p.part_lse, EQ_ROWS, r, acc);
+    const int64_t at = (q0 + R / p.group) * p.hq + item.y * p.group + R % p.group;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float acc[E], W = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int s = 0; s < parts; ++s) {
-            const int64_t at = (int64_t)list[s] * EQ_ROWS + r;
-            const float w = exp2f(p.part_lse[at] - ref);
-            W += w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += w * p.part_o[at * D + lane * E + e];
-        }
-        const float inv = W == 0.f ? 0.f : 1.f / W;
-        const int64_t at = (q0 + R / p.group) * p.hq + item.y * p.group + R % p.group;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        if (p.lse && lane == 0) p.lse[at] = W == 0.f ? -INFINITY : (M + log2f(W)) * EQ_LN2;
-    }
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) = pack_bf16x2(acc[e], acc[e + 1]);
+    if (p.lse && lane == 0) p.lse[at] = lse * EQ_LN2;
 }
 
 // The current device must be an sm_103: checked once per device.
@@ -995,7 +912,8 @@ static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
     cudaError_t e = launch_pdl(extend_q8_kernel<D, FMT>, EQ_CTAS, EQ_THREADS, smem, s, p);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(EQ_CTAS, EQ_ROWS / 32);
+        const int64_t items = (((int64_t)p.max_qo_len * p.group + EQ_ROWS - 1) / EQ_ROWS) * p.hkv * p.batch;
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, EQ_CTAS), EQ_ROWS / 4);
         cfg.blockDim = dim3(128);
         cfg.stream = s;
         cudaLaunchAttribute pdl[1];

@@ -7,13 +7,17 @@
 // each sum over its own running maximum: vs enters the exponent, so that what is weighed and rounded to 16 bits is 2^(y_j - max y)
 // next to the largest term of o, however far apart the rows' scales are.
 //
-// One CTA per (request, chunk of keys, row tile, kv head); 16-byte cp.async gathers of 64-key stages of codes, 3 deep,
-// and of their scales.  Each warp takes 16 keys of a stage: S^T = K Q^T with the keys in M of m16n8k16, then
-// O^T += V^T P^T.  Codes become f16 in registers, where they are exact (int8 and e4m3 both): K fragments by ldmatrix over 16-byte
-// rows, four neighbouring channels a lane, which the query fragments follow; V by ldmatrix.trans over byte
-// pairs, whose two channels are parted by the byte permutation that widens them.  Queries are f16 after a
-// power of two per row that brings the row's largest to 2^14 (bf16 is exact in that down to 2^-29 of the largest); f32 rows
-// and f32 rows' weights are two f16 parts each, 22 bits.
+// A CTA of eight warps takes a run of a request's keys, a row tile and 1, 2, 4 or 8 neighbouring kv heads: a warp a head, or 8, 4, 2
+// warps sharing one, 16 keys of a stage each.  The heads of a slot lie side by side in the pools, so a stage is
+// gathered (16-byte cp.async, three stages deep) in pieces of up to 1 KB: slots are scattered, and pieces of 128 bytes, a head
+// a CTA, cost a quarter of the bandwidth.  Short contexts are a CTA's each, whole.  Else the stages of all requests, one
+// after another, are shared out evenly over the CTAs that are resident at a time (with chunks of one size, the last round
+// of CTAs left SMs idle for a third of the time), and rows that a border cuts are merged from normalised parts by a second kernel.
+// S^T = K Q^T with the keys in M of m16n8k16, then O^T += V^T P^T.  Codes become f16 in registers, where they are exact
+// (int8 and e4m3 both): K fragments by ldmatrix over 16-byte rows, four neighbouring channels a lane, which the query
+// fragments follow; V by ldmatrix.trans over byte pairs, whose two channels are parted by the byte permutation that
+// widens them.  Queries are f16 after a power of two per row that brings the row's largest to 2^14 (bf16 is exact in that
+// down to 2^-29 of the largest); f32 rows' queries and weights are two f16 parts each, 22 bits.
 // Bound by HBM: 2 d + 8 bytes a key and kv head, read once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,24 +32,34 @@
 #include "rx_device.cuh"
 #include "rx_launch.h"
 #include "rx_q8.h"
+#include "share_out.cuh"
 
 namespace rx {
 
-constexpr int RQ_THREADS = 128;
-constexpr int RQ_STAGE = 64;          // keys per stage, 16 a warp
+constexpr int RQ_THREADS = 256;
+constexpr int RQ_WARPS = RQ_THREADS / 32;
+constexpr int RQ_KEYS = 16;           // keys of a warp's stage
 constexpr int RQ_NS = 3;              // stages
-constexpr int RQ_CHUNK = 1024;        // most keys per CTA (their slots are staged in shared memory)
+constexpr int RQ_CTAS = 152 * 3;      // most CTAs that stages are shared out to
 constexpr float RQ_LOG2E = 1.4426950408889634f, RQ_LN2 = 0.6931471805599453f;
 constexpr float RQ_TOP = 15.f;        // a row's largest weight is 2^15 in f16
 
 template <int D>
 struct RowsLayout {
-    static constexpr int CODES = RQ_STAGE * D;                         // one pool's codes of a stage
-    static constexpr int STAGE = 2 * CODES + RQ_STAGE * 8;             // K, V, scales
-    static constexpr int SLOTS = RQ_NS * STAGE;
-    static constexpr int BYTES = SLOTS + RQ_CHUNK * 4;
-    static constexpr int RS = D + 4;                                   // floats between merged rows
+    static constexpr int CODES = RQ_KEYS * D;                          // one pool's codes of a warp's stage
+    static constexpr int WARP = 2 * CODES + RQ_KEYS * 8;               // K, V, scales
+    static constexpr int STAGE = RQ_WARPS * WARP;
+    static constexpr int BYTES = RQ_NS * STAGE;
+    static constexpr int RS = D + 4;                                   // floats between rows that are joined
+    // eight warps' 8 rows, their statistics, weights and each row's lse
+    static constexpr int JOIN = RQ_WARPS * 8 * (RS + 5) * 4;
+    static_assert(JOIN <= BYTES, "the ring holds what is joined");
 };
+
+// CTAs an SM holds: registers.
+constexpr int rows_a_sm(bool f32, int D, int nt) { return nt > 1 ? 1 : f32 ? (D == 64 ? 2 : 1) : D == 64 ? 3 : 2; }
+template <typename T, int D, int NT>
+constexpr int rows_a_sm() { return rows_a_sm(sizeof(T) == 4, D, NT); }
 
 // 16-byte chunk c of key row `key`: rows of 128 bytes, or two of 64 to a line, so that 8 rows' chunks lie in different banks.
 template <int D>
@@ -53,8 +67,9 @@ __device__ __forceinline__ uint32_t code_at(int key, int c) {
     return D == 128 ? (uint32_t)(key * 128 + ((c ^ (key & 7)) << 4)) : (uint32_t)(key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// With the neighbouring 32-byte sector: scales of a slot's other heads, which other warps want at about the same time.
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // D(16x8 fp32) += A(16x16 f16, row) * B(16x8 f16, col)
@@ -83,7 +98,6 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
-// cells of the grid, kv head fastest, so that neighbouring CTAs share the lines of scales
 struct RowsParams {
     const void* q;
     const int64_t* qo_indptr;         // extend only
@@ -94,12 +108,15 @@ struct RowsParams {
     Q8Pools pools;
     int32_t batch, hq, hkv, group;
     int32_t max_qo_len, max_kv_len;
-    int32_t tiles, chunks, chunk;     // row tiles, splits of the keys, keys of a split (a multiple of RQ_STAGE)
+    int32_t tiles;                    // row tiles
+    int32_t shared;                   // 1: stages shared out over the CTAs; 0: a CTA a (request, row tile, group of heads)
+    int32_t hb;                       // log2 of the kv heads a CTA takes
     float scale_log2;
     void* out;
     float* lse;
-    float* part_o;                    // [batch * max_qo_len * hq][chunks][D], where chunks > 1
-    float* part_lse;
+    float* part_o;                    // [CTAs][2][heads of a CTA][rows of a tile][D], normalised
+    float* part_lse;                  // base 2
+    int4* meta;                       // [CTAs][2]: request (-1: no part), row tile, first head, whether its keys end here
     int32_t* status;
 };
 
@@ -120,6 +137,20 @@ __device__ __forceinline__ bool rows_of(const RowsParams& p, int b, bool tell, i
     return false;
 }
 
+// Stages of a row tile (one at least: a row of no keys is written too), and of all tiles and groups of heads of a request.
+__device__ __forceinline__ int tile_stages(const RowsParams& p, int n, int before, int tile, int rows_a_tile, int span) {
+    const int last = min((tile + 1) * rows_a_tile, n * p.group) - 1;
+    return max(before + last / p.group + span, span) / span;
+}
+
+__device__ __forceinline__ int64_t request_stages(const RowsParams& p, int b, bool tell, int rows_a_tile, int span) {
+    int64_t q0, sum = 0;
+    int n, before;
+    if (!rows_of(p, b, tell, q0, n, before)) return 0;
+    for (int t = 0; t * rows_a_tile < n * p.group; ++t) sum += tile_stages(p, n, before, t, rows_a_tile, span);
+    return sum * (p.hkv >> p.hb);
+}
+
 template <typename T>
 __device__ __forceinline__ void store_row2(T* p, float a, float b);
 template <>
@@ -128,44 +159,121 @@ template <>
 __device__ __forceinline__ void store_row2(__nv_bfloat16* p, float a, float b) { *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b); }
 
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(RQ_THREADS) rows_q8_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_kernel(const __grid_constant__ RowsParams p) {
     using LY = RowsLayout<D>;
     constexpr bool TWO = std::is_same<T, float>::value;     // two f16 parts
     constexpr int KS = D / 16;                              // 16-byte chunks of a row: steps of K, and of V's M
-    constexpr int CPT = RQ_STAGE * KS / RQ_THREADS;         // copies per thread, stage and pool
+    constexpr int CPT = RQ_WARPS * RQ_KEYS * KS / RQ_THREADS;    // copies per thread, stage and pool
+    constexpr int WPI = RQ_THREADS / 32;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t4 = lane & 3, r8 = lane >> 2;
-    int cell = blockIdx.x;
-    const int g = cell % p.hkv;
-    cell /= p.hkv;
-    const int tile = cell % p.tiles;
-    cell /= p.tiles;
-    const int c = cell % p.chunks, b = cell / p.chunks;
+    const int HB = 1 << p.hb, ways = WPI >> p.hb, way = warp >> p.hb, span = RQ_KEYS * ways;      // span: keys of a stage
+    constexpr int RT = 8 * NT;                                         // rows of a tile
+    const int G = p.group, groups = p.hkv >> p.hb;
+    __shared__ int64_t share[RQ_WARPS + 4];
+    int b, tile, gi, s0 = 0;             // the piece: request, row tile, group of heads, first stage
+    int64_t left = 1;                    // stages of this CTA's part
+    if (p.shared) {
+        auto locate = [&](int r, int64_t at, int& t, int& gr, int& stages) {       // stage `at` of request r's; returns the tile's
+            int64_t q;
+            int m, bf;
+            rows_of(p, r, false, q, m, bf);
+            for (t = 0;; ++t) {
+                stages = tile_stages(p, m, bf, t, RT, span);
+                if (at < (int64_t)stages * groups) break;
+                at -= (int64_t)stages * groups;
+            }
+            gr = (int)(at / stages);
+            return (int)(at - (int64_t)gr * stages);
+        };
+        share_out<RQ_THREADS>(
+            p.batch, 4, share, share + RQ_WARPS, [&](int r, bool tell) { return request_stages(p, r, tell, RT, span); },
+            [&](int r, int64_t at, int64_t near) {
+                int t, gr, stages;
+                const int j = locate(r, at, t, gr, stages);
+                return at + (j < near ? -j : stages - j < near ? stages - j : 0);
+            });
+        __syncthreads();
+        int64_t at = share[RQ_WARPS] - share[RQ_WARPS + 3];
+        left = share[RQ_WARPS + 1] - share[RQ_WARPS];
+        b = (int)share[RQ_WARPS + 2];
+        if (left > 0) {                  // the border may have moved past the end of its request
+            for (int64_t all; b + 1 < p.batch && at >= (all = request_stages(p, b, false, RT, span)); ++b) at -= all;
+            int stages;
+            s0 = locate(b, at, tile, gi, stages);
+        }
+    } else {
+        uint32_t cell = blockIdx.x;
+        gi = (int)(cell % (uint32_t)groups);
+        cell /= (uint32_t)groups;
+        tile = (int)(cell % (uint32_t)p.tiles);
+        b = (int)(cell / (uint32_t)p.tiles);
+    }
+    int4 told[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};
+    for (; left > 0;) {
+    const int g0 = gi << p.hb, g = g0 + (warp & (HB - 1)), R0 = tile * RT, k_begin = s0 * span;
+    // What this thread copies of a stage: 16-byte chunk `col` of the heads' HB * D bytes of every key it handles, and for the first
+    // 16 WPI threads one key's scales of one head.  The slots of a stage's keys are loaded two stages before their codes 
+    // the first ones up to the table's stride beside the request's lengths, not after them.
+    const int cols = KS << p.hb, col = tid & (cols - 1), row0 = tid / cols, rstep = RQ_THREADS / cols;
+    const int skey = tid >> p.hb, shead = tid & (HB - 1);              // scales: key of the stage, head
+    const int32_t* table = p.r2t + (int64_t)b * p.stride + k_begin;
+    const int64_t width = p.stride - k_begin;
+    int32_t sl[CPT], ss;
+    auto load_slots = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) {
+            const int key = i * span + row0 + x * rstep;
+            sl[x] = key < width ? table[key] : -1;
+        }
+        const int key = i * span + skey;
+        ss = skey < span && key < width ? table[key] : -1;
+    };
+    load_slots(0);
     int64_t q0;
     int n, before;
-    if (!rows_of(p, b, tid == 0 && g == 0 && tile == 0 && c == 0, q0, n, before)) return;
-    const int G = p.group, rows = n * G, R0 = tile * 8 * NT;
-    if (R0 >= rows) return;
-    const int last = min(R0 + 8 * NT, rows) - 1;
-    const int k_begin = c * p.chunk;
-    const int nk = min(before + last / G + 1 - k_begin, p.chunk);      // keys of this CTA
-    if (nk <= 0 && c > 0) return;                                      // chunk 0 writes the row of no keys
-    int32_t* slot_s = reinterpret_cast<int32_t*>(smem + LY::SLOTS);
-    const int nstages = max(nk + RQ_STAGE - 1, 0) / RQ_STAGE;
-    bool bad = false;
-    {
-        const int32_t* row = p.r2t + (int64_t)b * p.stride + k_begin;
-        for (int i = tid; i < nstages * RQ_STAGE; i += RQ_THREADS) {
-            int32_t s = i < nk ? row[i] : -1;
-            if (i < nk && (s < 0 || s >= p.num_slots)) {
-                report(p.status, RX_DEV_BAD_SLOT);
-                s = -1;
-                bad = true;
-            }
-            slot_s[i] = s;
+    const bool there = rows_of(p, b, !p.shared && tid == 0 && gi == 0 && tile == 0, q0, n, before);
+    const int rows = there ? n * G : 0;
+    if (R0 >= rows) break;                                             // no rows of this cell (not shared)
+    const int last = min(R0 + RT, rows) - 1, stages = tile_stages(p, n, before, tile, RT, span);
+    const int s1 = p.shared ? (int)min((int64_t)stages, s0 + left) : stages;
+    const bool whole = s0 == 0 && s1 == stages;
+    const int slot = s0 == 0 ? 1 : 0;
+    if (!whole) told[slot] = make_int4(b, tile, g0, s1 == stages ? 1 : 0);
+    const int nk = min(before + last / G + 1, s1 * span) - k_begin;    // keys of this piece
+    const int nstages = max(nk + span - 1, 0) / span;
+    const uint32_t ring = smem_u32(smem);
+    const int64_t pitch = (int64_t)p.hkv * D;
+    const uint8_t* kcol = p.pools.k + (int64_t)g0 * D + col * 16;
+    const uint8_t* vcol = p.pools.v + (int64_t)g0 * D + col * 16;
+    const float2* scol = p.pools.scales + g0 + shead;
+    // Copies stage i, whose slots have been loaded; a key behind the last or at a bad slot is zeros, its scales marked (0, -1).
+    auto load_stage = [&](int i) {
+        const uint32_t buf = ring + (uint32_t)(i % RQ_NS * LY::STAGE);
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) {
+            const int key = row0 + x * rstep;
+            const bool in = i * span + key < nk && sl[x] >= 0 && sl[x] < p.num_slots;
+            const int64_t off = in ? (int64_t)sl[x] * pitch : 0;
+            const uint32_t to = buf + (uint32_t)((((key >> 4) << p.hb) + col / KS) * LY::WARP) + code_at<D>(key & 15, col % KS);
+            cp_async_16(to, kcol + off, in ? 16u : 0u);
+            cp_async_16(to + LY::CODES, vcol + off, in ? 16u : 0u);
         }
+        if (skey < span) {
+            const uint32_t to = buf + (uint32_t)((((skey >> 4) << p.hb) + shead) * LY::WARP + 2 * LY::CODES + (skey & 15) * 8);
+            const bool in = i * span + skey < nk, good = in && ss >= 0 && ss < p.num_slots;
+            if (in && !good) report(p.status, RX_DEV_BAD_SLOT);
+            if (good) cp_async_8(to, scol + (int64_t)(ss >> p.pools.shift) * p.hkv);
+            else asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < RQ_NS - 1; ++i) {
+        if (i < nstages) load_stage(i);
+        cp_async_commit();
+        load_slots(i + 1);
     }
     // query fragments: columns of the B operand, row R0 + 8 t + r8, channels 16 s + 4 t4 ..+3; and each accumulator
     // column's factor, scale log2(e) over the row's power of two
@@ -208,35 +316,14 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_q8_kernel(const __grid_consta
         f[t][0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
         f[t][1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
     }
-    const bool any_bad = __syncthreads_or(bad);
     // the first key that each of this lane's columns may not see, relative to the chunk
     int end[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) end[t][e] = min(before + (R0 + 8 * t + 2 * t4 + e) / G + 1 - k_begin, nk);
-    const int least = min(before + R0 / G + 1 - k_begin, nk);           // every row sees the keys before this
+        for (int e = 0; e < 2; ++e) end[t][e] = before + (R0 + 8 * t + 2 * t4 + e) / G + 1 - k_begin;
+    const int least = before + R0 / G + 1 - k_begin;                   // every row sees the keys before this
 
-    const uint32_t sbase = smem_u32(smem);
-    const int64_t pitch = (int64_t)p.hkv * D;
-    const uint8_t* kcol = p.pools.k + (int64_t)g * D + (tid % KS) * 16;
-    const uint8_t* vcol = p.pools.v + (int64_t)g * D + (tid % KS) * 16;
-    auto load_stage = [&](int st) {
-        const uint32_t kb = sbase + (uint32_t)((st % RQ_NS) * LY::STAGE), vb = kb + LY::CODES;
-#pragma unroll
-        for (int x = 0; x < CPT; ++x) {
-            const int key = tid / KS + x * (RQ_THREADS / KS);
-            const int32_t s = slot_s[st * RQ_STAGE + key];
-            const int64_t off = (int64_t)max(s, 0) * pitch;
-            const uint32_t so = code_at<D>(key, tid % KS), bytes = s >= 0 ? 16u : 0u;
-            cp_async_16(kb + so, kcol + off, bytes);
-            cp_async_16(vb + so, vcol + off, bytes);
-        }
-        if (tid < RQ_STAGE) {
-            const int32_t s = slot_s[st * RQ_STAGE + tid];
-            cp_async_8(vb + LY::CODES + tid * 8, p.pools.scales + (int64_t)(max(s, 0) >> p.pools.shift) * p.hkv + g, s >= 0 ? 8u : 0u);
-        }
-    };
     float o[NT][KS][4];
     float mx[NT][2], l[NT][2], my[NT][2];      // of x in this lane, the sum, and of y in the warp
 #pragma unroll
@@ -246,23 +333,21 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_q8_kernel(const __grid_consta
         mx[t][0] = mx[t][1] = my[t][0] = my[t][1] = -INFINITY;
         l[t][0] = l[t][1] = 0.f;
     }
-#pragma unroll
-    for (int s = 0; s < RQ_NS - 1; ++s) {
-        if (s < nstages) load_stage(s);
-        cp_async_commit();
-    }
     for (int it = 0; it < nstages; ++it) {
         cp_async_wait<RQ_NS - 2>();
-        __syncthreads();                       // stage it is here, and every warp is done with stage it - 1
+        __syncthreads();                       // stage `it` is here, of all threads, and the one before it has been read
         if (it + RQ_NS - 1 < nstages) load_stage(it + RQ_NS - 1);
         cp_async_commit();
-        const int key0 = it * RQ_STAGE + warp * 16;
+        load_slots(it + RQ_NS);
+        const int key0 = it * span + way * RQ_KEYS;
         if (key0 >= nk) continue;
-        const uint32_t kb = sbase + (uint32_t)((it % RQ_NS) * LY::STAGE), vb = kb + LY::CODES;
-        const int mi = lane >> 3, lrow = warp * 16 + (mi & 1) * 8 + (lane & 7);
-        float sacc[NT][4];
+        const uint32_t kb = ring + (uint32_t)(it % RQ_NS * LY::STAGE + warp * LY::WARP), vb = kb + LY::CODES;
+        const int mi = lane >> 3, lrow = (mi & 1) * 8 + (lane & 7);
+        float sacc[NT][4], sodd[NT][4];        // of even and odd chunks: two chains of products
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sacc[t][0] = sacc[t][1] = sacc[t][2] = sacc[t][3] = 0.f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[t][e] = sodd[t][e] = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; s += 2) {
             uint32_t w[4];                     // keys r8, r8 + 8 of chunk s, then of chunk s + 1
@@ -275,14 +360,20 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_q8_kernel(const __grid_consta
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int u = 0; u < (TWO ? 2 : 1); ++u) mma_f16_16816(sacc[t], a, qb[t][u][s + j][0], qb[t][u][s + j][1]);
+                    for (int u = 0; u < (TWO ? 2 : 1); ++u)
+                        mma_f16_16816(j ? sodd[t] : sacc[t], a, qb[t][u][s + j][0], qb[t][u][s + j][1]);
             }
         }
-        const float2* sc = reinterpret_cast<const float2*>(smem + (it % RQ_NS) * LY::STAGE + 2 * LY::CODES) + warp * 16;
-        const float2 sa = sc[r8], sb = sc[r8 + 8];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sacc[t][e] += sodd[t][e];
+        float2 sa, sb;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(sa.x), "=f"(sa.y) : "r"(vb + LY::CODES + r8 * 8) : "memory");
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(sb.x), "=f"(sb.y) : "r"(vb + LY::CODES + r8 * 8 + 64) : "memory");
+        const bool oka = sa.y != -1.f, okb = sb.y != -1.f;
         const float la = fast_log2(sa.y), lb = fast_log2(sb.y);
-        const bool whole = key0 + 16 <= least && !any_bad;     // no key of these is hidden from any row
-        const bool oka = !any_bad || slot_s[key0 + r8] >= 0, okb = !any_bad || slot_s[key0 + r8 + 8] >= 0;
+        const bool whole = key0 + RQ_KEYS <= least && __all_sync(0xffffffffu, oka && okb);     // no key of these is hidden from any row
         uint32_t pb[NT][TWO ? 2 : 1][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -348,113 +439,130 @@ __global__ void __launch_bounds__(RQ_THREADS) rows_q8_kernel(const __grid_consta
     }
     cp_async_wait<0>();
 
-    // One row's parts of the four warps: O relative to 2^(my - 15), l relative to 2^mx.
-    constexpr int RS = LY::RS;
-    float* red_o = reinterpret_cast<float*>(smem);             // [4 warps][8 rows][RS]
-    float* red_m = red_o + 4 * 8 * RS;                         // [4][8]: mx, then l, then my
-    float* red_w = red_m + 3 * 32;                             // [4][8] weights
-    float* red_lse = red_w + 32;                               // [8]
+    // A row's channels 2 x, 2 x + 1 to where they belong: the output, or this part.
+    auto put = [&](int r, int head, int d, float a0, float a1, float lse, bool with_lse) {
+        if (whole) {
+            const int R = R0 + r, tok = R / G;
+            const int64_t at = (q0 + tok) * p.hq + (g0 + head) * G + R % G;
+            store_row2((T*)p.out + at * D + d, a0, a1);
+            if (with_lse && p.lse) p.lse[at] = lse * RQ_LN2;
+        } else {
+            const int64_t at = (((int64_t)blockIdx.x * 2 + slot) * HB + head) * RT + r;
+            *reinterpret_cast<float2*>(p.part_o + at * D + d) = make_float2(a0, a1);
+            if (with_lse) p.part_lse[at] = lse;
+        }
+    };
+    // O is relative to 2^(my - 15), l to 2^mx of its lane.
+    float* red_o = reinterpret_cast<float*>(smem);             // warps that share a head: [8 warps][8 rows][RS]
+    float* red_m = red_o + RQ_WARPS * 8 * LY::RS;              // mx, l, my, weight, lse of [8 warps][8 rows]
+    constexpr int M = RQ_WARPS * 8;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (R0 + 8 * t >= rows) break;                         // the same for the block
-        __syncthreads();                                       // the ring, or the tile before, is done with
+        if (ways > 1) __syncthreads();                         // the ring, or the tile before, is done with
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float m = mx[t][e];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            float s = l[t][e] * fast_exp2(mx[t][e] - (m == -INFINITY ? 0.f : m));
+            const float ref = m == -INFINITY ? 0.f : m;
+            float s = l[t][e] * fast_exp2(mx[t][e] - ref);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            if (ways == 1) {
+                const int r = 8 * t + 2 * t4 + e;
+                const float w = s == 0.f ? 0.f : exp2f(my[t][e] - RQ_TOP - ref) / s;      // no key: zeros
+                const float lse = s == 0.f ? -INFINITY : m + log2f(s);
+                if (R0 + r < rows)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) put(r, warp & (HB - 1), 16 * i + 2 * r8, o[t][i][e] * w, o[t][i][e + 2] * w, lse, i == 0 && r8 == 0);
+                continue;
+            }
             if (r8 == 0) {
                 red_m[warp * 8 + 2 * t4 + e] = m;
-                red_m[32 + warp * 8 + 2 * t4 + e] = s;
-                red_m[64 + warp * 8 + 2 * t4 + e] = my[t][e];
+                red_m[M + warp * 8 + 2 * t4 + e] = s;
+                red_m[2 * M + warp * 8 + 2 * t4 + e] = my[t][e];
             }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-                *reinterpret_cast<float2*>(red_o + (warp * 8 + 2 * t4 + e) * RS + 16 * i + 2 * r8) =
+                *reinterpret_cast<float2*>(red_o + (warp * 8 + 2 * t4 + e) * LY::RS + 16 * i + 2 * r8) =
                     make_float2(o[t][i][e], o[t][i][e + 2]);
         }
+        if (ways == 1) continue;
         __syncthreads();
-        if (tid < 8) {
-            float M = -INFINITY, L = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) M = fmaxf(M, red_m[w * 8 + tid]);
-            const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) L += red_m[32 + w * 8 + tid] * exp2f(red_m[w * 8 + tid] - ref);
-            const float inv = L == 0.f ? 0.f : 1.f / L;        // no key: zeros
-#pragma unroll
-            for (int w = 0; w < 4; ++w) red_w[w * 8 + tid] = exp2f(red_m[64 + w * 8 + tid] - RQ_TOP - ref) * inv;
-            red_lse[tid] = L == 0.f ? -INFINITY : M + log2f(L);
+        if (tid < 8 * HB) {                                    // a row of a head: entry tid + 8 HB w of warp w
+            const int step = 8 * HB;
+            float top = -INFINITY, L = 0.f;
+            for (int w = 0; w < ways; ++w) top = fmaxf(top, red_m[tid + step * w]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            for (int w = 0; w < ways; ++w) L += red_m[M + tid + step * w] * exp2f(red_m[tid + step * w] - ref);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            for (int w = 0; w < ways; ++w) red_m[3 * M + tid + step * w] = exp2f(red_m[2 * M + tid + step * w] - RQ_TOP - ref) * inv;
+            red_m[4 * M + tid] = L == 0.f ? -INFINITY : top + log2f(L);
         }
         __syncthreads();
         constexpr int HALF = D / 2;
-        const int nr = min(8, rows - R0 - 8 * t);
-        for (int idx = tid; idx < nr * HALF; idx += RQ_THREADS) {
-            const int r = idx / HALF, d = 2 * (idx % HALF), R = R0 + 8 * t + r, tok = R / G, h = g * G + R % G;
+        for (int idx = tid; idx < HB * 8 * HALF; idx += RQ_THREADS) {
+            const int hr = idx / HALF, d = 2 * (idx % HALF), r = 8 * t + (hr & 7);
+            if (R0 + r >= rows) continue;
             float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float wt = red_w[w * 8 + r];
-                const float2 v = *reinterpret_cast<const float2*>(red_o + (w * 8 + r) * RS + d);
+            for (int w = 0; w < ways; ++w) {
+                const int at = hr + 8 * HB * w;
+                const float wt = red_m[3 * M + at];
+                const float2 v = *reinterpret_cast<const float2*>(red_o + at * LY::RS + d);
                 a0 += wt * v.x;
                 a1 += wt * v.y;
             }
-            if (p.chunks == 1) {
-                const int64_t at = (q0 + tok) * p.hq + h;
-                store_row2((T*)p.out + at * D + d, a0, a1);
-                if (d == 0 && p.lse) p.lse[at] = red_lse[r] * RQ_LN2;
-            } else {
-                const int64_t at = (((int64_t)b * p.max_qo_len + tok) * p.hq + h) * p.chunks + c;
-                *reinterpret_cast<float2*>(p.part_o + at * D + d) = make_float2(a0, a1);
-                if (d == 0) p.part_lse[at] = red_lse[r];
-            }
+            put(r, hr >> 3, d, a0, a1, red_m[4 * M + hr], d == 0);
         }
     }
+    // on to the next group of heads, row tile, request
+    left -= p.shared ? s1 - s0 : 1;
+    if (left <= 0) break;
+    s0 = 0;
+    if (++gi == groups) {
+        gi = 0;
+        if (++tile * RT >= rows) {
+            tile = 0;
+            do ++b;
+            while (b < p.batch && !rows_of(p, b, false, q0, n, before));
+            if (b >= p.batch) break;
+        }
+    }
+    __syncthreads();                     // the ring has been read
+    }
+    if (p.shared && tid < 2) p.meta[blockIdx.x * 2 + tid] = tid == 0 ? told[0] : told[1];
 }
 
-// The chunks' parts of a row: one warp a (token, query head).
-template <typename T, int D>
-__global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constant__ RowsParams p) {
+// Rows from their parts: blockIdx.x the begun and not ended item, four rows a block with a warp each (WAYS 1), or one row a block
+// with all its warps.
+template <typename T, int D, int WAYS>
+__global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constant__ RowsParams p, int rows_a_tile, int ctas) {
+    constexpr int E = D / 32;
+    __shared__ int list[RQ_CTAS];
+    __shared__ uint32_t room[RQ_CTAS];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t per = (int64_t)p.max_qo_len * p.hq;
-    const int b = (int)(item / per);
-    if (b >= p.batch) return;
-    const int rest = (int)(item - b * per), tok = rest / p.hq, h = rest - tok * p.hq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int count = parts_of<RQ_CTAS>(p.meta, blockIdx.x, ctas, list, room);
+    if (count == 0) return;
+    const int4 what = p.meta[list[0]];
     int64_t q0;
     int n, before;
-    if (!rows_of(p, b, false, q0, n, before) || tok >= n) return;
-    // the chunks that the tile of this row went through (a chunk behind the row's own keys, of a tile with later rows, has no weight)
-    const int parts = max((before + tok + 1 + p.chunk - 1) / p.chunk, 1);
-    const float* pl = p.part_lse + item * p.chunks;
-    const float* po = p.part_o + item * p.chunks * D;
-    float M = -INFINITY;
-    for (int s = lane; s < parts; s += 32) M = fmaxf(M, pl[s]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float ref = M == -INFINITY ? 0.f : M;
-    constexpr int E = D / 32;
-    float acc[E], W = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-        const float w = exp2f(pl[s] - ref);
-        W += w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += w * po[(int64_t)s * D + lane * E + e];
-    }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    const int64_t at = (q0 + tok) * p.hq + h;
+    rows_of(p, what.x, false, q0, n, before);
+    const int r = blockIdx.y * (4 / WAYS) + (WAYS == 1 ? warp : 0);      // rows of a head, then the next head's
+    const int R = what.y * rows_a_tile + r % rows_a_tile;
+    if (R >= n * p.group) return;                                        // the same for all who share the row
+    float acc[E];
+    float lse;
+    if constexpr (WAYS == 1) lse = merge_few<D>(list, count, p.part_o, p.part_lse, rows_a_tile << p.hb, r, acc);
+    else lse = merge_many<D, RQ_CTAS>(list, count, p.part_o, p.part_lse, rows_a_tile << p.hb, r, acc);
+    if (WAYS > 1 && warp != 0) return;
+    const int64_t at = (q0 + R / p.group) * p.hq + (what.z + r / rows_a_tile) * p.group + R % p.group;
     T* row = (T*)p.out + at * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) store_row2(row + e, acc[e] * inv, acc[e + 1] * inv);
-    if (p.lse && lane == 0) p.lse[at] = W == 0.f ? -INFINITY : (M + log2f(W)) * RQ_LN2;
+    for (int e = 0; e < E; e += 2) store_row2(row + e, acc[e], acc[e + 1]);
+    if (p.lse && lane == 0) p.lse[at] = lse * RQ_LN2;
 }
 
 template <typename T, int D, int FMT, int NT>
@@ -473,9 +581,21 @@ static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaS
     });
     if (rc != RX_OK) return rc;
     launch_pdl(rows_q8_kernel<T, D, FMT, NT>, grid, RQ_THREADS, smem, s, p);
-    if (p.chunks > 1) {
-        const int64_t items = (int64_t)p.batch * p.max_qo_len * p.hq;
-        launch_pdl(rows_q8_merge_kernel<T, D>, (unsigned)((items + 3) / 4), 128, 0, s, p);
+    if (p.shared) {
+        // few items: each in many parts, so a block a row; many items: a few parts each, a warp a row
+        const int64_t items = (int64_t)p.batch * p.tiles * (p.hkv >> p.hb), rows = 8 * NT << p.hb;
+        const bool few = items <= 64;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, grid), (unsigned)(few ? rows : rows / 4));
+        cfg.blockDim = dim3(128);
+        cfg.stream = s;
+        cudaLaunchAttribute pdl[1];
+        pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        pdl[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = pdl;
+        cfg.numAttrs = 1;
+        if (few) cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 4>, p, 8 * NT, (int)grid);
+        else cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 1>, p, 8 * NT, (int)grid);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
@@ -505,18 +625,25 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     const int64_t rows = (int64_t)max_qo_len * (d->hq / d->hkv);
     L.nt = rows_nt(rows, d->dtype);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
-    // Long chunks amortise a CTA's start and end over more keys; short ones keep enough CTAs to fill 152 SMs.
-    const int64_t units = L.tiles * d->hkv * batch;
-    auto chunks = [&](int c) { return std::max<int64_t>(((int64_t)max_kv_len + c - 1) / c, 1); };
-    L.chunk = RQ_CHUNK;
-    while (L.chunk > 256 && units * chunks(L.chunk) < 152 * 8) L.chunk /= 2;
-    if (max_kv_len <= 512 && units >= 152) L.chunk = 512;
-    L.chunks = chunks(L.chunk);
-    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    if (L.chunks > 1) {
-        const size_t parts = (size_t)batch * max_qo_len * d->hq * L.chunks;
-        L.o_bytes = up(parts * d->head_dim * sizeof(float));
-        L.bytes = L.o_bytes + up(parts * sizeof(float));
+    // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
+    // many heads as take the least time.  In stages of a CTA, about a microsecond: its start and end cost four, sharing
+    // out and merging seven.
+    const int64_t slots = 152 * rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt), units = L.tiles * batch;
+    auto stages = [&](int hb) { return std::max<int64_t>(((int64_t)max_kv_len << hb) / (RQ_KEYS * RQ_WARPS), 0) + 1; };
+    auto rounds = [&](int hb) { return (units * (d->hkv >> hb) + slots - 1) / slots; };
+    int most = 3;
+    while (most > 0 && d->hkv % (1 << most) != 0) --most;
+    L.hb = most;
+    for (int hb = most - 1; hb >= 0; --hb)
+        if (rounds(hb) * (4 + stages(hb)) < rounds(L.hb) * (4 + stages(L.hb))) L.hb = hb;
+    L.shared = rounds(L.hb) * (4 + stages(L.hb)) > units * (d->hkv >> most) * stages(most) / slots + 4 + 7;
+    L.ctas = L.shared ? slots : units * (d->hkv >> L.hb);
+    if (L.shared) {
+        L.hb = most;
+        const size_t rows = (size_t)L.ctas * 2 * (8 * L.nt << L.hb);
+        L.lse_at = rows * d->head_dim * sizeof(float);
+        L.meta_at = L.lse_at + rows * sizeof(float);
+        L.bytes = L.meta_at + (size_t)L.ctas * 2 * sizeof(int4);
     }
     return L;
 }
@@ -524,8 +651,8 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
 int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,
                    cudaStream_t stream) {
     const RowsPlan L = rows_q8_plan(d, a.batch, a.max_qo_len, a.max_kv_len);
-    const int64_t grid = (int64_t)a.batch * L.chunks * L.tiles * d->hkv, items = (int64_t)a.batch * a.max_qo_len * d->hq;
-    RX_REQUIRE(grid < (1ll << 31) && (items + 3) / 4 < (1ll << 31), "%s: too many rows or chunks (split the batch)", fn);
+    RX_REQUIRE(L.ctas < (1ll << 31), "%s: too many rows (split the batch)", fn);
+    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - 64, "%s: too many rows in a request", fn);
     RX_REQUIRE(L.bytes == 0 || (ws && ws_bytes >= L.bytes && ((uintptr_t)ws & 255) == 0),
                "%s: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", fn, L.bytes, ws_bytes);
     RowsParams p{};
@@ -544,19 +671,20 @@ int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, c
     p.max_qo_len = a.max_qo_len;
     p.max_kv_len = a.max_kv_len;
     p.tiles = (int32_t)L.tiles;
-    p.chunks = (int32_t)L.chunks;
-    p.chunk = L.chunk;
+    p.shared = L.shared ? 1 : 0;
+    p.hb = L.hb;
     p.scale_log2 = d->scale * RQ_LOG2E;
     p.out = a.out;
     p.lse = a.lse;
     p.part_o = (float*)ws;
-    p.part_lse = (float*)((unsigned char*)ws + L.o_bytes);
+    p.part_lse = (float*)((unsigned char*)ws + L.lse_at);
+    p.meta = (int4*)((unsigned char*)ws + L.meta_at);
     p.status = a.status;
     if (d->dtype == RX_F32)
-        return d->head_dim == 128 ? launch_rows<float, 128>(fn, p, L.nt, q8->format, (unsigned)grid, stream)
-                                  : launch_rows<float, 64>(fn, p, L.nt, q8->format, (unsigned)grid, stream);
-    return d->head_dim == 128 ? launch_rows<__nv_bfloat16, 128>(fn, p, L.nt, q8->format, (unsigned)grid, stream)
-                              : launch_rows<__nv_bfloat16, 64>(fn, p, L.nt, q8->format, (unsigned)grid, stream);
+        return d->head_dim == 128 ? launch_rows<float, 128>(fn, p, L.nt, q8->format, (unsigned)L.ctas, stream)
+                                  : launch_rows<float, 64>(fn, p, L.nt, q8->format, (unsigned)L.ctas, stream);
+    return d->head_dim == 128 ? launch_rows<__nv_bfloat16, 128>(fn, p, L.nt, q8->format, (unsigned)L.ctas, stream)
+                              : launch_rows<__nv_bfloat16, 64>(fn, p, L.nt, q8->format, (unsigned)L.ctas, stream);
 }
 
 }  // namespace rx

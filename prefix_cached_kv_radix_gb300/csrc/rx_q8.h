@@ -27,11 +27,12 @@ struct RowsQ8Args {
     int32_t* status;
 };
 
-// How rows_q8.cu splits a call, and the workspace it needs (0 where no row's keys are split).
+// How rows_q8.cu shares out a call, and the workspace it needs for parts of rows (0: none).
 struct RowsPlan {
-    int nt, chunk;
-    int64_t tiles, chunks;
-    size_t o_bytes, bytes;
+    int nt, hb;                  // 8-row tiles of a CTA, log2 of its heads
+    bool shared;
+    int64_t tiles, ctas;
+    size_t lse_at, meta_at, bytes;
 };
 RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len);
 int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,
