@@ -24,10 +24,15 @@ namespace rx {
 
 constexpr int Q8_THREADS = 256;
 constexpr int Q8_TILE = Q8_THREADS * 4;            // slot-table entries per block
-constexpr int Q8_UNITS = 2;                        // (token, head) pairs in flight per lane group
 constexpr float Q8_LEAST = 0x1p-126f;              // no scale is smaller
 
-// Eight elements of a row.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight elements of a row.  Magnitudes are compared as integers: a NaN is above all others.
 template <typename T>
 struct Row8;
 template <>
@@ -41,6 +46,23 @@ struct Row8<float> {
         const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+        return m;
+    }
+    // the largest magnitudes of two rows, each spread over LANES lanes, as bits of float
+    template <int LANES>
+    static __device__ __forceinline__ void tops(const Row8& k, const Row8& v, uint32_t* t) {
+        t[0] = k.top(), t[1] = v.top();
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            t[0] = max(t[0], __shfl_xor_sync(0xffffffffu, t[0], o));
+            t[1] = max(t[1], __shfl_xor_sync(0xffffffffu, t[1], o));
+        }
     }
     static __device__ __forceinline__ void store(float* p, const float* f) {
         reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -59,20 +81,24 @@ struct Row8<__nv_bfloat16> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    // of the even and of the odd elements, in the two halves
+    __device__ __forceinline__ uint32_t top() const {
+        return max_u16x2(max_u16x2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), max_u16x2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    }
+    template <int LANES>
+    static __device__ __forceinline__ void tops(const Row8& k, const Row8& v, uint32_t* t) {
+        const uint32_t a = k.top(), b = v.top();
+        uint32_t m = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));      // K's low, V's high
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        t[0] = m << 16, t[1] = m & 0xffff0000u;
+    }
     // rounded once, from the 32-bit product
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
         *reinterpret_cast<uint4*>(p) =
             make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     }
 };
-
-// max |x| of 8 elements as bits: a NaN's are above all others.
-__device__ __forceinline__ uint32_t abs_bits(const float* f) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-    return m;
-}
 
 // The scale of a row whose largest magnitude has these bits.
 template <int FMT>
@@ -94,20 +120,22 @@ __device__ __forceinline__ float nearest_whole(float q, float x, float s) {
 
 template <bool FIXED>
 __device__ __forceinline__ uint2 codes_int8(const float* x, float s, float inv) {
+    // 1.5 * 2^23 + q: its last bits are q = x / s rounded to a whole number n; x - n s, which is exact, tells how near a half q was
+    constexpr float MAGIC = 12582912.f;
     float n[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float q = x[i] * inv;
-        if (FIXED) q = q == q ? fminf(fmaxf(q, -127.f), 127.f) : 0.f;
-        n[i] = q + 12582912.f;                     // 1.5 * 2^23: the sum's last bits are q rounded to a whole number
-        off = fmaxf(off, fabsf(q - (n[i] - 12582912.f)));
+        float y = x[i];
+        if (FIXED) y = y == y ? fminf(fmaxf(y, -127.f * s), 127.f * s) : 0.f;
+        n[i] = fmaf(y, inv, MAGIC);
+        off = fmaxf(off, fabsf(fmaf(MAGIC - n[i], s, y)));
     }
-    if (off >= 0.4999f) {                          // some quotient is next to a half
+    if (off >= 0.4999f * s) {                      // some quotient is next to a half
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float q = x[i] * inv;
             if (FIXED) q = q == q ? q : 0.f;
-            n[i] = fminf(fmaxf(fabsf(q) < 128.f ? nearest_whole(q, x[i], s) : q, -127.f), 127.f) + 12582912.f;
+            n[i] = fminf(fmaxf(fabsf(q) < 128.f ? nearest_whole(q, x[i], s) : q, -127.f), 127.f) + MAGIC;
         }
     }
     uint32_t w[2];
@@ -159,14 +187,15 @@ struct WriteQ8Params {
     uint8_t* k_pool;
     uint8_t* v_pool;
     float2* scales;
-    int32_t shift, hkv;
+    int32_t shift, hkv, step_rows, step_heads;     // a block's lane groups: so many rows and heads from a group's unit to its next
     int32_t* r2t;
     int64_t r2t_stride, num_slots, total;
     int32_t* status;
 };
 
-// Blocks [0, batch * tiles): the slot table.  The others: Q8_UNITS * (Q8_THREADS / (D / 8)) (token, head) pairs each.
-template <typename T, int D, int FMT, bool FIXED>
+// Blocks [0, batch * tiles): the slot table.  The others: Q8_UNITS * (Q8_THREADS / (D / 8)) (token, head) pairs each, Q8_UNITS in flight
+// per lane group.
+template <typename T, int D, int FMT, bool FIXED, int Q8_UNITS>
 __global__ void __launch_bounds__(Q8_THREADS) kv_pool_write_q8_kernel(const __grid_constant__ WriteQ8Params p) {
     constexpr int LANES = D / 8;                   // lanes of a row
     constexpr int ROWS = Q8_THREADS / LANES;       // pairs a block has in hand at a time
@@ -179,57 +208,54 @@ __global__ void __launch_bounds__(Q8_THREADS) kv_pool_write_q8_kernel(const __gr
         return;
     }
     const int64_t block = blockIdx.x - table_blocks;
-    // rows of the batch only: what lies before its first and behind its last request is not written
-    const int64_t first = p.qo_indptr[0], end = p.qo_indptr[p.batch];
-    const int64_t lo = max(first, (int64_t)0), hi = min(end, p.total);
-    if (block == 0 && threadIdx.x == 0 && (end > p.total || first < 0 || end < first)) report(p.status, RX_DEV_BAD_LENGTH);
     const int lane = threadIdx.x % LANES;
     const int64_t b0 = block * (ROWS * Q8_UNITS), tb = b0 / p.hkv;
-    const uint32_t u0 = (uint32_t)(b0 - tb * p.hkv) + threadIdx.x / LANES;
+    const uint32_t u0 = (uint32_t)(b0 - tb * p.hkv) + threadIdx.x / LANES, r0 = u0 / (uint32_t)p.hkv;
     Row8<T> k[Q8_UNITS], v[Q8_UNITS];
     int32_t slot[Q8_UNITS];
-    int head[Q8_UNITS];
+    int64_t t = tb + r0;
+    int h = (int)(u0 - r0 * p.hkv);
+    // the rows (total of them there are) and their slots beside the batch's boundaries, not after them
 #pragma unroll
     for (int i = 0; i < Q8_UNITS; ++i) {
-        const uint32_t u = u0 + i * ROWS, ut = u / (uint32_t)p.hkv;
-        const int64_t t = tb + ut;
-        const int h = (int)(u - ut * p.hkv);
-        const bool in = t >= lo && t < hi;
-        head[i] = h;
-        slot[i] = in ? p.new_slots[t] : -1;
-        if (in) {
+        slot[i] = -1;
+        if (t < p.total) {
+            slot[i] = p.new_slots[t];
             k[i].load((const T*)p.k + t * p.k_stride + h * D + lane * 8);
             v[i].load((const T*)p.v + t * p.v_stride + h * D + lane * 8);
         }
-        if (in && (slot[i] < 0 || slot[i] >= p.num_slots)) {
-            if (h == 0 && lane == 0) report(p.status, RX_DEV_BAD_SLOT);
-            slot[i] = -1;
-        }
+        t += p.step_rows;
+        h += p.step_heads;
+        if (h >= p.hkv) h -= p.hkv, ++t;
     }
+    // rows of the batch only: what lies before its first and behind its last request is not written
+    const int64_t first = p.qo_indptr[0], end = p.qo_indptr[p.batch];
+    if (block == 0 && threadIdx.x == 0 && (end > p.total || first < 0 || end < first)) report(p.status, RX_DEV_BAD_LENGTH);
+    t = tb + r0;
+    h = (int)(u0 - r0 * p.hkv);
 #pragma unroll
     for (int i = 0; i < Q8_UNITS; ++i) {
-        const bool in = slot[i] >= 0;              // the same in all lanes of a row
-        const int64_t row = in ? (int64_t)slot[i] * p.hkv + head[i] : 0;
-        float x[2][8];
+        const int head = h;
+        const bool inside = t >= first && t < end && t < p.total;
+        if (inside && (slot[i] < 0 || slot[i] >= p.num_slots) && head == 0 && lane == 0) report(p.status, RX_DEV_BAD_SLOT);
+        const bool in = inside && slot[i] >= 0 && slot[i] < p.num_slots;      // the same in all lanes of a row
+        t += p.step_rows;
+        h += p.step_heads;
+        if (h >= p.hkv) h -= p.hkv, ++t;
+        const int64_t row = in ? (int64_t)slot[i] * p.hkv + head : 0;
         uint32_t top[2] = {0, 0};
         float s[2];
-        if (in) {
-            k[i].get(x[0]);
-            v[i].get(x[1]);
-        }
         if (FIXED) {
-            const float2 given = p.scales[in ? (int64_t)(slot[i] >> p.shift) * p.hkv + head[i] : 0];
+            const float2 given = p.scales[in ? (int64_t)(slot[i] >> p.shift) * p.hkv + head : 0];
             s[0] = given.x, s[1] = given.y;
         } else {
-            if (in) top[0] = abs_bits(x[0]), top[1] = abs_bits(x[1]);
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o >>= 1) {
-                top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
-                top[1] = max(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
-            }
+            Row8<T>::template tops<LANES>(k[i], v[i], top);                   // (rows that are not there: anything, and not used)
             s[0] = scale_of<FMT>(top[0]), s[1] = scale_of<FMT>(top[1]);
         }
         if (!in) continue;
+        float x[2][8];
+        k[i].get(x[0]);
+        v[i].get(x[1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint2 c = make_uint2(0u, 0u);
@@ -255,7 +281,7 @@ struct ReadQ8Params {
 };
 
 // One (slot, head) pair per lane group and step, Q8_UNITS in flight.
-template <typename T, int D, int FMT>
+template <typename T, int D, int FMT, int Q8_UNITS>
 __global__ void __launch_bounds__(Q8_THREADS) kv_pool_read_q8_kernel(const __grid_constant__ ReadQ8Params p) {
     constexpr int LANES = D / 8;
     constexpr int ROWS = Q8_THREADS / LANES;
@@ -304,20 +330,39 @@ __global__ void __launch_bounds__(Q8_THREADS) kv_pool_read_q8_kernel(const __gri
     }
 }
 
-template <typename T, int D>
-static void launch_write(const WriteQ8Params& p, const rx_q8_desc* q8, unsigned grid, cudaStream_t s) {
-    if (q8->format == RX_Q8_INT8)
-        q8->fixed ? launch_pdl(kv_pool_write_q8_kernel<T, D, RX_Q8_INT8, true>, grid, Q8_THREADS, 0, s, p)
-                  : launch_pdl(kv_pool_write_q8_kernel<T, D, RX_Q8_INT8, false>, grid, Q8_THREADS, 0, s, p);
-    else
-        q8->fixed ? launch_pdl(kv_pool_write_q8_kernel<T, D, RX_Q8_E4M3, true>, grid, Q8_THREADS, 0, s, p)
-                  : launch_pdl(kv_pool_write_q8_kernel<T, D, RX_Q8_E4M3, false>, grid, Q8_THREADS, 0, s, p);
+// (token, head) pairs per lane group: one where that leaves few blocks (64 decode tokens: 4.3 us, and 6.1 with four), else
+// four (24 ragged prompts: 31.8 us, with two 37.3), or two of the twice as wide f32 rows (7 x 1500: 17.0 us, with four 19.9).
+static int q8_units(int64_t pairs, const rx_attn_desc* d) {
+    const int64_t rows = Q8_THREADS / (d->head_dim / 8);
+    const int most = d->dtype == RX_F32 ? 2 : 4;
+    return pairs < rows * most * 152 * 4 ? 1 : most;
+}
+
+template <typename T, int D, int FMT, bool FIXED>
+static void launch_write(const WriteQ8Params& p, int units, unsigned grid, cudaStream_t s) {
+    constexpr int MOST = sizeof(T) == 4 ? 2 : 4;
+    units == 1 ? launch_pdl(kv_pool_write_q8_kernel<T, D, FMT, FIXED, 1>, grid, Q8_THREADS, 0, s, p)
+               : launch_pdl(kv_pool_write_q8_kernel<T, D, FMT, FIXED, MOST>, grid, Q8_THREADS, 0, s, p);
 }
 
 template <typename T, int D>
-static void launch_read(const ReadQ8Params& p, int format, unsigned grid, cudaStream_t s) {
-    format == RX_Q8_INT8 ? launch_pdl(kv_pool_read_q8_kernel<T, D, RX_Q8_INT8>, grid, Q8_THREADS, 0, s, p)
-                         : launch_pdl(kv_pool_read_q8_kernel<T, D, RX_Q8_E4M3>, grid, Q8_THREADS, 0, s, p);
+static void launch_write(const WriteQ8Params& p, const rx_q8_desc* q8, int units, unsigned grid, cudaStream_t s) {
+    if (q8->format == RX_Q8_INT8)
+        q8->fixed ? launch_write<T, D, RX_Q8_INT8, true>(p, units, grid, s) : launch_write<T, D, RX_Q8_INT8, false>(p, units, grid, s);
+    else
+        q8->fixed ? launch_write<T, D, RX_Q8_E4M3, true>(p, units, grid, s) : launch_write<T, D, RX_Q8_E4M3, false>(p, units, grid, s);
+}
+
+template <typename T, int D, int FMT>
+static void launch_read(const ReadQ8Params& p, int units, unsigned grid, cudaStream_t s) {
+    constexpr int MOST = sizeof(T) == 4 ? 2 : 4;
+    units == 1 ? launch_pdl(kv_pool_read_q8_kernel<T, D, FMT, 1>, grid, Q8_THREADS, 0, s, p)
+               : launch_pdl(kv_pool_read_q8_kernel<T, D, FMT, MOST>, grid, Q8_THREADS, 0, s, p);
+}
+
+template <typename T, int D>
+static void launch_read(const ReadQ8Params& p, int format, int units, unsigned grid, cudaStream_t s) {
+    format == RX_Q8_INT8 ? launch_read<T, D, RX_Q8_INT8>(p, units, grid, s) : launch_read<T, D, RX_Q8_E4M3>(p, units, grid, s);
 }
 
 static int q8_launched(const char* fn) {
@@ -357,7 +402,8 @@ extern "C" int kv_pool_write_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, 
     RX_REQUIRE(((uintptr_t)d_k_pool & 15) == 0 && ((uintptr_t)d_v_pool & 15) == 0 && ((uintptr_t)d_scales & 7) == 0,
                "kv_pool_write_q8: pools must be 16-byte aligned, scales 8-byte");
     const int64_t tiles = d_req_to_token ? std::max<int64_t>(1, (r2t_stride + Q8_TILE - 1) / Q8_TILE) : 0;
-    const int64_t per = (int64_t)Q8_UNITS * (Q8_THREADS / (desc->head_dim / 8));
+    const int units = q8_units(total_new * desc->hkv, desc);
+    const int64_t per = (int64_t)units * (Q8_THREADS / (desc->head_dim / 8));
     const int64_t grid = batch * tiles + (total_new * desc->hkv + per - 1) / per;
     RX_REQUIRE(grid < (1ll << 31) && tiles < (1ll << 31), "kv_pool_write_q8: batch, stride or rows too large");
     WriteQ8Params p{};
@@ -376,6 +422,8 @@ extern "C" int kv_pool_write_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, 
     p.scales = (float2*)d_scales;
     p.shift = q8_shift(q8);
     p.hkv = desc->hkv;
+    p.step_rows = Q8_THREADS / (desc->head_dim / 8) / desc->hkv;
+    p.step_heads = Q8_THREADS / (desc->head_dim / 8) % desc->hkv;
     p.r2t = d_req_to_token;
     p.r2t_stride = r2t_stride;
     p.num_slots = desc->num_slots;
@@ -383,10 +431,10 @@ extern "C" int kv_pool_write_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, 
     p.status = d_status;
     cudaStream_t s = (cudaStream_t)stream;
     if (desc->dtype == RX_F32)
-        desc->head_dim == 128 ? launch_write<float, 128>(p, q8, (unsigned)grid, s) : launch_write<float, 64>(p, q8, (unsigned)grid, s);
+        desc->head_dim == 128 ? launch_write<float, 128>(p, q8, units, (unsigned)grid, s) : launch_write<float, 64>(p, q8, units, (unsigned)grid, s);
     else
-        desc->head_dim == 128 ? launch_write<__nv_bfloat16, 128>(p, q8, (unsigned)grid, s)
-                              : launch_write<__nv_bfloat16, 64>(p, q8, (unsigned)grid, s);
+        desc->head_dim == 128 ? launch_write<__nv_bfloat16, 128>(p, q8, units, (unsigned)grid, s)
+                              : launch_write<__nv_bfloat16, 64>(p, q8, units, (unsigned)grid, s);
     return q8_launched("kv_pool_write_q8");
 }
 
@@ -409,7 +457,8 @@ extern "C" int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, i
                    "kv_pool_read_q8: rows must be 16-byte aligned and at least a row apart");
     RX_REQUIRE(((uintptr_t)d_k_pool & 15) == 0 && ((uintptr_t)d_v_pool & 15) == 0 && ((uintptr_t)d_scales & 7) == 0,
                "kv_pool_read_q8: pools must be 16-byte aligned, scales 8-byte");
-    const int64_t per = (int64_t)Q8_UNITS * (Q8_THREADS / (desc->head_dim / 8));
+    const int units = q8_units(n * desc->hkv, desc);
+    const int64_t per = (int64_t)units * (Q8_THREADS / (desc->head_dim / 8));
     const int64_t grid = (n * desc->hkv + per - 1) / per;
     RX_REQUIRE(grid < (1ll << 31), "kv_pool_read_q8: too many rows");
     ReadQ8Params p{};
@@ -425,10 +474,10 @@ extern "C" int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, i
     p.status = d_status;
     cudaStream_t s = (cudaStream_t)stream;
     if (desc->dtype == RX_F32)
-        desc->head_dim == 128 ? launch_read<float, 128>(p, q8->format, (unsigned)grid, s)
-                              : launch_read<float, 64>(p, q8->format, (unsigned)grid, s);
+        desc->head_dim == 128 ? launch_read<float, 128>(p, q8->format, units, (unsigned)grid, s)
+                              : launch_read<float, 64>(p, q8->format, units, (unsigned)grid, s);
     else
-        desc->head_dim == 128 ? launch_read<__nv_bfloat16, 128>(p, q8->format, (unsigned)grid, s)
-                              : launch_read<__nv_bfloat16, 64>(p, q8->format, (unsigned)grid, s);
+        desc->head_dim == 128 ? launch_read<__nv_bfloat16, 128>(p, q8->format, units, (unsigned)grid, s)
+                              : launch_read<__nv_bfloat16, 64>(p, q8->format, units, (unsigned)grid, s);
     return q8_launched("kv_pool_read_q8");
 }

@@ -607,9 +607,7 @@ static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaS
 
 template <typename T, int D, int FMT>
 static int launch_fmt(const char* fn, const RowsParams& p, int nt, unsigned grid, cudaStream_t s) {
-    if (nt == 1) return launch_tile<T, D, FMT, 1>(fn, p, grid, s);
-    if constexpr (std::is_same<T, float>::value) return launch_tile<T, D, FMT, 2>(fn, p, grid, s);
-    else return nt == 2 ? launch_tile<T, D, FMT, 2>(fn, p, grid, s) : launch_tile<T, D, FMT, 4>(fn, p, grid, s);
+    return nt == 1 ? launch_tile<T, D, FMT, 1>(fn, p, grid, s) : launch_tile<T, D, FMT, 2>(fn, p, grid, s);
 }
 
 template <typename T, int D>
@@ -617,13 +615,14 @@ static int launch_rows(const char* fn, const RowsParams& p, int nt, int format, 
     return format == RX_Q8_INT8 ? launch_fmt<T, D, RX_Q8_INT8>(fn, p, nt, grid, s) : launch_fmt<T, D, RX_Q8_E4M3>(fn, p, nt, grid, s);
 }
 
-// 8-row tiles that a CTA takes: as many as the rows fill, up to four (f32 rows, with two parts each, two: registers).
-static int rows_nt(int64_t rows, int dtype) { return rows <= 8 ? 1 : rows <= 16 || dtype == RX_F32 ? 2 : 4; }
+// 8-row tiles that a CTA takes.  Not more than two: four take 255 registers and spill (64 requests with 32 heads to a kv head: 127
+// us; by two tiles of two, 70).
+static int rows_nt(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
     RowsPlan L{};
     const int64_t rows = (int64_t)max_qo_len * (d->hq / d->hkv);
-    L.nt = rows_nt(rows, d->dtype);
+    L.nt = rows_nt(rows);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
     // many heads as take the least time.  In stages of a CTA, about a microsecond: its start and end cost four, sharing

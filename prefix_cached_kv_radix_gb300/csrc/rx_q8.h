@@ -39,7 +39,7 @@ int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, c
                    cudaStream_t stream);
 
 // bf16 rows past what a tile of rows_q8.cu takes: the tensor-core kernel of extend_q8.cu and its workspace.
-constexpr int64_t ROWS_Q8_MOST = 32;
+constexpr int64_t ROWS_Q8_MOST = 16;
 size_t extend_q8_bytes(const rx_attn_desc* d);
 int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream);
 
