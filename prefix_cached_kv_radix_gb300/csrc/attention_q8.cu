@@ -23,6 +23,11 @@ static int attention_q8_pointers(const char* fn, const RowsQ8Args& a) {
     return RX_OK;
 }
 
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// f32 rows read each request's own keys.
+static bool uses_groups(const rx_attn_desc* d, const rx_shared_groups* g) { return g && g->num_groups > 0 && d->dtype == RX_BF16; }
+
 static bool workspace_shape(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
     return d && batch > 0 && max_qo_len > 0 && max_kv_len >= 0 && d->hkv > 0 && d->hq > 0 && d->hq % d->hkv == 0 && d->head_dim > 0;
 }
@@ -35,7 +40,8 @@ static bool many_rows(const rx_attn_desc* d, int32_t max_qo_len) {
 extern "C" size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_kv_len,
                                             const rx_shared_groups* groups) {
     if (!workspace_shape(desc, batch, 1, max_kv_len)) return 0;
-    return rows_q8_plan(desc, batch, 1, max_kv_len).bytes;
+    const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).bytes);
+    return uses_groups(desc, groups) ? own + shared_q8_bytes(desc, batch, groups->num_groups) : own;
 }
 
 extern "C" size_t extend_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
@@ -54,10 +60,20 @@ extern "C" int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q
     int rc = attention_q8_check(fn, desc, q8, batch, r2t_stride, 1, max_kv_len);
     if (rc != RX_OK || batch == 0) return rc;
     RX_REQUIRE(d_kv_lens, "%s: null device pointer", fn);
-    const RowsQ8Args a{d_q,  nullptr, nullptr, d_kv_lens, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool, (const uint8_t*)d_v_pool,
-                       (const float2*)d_scales, d_out, d_lse, batch, 1, max_kv_len, d_status};
+    RowsQ8Args a{d_q,  nullptr, nullptr, d_kv_lens, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool, (const uint8_t*)d_v_pool,
+                 (const float2*)d_scales, d_out, d_lse, batch, 1, max_kv_len, d_status};
     rc = attention_q8_pointers(fn, a);
     if (rc != RX_OK) return rc;
+    if (uses_groups(desc, groups)) {
+        RX_REQUIRE(groups->d_group_indptr && groups->d_group_members && groups->d_group_len && groups->max_group_size >= 1 &&
+                       groups->max_group_len >= 1,
+                   "%s: incomplete shared groups", fn);
+        const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).bytes), need = own + shared_q8_bytes(desc, batch, groups->num_groups);
+        RX_REQUIRE(d_workspace && ws_bytes >= need && ((uintptr_t)d_workspace & 255) == 0,
+                   "%s: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", fn, need, ws_bytes);
+        rc = shared_q8_launch(a, desc, q8, groups, (unsigned char*)d_workspace + own, (cudaStream_t)stream);
+        if (rc != RX_OK) return rc;
+    }
     return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
 }
 

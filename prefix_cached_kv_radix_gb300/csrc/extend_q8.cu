@@ -64,6 +64,13 @@ struct ExtendQ8Params {
     float* part_o;                     // [CTAs][2][EQ_ROWS][D], normalised
     float* part_lse;                   // [CTAs][2][EQ_ROWS], base 2
     int4* meta;                        // [CTAs][2]: request (-1: no part), kv head, first row, whether the item ends here
+    // Shared runs of a decode batch (groups non-null): the "requests" are groups, a group's rows the heads of its members' one
+    // token each, its keys the first len slots of a member's table row, all of them seen by every row.  A row's result goes,
+    // normalised and in 32 bits, to shared_o [requests * hq][D], its log-sum-exp (base 2) to shared_lse.
+    const SharedGroup* groups;
+    const int32_t* members;            // request, or -1
+    float* shared_o;
+    float* shared_lse;
     int32_t q_map_ok;
     CUtensorMap q_map;
 };
@@ -103,6 +110,11 @@ struct EqItem {
 
 // A request's rows and keys; n = 0 where there is none to do.
 __device__ __forceinline__ void eq_request(const ExtendQ8Params& p, int b, bool tell, int64_t& q0, int& n, int& before) {
+    if (p.groups) {
+        const SharedGroup g = p.groups[b];
+        q0 = g.first, n = g.count, before = g.len - 1;
+        return;
+    }
     q0 = p.qo_indptr[b];
     const int64_t m = p.qo_indptr[b + 1] - q0, P = p.prefix_lens[b];
     n = (int)m, before = (int)P;
@@ -111,9 +123,13 @@ __device__ __forceinline__ void eq_request(const ExtendQ8Params& p, int b, bool 
     n = 0;
 }
 
-// K/V tiles of the item that starts at packed row `row0`.
-__device__ __forceinline__ int eq_tiles(int row0, int rows, int G, int before) {
-    return (before + (min(row0 + EQ_ROWS, rows) - 1) / G) / EQ_BN + 1;
+// Keys and K/V tiles of the item that starts at packed row `row0`.
+__device__ __forceinline__ int eq_keys(const ExtendQ8Params& p, int row0, int rows, int before) {
+    return before + (p.groups ? 0 : (min(row0 + EQ_ROWS, rows) - 1) / p.group) + 1;
+}
+
+__device__ __forceinline__ int eq_tiles(const ExtendQ8Params& p, int row0, int rows, int before) {
+    return (eq_keys(p, row0, rows, before) + EQ_BN - 1) / EQ_BN;
 }
 
 // K/V tiles of all of a request's items, for one kv head.
@@ -122,7 +138,7 @@ __device__ __forceinline__ int64_t eq_units(const ExtendQ8Params& p, int b, bool
     int n, before;
     eq_request(p, b, tell, q0, n, before);
     const int rows = n * p.group;
-    for (int r = 0; r < rows; r += EQ_ROWS) sum += eq_tiles(r, rows, p.group, before);
+    for (int r = 0; r < rows; r += EQ_ROWS) sum += eq_tiles(p, r, rows, before);
     return sum;
 }
 
@@ -134,7 +150,7 @@ __device__ __forceinline__ void eq_locate(const ExtendQ8Params& p, int b, int64_
     g = (int)(at / units);
     int64_t left = at - g * units;
     for (row0 = 0;; row0 += EQ_ROWS) {
-        tiles = eq_tiles(row0, n * p.group, p.group, before);
+        tiles = eq_tiles(p, row0, n * p.group, before);
         if (left < tiles) break;
         left -= tiles;
     }
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 if (lane == 0) {
                     ring[3 * e] = make_int4(b, g, row0, ntiles);
                     ring[3 * e + 1] = make_int4(n, before, j, j1);
-                    ring[3 * e + 2] = make_int4(before + (min(row0 + EQ_ROWS, rows) - 1) / G + 1, (whole ? 1 : 0) | (slot << 1),
+                    ring[3 * e + 2] = make_int4(eq_keys(p, row0, rows, before), (whole ? 1 : 0) | (slot << 1),
                                                 (int)(uint32_t)q0, (int)(q0 >> 32));
                     mbar_arrive(bar(LY::BAR_IF + e));
                 }
@@ -324,7 +340,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 quse1 += ntiles > 1 ? 1 : 0;
                 // full 128-row tiles by TMA, one box per 64 columns; a ragged one row by row, two lanes a row, the rows
                 // past the end like the last
-                const int full = p.q_map_ok && q0 + n <= INT32_MAX ? min(ntiles, (rows - row0) >> 7) : 0;
+                const int full = p.q_map_ok && !p.groups && q0 + n <= INT32_MAX ? min(ntiles, (rows - row0) >> 7) : 0;
                 if (lane == 0) {
                     fence_proxy_async_smem();
                     mbar_arrive_expect_tx(bar(LY::BAR_Q), (uint32_t)(full * LY::Q_TILE));
@@ -335,7 +351,8 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 }
                 for (int rr = full * 128 + (lane >> 1); rr < ntiles * 128; rr += 16) {
                     const int t = rr >> 7, r = rr & 127, R = min(row0 + rr, rows - 1);
-                    const __nv_bfloat16* src = p.q + ((q0 + R / G) * p.hq + g * G + R % G) * D;
+                    const int64_t token = p.groups ? max(p.members[q0 + R / G], 0) : q0 + R / G;
+                    const __nv_bfloat16* src = p.q + (token * p.hq + g * G + R % G) * D;
                     const uint32_t to = qs + (uint32_t)(t * LY::Q_TILE + r * 128);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                         if (n == 0) break;
                     }
                 }
-                tiles = eq_tiles(row0, n * G, G, before);
+                tiles = eq_tiles(p, row0, n * G, before);
             }
             if (ok) {
                 const int e = k % EQ_RING;
@@ -453,7 +470,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             const float2* sb = nullptr;
             int32_t sl[NX], ss = -1;
             auto begin = [&]() {
-                slots = p.r2t + (int64_t)it.b * p.stride;
+                slots = p.r2t + (int64_t)(p.groups ? p.groups[it.b].src : it.b) * p.stride;
                 kb = p.pools.k + (size_t)it.g * D + c * 16;
                 vb = p.pools.v + (size_t)it.g * D + c * 16;
                 sb = p.pools.scales + it.g;
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             float m_ref[4], l[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                lim[i] = it.before + min(first + 8 * i + r8, rows - 1) / G - it.j0 * EQ_BN;
+                lim[i] = it.before + (p.groups ? 0 : min(first + 8 * i + r8, rows - 1) / G) - it.j0 * EQ_BN;
                 m_ref[i] = -INFINITY, l[i] = 0.f;
             }
             for (int j = 0; j < nkv; ++j, ++gt) {
@@ -772,18 +789,19 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             }
             const float sum = of_row(l), top = of_row(m_ref);
-            const int r = quarter * 32 + lane, R = first + lane;
-            const bool valid = R < rows;
+            const int R = first + lane;
             const int tok = min(R, rows - 1) / G, h = it.g * G + min(R, rows - 1) % G;
-            const int64_t at = (it.q0 + tok) * p.hq + h;
+            const int64_t token = p.groups ? p.members[it.q0 + tok] : it.q0 + tok, at = token * p.hq + h;
+            const bool valid = R < rows && token >= 0, final = it.whole && !p.groups;
+            float* const part_row = it.whole ? p.shared_o + at * D
+                                             : p.part_o + (((int64_t)blockIdx.x * 2 + it.slot) * EQ_ROWS + t * 128 + quarter * 32 + lane) * D;
             const float inv = sum == 0.f ? 0.f : 1.f / sum, lse = sum == 0.f ? -INFINITY : top + log2f(sum);      // no key: zeros
-            const int64_t part = ((int64_t)blockIdx.x * 2 + it.slot) * EQ_ROWS + t * 128 + r;
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 32) {
                 float ov[32];
                 tmem_ld32(o_addr + cc, ov);
                 tmem_wait_ld();
-                if (valid && it.whole) {
+                if (valid && final) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         *reinterpret_cast<uint4*>(p.out + at * D + cc + e) =
@@ -792,13 +810,13 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 } else if (valid) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(p.part_o + part * D + cc + e) =
+                        *reinterpret_cast<float4*>(part_row + cc + e) =
                             make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
                 }
                 __syncwarp();                    // the whole warp reads the next columns
             }
-            if (valid && it.whole && p.lse) p.lse[at] = lse * EQ_LN2;
-            if (valid && !it.whole) p.part_lse[part] = lse;
+            if (valid && final && p.lse) p.lse[at] = lse * EQ_LN2;
+            if (valid && !final) (it.whole ? p.shared_lse[at] : p.part_lse[(part_row - p.part_o) / D]) = lse;
             __syncwarp();
             tc_fence_before();
         }
@@ -840,7 +858,15 @@ __global__ void __launch_bounds__(128) extend_q8_merge_kernel(const __grid_const
     if (R >= n * p.group) return;
     float acc[E];
     const float lse = merge_few<D>(list, count, p.part_o, p.part_lse, EQ_ROWS, r, acc);
-    const int64_t at = (q0 + R / p.group) * p.hq + item.y * p.group + R % p.group;
+    const int64_t token = p.groups ? p.members[q0 + R / p.group] : q0 + R / p.group;
+    const int64_t at = token * p.hq + item.y * p.group + R % p.group;
+    if (p.groups) {
+        if (token < 0) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e) p.shared_o[at * D + lane * E + e] = acc[e];
+        if (lane == 0) p.shared_lse[at] = lse;
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) = pack_bf16x2(acc[e], acc[e + 1]);
     if (p.lse && lane == 0) p.lse[at] = lse * EQ_LN2;
@@ -913,7 +939,7 @@ static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         const int64_t items = (((int64_t)p.max_qo_len * p.group + EQ_ROWS - 1) / EQ_ROWS) * p.hkv * p.batch;
-        cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, EQ_CTAS), EQ_ROWS / 4);
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(p.groups ? EQ_CTAS : items, EQ_CTAS), EQ_ROWS / 4);
         cfg.blockDim = dim3(128);
         cfg.stream = s;
         cudaLaunchAttribute pdl[1];
@@ -931,14 +957,7 @@ static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
     return RX_OK;
 }
 
-int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream) {
-    const int dc = eq_device();
-    if (dc != RX_OK) return dc;
-    const size_t need = extend_q8_bytes(d);
-    RX_REQUIRE(ws && ws_bytes >= need && ((uintptr_t)ws & 255) == 0,
-               "prefix_extend_attention_q8: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", need, ws_bytes);
-    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - EQ_ROWS, "prefix_extend_attention_q8: too many rows in a request");
-    ExtendQ8Params p{};
+static void eq_params(ExtendQ8Params& p, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws) {
     p.q = (const __nv_bfloat16*)a.q;
     p.qo_indptr = a.qo_indptr;
     p.prefix_lens = a.prefix_lens;
@@ -960,10 +979,95 @@ int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_des
     p.part_o = (float*)ws;
     p.part_lse = p.part_o + rows * d->head_dim;
     p.meta = (int4*)(p.part_lse + rows);
-    p.q_map_ok = eq_rows_map(&p.q_map, a.q, d->hq, d->head_dim, p.group) ? 1 : 0;
+}
+
+static int launch_extend(const ExtendQ8Params& p, const rx_attn_desc* d, const rx_q8_desc* q8, cudaStream_t stream) {
     if (d->head_dim == 128)
         return q8->format == RX_Q8_INT8 ? launch_extend<128, RX_Q8_INT8>(p, stream) : launch_extend<128, RX_Q8_E4M3>(p, stream);
     return q8->format == RX_Q8_INT8 ? launch_extend<64, RX_Q8_INT8>(p, stream) : launch_extend<64, RX_Q8_E4M3>(p, stream);
+}
+
+int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    const int dc = eq_device();
+    if (dc != RX_OK) return dc;
+    const size_t need = extend_q8_bytes(d);
+    RX_REQUIRE(ws && ws_bytes >= need && ((uintptr_t)ws & 255) == 0,
+               "prefix_extend_attention_q8: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", need, ws_bytes);
+    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - EQ_ROWS, "prefix_extend_attention_q8: too many rows in a request");
+    ExtendQ8Params p{};
+    eq_params(p, a, d, q8, ws);
+    p.q_map_ok = eq_rows_map(&p.q_map, a.q, d->hq, d->head_dim, p.group) ? 1 : 0;
+    return launch_extend(p, d, q8, stream);
+}
+
+// A decode batch's groups as the kernels take them: SharedGroup per group, members (-1: not one), and the keys that each
+// request takes from its group's shared run.  A group with bad boundaries is left out (its members read their own keys), and so is a member
+// that is no request or has fewer keys than the run.
+__global__ void __launch_bounds__(512) shared_q8_groups_kernel(rx_shared_groups g, int32_t batch, const int32_t* kv_lens, int64_t stride,
+                                                               int32_t max_kv_len, SharedGroup* groups, int32_t* members,
+                                                               int32_t* shared_of, int32_t* status) {
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int b = threadIdx.x; b < batch; b += blockDim.x) shared_of[b] = 0, members[b] = -1;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = warp; i < g.num_groups; i += blockDim.x / 32) {
+        const int32_t first = g.d_group_indptr[i], end = g.d_group_indptr[i + 1], len = g.d_group_len[i];
+        const bool good = first >= 0 && end >= first && end <= batch && len >= 1 && len <= stride && len <= max_kv_len;
+        if (!good && lane == 0) report(status, RX_DEV_BAD_LENGTH);
+        int src = -1;
+        for (int m0 = first; good && m0 < end; m0 += 32) {
+            const int m = m0 + lane;
+            int b = m < end ? g.d_group_members[m] : -1;
+            const bool is = b >= 0 && b < batch;
+            if (m < end && !is) report(status, RX_DEV_BAD_LENGTH);
+            if (!is || kv_lens[b] < len || kv_lens[b] > stride || kv_lens[b] > max_kv_len) b = -1;
+            if (m < end) members[m] = b;
+            if (b >= 0) shared_of[b] = len;
+            const unsigned any = __ballot_sync(0xffffffffu, b >= 0);
+            if (src < 0 && any) src = __shfl_sync(0xffffffffu, b, __ffs(any) - 1);
+        }
+        if (lane == 0) groups[i] = SharedGroup{first, src >= 0 ? end - first : 0, len, src};
+    }
+}
+
+struct SharedLayout {
+    size_t lse, of, members, groups, total;      // shared_o first, the tiles' parts last
+};
+
+static SharedLayout shared_layout(const rx_attn_desc* d, int32_t batch, int32_t num_groups) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    SharedLayout L{};
+    L.lse = up((size_t)batch * d->hq * d->head_dim * sizeof(float));
+    L.of = L.lse + up((size_t)batch * d->hq * sizeof(float));
+    L.members = L.of + up((size_t)batch * sizeof(int32_t));
+    L.groups = L.members + up((size_t)batch * sizeof(int32_t));
+    L.total = L.groups + up((size_t)num_groups * sizeof(SharedGroup));
+    return L;
+}
+
+size_t shared_q8_bytes(const rx_attn_desc* d, int32_t batch, int32_t num_groups) {
+    return shared_layout(d, batch, num_groups).total + extend_q8_bytes(d);
+}
+
+int shared_q8_launch(RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws, cudaStream_t stream) {
+    const int dc = eq_device();
+    if (dc != RX_OK) return dc;
+    const SharedLayout L = shared_layout(d, a.batch, g->num_groups);
+    unsigned char* w = (unsigned char*)ws;
+    ExtendQ8Params p{};
+    eq_params(p, a, d, q8, w + L.total);
+    p.batch = g->num_groups;
+    p.shared_o = (float*)w;
+    p.shared_lse = (float*)(w + L.lse);
+    p.members = (const int32_t*)(w + L.members);
+    p.groups = (const SharedGroup*)(w + L.groups);
+    launch_pdl(shared_q8_groups_kernel, 1, 512, 0, stream, *g, a.batch, a.kv_lens, a.stride, a.max_kv_len, (SharedGroup*)(w + L.groups),
+               (int32_t*)(w + L.members), (int32_t*)(w + L.of), a.status);
+    a.shared_of = (const int32_t*)(w + L.of);
+    a.shared_o = p.shared_o;
+    a.shared_lse = p.shared_lse;
+    return launch_extend(p, d, q8, stream);
 }
 
 }  // namespace rx

@@ -116,15 +116,29 @@ struct RowsParams {
     float* lse;
     float* part_o;                    // [CTAs][2][heads of a CTA][rows of a tile][D], normalised
     float* part_lse;                  // base 2
+    const int32_t* shared_of;         // decode with shared runs: leading keys that are not read here (null: none),
+    const float* shared_o;            // and their part of the rows [batch * hq][D], normalised
+    const float* shared_lse;          // base 2
     int4* meta;                       // [CTAs][2]: request (-1: no part), row tile, first head, whether its keys end here
     int32_t* status;
 };
+
+// A row's part from a shared run, if it has one, joined to its own: two factors, of the row's own and of the run's, and
+// the log-sum-exp of both.
+__device__ __forceinline__ float2 join_shared(const RowsParams& p, int64_t at, int64_t request, float& lse) {
+    if (!p.shared_of || p.shared_of[request] == 0) return make_float2(1.f, 0.f);
+    const float other = p.shared_lse[at], M = fmaxf(lse, other), ref = M == -INFINITY ? 0.f : M;
+    const float a = exp2f(lse - ref), b = exp2f(other - ref), sum = a + b;
+    if (sum == 0.f) return make_float2(1.f, 0.f);
+    lse = M + log2f(sum);
+    return make_float2(a / sum, b / sum);
+}
 
 // A request's rows: where its first is, how many tokens, and how many keys lie before them; false where there is none to do.
 __device__ __forceinline__ bool rows_of(const RowsParams& p, int b, bool tell, int64_t& q0, int& n, int& before) {
     if (p.kv_lens) {
         const int32_t L = p.kv_lens[b];
-        q0 = b, n = 1, before = L - 1;
+        q0 = b, n = 1, before = L - 1 - (p.shared_of ? p.shared_of[b] : 0);
         if (L >= 0 && L <= p.max_kv_len && L <= p.stride) return true;
     } else {
         q0 = p.qo_indptr[b];
@@ -219,8 +233,9 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
     // the first ones up to the table's stride beside the request's lengths, not after them.
     const int cols = KS << p.hb, col = tid & (cols - 1), row0 = tid / cols, rstep = RQ_THREADS / cols;
     const int skey = tid >> p.hb, shead = tid & (HB - 1);              // scales: key of the stage, head
-    const int32_t* table = p.r2t + (int64_t)b * p.stride + k_begin;
-    const int64_t width = p.stride - k_begin;
+    const int64_t skip = (p.shared_of ? p.shared_of[b] : 0) + k_begin;      // keys of the request before this piece's
+    const int32_t* table = p.r2t + (int64_t)b * p.stride + skip;
+    const int64_t width = p.stride - skip;
     int32_t sl[CPT], ss;
     auto load_slots = [&](int i) {
 #pragma unroll
@@ -444,6 +459,11 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         if (whole) {
             const int R = R0 + r, tok = R / G;
             const int64_t at = (q0 + tok) * p.hq + (g0 + head) * G + R % G;
+            const float2 f = join_shared(p, at, q0, lse);
+            if (f.y != 0.f) {
+                const float2 s = *reinterpret_cast<const float2*>(p.shared_o + at * D + d);
+                a0 = a0 * f.x + s.x * f.y, a1 = a1 * f.x + s.y * f.y;
+            }
             store_row2((T*)p.out + at * D + d, a0, a1);
             if (with_lse && p.lse) p.lse[at] = lse * RQ_LN2;
         } else {
@@ -559,6 +579,10 @@ __global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constan
     else lse = merge_many<D, RQ_CTAS>(list, count, p.part_o, p.part_lse, rows_a_tile << p.hb, r, acc);
     if (WAYS > 1 && warp != 0) return;
     const int64_t at = (q0 + R / p.group) * p.hq + (what.z + r / rows_a_tile) * p.group + R % p.group;
+    const float2 f = join_shared(p, at, q0, lse);
+    if (f.y != 0.f)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f.x + p.shared_o[at * D + lane * E + e] * f.y;
     T* row = (T*)p.out + at * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2) store_row2(row + e, acc[e], acc[e + 1]);
@@ -678,6 +702,9 @@ int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, c
     p.part_o = (float*)ws;
     p.part_lse = (float*)((unsigned char*)ws + L.lse_at);
     p.meta = (int4*)((unsigned char*)ws + L.meta_at);
+    p.shared_of = a.shared_of;
+    p.shared_o = a.shared_o;
+    p.shared_lse = a.shared_lse;
     p.status = a.status;
     if (d->dtype == RX_F32)
         return d->head_dim == 128 ? launch_rows<float, 128>(fn, p, L.nt, q8->format, (unsigned)L.ctas, stream)

@@ -25,6 +25,17 @@ struct RowsQ8Args {
     float* lse;
     int32_t batch, max_qo_len, max_kv_len;
     int32_t* status;
+    // decode with shared runs: the keys that each request leaves to its group's run (0: none), and that run's part of its rows
+    const int32_t* shared_of;
+    const float* shared_o;
+    const float* shared_lse;
+};
+
+// A group of requests of a decode batch with a shared run of keys.
+struct SharedGroup {
+    int32_t first, count;        // members
+    int32_t len;                 // keys
+    int32_t src;                 // a member, whose slot-table row has them
 };
 
 // How rows_q8.cu shares out a call, and the workspace it needs for parts of rows (0: none).
@@ -42,5 +53,9 @@ int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, c
 constexpr int64_t ROWS_Q8_MOST = 16;
 size_t extend_q8_bytes(const rx_attn_desc* d);
 int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+// The shared runs of a decode batch's groups on that kernel; sets a's shared_* for the call of rows_q8_launch that does the rest.
+size_t shared_q8_bytes(const rx_attn_desc* d, int32_t batch, int32_t num_groups);
+int shared_q8_launch(RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws, cudaStream_t stream);
 
 }  // namespace rx

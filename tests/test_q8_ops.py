@@ -352,6 +352,37 @@ def test_write_q8_bad_slots_and_lengths(dev):
         assert sorted(touched) == sorted(written)
 
 
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt,hkv,d,block", [(BF, 8, 128, 1), (F, 8, 128, 16), (BF, 3, 64, 1), (F, 5, 64, 1)])
+def test_write_q8_many_rows(dev, fmt, dt, hkv, d, block):
+    """Calls of a size where several rows are in flight at once, with odd numbers of rows and heads."""
+    n = 20011 if d == 128 else 70001 // hkv * 2
+    x = torch.randn(n, 2 * hkv, d, device=dev).to(dt)
+    k, v = x[:, :hkv], x[:, hkv:]
+    slots = n + 5
+    new = torch.randperm(slots, device=dev)[:n].to(torch.int32)
+    c = api.q8_desc(fmt, block, block > 1)
+    pools = [torch.zeros(slots, hkv, d, dtype=torch.int8, device=dev).view(TYPE[fmt]) for _ in range(2)]
+    scales = (1 + torch.rand(-(-slots // block), hkv, 2, device=dev)) * (3.0 / TOP[fmt]) if block > 1 else torch.zeros(slots, hkv, 2, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    desc = desc_of(dt, hkv, hkv, d, slots)
+    api.kv_pool_write_q8(desc, c, 1, None, None, new, i64([1, n - 1], dev), k, v, *pools, scales, None, n, st)
+    out = [torch.full((n, hkv, d), 7.0, dtype=dt, device=dev) for _ in range(2)]
+    api.kv_pool_read_q8(desc, c, new, *pools, scales, *out, st)
+    assert int(st) == 0
+    at = new[1:n - 1].long()
+    for j, y in enumerate((k, v)):
+        s = scales[at // block, :, j].double()
+        if block == 1:
+            assert torch.equal(s, scales_of(y[1:n - 1], fmt))
+        want = codes_of(y[1:n - 1], s, fmt)
+        got = bytes_of(pools[j])[at].view(TYPE[fmt]).double()
+        assert torch.equal(got, want)
+        assert torch.equal(out[j][1:n - 1], (got.float() * s.float()[..., None]).to(dt))
+        assert (bytes_of(pools[j])[new[[0, n - 1]].long()] == 0).all()
+
+
 # ============================================================================ reading
 @gpu
 @pytest.mark.parametrize("fmt", [INT8, E4M3])
@@ -388,6 +419,14 @@ def test_read_q8(dev, fmt, dt, hkv, d, block, n):
 
 
 # ============================================================================ decode
+def groups_of(dev, indptr_, members, lens, size, longest):
+    """The struct holds addresses: the arrays stay with it."""
+    arrays = i32(indptr_, dev), i32(members, dev), i32(lens, dev)
+    g = api.shared_groups_struct(len(indptr_) - 1, size, *arrays, longest)
+    g._keep = arrays
+    return g
+
+
 def table_of(lens, stride, slots, dev, seed=0):
     """Slot tables of requests that share nothing; unused entries -1.  Returns it and the slots in use."""
     ids = torch.randperm(slots, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
@@ -538,12 +577,66 @@ def test_decode_q8_groups(dev, fmt, dt):
     r2t[[1, 2, 5], :300] = r2t[0, :300].clone()
     r2t[4, :77] = r2t[3, :77].clone()
     cache = Cache(dev, fmt, slots, hkv, d, seed=4)
-    g = api.shared_groups_struct(2, 4, i32([0, 4, 6], dev), i32([0, 1, 2, 5, 4, 3], dev), i32([300, 77], dev), 300)
+    g = groups_of(dev, [0, 4, 6], [0, 1, 2, 5, 4, 3], [300, 77], 4, 300)
     q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=g)
     assert st == 0
     for b, n in enumerate(lens):
         k, v = cache.values(r2t[b, :n])
         agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), dt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt,block,hq,hkv,d,members,shared", [(E4M3, 1, 32, 8, 128, 70, 4001), (INT8, 64, 12, 12, 64, 300, 129),
+                                                             (INT8, 1, 8, 1, 128, 5, 20000), (E4M3, 1, 6, 2, 64, 200, 1)])
+def test_decode_q8_large_groups(dev, fmt, block, hq, hkv, d, members, shared):
+    """Groups whose rows fill several tiles, runs that several SMs share; members that have nothing of their own; others
+    between them."""
+    b = members + 6
+    lens = [shared + 3 * (i % 4) for i in range(members)] + [0, 1, 40, shared, 2, 7]
+    slots = shared + sum(n - shared for n in lens[:members]) + sum(lens[members:]) + 9
+    ids = torch.randperm(slots, device=dev).to(torch.int32)
+    stride = (max(lens) + 7) // 8 * 8
+    r2t = torch.full((b, stride), -1, dtype=torch.int32, device=dev)
+    at = shared
+    for i, n in enumerate(lens):
+        k = shared if i < members else 0
+        r2t[i, :k] = ids[:k]
+        r2t[i, k:n] = ids[at:at + n - k]
+        at += n - k
+    cache = Cache(dev, fmt, slots, hkv, d, block, seed=8)
+    g = groups_of(dev, [0, members], np.random.default_rng(0).permutation(members), [shared], members, shared)
+    q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens, r2t, groups=g)
+    assert st == 0
+    for i in [0, 1, 2, members - 1] + list(range(members, b)):
+        k, v = cache.values(r2t[i, :lens[i]])
+        agree(out[i:i + 1], lse[i:i + 1], attend(q[i:i + 1], k, v, 1 / math.sqrt(d), lens[i] - 1), BF)
+    alone = decode(dev, cache, BF, hq, hkv, d, lens, r2t)
+    # the same sums in another order: each within the bound above, so twice its rounding apart
+    assert ((out - alone[1]).float().abs().max() <= 2.0 ** -6 * out.float().abs().max())
+    assert torch.equal(lse.isinf(), alone[2].isinf()) and (lse - alone[2]).nan_to_num(0.0).abs().max() < 1e-3
+
+
+@gpu
+def test_decode_q8_bad_groups(dev):
+    """Members that are no request, runs longer than a member or than the table, boundaries that decrease: reported or left out,
+    and every request gets its row."""
+    hq, hkv, d = 8, 2, 128
+    lens = [90, 80, 50, 90]
+    r2t, _ = table_of(lens, 96, 400, dev)
+    r2t[1, :80] = r2t[0, :80]
+    r2t[3, :90] = r2t[0, :90]
+    cache = Cache(dev, INT8, 400, hkv, d, seed=4)
+    for ind, mem, length, code in (([0, 3], [0, 7, 1], [80], api.RX_DEV_BAD_LENGTH), ([0, 2], [0, -1], [60], api.RX_DEV_BAD_LENGTH),
+                                   ([0, 3], [0, 1, 3], [85], 0), ([0, 2], [0, 1], [97], api.RX_DEV_BAD_LENGTH),
+                                   ([0, 2, 1], [0, 1], [80, 5], api.RX_DEV_BAD_LENGTH), ([0, 9], [0, 1], [80], api.RX_DEV_BAD_LENGTH),
+                                   ([0, 0], [0], [80], 0), ([0, 2], [0, 1], [0], api.RX_DEV_BAD_LENGTH)):
+        mem = mem + [0] * 8
+        g = groups_of(dev, ind, mem, length, 3, 90)
+        q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens, r2t, groups=g)
+        assert st == code, (ind, mem, length)
+        for b, n in enumerate(lens):
+            k, v = cache.values(r2t[b, :n])
+            agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), BF)
 
 
 # ============================================================================ extend
@@ -736,6 +829,87 @@ def test_serving_steps_q8(dev, fmt, dt, captured):
         for i, x in enumerate(tables):
             kk, vv = cache.values(x)
             agree(od[i:i + 1], ld[i:i + 1], attend(qd[i:i + 1], kk, vv, 1 / math.sqrt(d), len(x) - 1), dt)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+def test_q8_calls_at_once(dev, dt):
+    """Calls on three streams, and two captured graphs replayed side by side, with workspaces of their own, give what each gives
+    alone."""
+    hq, hkv, d, slots = 16, 4, 128, 9000
+    cache = Cache(dev, E4M3, slots, hkv, d, seed=12)
+    desc = desc_of(dt, hq, hkv, d, slots)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    jobs = []
+    for i, (lens, pre) in enumerate((([40, 300], [3000, 0]), ([1] * 9, [900] * 9), ([700], [1200]))):
+        total = [a + b for a, b in zip(lens, pre)]
+        stride = (max(total) + 7) // 8 * 8
+        r2t, _ = table_of(total, stride, slots, dev, seed=i)
+        q = torch.randn(sum(lens), hq, d, device=dev).to(dt)
+        ws = [torch.empty(max(n, 256), dtype=torch.uint8, device=dev) for n in
+              (api.extend_q8_workspace_bytes(desc, len(lens), max(lens), stride), api.decode_q8_workspace_bytes(desc, len(lens), stride))]
+        jobs.append(dict(r2t=r2t, lens=lens, ind=indptr(lens, dev), pre=i32(pre, dev), kv=i32(total, dev), q=q, ws=ws, stride=stride,
+                         out=torch.zeros_like(q), dec=torch.zeros(len(lens), hq, d, dtype=dt, device=dev), dq=q[:len(lens)].contiguous()))
+
+    def run(j):
+        api.prefix_extend_attention_q8(desc, cache.q8, len(j["lens"]), j["q"], j["ind"], j["pre"], j["r2t"], cache.k, cache.v, cache.scales,
+                                       j["out"], None, max(j["lens"]), j["ws"][0], st)
+        api.decode_attention_q8(desc, cache.q8, len(j["lens"]), j["dq"], j["r2t"], j["kv"], cache.k, cache.v, cache.scales, j["dec"], None,
+                                j["stride"], j["ws"][1], st)
+    want = []
+    for j in jobs:
+        run(j)
+        torch.cuda.synchronize()
+        want.append((j["out"].clone(), j["dec"].clone()))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    graphs = []
+    for j, s in zip(jobs[:2], streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            run(j)
+    for captured in (False, True):
+        for j in jobs:
+            j["out"].zero_(), j["dec"].zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i, (j, s) in enumerate(zip(jobs, streams)):
+                with torch.cuda.stream(s):
+                    graphs[i].replay() if captured and i < 2 else run(j)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        for j, w in zip(jobs, want):
+            assert torch.equal(j["out"], w[0]) and torch.equal(j["dec"], w[1])
+
+
+@gpu
+def test_q8_slots_past_32_bits(dev):
+    """Pools of more than 2^31 bytes, slots at their ends."""
+    hq, hkv, d = 32, 16, 128
+    slots = (1 << 31) // (hkv * d) + 5000
+    q8 = api.q8_desc(E4M3)
+    pools = [torch.zeros(slots, hkv, d, dtype=torch.int8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = torch.zeros(slots, hkv, 2, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    desc = desc_of(BF, hq, hkv, d, slots)
+    n = 400
+    new = (slots - 1 - torch.randperm(4000, device=dev)[:n]).to(torch.int32)
+    k, v = (torch.randn(n, hkv, d, device=dev).to(BF) for _ in range(2))
+    r2t = torch.empty(1, n, dtype=torch.int32, device=dev)
+    api.kv_pool_write_q8(desc, q8, 1, None, i64([0, 0], dev), new, i64([0, n], dev), k, v, *pools, scales, r2t, n, st)
+    out = [torch.empty_like(k) for _ in range(2)]
+    api.kv_pool_read_q8(desc, q8, new, *pools, scales, *out, st)
+    for y, o in zip((k, v), out):
+        assert torch.equal(o.double(), codes_of(y, scales_of(y, E4M3), E4M3) * scales_of(y, E4M3)[..., None])
+    q = torch.randn(60, hq, d, device=dev).to(BF)
+    got, lse = torch.empty_like(q), torch.empty(60, hq, device=dev)
+    ws = torch.empty(max(api.extend_q8_workspace_bytes(desc, 1, 60, n), api.decode_q8_workspace_bytes(desc, 1, n), 256),
+                     dtype=torch.uint8, device=dev)
+    api.prefix_extend_attention_q8(desc, q8, 1, q, i64([0, 60], dev), i32([n - 60], dev), r2t, *pools, scales, got, lse, 60, ws, st)
+    values = [o.double() for o in out]
+    agree(got, lse, attend(q, *values, 1 / math.sqrt(d), n - 60), BF)
+    api.decode_attention_q8(desc, q8, 1, q[:1], r2t, i32([n], dev), *pools, scales, got[:1], lse[:1], n, ws, st)
+    agree(got[:1], lse[:1], attend(q[:1], *values, 1 / math.sqrt(d), n - 1), BF)
+    assert int(st) == 0
 
 
 @gpu
