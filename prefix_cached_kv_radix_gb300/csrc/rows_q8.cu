@@ -38,26 +38,28 @@ namespace rx {
 
 constexpr int RQ_THREADS = 256;
 constexpr int RQ_WARPS = RQ_THREADS / 32;
-constexpr int RQ_KEYS = 16;           // keys of a warp's stage
 constexpr int RQ_NS = 3;              // stages
-constexpr int RQ_CTAS = 152 * 3;      // most CTAs that stages are shared out to
+constexpr int RQ_RUN = 512;           // keys whose slots are read at a time: two stages at least
+constexpr int RQ_CTAS = 152 * 2;      // most CTAs that stages are shared out to
 constexpr float RQ_LOG2E = 1.4426950408889634f, RQ_LN2 = 0.6931471805599453f;
 constexpr float RQ_TOP = 15.f;        // a row's largest weight is 2^15 in f16
 
 template <int D>
 struct RowsLayout {
-    static constexpr int CODES = RQ_KEYS * D;                          // one pool's codes of a warp's stage
-    static constexpr int WARP = 2 * CODES + RQ_KEYS * 8;               // K, V, scales
+    static constexpr int SUB = 128 / D, KEYS = 16 * SUB;               // tiles of 16 keys, and keys, of a warp's stage
+    static constexpr int CODES = KEYS * D;                             // one pool's codes of it
+    static constexpr int WARP = 2 * CODES + KEYS * 8;                  // K, V, scales
     static constexpr int STAGE = RQ_WARPS * WARP;
-    static constexpr int BYTES = RQ_NS * STAGE;
+    static constexpr int LIST = RQ_NS * STAGE;                         // slots of two runs of RQ_RUN keys
+    static constexpr int BYTES = LIST + 2 * RQ_RUN * 4;
     static constexpr int RS = D + 4;                                   // floats between rows that are joined
     // eight warps' 8 rows, their statistics, weights and each row's lse
     static constexpr int JOIN = RQ_WARPS * 8 * (RS + 5) * 4;
-    static_assert(JOIN <= BYTES, "the ring holds what is joined");
+    static_assert(JOIN <= LIST, "the ring holds what is joined");
 };
 
 // CTAs an SM holds: registers.
-constexpr int rows_a_sm(bool f32, int D, int nt) { return nt > 1 ? 1 : f32 ? (D == 64 ? 2 : 1) : D == 64 ? 3 : 2; }
+constexpr int rows_a_sm(bool f32, int D, int nt) { return nt > 1 || (f32 && D == 128) ? 1 : 2; }
 template <typename T, int D, int NT>
 constexpr int rows_a_sm() { return rows_a_sm(sizeof(T) == 4, D, NT); }
 
@@ -126,7 +128,7 @@ struct RowsParams {
 // A row's part from a shared run, if it has one, joined to its own: two factors, of the row's own and of the run's, and
 // the log-sum-exp of both.
 __device__ __forceinline__ float2 join_shared(const RowsParams& p, int64_t at, int64_t request, float& lse) {
-    if (!p.shared_of || p.shared_of[request] == 0) return make_float2(1.f, 0.f);
+    if (p.shared_of[request] == 0) return make_float2(1.f, 0.f);
     const float other = p.shared_lse[at], M = fmaxf(lse, other), ref = M == -INFINITY ? 0.f : M;
     const float a = exp2f(lse - ref), b = exp2f(other - ref), sum = a + b;
     if (sum == 0.f) return make_float2(1.f, 0.f);
@@ -135,10 +137,11 @@ __device__ __forceinline__ float2 join_shared(const RowsParams& p, int64_t at, i
 }
 
 // A request's rows: where its first is, how many tokens, and how many keys lie before them; false where there is none to do.
+template <bool RUNS>
 __device__ __forceinline__ bool rows_of(const RowsParams& p, int b, bool tell, int64_t& q0, int& n, int& before) {
     if (p.kv_lens) {
         const int32_t L = p.kv_lens[b];
-        q0 = b, n = 1, before = L - 1 - (p.shared_of ? p.shared_of[b] : 0);
+        q0 = b, n = 1, before = L - 1 - (RUNS ? p.shared_of[b] : 0);
         if (L >= 0 && L <= p.max_kv_len && L <= p.stride) return true;
     } else {
         q0 = p.qo_indptr[b];
@@ -157,10 +160,11 @@ __device__ __forceinline__ int tile_stages(const RowsParams& p, int n, int befor
     return max(before + last / p.group + span, span) / span;
 }
 
+template <bool RUNS>
 __device__ __forceinline__ int64_t request_stages(const RowsParams& p, int b, bool tell, int rows_a_tile, int span) {
     int64_t q0, sum = 0;
     int n, before;
-    if (!rows_of(p, b, tell, q0, n, before)) return 0;
+    if (!rows_of<RUNS>(p, b, tell, q0, n, before)) return 0;
     for (int t = 0; t * rows_a_tile < n * p.group; ++t) sum += tile_stages(p, n, before, t, rows_a_tile, span);
     return sum * (p.hkv >> p.hb);
 }
@@ -172,18 +176,20 @@ __device__ __forceinline__ void store_row2(float* p, float a, float b) { *reinte
 template <>
 __device__ __forceinline__ void store_row2(__nv_bfloat16* p, float a, float b) { *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b); }
 
-template <typename T, int D, int FMT, int NT>
+// RUNS: some requests' leading keys are shared runs, not read here.
+template <typename T, int D, int FMT, int NT, bool RUNS>
 __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_kernel(const __grid_constant__ RowsParams p) {
     using LY = RowsLayout<D>;
     constexpr bool TWO = std::is_same<T, float>::value;     // two f16 parts
     constexpr int KS = D / 16;                              // 16-byte chunks of a row: steps of K, and of V's M
-    constexpr int CPT = RQ_WARPS * RQ_KEYS * KS / RQ_THREADS;    // copies per thread, stage and pool
+    constexpr int SUB = LY::SUB, KEYS = LY::KEYS;
+    constexpr int CPT = RQ_WARPS * KEYS * KS / RQ_THREADS;    // copies per thread, stage and pool
     constexpr int WPI = RQ_THREADS / 32;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t4 = lane & 3, r8 = lane >> 2;
-    const int HB = 1 << p.hb, ways = WPI >> p.hb, way = warp >> p.hb, span = RQ_KEYS * ways;      // span: keys of a stage
+    const int HB = 1 << p.hb, ways = WPI >> p.hb, way = warp >> p.hb, span = KEYS * ways;      // span: keys of a stage
     constexpr int RT = 8 * NT;                                         // rows of a tile
     const int G = p.group, groups = p.hkv >> p.hb;
     __shared__ int64_t share[RQ_WARPS + 4];
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         auto locate = [&](int r, int64_t at, int& t, int& gr, int& stages) {       // stage `at` of request r's; returns the tile's
             int64_t q;
             int m, bf;
-            rows_of(p, r, false, q, m, bf);
+            rows_of<RUNS>(p, r, false, q, m, bf);
             for (t = 0;; ++t) {
                 stages = tile_stages(p, m, bf, t, RT, span);
                 if (at < (int64_t)stages * groups) break;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
             return (int)(at - (int64_t)gr * stages);
         };
         share_out<RQ_THREADS>(
-            p.batch, 4, share, share + RQ_WARPS, [&](int r, bool tell) { return request_stages(p, r, tell, RT, span); },
+            p.batch, 4, share, share + RQ_WARPS, [&](int r, bool tell) { return request_stages<RUNS>(p, r, tell, RT, span); },
             [&](int r, int64_t at, int64_t near) {
                 int t, gr, stages;
                 const int j = locate(r, at, t, gr, stages);
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         left = share[RQ_WARPS + 1] - share[RQ_WARPS];
         b = (int)share[RQ_WARPS + 2];
         if (left > 0) {                  // the border may have moved past the end of its request
-            for (int64_t all; b + 1 < p.batch && at >= (all = request_stages(p, b, false, RT, span)); ++b) at -= all;
+            for (int64_t all; b + 1 < p.batch && at >= (all = request_stages<RUNS>(p, b, false, RT, span)); ++b) at -= all;
             int stages;
             s0 = locate(b, at, tile, gi, stages);
         }
@@ -228,28 +234,32 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
     int4 told[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};
     for (; left > 0;) {
     const int g0 = gi << p.hb, g = g0 + (warp & (HB - 1)), R0 = tile * RT, k_begin = s0 * span;
-    // What this thread copies of a stage: 16-byte chunk `col` of the heads' HB * D bytes of every key it handles, and for the first
-    // 16 WPI threads one key's scales of one head.  The slots of a stage's keys are loaded two stages before their codes 
-    // the first ones up to the table's stride beside the request's lengths, not after them.
+    // What this thread copies of a stage: 16-byte chunk `col` of the heads' HB * D bytes of every key it handles, and one key's scales
+    // of one head.
     const int cols = KS << p.hb, col = tid & (cols - 1), row0 = tid / cols, rstep = RQ_THREADS / cols;
     const int skey = tid >> p.hb, shead = tid & (HB - 1);              // scales: key of the stage, head
-    const int64_t skip = (p.shared_of ? p.shared_of[b] : 0) + k_begin;      // keys of the request before this piece's
+    // Slots: runs of RQ_RUN keys in shared memory, two in turn.  The first ones are loaded, up to the table's stride, beside the
+    // request's lengths, not after them; a later one while the one before it is used.
+    const int64_t skip = (RUNS ? p.shared_of[b] : 0) + (int64_t)k_begin;      // keys of the request before this piece's
     const int32_t* table = p.r2t + (int64_t)b * p.stride + skip;
     const int64_t width = p.stride - skip;
-    int32_t sl[CPT], ss;
-    auto load_slots = [&](int i) {
+    int32_t* list = reinterpret_cast<int32_t*>(smem + LY::LIST);
+    int32_t run[2];                      // two keys a thread, of a run on its way to the list
+    auto load_run = [&](int i) {
 #pragma unroll
-        for (int x = 0; x < CPT; ++x) {
-            const int key = i * span + row0 + x * rstep;
-            sl[x] = key < width ? table[key] : -1;
+        for (int x = 0; x < 2; ++x) {
+            const int key = i * RQ_RUN + tid + x * RQ_THREADS;
+            run[x] = key < width ? table[key] : -1;
         }
-        const int key = i * span + skey;
-        ss = skey < span && key < width ? table[key] : -1;
     };
-    load_slots(0);
+    auto keep_run = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) list[(i & 1) * RQ_RUN + tid + x * RQ_THREADS] = run[x];
+    };
+    load_run(0);
     int64_t q0;
     int n, before;
-    const bool there = rows_of(p, b, !p.shared && tid == 0 && gi == 0 && tile == 0, q0, n, before);
+    const bool there = rows_of<RUNS>(p, b, !p.shared && tid == 0 && gi == 0 && tile == 0, q0, n, before);
     const int rows = there ? n * G : 0;
     if (R0 >= rows) break;                                             // no rows of this cell (not shared)
     const int last = min(R0 + RT, rows) - 1, stages = tile_stages(p, n, before, tile, RT, span);
@@ -264,31 +274,37 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
     const uint8_t* kcol = p.pools.k + (int64_t)g0 * D + col * 16;
     const uint8_t* vcol = p.pools.v + (int64_t)g0 * D + col * 16;
     const float2* scol = p.pools.scales + g0 + shead;
-    // Copies stage i, whose slots have been loaded; a key behind the last or at a bad slot is zeros, its scales marked (0, -1).
+    // Copies stage i, whose slots are in the list; a key behind the last or at a bad slot is zeros, its scales marked (0, -1).
     auto load_stage = [&](int i) {
         const uint32_t buf = ring + (uint32_t)(i % RQ_NS * LY::STAGE);
+        const int32_t* slots = list + i * span % (2 * RQ_RUN);
 #pragma unroll
         for (int x = 0; x < CPT; ++x) {
             const int key = row0 + x * rstep;
-            const bool in = i * span + key < nk && sl[x] >= 0 && sl[x] < p.num_slots;
-            const int64_t off = in ? (int64_t)sl[x] * pitch : 0;
-            const uint32_t to = buf + (uint32_t)((((key >> 4) << p.hb) + col / KS) * LY::WARP) + code_at<D>(key & 15, col % KS);
+            const int32_t s = slots[key];
+            const bool in = i * span + key < nk && s >= 0 && s < p.num_slots;
+            const int64_t off = in ? (int64_t)s * pitch : 0;
+            const uint32_t to = buf + (uint32_t)(((key / KEYS << p.hb) + col / KS) * LY::WARP) + code_at<D>(key % KEYS, col % KS);
             cp_async_16(to, kcol + off, in ? 16u : 0u);
             cp_async_16(to + LY::CODES, vcol + off, in ? 16u : 0u);
         }
         if (skey < span) {
-            const uint32_t to = buf + (uint32_t)((((skey >> 4) << p.hb) + shead) * LY::WARP + 2 * LY::CODES + (skey & 15) * 8);
-            const bool in = i * span + skey < nk, good = in && ss >= 0 && ss < p.num_slots;
+            const uint32_t to = buf + (uint32_t)(((skey / KEYS << p.hb) + shead) * LY::WARP + 2 * LY::CODES + skey % KEYS * 8);
+            const int32_t s = slots[skey];
+            const bool in = i * span + skey < nk, good = in && s >= 0 && s < p.num_slots;
             if (in && !good) report(p.status, RX_DEV_BAD_SLOT);
-            if (good) cp_async_8(to, scol + (int64_t)(ss >> p.pools.shift) * p.hkv);
+            if (good) cp_async_8(to, scol + (int64_t)(s >> p.pools.shift) * p.hkv);
             else asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
         }
     };
+    const int a_run = RQ_RUN / span;     // stages of a run
+    keep_run(0);
+    load_run(1);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < RQ_NS - 1; ++i) {
         if (i < nstages) load_stage(i);
         cp_async_commit();
-        load_slots(i + 1);
     }
     // query fragments: columns of the B operand, row R0 + 8 t + r8, channels 16 s + 4 t4 ..+3; and each accumulator
     // column's factor, scale log2(e) over the row's power of two
@@ -348,67 +364,82 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         mx[t][0] = mx[t][1] = my[t][0] = my[t][1] = -INFINITY;
         l[t][0] = l[t][1] = 0.f;
     }
+    keep_run(1);                         // seen after the next barrier; its first stage is copied after that
     for (int it = 0; it < nstages; ++it) {
         cp_async_wait<RQ_NS - 2>();
         __syncthreads();                       // stage `it` is here, of all threads, and the one before it has been read
-        if (it + RQ_NS - 1 < nstages) load_stage(it + RQ_NS - 1);
+        const int nx = it + RQ_NS - 1;         // the stage to be copied; the first of a run brings the run after it
+        if (nx < nstages) load_stage(nx);
         cp_async_commit();
-        load_slots(it + RQ_NS);
-        const int key0 = it * span + way * RQ_KEYS;
+        if (nx >= a_run) {
+            if (nx % a_run == 0) load_run(nx / a_run + 1);
+            else if (nx % a_run == 1) keep_run(nx / a_run + 1);
+        }
+        const int key0 = it * span + way * KEYS;
         if (key0 >= nk) continue;
         const uint32_t kb = ring + (uint32_t)(it % RQ_NS * LY::STAGE + warp * LY::WARP), vb = kb + LY::CODES;
         const int mi = lane >> 3, lrow = (mi & 1) * 8 + (lane & 7);
-        float sacc[NT][4], sodd[NT][4];        // of even and odd chunks: two chains of products
+        float sacc[SUB][NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < SUB; ++u) {
+            float sodd[NT][4];                 // of odd chunks: two chains of products
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[t][e] = sodd[t][e] = 0.f;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int s = 0; s < KS; s += 2) {
-            uint32_t w[4];                     // keys r8, r8 + 8 of chunk s, then of chunk s + 1
-            ldmatrix_x4(kb + code_at<D>(lrow, s + (mi >> 1)), w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 4; ++e) sacc[u][t][e] = sodd[t][e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t a[4];
-                q8_to_f16<FMT, false>(w[2 * j], a[0], a[2]);
-                q8_to_f16<FMT, false>(w[2 * j + 1], a[1], a[3]);
+            for (int s = 0; s < KS; s += 2) {
+                uint32_t w[4];                 // keys r8, r8 + 8 of chunk s, then of chunk s + 1
+                ldmatrix_x4(kb + code_at<D>(16 * u + lrow, s + (mi >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t a[4];
+                    q8_to_f16<FMT, false>(w[2 * j], a[0], a[2]);
+                    q8_to_f16<FMT, false>(w[2 * j + 1], a[1], a[3]);
 #pragma unroll
-                    for (int u = 0; u < (TWO ? 2 : 1); ++u)
-                        mma_f16_16816(j ? sodd[t] : sacc[t], a, qb[t][u][s + j][0], qb[t][u][s + j][1]);
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < (TWO ? 2 : 1); ++i)
+                            mma_f16_16816(j ? sodd[t] : sacc[u][t], a, qb[t][i][s + j][0], qb[t][i][s + j][1]);
+                }
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[u][t][e] += sodd[t][e];
         }
+        float ks[2 * SUB], lv[2 * SUB];        // of keys 8 i + r8: K's scale, log2 of V's
+        bool ok[2 * SUB], all_ok = true;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[t][e] += sodd[t][e];
-        float2 sa, sb;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(sa.x), "=f"(sa.y) : "r"(vb + LY::CODES + r8 * 8) : "memory");
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(sb.x), "=f"(sb.y) : "r"(vb + LY::CODES + r8 * 8 + 64) : "memory");
-        const bool oka = sa.y != -1.f, okb = sb.y != -1.f;
-        const float la = fast_log2(sa.y), lb = fast_log2(sb.y);
-        const bool whole = key0 + RQ_KEYS <= least && __all_sync(0xffffffffu, oka && okb);     // no key of these is hidden from any row
-        uint32_t pb[NT][TWO ? 2 : 1][2];
+        for (int i = 0; i < 2 * SUB; ++i) {
+            float vs;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks[i]), "=f"(vs) : "r"(vb + LY::CODES + r8 * 8 + 64 * i) : "memory");
+            ok[i] = vs != -1.f;
+            all_ok &= ok[i];
+            lv[i] = fast_log2(vs);
+        }
+        const bool whole = key0 + KEYS <= least && __all_sync(0xffffffffu, all_ok);     // no key of these is hidden from any row
+        uint32_t pb[SUB][NT][TWO ? 2 : 1][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float x[4] = {sacc[t][0] * (f[t][0] * sa.x), sacc[t][1] * (f[t][1] * sa.x), sacc[t][2] * (f[t][0] * sb.x),
-                          sacc[t][3] * (f[t][1] * sb.x)};
-            float y[4] = {x[0] + la, x[1] + la, x[2] + lb, x[3] + lb};
-            if (!whole) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (key0 + r8 + (e >> 1) * 8 >= end[t][e & 1] || !(e < 2 ? oka : okb)) x[e] = y[e] = -INFINITY;
-            }
-            float w[4];
+            float x[2 * SUB][2], y[2 * SUB][2], w[2 * SUB][2], up[2];
             bool moved = false;
-            float up[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float a = fmaxf(mx[t][e], fmaxf(x[e], x[e + 2])), ra = a == -INFINITY ? 0.f : a;
-                l[t][e] = l[t][e] * fast_exp2(mx[t][e] - ra) + fast_exp2(x[e] - ra) + fast_exp2(x[e + 2] - ra);
+                float a = mx[t][e], m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 2 * SUB; ++i) {
+                    x[i][e] = sacc[i / 2][t][2 * (i & 1) + e] * (f[t][e] * ks[i]);
+                    y[i][e] = x[i][e] + lv[i];
+                    if (!whole && (key0 + 8 * i + r8 >= end[t][e] || !ok[i])) x[i][e] = y[i][e] = -INFINITY;
+                    a = fmaxf(a, x[i][e]);
+                    m = fmaxf(m, y[i][e]);
+                }
+                const float ra = a == -INFINITY ? 0.f : a;
+                l[t][e] *= fast_exp2(mx[t][e] - ra);
+#pragma unroll
+                for (int i = 0; i < 2 * SUB; ++i) l[t][e] += fast_exp2(x[i][e] - ra);
                 mx[t][e] = a;
-                float m = fmaxf(y[e], y[e + 2]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
                 m = fmaxf(m, my[t][e]);
@@ -416,8 +447,8 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
                 up[e] = fast_exp2(my[t][e] - rm);
                 moved |= m != my[t][e];
                 my[t][e] = m;
-                w[e] = fast_exp2(y[e] - (rm - RQ_TOP));
-                w[e + 2] = fast_exp2(y[e + 2] - (rm - RQ_TOP));
+#pragma unroll
+                for (int i = 0; i < 2 * SUB; ++i) w[i][e] = fast_exp2(y[i][e] - (rm - RQ_TOP));
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -428,29 +459,30 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
                     o[t][i][3] *= up[1];
                 }
             }
-            const uint32_t h0 = pack_f16x2(w[0], w[1]), h1 = pack_f16x2(w[2], w[3]);
-            pb[t][0][0] = movmatrix_trans(h0);
-            pb[t][0][1] = movmatrix_trans(h1);
-            if (TWO) {
-                pb[t][TWO ? 1 : 0][0] = movmatrix_trans(pack_rest_f16x2(w[0], w[1], h0));
-                pb[t][TWO ? 1 : 0][1] = movmatrix_trans(pack_rest_f16x2(w[2], w[3], h1));
+#pragma unroll
+            for (int i = 0; i < 2 * SUB; ++i) {
+                const uint32_t h = pack_f16x2(w[i][0], w[i][1]);
+                pb[i / 2][t][0][i & 1] = movmatrix_trans(h);
+                if (TWO) pb[i / 2][t][TWO ? 1 : 0][i & 1] = movmatrix_trans(pack_rest_f16x2(w[i][0], w[i][1], h));
             }
         }
 #pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-            uint32_t w[4];                     // byte pairs of channels 2 r8, 2 r8 + 1: keys 2 t4, 2 t4 + 1, then those + 8; two chunks
-            ldmatrix_x4_trans(vb + code_at<D>(lrow, i + (mi >> 1)), w[0], w[1], w[2], w[3]);
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t a[4];                 // rows r8: channel 2 r8, rows r8 + 8: channel 2 r8 + 1
-                q8_to_f16<FMT, true>(w[2 * j], a[0], a[1]);
-                q8_to_f16<FMT, true>(w[2 * j + 1], a[2], a[3]);
+            for (int i = 0; i < KS; i += 2) {
+                uint32_t w[4];                 // byte pairs of channels 2 r8, 2 r8 + 1: keys 2 t4, 2 t4 + 1, then those + 8; two chunks
+                ldmatrix_x4_trans(vb + code_at<D>(16 * u + lrow, i + (mi >> 1)), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t a[4];             // rows r8: channel 2 r8, rows r8 + 8: channel 2 r8 + 1
+                    q8_to_f16<FMT, true>(w[2 * j], a[0], a[1]);
+                    q8_to_f16<FMT, true>(w[2 * j + 1], a[2], a[3]);
 #pragma unroll
-                    for (int u = 0; u < (TWO ? 2 : 1); ++u) mma_f16_16816(o[t][i + j], a, pb[t][u][0], pb[t][u][1]);
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int n = 0; n < (TWO ? 2 : 1); ++n) mma_f16_16816(o[t][i + j], a, pb[u][t][n][0], pb[u][t][n][1]);
+                }
             }
-        }
     }
     cp_async_wait<0>();
 
@@ -459,10 +491,12 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         if (whole) {
             const int R = R0 + r, tok = R / G;
             const int64_t at = (q0 + tok) * p.hq + (g0 + head) * G + R % G;
-            const float2 f = join_shared(p, at, q0, lse);
-            if (f.y != 0.f) {
-                const float2 s = *reinterpret_cast<const float2*>(p.shared_o + at * D + d);
-                a0 = a0 * f.x + s.x * f.y, a1 = a1 * f.x + s.y * f.y;
+            if (RUNS) {
+                const float2 f = join_shared(p, at, q0, lse);
+                if (f.y != 0.f) {
+                    const float2 s = *reinterpret_cast<const float2*>(p.shared_o + at * D + d);
+                    a0 = a0 * f.x + s.x * f.y, a1 = a1 * f.x + s.y * f.y;
+                }
             }
             store_row2((T*)p.out + at * D + d, a0, a1);
             if (with_lse && p.lse) p.lse[at] = lse * RQ_LN2;
@@ -545,7 +579,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
         if (++tile * RT >= rows) {
             tile = 0;
             do ++b;
-            while (b < p.batch && !rows_of(p, b, false, q0, n, before));
+            while (b < p.batch && !rows_of<RUNS>(p, b, false, q0, n, before));
             if (b >= p.batch) break;
         }
     }
@@ -556,7 +590,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
 
 // Rows from their parts: blockIdx.x the begun and not ended item, four rows a block with a warp each (WAYS 1), or one row a block
 // with all its warps.
-template <typename T, int D, int WAYS>
+template <typename T, int D, int WAYS, bool RUNS>
 __global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constant__ RowsParams p, int rows_a_tile, int ctas) {
     constexpr int E = D / 32;
     __shared__ int list[RQ_CTAS];
@@ -569,7 +603,7 @@ __global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constan
     const int4 what = p.meta[list[0]];
     int64_t q0;
     int n, before;
-    rows_of(p, what.x, false, q0, n, before);
+    rows_of<RUNS>(p, what.x, false, q0, n, before);
     const int r = blockIdx.y * (4 / WAYS) + (WAYS == 1 ? warp : 0);      // rows of a head, then the next head's
     const int R = what.y * rows_a_tile + r % rows_a_tile;
     if (R >= n * p.group) return;                                        // the same for all who share the row
@@ -579,7 +613,7 @@ __global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constan
     else lse = merge_many<D, RQ_CTAS>(list, count, p.part_o, p.part_lse, rows_a_tile << p.hb, r, acc);
     if (WAYS > 1 && warp != 0) return;
     const int64_t at = (q0 + R / p.group) * p.hq + (what.z + r / rows_a_tile) * p.group + R % p.group;
-    const float2 f = join_shared(p, at, q0, lse);
+    const float2 f = RUNS ? join_shared(p, at, q0, lse) : make_float2(1.f, 0.f);
     if (f.y != 0.f)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = acc[e] * f.x + p.shared_o[at * D + lane * E + e] * f.y;
@@ -589,12 +623,12 @@ __global__ void __launch_bounds__(128) rows_q8_merge_kernel(const __grid_constan
     if (p.lse && lane == 0) p.lse[at] = lse * RQ_LN2;
 }
 
-template <typename T, int D, int FMT, int NT>
+template <typename T, int D, int FMT, int NT, bool RUNS>
 static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaStream_t s) {
     constexpr int smem = RowsLayout<D>::BYTES;
     static PerDeviceOnce attr;
     const int rc = per_device_once(attr, [&] {
-        auto* k = rows_q8_kernel<T, D, FMT, NT>;
+        auto* k = rows_q8_kernel<T, D, FMT, NT, RUNS>;
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess) (void)cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) {
@@ -604,7 +638,7 @@ static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaS
         return (int)RX_OK;
     });
     if (rc != RX_OK) return rc;
-    launch_pdl(rows_q8_kernel<T, D, FMT, NT>, grid, RQ_THREADS, smem, s, p);
+    launch_pdl(rows_q8_kernel<T, D, FMT, NT, RUNS>, grid, RQ_THREADS, smem, s, p);
     if (p.shared) {
         // few items: each in many parts, so a block a row; many items: a few parts each, a warp a row
         const int64_t items = (int64_t)p.batch * p.tiles * (p.hkv >> p.hb), rows = 8 * NT << p.hb;
@@ -618,8 +652,8 @@ static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaS
         pdl[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = pdl;
         cfg.numAttrs = 1;
-        if (few) cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 4>, p, 8 * NT, (int)grid);
-        else cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 1>, p, 8 * NT, (int)grid);
+        if (few) cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 4, RUNS>, p, 8 * NT, (int)grid);
+        else cudaLaunchKernelEx(&cfg, rows_q8_merge_kernel<T, D, 1, RUNS>, p, 8 * NT, (int)grid);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
@@ -631,7 +665,9 @@ static int launch_tile(const char* fn, const RowsParams& p, unsigned grid, cudaS
 
 template <typename T, int D, int FMT>
 static int launch_fmt(const char* fn, const RowsParams& p, int nt, unsigned grid, cudaStream_t s) {
-    return nt == 1 ? launch_tile<T, D, FMT, 1>(fn, p, grid, s) : launch_tile<T, D, FMT, 2>(fn, p, grid, s);
+    if constexpr (!std::is_same<T, float>::value)
+        if (p.shared_of) return nt == 1 ? launch_tile<T, D, FMT, 1, true>(fn, p, grid, s) : launch_tile<T, D, FMT, 2, true>(fn, p, grid, s);
+    return nt == 1 ? launch_tile<T, D, FMT, 1, false>(fn, p, grid, s) : launch_tile<T, D, FMT, 2, false>(fn, p, grid, s);
 }
 
 template <typename T, int D>
@@ -649,17 +685,17 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     L.nt = rows_nt(rows);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
-    // many heads as take the least time.  In stages of a CTA, about a microsecond: its start and end cost four, sharing
-    // out and merging seven.
+    // many heads as take the least time.  In microseconds: a CTA's start and end four, sharing out and merging seven.
+    const double stage = d->dtype == RX_F32 ? 1.7 : 1.1;
     const int64_t slots = 152 * rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt), units = L.tiles * batch;
-    auto stages = [&](int hb) { return std::max<int64_t>(((int64_t)max_kv_len << hb) / (RQ_KEYS * RQ_WARPS), 0) + 1; };
-    auto rounds = [&](int hb) { return (units * (d->hkv >> hb) + slots - 1) / slots; };
+    auto stages = [&](int hb) { return ((int64_t)max_kv_len << hb) / (16 * (128 / d->head_dim) * RQ_WARPS) + 1; };
+    auto whole = [&](int hb) { return (double)((units * (d->hkv >> hb) + slots - 1) / slots) * (4 + stage * stages(hb)); };
     int most = 3;
     while (most > 0 && d->hkv % (1 << most) != 0) --most;
     L.hb = most;
     for (int hb = most - 1; hb >= 0; --hb)
-        if (rounds(hb) * (4 + stages(hb)) < rounds(L.hb) * (4 + stages(L.hb))) L.hb = hb;
-    L.shared = rounds(L.hb) * (4 + stages(L.hb)) > units * (d->hkv >> most) * stages(most) / slots + 4 + 7;
+        if (whole(hb) < whole(L.hb)) L.hb = hb;
+    L.shared = whole(L.hb) > 4 + 7 + stage * units * (d->hkv >> most) * stages(most) / slots;
     L.ctas = L.shared ? slots : units * (d->hkv >> L.hb);
     if (L.shared) {
         L.hb = most;
