@@ -44,7 +44,7 @@ constexpr int EQ_CTAS = 152;
 constexpr int EQ_RING = 4;             // items in flight between the roles
 constexpr int EQ_CONSUMERS = 15;       // MMA warp, six converter warps, eight softmax warps
 constexpr int EQ_CONV = 192;           // converter threads
-constexpr uint32_t EQ_REGS_SOFTMAX = 168, EQ_REGS_OTHER = 88, EQ_REGS_LAUNCH = 128;   // 2*128*88 + 2*128*168 = 512*128
+constexpr uint32_t EQ_REGS_SOFTMAX = 176, EQ_REGS_OTHER = 80, EQ_REGS_LAUNCH = 128;   // 2*128*80 + 2*128*176 = 512*128
 constexpr float EQ_LOG2E = 1.4426950408889634f, EQ_LN2 = 0.6931471805599453f;
 constexpr float EQ_RESCALE = 8.0f;     // log2 units
 
