@@ -685,17 +685,26 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     L.nt = rows_nt(rows);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
-    // many heads as take the least time.  In microseconds: a CTA's start and end four, sharing out and merging seven.
-    const double stage = d->dtype == RX_F32 ? 1.7 : 1.1;
-    const int64_t slots = 152 * rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt), units = L.tiles * batch;
+    // many heads as take the least time.  In microseconds: a CTA's start and end four, a stage `stage`, two fifths more with two
+    // CTAs an SM; sharing out and merging eleven or more, twice that with two tiles, which are a CTA an SM and more rows a
+    // part; what is shared out is a tenth less than the greatest length allows.  With a cold L2, shared out and whole:
+    // decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9, of 4 of up to 3000 23.6 and 33.6; 9 f32
+    // prompts of up to 101 over up to 1201 48.8 and 35.6; 40 of up to 9 over up to 5000 74 and 146.
+    const bool f32 = d->dtype == RX_F32;
+    const int a_sm = rows_a_sm(f32, d->head_dim, L.nt);
+    const double stage = f32 ? 1.5 : 1.1, both = 1.4 * stage, joining = (f32 ? 13 : 11) * L.nt;
+    const int64_t slots = 152 * a_sm, units = L.tiles * batch;
     auto stages = [&](int hb) { return ((int64_t)max_kv_len << hb) / (16 * (128 / d->head_dim) * RQ_WARPS) + 1; };
-    auto whole = [&](int hb) { return (double)((units * (d->hkv >> hb) + slots - 1) / slots) * (4 + stage * stages(hb)); };
+    auto whole = [&](int hb) {
+        const int64_t ctas = units * (d->hkv >> hb);
+        return (double)((ctas + slots - 1) / slots) * (4 + (a_sm > 1 && ctas > 152 ? both : stage) * stages(hb));
+    };
     int most = 3;
     while (most > 0 && d->hkv % (1 << most) != 0) --most;
     L.hb = most;
     for (int hb = most - 1; hb >= 0; --hb)
         if (whole(hb) < whole(L.hb)) L.hb = hb;
-    L.shared = whole(L.hb) > 4 + 7 + stage * units * (d->hkv >> most) * stages(most) / slots;
+    L.shared = whole(L.hb) > 4 + joining + 0.9 * (a_sm > 1 ? both : stage) * units * (d->hkv >> most) * stages(most) / slots;
     L.ctas = L.shared ? slots : units * (d->hkv >> L.hb);
     if (L.shared) {
         L.hb = most;
