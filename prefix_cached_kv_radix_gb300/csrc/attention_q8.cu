@@ -1,4 +1,6 @@
 // The entry points of attention over 8-bit pools: argument checks, and which kernel takes a call.
+#include <cmath>
+
 #include "kv_q8.cuh"
 #include "radix_attn.h"
 #include "rx_common.h"
@@ -11,6 +13,7 @@ static int attention_q8_check(const char* fn, const rx_attn_desc* desc, const rx
     const int rc = q8_check(fn, desc, q8, true);
     if (rc != RX_OK) return rc;
     RX_REQUIRE(batch >= 0 && max_qo_len >= 0 && max_kv_len >= 0 && r2t_stride >= 0, "%s: bad arguments", fn);
+    RX_REQUIRE(std::isfinite(desc->scale * 1.4426950408889634f), "%s: the scale must be finite", fn);
     return RX_OK;
 }
 
@@ -29,7 +32,8 @@ static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 static bool uses_groups(const rx_attn_desc* d, const rx_shared_groups* g) { return g && g->num_groups > 0 && d->dtype == RX_BF16; }
 
 static bool workspace_shape(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
-    return d && batch > 0 && max_qo_len > 0 && max_kv_len >= 0 && d->hkv > 0 && d->hq > 0 && d->hq % d->hkv == 0 && d->head_dim > 0;
+    return d && batch > 0 && max_qo_len > 0 && max_kv_len >= 0 && d->hkv > 0 && d->hkv <= 4096 && d->hq > 0 && d->hq <= 4096 &&
+           d->hq % d->hkv == 0 && (d->head_dim == 64 || d->head_dim == 128);
 }
 
 // bf16 rows that fill a tile of 128 at least in part go to the tcgen05 kernel; f32 rows keep 32-bit results on mma.sync.

@@ -938,8 +938,8 @@ static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
     cudaError_t e = launch_pdl(extend_q8_kernel<D, FMT>, EQ_CTAS, EQ_THREADS, smem, s, p);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
-        const int64_t items = (((int64_t)p.max_qo_len * p.group + EQ_ROWS - 1) / EQ_ROWS) * p.hkv * p.batch;
-        cfg.gridDim = dim3((unsigned)std::min<int64_t>(p.groups ? EQ_CTAS : items, EQ_CTAS), EQ_ROWS / 4);
+        const double items = (double)(((int64_t)p.max_qo_len * p.group + EQ_ROWS - 1) / EQ_ROWS) * p.hkv * p.batch;
+        cfg.gridDim = dim3((unsigned)std::min<double>(p.groups ? EQ_CTAS : items, EQ_CTAS), EQ_ROWS / 4);
         cfg.blockDim = dim3(128);
         cfg.stream = s;
         cudaLaunchAttribute pdl[1];
@@ -1002,7 +1002,7 @@ int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_des
 
 // A decode batch's groups as the kernels take them: SharedGroup per group, members (-1: not one), and the keys that each
 // request takes from its group's shared run.  A group with bad boundaries is left out (its members read their own keys), and so is a member
-// that is no request or has fewer keys than the run.
+// that is no request, has fewer keys than the run or is a member already.
 __global__ void __launch_bounds__(512) shared_q8_groups_kernel(rx_shared_groups g, int32_t batch, const int32_t* kv_lens, int64_t stride,
                                                                int32_t max_kv_len, SharedGroup* groups, int32_t* members,
                                                                int32_t* shared_of, int32_t* status) {
@@ -1022,8 +1022,11 @@ __global__ void __launch_bounds__(512) shared_q8_groups_kernel(rx_shared_groups 
             const bool is = b >= 0 && b < batch;
             if (m < end && !is) report(status, RX_DEV_BAD_LENGTH);
             if (!is || kv_lens[b] < len || kv_lens[b] > stride || kv_lens[b] > max_kv_len) b = -1;
+            if (b >= 0 && atomicCAS(shared_of + b, 0, len) != 0) {
+                report(status, RX_DEV_BAD_LENGTH);
+                b = -1;
+            }
             if (m < end) members[m] = b;
-            if (b >= 0) shared_of[b] = len;
             const unsigned any = __ballot_sync(0xffffffffu, b >= 0);
             if (src < 0 && any) src = __shfl_sync(0xffffffffu, b, __ffs(any) - 1);
         }

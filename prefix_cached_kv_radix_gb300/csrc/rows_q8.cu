@@ -684,6 +684,8 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     const int64_t rows = (int64_t)max_qo_len * (d->hq / d->hkv);
     L.nt = rows_nt(rows);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
+    L.ctas = INT64_MAX;                  // what the launch refuses; the products below stay within 63 bits
+    if ((double)L.tiles * batch > 0x1p40) return L;
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
     // many heads as take the least time.  In microseconds: a CTA's start and end four, a stage `stage`, two fifths more with two
     // CTAs an SM; sharing out and merging eleven or more, twice that with two tiles, which are a CTA an SM and more rows a

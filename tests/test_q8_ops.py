@@ -210,6 +210,22 @@ def test_extend_q8_refuses():
         call(**kw)
 
 
+def test_attention_q8_scales_and_sizes_refused():
+    """Scales that are not finite, or not once in base 2; more rows than a launch has blocks; workspaces of shapes that no call takes."""
+    c = ctypes.byref(api.q8_desc(INT8))
+    for scale in (math.inf, -math.inf, math.nan, 3e38):
+        d = desc_of(BF, 4, 2, 64)
+        d.scale = scale
+        refused("decode_attention_q8", ctypes.byref(d), c, 1, A, A, 8, A, None, A, A, A, A, None, 8, A, 1 << 40, None, None)
+        refused("prefix_extend_attention_q8", ctypes.byref(d), c, 1, A, A, A, A, 8, A, A, A, A, None, 4, 8, A, 1 << 40, None, None)
+    most = 2 ** 31 - 1
+    for hq, hkv in ((4096, 4096), (4096, 1)):
+        refused("prefix_extend_attention_q8", ctypes.byref(desc_of(F, hq, hkv, 64)), c, most, A, A, A, A, most, A, A, A, A, None, most,
+                most, A, 1 << 60, None, None)
+    for d in (desc_of(BF, 4, 2, 256), desc_of(F, 4, 2, 0, scale=1.0), desc_of(BF, 4, 3, 64), desc_of(BF, 4, 0, 64)):
+        assert api.decode_q8_workspace_bytes(d, 4, 100) == 0 and api.extend_q8_workspace_bytes(d, 4, 5, 100) == 0
+
+
 def test_nothing_to_do_is_no_error():
     """No requests, no rows, no slots: fine, without a device."""
     d, c = desc_of(BF, 4, 2, 64), api.q8_desc(E4M3)
@@ -636,6 +652,25 @@ def test_decode_q8_bad_groups(dev):
         assert st == code, (ind, mem, length)
         for b, n in enumerate(lens):
             k, v = cache.values(r2t[b, :n])
+            agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), BF)
+
+
+@gpu
+def test_decode_q8_requests_named_twice(dev):
+    """A request that is named twice, in a group or in two of different lengths, is reported and has its row all the same."""
+    hq, hkv, d = 8, 2, 128
+    lens = [90, 80, 50, 90, 64]
+    r2t, _ = table_of(lens, 96, 600, dev)
+    for b in (1, 2, 3, 4):
+        r2t[b, :50] = r2t[0, :50]
+    cache = Cache(dev, E4M3, 600, hkv, d, seed=6)
+    for ind, mem, length in (([0, 3], [0, 1, 0], [50]), ([0, 2, 4], [0, 1, 1, 3], [50, 20]), ([0, 40], [4] * 40, [50]),
+                             ([0, 3, 6], [0, 1, 2, 2, 1, 0], [40, 40])):
+        g = groups_of(dev, ind, mem, length, 40, 50)
+        q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens * 8, r2t.repeat(8, 1), groups=g)
+        assert st == api.RX_DEV_BAD_LENGTH
+        for b, n in enumerate(lens * 8):
+            k, v = cache.values(r2t[b % 5, :n])
             agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), BF)
 
 
