@@ -687,14 +687,14 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     L.ctas = INT64_MAX;                  // what the launch refuses; the products below stay within 63 bits
     if ((double)L.tiles * batch > 0x1p40) return L;
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
-    // many heads as take the least time.  In microseconds: a CTA's start and end four, a stage `stage`, two fifths more with two
-    // CTAs an SM; sharing out and merging eleven or more, twice that with two tiles, which are a CTA an SM and more rows a
-    // part; what is shared out is a tenth less than the greatest length allows.  With a cold L2, shared out and whole:
-    // decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9, of 4 of up to 3000 23.6 and 33.6; 9 f32
-    // prompts of up to 101 over up to 1201 48.8 and 35.6; 40 of up to 9 over up to 5000 74 and 146.
-    const bool f32 = d->dtype == RX_F32;
-    const int a_sm = rows_a_sm(f32, d->head_dim, L.nt);
-    const double stage = f32 ? 1.5 : 1.1, both = 1.4 * stage, joining = (f32 ? 13 : 11) * L.nt;
+    // many heads as take the least time.  In microseconds: a CTA's start and end four, a stage 1.1, or 1.7 with its twice as
+    // many keys at 64 channels, a quarter more with two CTAs an SM; sharing out and merging nine, or 26 with two tiles, which
+    // are a CTA an SM and more rows a part.  Fitted to 144 sizes with a cold L2, of which it costs three more than a
+    // twentieth, at most a tenth.  Shared out and whole: decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9
+    // us, of 4 of up to 3000 23.6 and 33.6; 9 f32 prompts of up to 101 over up to 1201 48.8 and 35.6; 40 of up to 9 over up
+    // to 5000 74 and 146.
+    const int a_sm = rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt);
+    const double stage = d->head_dim == 64 ? 1.7 : 1.1, both = 1.25 * stage, joining = L.nt == 1 ? 9 : 26;
     const int64_t slots = 152 * a_sm, units = L.tiles * batch;
     auto stages = [&](int hb) { return ((int64_t)max_kv_len << hb) / (16 * (128 / d->head_dim) * RQ_WARPS) + 1; };
     auto whole = [&](int hb) {
@@ -706,7 +706,7 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     L.hb = most;
     for (int hb = most - 1; hb >= 0; --hb)
         if (whole(hb) < whole(L.hb)) L.hb = hb;
-    L.shared = whole(L.hb) > 4 + joining + 0.9 * (a_sm > 1 ? both : stage) * units * (d->hkv >> most) * stages(most) / slots;
+    L.shared = whole(L.hb) > 4 + joining + (a_sm > 1 ? both : stage) * units * (d->hkv >> most) * stages(most) / slots;
     L.ctas = L.shared ? slots : units * (d->hkv >> L.hb);
     if (L.shared) {
         L.hb = most;
