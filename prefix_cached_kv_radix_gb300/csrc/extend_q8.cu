@@ -15,7 +15,14 @@
 //   warp 1       issues the tcgen05.mma: O_t += P_t(j) V(j) in two halves, then at once S_t(j+1) = Q_t K(j+1)^T
 //   warps 2, 3, 12-15  K/V tiles: codes by 16-byte loads through the slot table, a tile ahead in registers, widened to
 //                bf16 and stored in the 128B-swizzled layout that tcgen05 reads; the keys' scales beside the V tile
-//   warps 4-7, 8-11  softmax of Q tile 0 and 1, a row per thread, and the item's output
+//   warps 4-7, 8-11  softmax of Q tile 0 and 1, in the tensor core's fragment layout, and the item's output
+// Bound by the tensor core and the softmax taking turns.  4 prompts of 512 over 16384 (64/8 heads x 128): int8 1205 us, 927
+// TFLOP/s.  A pair of Q tiles and a K/V tile take some 4900 clocks: the products 2150 of them, either Q tile's softmax
+// 2700 from its scores to its last weights (both together, they use half the issue slots), and the next scores wait for
+// both.  Without widening and storing the codes at all it would be 971 TFLOP/s (e4m3, of 909), so that is not what bounds it.  Tried and
+// slower: scores and weights in halves of 64 keys with columns of their own (700: products of 64 columns keep the tensor core
+// waiting for their rows), softmax warpgroups in strict turns (800), pairs of CTAs that widen half a tile each and copy it
+// to the other (567), V's products without waiting for the next K tile (840).
 // TMEM columns: S0/P0 [0,128) S1/P1 [128,256) O0 [256,256+D) O1 after.  Every wait is bounded; on time-out the kernel
 // records RX_DEV_TIMEOUT, waits for its copies, frees TMEM and returns.
 #include <cuda.h>
@@ -44,6 +51,7 @@ constexpr int EQ_CTAS = 152;
 constexpr int EQ_RING = 4;             // items in flight between the roles
 constexpr int EQ_CONSUMERS = 15;       // MMA warp, six converter warps, eight softmax warps
 constexpr int EQ_CONV = 192;           // converter threads
+// 168 / 88 registers: 16 prompts of 1024 over 1000, 12 heads x 64, 188 us, 178 so; 184 / 72 1427 us instead of 1205 above (spills)
 constexpr uint32_t EQ_REGS_SOFTMAX = 176, EQ_REGS_OTHER = 80, EQ_REGS_LAUNCH = 128;   // 2*128*80 + 2*128*176 = 512*128
 constexpr float EQ_LOG2E = 1.4426950408889634f, EQ_LN2 = 0.6931471805599453f;
 constexpr float EQ_RESCALE = 8.0f;     // log2 units

@@ -114,8 +114,8 @@ __device__ __forceinline__ int parts_of(const int4* meta, int which, int ctas, i
 
 // A row of D channels from its parts, list[0 .. parts - 1] (MOST at most), by a whole block of 128 threads.  Part i's row is row `r` of `rows`
 // (normalised, its log-sum-exp to base 2).  Afterwards the first warp has the row, channels lane * D / 32 .., in acc; returns its
-// log-sum-exp (-infinity: no key, and acc is zeros).  A warp takes every fourth part; the rows travel by cp.async, 16 a warp at a
-// time (as loads, the compiler put each next to its use, and 256 parts took 38 us).
+// log-sum-exp (-infinity: no key, and acc is zeros).  A warp takes every fourth part; the rows travel by cp.async, eight a
+// warp at a time, twice (as loads, the compiler put each next to its use, and 256 parts took 38 us).
 template <int D, int MOST>
 __device__ __forceinline__ float merge_many(const int* list, int parts, const float* part_o, const float* part_lse, int rows, int r,
                                             float* acc) {
