@@ -13,8 +13,9 @@
 // parts in the workspace by a second kernel.  (Borders close to an item's end move there.)  Roles (512 threads):
 //   warp 0       items in order, handed on through a ring in shared memory, and their Q tiles
 //   warp 1       issues the tcgen05.mma: O_t += P_t(j) V(j) in two halves, then at once S_t(j+1) = Q_t K(j+1)^T
-//   warps 2, 3, 12-15  K/V tiles: codes by 16-byte loads through the slot table, a tile ahead in registers, widened to
-//                bf16 and stored in the 128B-swizzled layout that tcgen05 reads; the keys' scales beside the V tile
+//   warps 2, 3, 12-15  K/V tiles: codes by 16-byte loads through the slot table, a tile ahead (K's by cp.async, V's in
+//                registers), widened to bf16 and stored in the 128B-swizzled layout that tcgen05 reads; the keys' scales beside
+//                the V tile
 //   warps 4-7, 8-11  softmax of Q tile 0 and 1, in the tensor core's fragment layout, and the item's output
 // Bound by the tensor core and the softmax taking turns.  4 prompts of 512 over 16384 (64/8 heads x 128): int8 1205 us, 927
 // TFLOP/s.  A pair of Q tiles and a K/V tile take some 4900 clocks: the products 2150 of them, either Q tile's softmax
