@@ -555,7 +555,8 @@ int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int64_t n, c
  *    read their own keys; so does a member with fewer keys than the run, and a request that is named once more.  Worth
  *    it for long shared runs: 256 requests take 398 us instead of 537 with 4096 keys of up to 8192 shared, but 64 of up to
  *    1500 keys with 409 shared 90 us instead of 55.
- *  - d_workspace: >= decode_q8_workspace_bytes(...) bytes, 256-byte aligned.  Calls that may overlap (other streams, graphs that
+ *  - d_workspace: >= decode_q8_workspace_bytes(...) bytes, 256-byte aligned; what it is for the greatest batch, length and
+ *    number of groups serves all smaller calls.  Calls that may overlap (other streams, graphs that
  *    run at once) need workspaces of their own.  Any ratio hq / hkv; a call of 2^31 blocks or more is refused (RX_EINVAL). */
 int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
                         const int32_t* d_req_to_token, int64_t r2t_stride, const int32_t* d_kv_lens,
@@ -572,7 +573,8 @@ size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_
  *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most) where max_qo_len * hq / hkv is above 16,
  *    and to 11 bits below; f32 as in decode.
  *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request; it decides how far few rows over long
- *    contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned). */
+ *    contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned; what it is for the
+ *    greatest batch and lengths serves all smaller calls). */
 int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
                                const int64_t* d_qo_indptr, const int32_t* d_prefix_lens, const int32_t* d_req_to_token,
                                int64_t r2t_stride, const void* d_k_pool, const void* d_v_pool, const float* d_scales,

@@ -44,14 +44,14 @@ static bool many_rows(const rx_attn_desc* d, int32_t max_qo_len) {
 extern "C" size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_kv_len,
                                             const rx_shared_groups* groups) {
     if (!workspace_shape(desc, batch, 1, max_kv_len)) return 0;
-    const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).bytes);
+    const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).room);
     return uses_groups(desc, groups) ? own + shared_q8_bytes(desc, batch, groups->num_groups) : own;
 }
 
 extern "C" size_t extend_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_t max_qo_len, int32_t max_kv_len) {
     if (!workspace_shape(desc, batch, max_qo_len, max_kv_len)) return 0;
     if (many_rows(desc, max_qo_len)) return extend_q8_bytes(desc);
-    return rows_q8_plan(desc, batch, max_qo_len, max_kv_len).bytes;
+    return rows_q8_plan(desc, batch, max_qo_len, max_kv_len).room;
 }
 
 extern "C" int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,

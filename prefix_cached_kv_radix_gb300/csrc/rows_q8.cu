@@ -705,6 +705,14 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     const int64_t rows = (int64_t)max_qo_len * (d->hq / d->hkv);
     L.nt = rows_nt(rows);
     L.tiles = (rows + 8 * L.nt - 1) / (8 * L.nt);
+    const int a_sm = rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt);
+    int most = 3;
+    while (most > 0 && d->hkv % (1 << most) != 0) --most;
+    const int64_t slots = 152 * a_sm;
+    const size_t parts = (size_t)slots * 2 * (8 * L.nt << most);       // rows
+    L.lse_at = parts * d->head_dim * sizeof(float);
+    L.meta_at = L.lse_at + parts * sizeof(float);
+    L.room = L.meta_at + (size_t)RQ_CTAS * 2 * sizeof(int4);
     L.ctas = INT64_MAX;                  // what the launch refuses; the products below stay within 63 bits
     if ((double)L.tiles * batch > 0x1p40) return L;
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
@@ -714,28 +722,19 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     // twentieth, at most a tenth.  Shared out and whole: decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9
     // us, of 4 of up to 3000 23.6 and 33.6; 9 f32 prompts of up to 101 over up to 1201 48.8 and 35.6; 40 of up to 9 over up
     // to 5000 74 and 146.
-    const int a_sm = rows_a_sm(d->dtype == RX_F32, d->head_dim, L.nt);
     const double stage = d->head_dim == 64 ? 1.7 : 1.1, both = 1.25 * stage, joining = L.nt == 1 ? 9 : 26;
-    const int64_t slots = 152 * a_sm, units = L.tiles * batch;
+    const int64_t units = L.tiles * batch;
     auto stages = [&](int hb) { return ((int64_t)max_kv_len << hb) / (16 * (128 / d->head_dim) * RQ_WARPS) + 1; };
     auto whole = [&](int hb) {
         const int64_t ctas = units * (d->hkv >> hb);
         return (double)((ctas + slots - 1) / slots) * (4 + (a_sm > 1 && ctas > 152 ? both : stage) * stages(hb));
     };
-    int most = 3;
-    while (most > 0 && d->hkv % (1 << most) != 0) --most;
     L.hb = most;
     for (int hb = most - 1; hb >= 0; --hb)
         if (whole(hb) < whole(L.hb)) L.hb = hb;
     L.shared = whole(L.hb) > 4 + joining + (a_sm > 1 ? both : stage) * units * (d->hkv >> most) * stages(most) / slots;
     L.ctas = L.shared ? slots : units * (d->hkv >> L.hb);
-    if (L.shared) {
-        L.hb = most;
-        const size_t rows = (size_t)L.ctas * 2 * (8 * L.nt << L.hb);
-        L.lse_at = rows * d->head_dim * sizeof(float);
-        L.meta_at = L.lse_at + rows * sizeof(float);
-        L.bytes = L.meta_at + (size_t)L.ctas * 2 * sizeof(int4);
-    }
+    if (L.shared) L.hb = most, L.bytes = L.room;
     return L;
 }
 

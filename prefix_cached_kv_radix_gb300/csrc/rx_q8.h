@@ -38,12 +38,13 @@ struct SharedGroup {
     int32_t src;                 // a member, whose slot-table row has them
 };
 
-// How rows_q8.cu shares out a call, and the workspace it needs for parts of rows (0: none).
+// How rows_q8.cu shares out a call, and the workspace it needs for parts of rows (0: none).  room: what calls of any smaller
+// batch and lengths need at most, which is not always less: long contexts of few requests are shared out, of many not.
 struct RowsPlan {
     int nt, hb;                  // 8-row tiles of a CTA, log2 of its heads
     bool shared;
     int64_t tiles, ctas;
-    size_t lse_at, meta_at, bytes;
+    size_t lse_at, meta_at, bytes, room;
 };
 RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, int32_t max_kv_len);
 int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,

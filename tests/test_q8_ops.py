@@ -226,6 +226,20 @@ def test_attention_q8_scales_and_sizes_refused():
         assert api.decode_q8_workspace_bytes(d, 4, 100) == 0 and api.extend_q8_workspace_bytes(d, 4, 5, 100) == 0
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d", [(12, 12, 64), (32, 8, 128), (64, 1, 128), (16, 4, 64)])
+def test_attention_q8_workspaces_grow(dt, hq, hkv, d):
+    """A workspace made for the greatest call is enough for every smaller one."""
+    desc = desc_of(dt, hq, hkv, d, 10 ** 6)
+    decode_most = api.decode_q8_workspace_bytes(desc, 300, 9000)
+    extend_most = api.extend_q8_workspace_bytes(desc, 300, 200, 9000)
+    for batch in (1, 4, 16, 64, 300):
+        for longest in (1, 300, 3000, 9000):
+            assert api.decode_q8_workspace_bytes(desc, batch, longest) <= decode_most
+            for rows in (1, 2, 9, 16, 17, 200):
+                assert api.extend_q8_workspace_bytes(desc, batch, rows, longest) <= extend_most
+
+
 def test_nothing_to_do_is_no_error():
     """No requests, no rows, no slots: fine, without a device."""
     d, c = desc_of(BF, 4, 2, 64), api.q8_desc(E4M3)
@@ -453,7 +467,7 @@ def table_of(lens, stride, slots, dev, seed=0):
     return t.to(dev), ids[:at].long().to(dev)
 
 
-def decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=None, scale=None, q=None, longest=None):
+def decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=None, scale=None, q=None, longest=None, ws=None):
     b = len(lens)
     desc = desc_of(dt, hq, hkv, d, cache.k.shape[0], scale)
     if q is None:
@@ -461,7 +475,8 @@ def decode(dev, cache, dt, hq, hkv, d, lens, r2t, groups=None, scale=None, q=Non
     out, lse = torch.full_like(q, 9.0), torch.full((b, hq), 9.0, device=dev)
     longest = max(max(lens), 1) if longest is None else longest
     nbytes = api.decode_q8_workspace_bytes(desc, b, longest, groups)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    if ws is None and nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     st = torch.zeros(1, dtype=torch.int32, device=dev)
     api.decode_attention_q8(desc, cache.q8, b, q, r2t, i32(lens, dev), cache.k, cache.v, cache.scales, out, lse, longest, ws, st,
                             groups=groups)
@@ -650,6 +665,22 @@ def test_decode_q8_bad_groups(dev):
         g = groups_of(dev, ind, mem, length, 3, 90)
         q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens, r2t, groups=g)
         assert st == code, (ind, mem, length)
+        for b, n in enumerate(lens):
+            k, v = cache.values(r2t[b, :n])
+            agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), BF)
+
+
+@gpu
+def test_decode_q8_one_workspace_for_all(dev):
+    """The workspace of the greatest call, for calls that share contexts out and calls that do not."""
+    hq, hkv, d = 12, 12, 64
+    desc = desc_of(BF, hq, hkv, d, 40000)
+    ws = torch.empty(api.decode_q8_workspace_bytes(desc, 16, 3000), dtype=torch.uint8, device=dev)
+    for lens in ([3000], [2500, 3000], [3000, 1] * 8, [30] * 16, [2000] * 9):
+        r2t, _ = table_of(lens, 3000, 40000, dev)
+        cache = Cache(dev, E4M3, 40000, hkv, d, seed=6)
+        q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens, r2t, ws=ws)
+        assert st == 0
         for b, n in enumerate(lens):
             k, v = cache.values(r2t[b, :n])
             agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), n - 1), BF)
