@@ -822,6 +822,32 @@ def test_extend_q8_bad_slots_and_lengths(dev, dt):
         extend_agrees(cache, dt, d, [20], [30], good, q, out, lse)
 
 
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows", [1, 8, 40, 5000])
+def test_attention_q8_bounds_far_above(dev, dt, rows):
+    """The host's bounds may be far above the lengths; batches without any new token or key."""
+    hq, hkv, d, most = 4, 2, 64, 2 ** 31 - 1
+    desc = desc_of(dt, hq, hkv, d, 300)
+    cache = Cache(dev, E4M3, 300, hkv, d, seed=3)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    for lens, pre in (([0, 0, 0], [5, 0, 70]), ([0, 1, 0, 0, 1], [0, 0, 9, 3, 90])):
+        r2t, _ = table_of([n + p for n, p in zip(lens, pre)], 96, 300, dev)
+        q = torch.randn(sum(lens) + 1, hq, d, device=dev).to(dt)
+        out = torch.full_like(q, 9.0)
+        lse = torch.full((len(q), hq), 9.0, device=dev)
+        ws = torch.empty(max(api.extend_q8_workspace_bytes(desc, len(lens), rows, most), 1), dtype=torch.uint8, device=dev)
+        api.prefix_extend_attention_q8(desc, cache.q8, len(lens), q, indptr(lens, dev), i32(pre, dev), r2t, cache.k, cache.v,
+                                       cache.scales, out, lse, rows, ws, st, max_kv_len=most)
+        assert int(st) == 0 and (out[-1] == 9.0).all() and (lse[-1] == 9.0).all()
+        extend_agrees(cache, dt, d, lens, pre, r2t, q, out, lse)
+    r2t, _ = table_of([0, 7, 0], 8, 300, dev)
+    q, out, lse, code = decode(dev, cache, dt, hq, hkv, d, [0, 7, 0], r2t, longest=most)
+    k, v = cache.values(r2t[1, :7])
+    assert code == 0 and (out[[0, 2]] == 0).all() and lse[[0, 2]].isneginf().all()
+    agree(out[1:2], lse[1:2], attend(q[1:2], k, v, 1 / math.sqrt(d), 6), dt)
+
+
 # ============================================================================ together
 @gpu
 @pytest.mark.parametrize("fmt", [INT8, E4M3])
