@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     const int key = key0 + x * STEP;
                     sl[x] = key < EQ_BN && key < left ? slots[j * EQ_BN + key] : -2;     // -2: no key
                 }
-                ss = lt < EQ_BN && lt < left ? slots[j * EQ_BN + lt] : -2;
+                ss = lt < EQ_BN && lt < left ? max(slots[j * EQ_BN + lt], -1) : -2;     // the table may hold any value
             };
             auto next = [&]() {
                 if (++j == it.j1) {

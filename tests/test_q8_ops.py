@@ -1035,3 +1035,52 @@ def test_binding_refuses(dev):
                     api.kv_pool_read_q8(desc, cache.q8, i32([1, 2, 3], dev), cache.k, cache.v, a["s"], a["k"], rows, st)
     finally:
         api._ops_ext = ext
+
+
+# ============================================================================ what the table may hold, any value of it
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("d,block", [(64, 1), (128, 16)])
+@pytest.mark.parametrize("bad", [-2, -1, -3, -2 ** 31, 2 ** 31 - 1])
+def test_extend_q8_any_bad_slot(dev, dt, d, block, bad):
+    """Whatever a bad entry's value: reported and left out, by calls of few rows and of many, beside the others and alone."""
+    hq, hkv, slots = 8, 2, 800
+    for lens, pre in (([30, 5, 40], [200, 9, 0]), ([1, 2, 2], [200, 9, 0])):
+        total = [n + p for n, p in zip(lens, pre)]
+        for places in ([(0, 7)], [(0, 7), (0, 130), (0, total[0] - 1), (1, 0), (1, 9)], [(2, 0), (2, 1)]):
+            r2t, _ = table_of(total, 240, slots, dev)
+            cache = Cache(dev, INT8, slots, hkv, d, block, seed=2)
+            for b, i in places:
+                r2t[b, i] = bad
+            q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t)
+            assert st == api.RX_DEV_BAD_SLOT
+            at = 0
+            for b, (n, p) in enumerate(zip(lens, pre)):
+                for i in range(n):
+                    ok = r2t[b, :p + i + 1]
+                    ok = ok[(ok >= 0) & (ok < slots)]
+                    agree(out[at:at + 1], lse[at:at + 1], attend(q[at:at + 1], *cache.values(ok), 1 / math.sqrt(d), len(ok) - 1), dt)
+                    at += 1
+
+
+@gpu
+@pytest.mark.parametrize("bad", [-2, -1, -2 ** 31, 2 ** 31 - 1])
+def test_decode_q8_any_bad_slot_in_a_shared_run(dev, bad):
+    """A bad entry in a group's run, or behind it, is reported and left out."""
+    hq, hkv, d, slots = 8, 2, 128, 3000
+    lens = [300, 411, 301, 90, 640, 300]
+    for place in (0, 131, 299, 300):
+        r2t, _ = table_of(lens, 648, slots, dev)
+        r2t[[1, 2, 5], :300] = r2t[0, :300].clone()
+        if place < 300:
+            r2t[[0, 1, 2, 5], place] = bad
+        else:
+            r2t[1, place] = bad
+        cache = Cache(dev, E4M3, slots, hkv, d, seed=4)
+        g = groups_of(dev, [0, 4], [0, 1, 2, 5], [300], 4, 300)
+        q, out, lse, st = decode(dev, cache, BF, hq, hkv, d, lens, r2t, groups=g)
+        assert st == api.RX_DEV_BAD_SLOT
+        for b, n in enumerate(lens):
+            ok = r2t[b, :n]
+            ok = ok[(ok >= 0) & (ok < slots)]
+            agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], *cache.values(ok), 1 / math.sqrt(d), len(ok) - 1), BF)
