@@ -94,7 +94,7 @@ struct EqLayout {
     static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
     static constexpr int OFF_V = OFF_K + NK * KV_TILE;
     static constexpr int OFF_KS = OFF_V + NV * KV_TILE;              // [NV][128] K scales times scale log2(e)
-    static constexpr int OFF_VS = OFF_KS + NV * EQ_BN * 4;           // [NV][128] V scales, -1 for no key
+    static constexpr int OFF_VS = OFF_KS + NV * EQ_BN * 4;           // [NV][128] V scales, -1 for a key at a bad slot
     static constexpr int OFF_FLAG = OFF_VS + NV * EQ_BN * 4;         // [NV] int4: some key of the tile is at a bad slot or has a scale that is not finite
     static constexpr int OFF_RING = OFF_FLAG + NV * 16;              // 3 int4 an entry
     static constexpr int OFF_SCAN = OFF_RING + EQ_RING * 48;         // int64 per warp, and four results
@@ -489,9 +489,12 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     const int key = key0 + x * STEP;
-                    sl[x] = key < EQ_BN && key < left ? slots[j * EQ_BN + key] : -2;     // -2: no key
+                    sl[x] = key < EQ_BN && key < left ? slots[j * EQ_BN + key] : -1;
                 }
-                ss = lt < EQ_BN && lt < left ? max(slots[j * EQ_BN + lt], -1) : -2;     // the table may hold any value
+                // A place behind the last key has that key's scales, which no row sees: the table may hold any value, so none
+                // can say that there is no key.  (With the value changed as it is loaded, or the place kept or worked out again
+                // where the scale is, the four long chats took 1710 to 1820 us.)
+                ss = lt < EQ_BN ? slots[min(j * EQ_BN + lt, it.kv_end - 1)] : 0;
             };
             auto next = [&]() {
                 if (++j == it.j1) {
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             const uint32_t codes = base + LY::OFF_CODES + lt * 16;
             uint4 vr[NX];
             float2 sc = make_float2(0.f, 0.f);
-            int32_t kept = -2;                               // ss of the V tile in the registers
+            int32_t kept = 0;                                // ss of the V tile in the registers
             auto fetch_k = [&](int x) {
                 const bool in = (uint32_t)sl[x] < nslots;
                 cp_async_16(codes + x * EQ_CONV * 16, kb + (size_t)(in ? (uint32_t)sl[x] : 0u) * pitch, in ? 16u : 0u);
@@ -519,9 +522,9 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             };
             auto load_scale = [&]() {
                 kept = ss;
-                sc = make_float2(1.f, -1.f);                 // no key
+                sc = make_float2(1.f, -1.f);                 // left out
                 if ((uint32_t)ss < nslots) sc = sb[(int64_t)(ss >> p.pools.shift) * p.hkv];
-                else if (ss != -2) report(p.status, RX_DEV_BAD_SLOT);
+                else report(p.status, RX_DEV_BAD_SLOT);
             };
             // channels 16 c .. + 15: two 16-byte pieces of the row's 64-channel half
             const uint32_t piece = (uint32_t)((c >> 2) * EQ_BN * 128 + key0 * 128 + ((2 * c) & 7) * 16) ^ (uint32_t)((key0 & 7) * 16);
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                 if (lt < EQ_BN) {
                     reinterpret_cast<float*>(gbase + LY::OFF_KS)[vs * EQ_BN + lt] = sc.x * p.scale_log2;
                     reinterpret_cast<float*>(gbase + LY::OFF_VS)[vs * EQ_BN + lt] = sc.y;
-                    const bool bad = __any_sync(0xffffffffu, (kept != -2 && (uint32_t)kept >= nslots) || !isfinite(sc.x) || !isfinite(sc.y));
+                    const bool bad = __any_sync(0xffffffffu, (uint32_t)kept >= nslots || !isfinite(sc.x) || !isfinite(sc.y));
                     if (lane == 0) reinterpret_cast<int*>(gbase + LY::OFF_FLAG)[vs * 4 + lt / 32] = bad ? 1 : 0;
                 }
 #pragma unroll
