@@ -547,7 +547,8 @@ int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int64_t n, c
 /* decode_attention over 8-bit pools: arguments, layouts and errors are its, but for what is said here.
  *  - Codes go into the products as they are, scales in 32 bits; sums and softmax statistics are 32-bit.
  *    desc->dtype f32 gives 32-bit results, on the tensor cores as well (queries and weighted probabilities in two 16-bit
- *    parts each); bf16 rounds the weighted probabilities to 11 bits, those of a group's shared run to bf16.
+ *    parts each); bf16 rounds the weighted probabilities to 11 bits (and takes the logarithm of V's scale, within 2^-15, into
+ *    their exponent), those of a group's shared run to bf16 (as prefix_extend_attention_q8 does those of many rows).
  *  - A request of length 0 (a padded batch) gives a row of zeros and a log-sum-exp of -infinity.
  *  - A key at a slot outside [0, num_slots) is reported and left out.
  *  - groups: as for decode_attention; used for bf16 rows (f32 rows read each request's own keys, with the same result).
@@ -570,8 +571,9 @@ size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_
  *  - A key at a slot outside [0, num_slots) is reported and left out; a row that is left no key is
  *    zeros, its log-sum-exp -infinity.
  *  - Rows before qo_indptr[0] and from qo_indptr[batch] on are left as they were.
- *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most) where max_qo_len * hq / hkv is above 16,
- *    and to 11 bits below; f32 as in decode.
+ *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most, for scales of 2^-100 and more: a product
+ *    below 2^-126 has fewer bits, and one below 2^-134 is zero) where max_qo_len * hq / hkv is above 16, and as in decode below;
+ *    f32 as in decode.
  *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request; it decides how far few rows over long
  *    contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned; what it is for the
  *    greatest batch and lengths serves all smaller calls). */

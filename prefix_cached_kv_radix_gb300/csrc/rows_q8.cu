@@ -5,7 +5,10 @@
 //   x_j = c ks_j (q . kc_j),  y_j = x_j + log2 vs_j     (c = scale log2 e)
 //   o = sum_j 2^y_j vc_j / sum_j 2^x_j,
 // each sum over its own running maximum: vs enters the exponent, so that what is weighed and rounded to 16 bits is 2^(y_j - max y)
-// next to the largest term of o, however far apart the rows' scales are.
+// next to the largest term of o, however far apart the rows' scales are.  For f32 rows only the exponent of vs = v 2^e does,
+// 1/2 <= v < 1: a logarithm of 32 bits is off by up to 2^-18.  The sums' references are then the maxima rounded up to whole
+// numbers, so that x_j - (max y - e_j) loses nothing of x_j (errors of 3e-7 to 5e-7 of the norm, where they were 5e-7
+// to 1.1e-6 and 3e-6 at scales of 2^-110).
 //
 // A CTA of eight warps takes a run of a request's keys, a row tile and 1, 2, 4 or 8 neighbouring kv heads: a warp a head, or 8, 4, 2
 // warps sharing one, 16 keys of a stage each.  The heads of a slot lie side by side in the pools, so a stage is
@@ -45,7 +48,7 @@ constexpr int RQ_NS = 3;              // stages
 constexpr int RQ_RUN = 512;           // keys whose slots are read at a time: two stages at least
 constexpr int RQ_CTAS = 152 * 2;      // most CTAs that stages are shared out to
 constexpr float RQ_LOG2E = 1.4426950408889634f, RQ_LN2 = 0.6931471805599453f;
-constexpr float RQ_TOP = 15.f;        // a row's largest weight is 2^15 in f16
+constexpr float RQ_TOP = 15.f;        // a row's largest weight is at most 2^15 in f16
 
 template <int D>
 struct RowsLayout {
@@ -97,10 +100,19 @@ __device__ __forceinline__ uint32_t pack_rest_f16x2(float lo, float hi, uint32_t
     return pack_f16x2(lo - p.x, hi - p.y);
 }
 
+// Off by 2^-22 of itself, 2^-15 at most: bf16 rows' weights are rounded by 2^-11.
 __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// x = part 2^power, part in [1/2, 1); what is no positive normal number is its own part, of power 0.
+__device__ __forceinline__ void split_scale(float x, float& part, float& power) {
+    const uint32_t bits = __float_as_uint(x), e = bits >> 23;
+    const bool normal = e - 1u < 254u;
+    part = normal ? __uint_as_float((bits & 0x7fffffu) | 0x3f000000u) : x;
+    power = normal ? (float)((int)e - 126) : 0.f;
 }
 
 struct RowsParams {
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
     const int least = before + R0 / G + 1 - k_begin;                   // every row sees the keys before this
 
     float o[NT][KS][4];
-    float mx[NT][2], l[NT][2], my[NT][2];      // of x in this lane, the sum, and of y in the warp
+    float mx[NT][2], l[NT][2], my[NT][2];      // references of x in this lane, the sum, and of y in the warp
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sacc[u][t][e] += sodd[t][e];
         }
-        float ks[2 * SUB], lv[2 * SUB];        // of keys 8 i + r8: K's scale, log2 of V's
+        float ks[2 * SUB], vp[2 * SUB], lv[2 * SUB];       // of keys 8 i + r8: K's scale, log2 of V's, or its part and exponent
         bool ok[2 * SUB], all_ok = true;
 #pragma unroll
         for (int i = 0; i < 2 * SUB; ++i) {
@@ -419,47 +431,98 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
             asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks[i]), "=f"(vs) : "r"(vb + LY::CODES + r8 * 8 + 64 * i) : "memory");
             ok[i] = vs != -1.f;
             all_ok &= ok[i];
-            lv[i] = fast_log2(vs);
+            if (TWO) split_scale(vs, vp[i], lv[i]);
+            else lv[i] = fast_log2(vs);
         }
         const bool whole = key0 + KEYS <= least && __all_sync(0xffffffffu, all_ok);     // no key of these is hidden from any row
         uint32_t pb[SUB][NT][TWO ? 2 : 1][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float x[2 * SUB][2], y[2 * SUB][2], w[2 * SUB][2], up[2];
+            // (Two forms of one step: with f32's second half after the branch it is 2 % faster, with bf16's there 1 % slower.)
+            float x[2 * SUB][2], w[2 * SUB][2], up[2];
             bool moved = false;
+            if constexpr (TWO) {
+                float m[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float a = mx[t][e], m = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    float a = mx[t][e];
+                    m[e] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2 * SUB; ++i) {
-                    x[i][e] = sacc[i / 2][t][2 * (i & 1) + e] * (f[t][e] * ks[i]);
-                    y[i][e] = x[i][e] + lv[i];
-                    if (!whole && (key0 + 8 * i + r8 >= end[t][e] || !ok[i])) x[i][e] = y[i][e] = -INFINITY;
-                    a = fmaxf(a, x[i][e]);
-                    m = fmaxf(m, y[i][e]);
+                    for (int i = 0; i < 2 * SUB; ++i) {
+                        x[i][e] = sacc[i / 2][t][2 * (i & 1) + e] * (f[t][e] * ks[i]);
+                        if (!whole && (key0 + 8 * i + r8 >= end[t][e] || !ok[i])) x[i][e] = -INFINITY;
+                        a = fmaxf(a, x[i][e]);
+                        m[e] = fmaxf(m[e], x[i][e] + lv[i]);
+                    }
+                    a = ceilf(a);
+                    const float ra = a == -INFINITY ? 0.f : a;
+                    l[t][e] *= fast_exp2(mx[t][e] - ra);
+#pragma unroll
+                    for (int i = 0; i < 2 * SUB; ++i) l[t][e] += fast_exp2(x[i][e] - ra);
+                    mx[t][e] = a;
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], off));
+                    moved |= m[e] > my[t][e];
                 }
-                const float ra = a == -INFINITY ? 0.f : a;
-                l[t][e] *= fast_exp2(mx[t][e] - ra);
+                if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int i = 0; i < 2 * SUB; ++i) l[t][e] += fast_exp2(x[i][e] - ra);
-                mx[t][e] = a;
+                    for (int e = 0; e < 2; ++e) {
+                        const float to = fmaxf(ceilf(m[e]), my[t][e]);
+                        up[e] = fast_exp2(my[t][e] - (to == -INFINITY ? 0.f : to));
+                        my[t][e] = to;
+                    }
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                m = fmaxf(m, my[t][e]);
-                const float rm = m == -INFINITY ? 0.f : m;
-                up[e] = fast_exp2(my[t][e] - rm);
-                moved |= m != my[t][e];
-                my[t][e] = m;
+                    for (int i = 0; i < KS; ++i) {
+                        o[t][i][0] *= up[0];
+                        o[t][i][1] *= up[1];
+                        o[t][i][2] *= up[0];
+                        o[t][i][3] *= up[1];
+                    }
+                }
 #pragma unroll
-                for (int i = 0; i < 2 * SUB; ++i) w[i][e] = fast_exp2(y[i][e] - (rm - RQ_TOP));
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                for (int e = 0; e < 2; ++e) {
+                    const float top = (my[t][e] == -INFINITY ? 0.f : my[t][e]) - RQ_TOP;
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    o[t][i][0] *= up[0];
-                    o[t][i][1] *= up[1];
-                    o[t][i][2] *= up[0];
-                    o[t][i][3] *= up[1];
+                    for (int i = 0; i < 2 * SUB; ++i) {
+                        w[i][e] = fast_exp2(x[i][e] - (top - lv[i])) * vp[i];
+                        if (!whole && x[i][e] == -INFINITY) w[i][e] = 0.f;       // hidden, whatever its scale
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float a = mx[t][e], m = -INFINITY, y[2 * SUB];
+#pragma unroll
+                    for (int i = 0; i < 2 * SUB; ++i) {
+                        x[i][e] = sacc[i / 2][t][2 * (i & 1) + e] * (f[t][e] * ks[i]);
+                        y[i] = x[i][e] + lv[i];
+                        if (!whole && (key0 + 8 * i + r8 >= end[t][e] || !ok[i])) x[i][e] = y[i] = -INFINITY;
+                        a = fmaxf(a, x[i][e]);
+                        m = fmaxf(m, y[i]);
+                    }
+                    const float ra = a == -INFINITY ? 0.f : a;
+                    l[t][e] *= fast_exp2(mx[t][e] - ra);
+#pragma unroll
+                    for (int i = 0; i < 2 * SUB; ++i) l[t][e] += fast_exp2(x[i][e] - ra);
+                    mx[t][e] = a;
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    m = fmaxf(m, my[t][e]);
+                    const float rm = m == -INFINITY ? 0.f : m;
+                    up[e] = fast_exp2(my[t][e] - rm);
+                    moved |= m != my[t][e];
+                    my[t][e] = m;
+#pragma unroll
+                    for (int i = 0; i < 2 * SUB; ++i) w[i][e] = fast_exp2(y[i] - (rm - RQ_TOP));
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[t][i][0] *= up[0];
+                        o[t][i][1] *= up[1];
+                        o[t][i][2] *= up[0];
+                        o[t][i][3] *= up[1];
+                    }
                 }
             }
 #pragma unroll
@@ -529,7 +592,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
     };
     // O is relative to 2^(my - 15), l to 2^mx of its lane.
     float* red_o = reinterpret_cast<float*>(smem);             // warps that share a head: [8 warps][8 rows][RS]
-    float* red_m = red_o + RQ_WARPS * 8 * LY::RS;              // mx, l, my, weight, lse of [8 warps][8 rows]
+    float* red_m = red_o + RQ_WARPS * 8 * LY::RS;              // mx (then the row's factor), l, my, weight, lse of [8 warps][8 rows]
     constexpr int M = RQ_WARPS * 8;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -546,11 +609,12 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
             for (int off = 4; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
             if (ways == 1) {
                 const int r = 8 * t + 2 * t4 + e;
-                const float w = s == 0.f ? 0.f : exp2f(my[t][e] - RQ_TOP - ref) / s;      // no key: zeros
+                // two factors, -127 < my - ref <= 128: their product may be below the normal numbers, where the row is not
+                const float w = s == 0.f ? 0.f : 0x1p-13f / s, f = exp2f((my[t][e] == -INFINITY ? ref : my[t][e]) - ref - (RQ_TOP - 13.f));
                 const float lse = s == 0.f ? -INFINITY : m + log2f(s);
                 if (R0 + r < rows)
 #pragma unroll
-                    for (int i = 0; i < KS; ++i) put(r, warp & (HB - 1), 16 * i + 2 * r8, o[t][i][e] * w, o[t][i][e + 2] * w, lse, i == 0 && r8 == 0);
+                    for (int i = 0; i < KS; ++i) put(r, warp & (HB - 1), 16 * i + 2 * r8, o[t][i][e] * w * f, o[t][i][e + 2] * w * f, lse, i == 0 && r8 == 0);
                 continue;
             }
             if (r8 == 0) {
@@ -572,21 +636,23 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
             const float ref = top == -INFINITY ? 0.f : top;
             for (int w = 0; w < ways; ++w) L += red_m[M + tid + step * w] * exp2f(red_m[tid + step * w] - ref);
             const float inv = L == 0.f ? 0.f : 1.f / L;
-            for (int w = 0; w < ways; ++w) red_m[3 * M + tid + step * w] = exp2f(red_m[2 * M + tid + step * w] - RQ_TOP - ref) * inv;
+            for (int w = 0; w < ways; ++w) red_m[3 * M + tid + step * w] = exp2f(red_m[2 * M + tid + step * w] - ref - (RQ_TOP - 13.f));
             red_m[4 * M + tid] = L == 0.f ? -INFINITY : top + log2f(L);
+            red_m[tid] = 0x1p-13f * inv;                       // two factors, as above
         }
         __syncthreads();
         constexpr int HALF = D / 2;
         for (int idx = tid; idx < HB * 8 * HALF; idx += RQ_THREADS) {
             const int hr = idx / HALF, d = 2 * (idx % HALF), r = 8 * t + (hr & 7);
             if (R0 + r >= rows) continue;
+            const float f = red_m[hr];
             float a0 = 0.f, a1 = 0.f;
             for (int w = 0; w < ways; ++w) {
                 const int at = hr + 8 * HB * w;
                 const float wt = red_m[3 * M + at];
                 const float2 v = *reinterpret_cast<const float2*>(red_o + at * LY::RS + d);
-                a0 += wt * v.x;
-                a1 += wt * v.y;
+                a0 += wt * (f * v.x);
+                a1 += wt * (f * v.y);
             }
             put(r, hr >> 3, d, a0, a1, red_m[4 * M + hr], d == 0);
         }

@@ -1084,3 +1084,64 @@ def test_decode_q8_any_bad_slot_in_a_shared_run(dev, bad):
             ok = r2t[b, :n]
             ok = ok[(ok >= 0) & (ok < slots)]
             agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], *cache.values(ok), 1 / math.sqrt(d), len(ok) - 1), BF)
+
+
+# ============================================================================ value scales of any size, f32 rows
+def one_product(dev, fmt, n, hq, hkv, d, rows, power, seed=0):
+    """Queries and a cache whose scores are one product each, at most 1, so that little of the score is rounded: channel 5
+    alone, of 24 bits.  V's scales are 1 to 2 times 2^power."""
+    g = torch.Generator(device=dev).manual_seed(seed + n + hq + rows)
+    cache = Cache(dev, fmt, n, hkv, d, seed=seed)
+    cache.scales[..., 0] = math.sqrt(d) / TOP[fmt]
+    cache.scales[..., 1] = (1 + torch.rand(n, hkv, generator=g, device=dev)) * 2.0 ** power
+    q = torch.zeros(rows, hq, d, device=dev)
+    q[..., 5] = 0.5 + 0.5 * torch.rand(rows, hq, generator=g, device=dev)
+    r2t = torch.randperm(n, generator=g, device=dev).to(torch.int32)[None].contiguous()
+    return cache, q, r2t
+
+
+def agree_f32(out, want, keys):
+    """f32 rows of scores of one product, |score| <= 1.  A score is off by 2.5 * 2^-22 of itself (two f16 parts of a query, the sum
+    of their products, five roundings of the factors) and a rounding of its distance from the reference, an exponential by
+    2^-22, a weight by its two parts' 2^-22 and its product's 2^-24: below 2^-19.2 of each p_j, and again of their sum.  The tensor
+    core adds 16 products to a sum, each cut off at 2^-23 of the largest: 17 * 2^-23 of sum p |v| an instruction, two of them a
+    16 keys of a warp."""
+    o, _, a, _, _, _ = want
+    tol = a * (2 ** -18.2 + 2 * math.ceil(keys / 16) * 17 * 2.0 ** -23 + 2.0 ** -23)
+    assert (out.double() - o).abs().le(tol).all(), float(((out.double() - o).abs() / tol).max())
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 8, 64), (2, 1, 128), (16, 8, 128), (12, 4, 64)])
+@pytest.mark.parametrize("power", [0, -10, -60, -110, -120, -126, 100])
+def test_q8_value_scales_of_any_size(dev, fmt, hq, hkv, d, power):
+    """f32 rows are as exact with values near the smallest and largest numbers as with others."""
+    n = 16
+    cache, q, r2t = one_product(dev, fmt, n, hq, hkv, d, 1, power)
+    q, out, lse, st = decode(dev, cache, F, hq, hkv, d, [n], r2t, q=q)
+    assert st == 0
+    agree_f32(out, attend(q, *cache.values(r2t[0]), 1 / math.sqrt(d), n - 1), n)
+    rows = 12
+    cache, q, r2t = one_product(dev, fmt, n, hq, hkv, d, rows, power)
+    q, out, lse, st = extend(dev, cache, F, hq, hkv, d, [rows], [n - rows], r2t, q=torch.cat([q, q[:2]]))
+    assert st == 0
+    agree_f32(out[:rows], attend(q[:rows], *cache.values(r2t[0]), 1 / math.sqrt(d), n - rows), n)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 8, 64), (2, 1, 128), (16, 8, 128)])
+def test_decode_q8_many_keys_of_tiny_values(dev, dt, hq, hkv, d):
+    """A thousand keys that count alike, with the smallest scale that the write makes: their mean, a normal number.  (Weights of
+    one are exact in any type; a sum of 1000 / 16 instructions, cut off 17 * 2^-23 each at most, and the output's rounding.)"""
+    n = 1000
+    cache = Cache(dev, INT8, n, hkv, d, seed=1)
+    cache.scales[..., 1] = 2.0 ** -126
+    cache.k.zero_()
+    r2t = torch.randperm(n, device=dev).to(torch.int32)[None].contiguous()
+    q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, [n], r2t)
+    assert st == 0
+    o, _, a, _, _, _ = attend(q, *cache.values(r2t[0]), 1 / math.sqrt(d), n - 1)
+    tol = a * (64 * 2 * 17 * 2.0 ** -23) + (o.abs() * 2.0 ** -8 + 2.0 ** -133 if dt == BF else 0)
+    assert (out.double() - o).abs().le(tol).all(), float(((out.double() - o).abs() / a).max())
