@@ -132,7 +132,8 @@ __device__ __forceinline__ uint2 codes_int8(const float* x, float s, float inv) 
         n[i] = fmaf(y, inv, MAGIC);
         off = fmaxf(off, fabsf(fmaf(MAGIC - n[i], s, y)));
     }
-    if (off >= 0.4999f * s) {                      // some quotient is next to a half
+    // some quotient is next to a half, or 127 s is no number that an infinity could be cut to
+    if (off >= 0.4999f * s || (FIXED && s > 0x1p121f)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float q = x[i] * inv;

@@ -1145,3 +1145,20 @@ def test_decode_q8_many_keys_of_tiny_values(dev, dt, hq, hkv, d):
     o, _, a, _, _, _ = attend(q, *cache.values(r2t[0]), 1 / math.sqrt(d), n - 1)
     tol = a * (64 * 2 * 17 * 2.0 ** -23) + (o.abs() * 2.0 ** -8 + 2.0 ** -133 if dt == BF else 0)
     assert (out.double() - o).abs().le(tol).all(), float(((out.double() - o).abs() / a).max())
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("s", [2.0 ** -126, 1.5 * 2.0 ** -100, 2.0 ** 120, 1.25 * 2.0 ** 121, 1.75 * 2.0 ** 126, 2.0 ** 127])
+def test_write_q8_given_scales_of_any_size(dev, fmt, dt, s):
+    """Given scales from the smallest to the largest normal numbers, with rows of any size: codes of the real quotient, cut."""
+    x = torch.tensor([math.inf, -math.inf, 3.3e38, -3.3e38, 1e38, -1e38, 1.0, 2.0 ** -120, -(2.0 ** -126), 2.0 ** -133, s, -s, 3 * s, 2.5 * s, 1.5 * s,
+                      0.0] * 4, device=dev, dtype=torch.float64).float().to(dt).view(1, 1, 64)
+    c, desc = api.q8_desc(fmt, 1, True), desc_of(dt, 1, 1, 64, 1)
+    pools = [torch.zeros(1, 1, 64, dtype=torch.int8, device=dev).view(TYPE[fmt]) for _ in range(2)]
+    scales, st = torch.full((1, 1, 2), s, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    api.kv_pool_write_q8(desc, c, 1, None, None, i32([0], dev), i64([0, 1], dev), x, x, *pools, scales, None, 1, st)
+    want = codes_of(x[0], scales[0, :, 0], fmt)
+    for p in pools:
+        assert torch.equal(p[0].double(), want), (p[0].double() - want).nonzero()
