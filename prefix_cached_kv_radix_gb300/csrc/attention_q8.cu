@@ -75,7 +75,7 @@ extern "C" int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q
         const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).bytes), need = own + shared_q8_bytes(desc, batch, groups->num_groups);
         RX_REQUIRE(d_workspace && ws_bytes >= need && ((uintptr_t)d_workspace & 255) == 0,
                    "%s: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", fn, need, ws_bytes);
-        rc = shared_q8_launch(a, desc, q8, groups, (unsigned char*)d_workspace + own, (cudaStream_t)stream);
+        rc = shared_q8_launch(fn, a, desc, q8, groups, (unsigned char*)d_workspace + own, (cudaStream_t)stream);
         if (rc != RX_OK) return rc;
     }
     return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
@@ -94,6 +94,6 @@ extern "C" int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_
                        (const uint8_t*)d_v_pool, (const float2*)d_scales, d_out, d_lse, batch, max_qo_len, max_kv_len, d_status};
     rc = attention_q8_pointers(fn, a);
     if (rc != RX_OK) return rc;
-    if (many_rows(desc, max_qo_len)) return extend_q8_launch(a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
+    if (many_rows(desc, max_qo_len)) return extend_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
     return rows_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);
 }

@@ -885,17 +885,17 @@ __global__ void __launch_bounds__(128) extend_q8_merge_kernel(const __grid_const
 }
 
 // The current device must be an sm_103: checked once per device.
-static int eq_device() {
+static int eq_device(const char* fn) {
     static PerDeviceOnce checked;
-    return per_device_once(checked, [] {
+    return per_device_once(checked, [&] {
         int dev = 0, major = 0, minor = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-            set_error("prefix_extend_attention_q8: cannot query the device");
+            set_error("%s: cannot query the device", fn);
             return (int)RX_ECUDA;
         }
         if (major != 10 || minor != 3) {
-            set_error("prefix_extend_attention_q8: the tcgen05 kernel needs an sm_103 (GB300) device");
+            set_error("%s: the tcgen05 kernel needs an sm_103 (GB300) device", fn);
             return (int)RX_EDEVICE;
         }
         return (int)RX_OK;
@@ -928,19 +928,19 @@ size_t extend_q8_bytes(const rx_attn_desc* d) {
 }
 
 template <int D, int FMT>
-static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
+static int launch_extend(const char* fn, const ExtendQ8Params& p, cudaStream_t s) {
     static PerDeviceOnce attr;
     constexpr int smem = EqLayout<D>::ALLOC;
     const int rc = per_device_once(attr, [&] {
         const cudaError_t e = cudaFuncSetAttribute(extend_q8_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) {
-            set_error("prefix_extend_attention_q8: cannot set shared memory size: %s", cudaGetErrorString(e));
+            set_error("%s: cannot set shared memory size: %s", fn, cudaGetErrorString(e));
             return (int)RX_ECUDA;
         }
         // the warpgroups share out the registers the block is launched with: fewer, and they would wait forever
         cudaFuncAttributes fa{};
         if (cudaFuncGetAttributes(&fa, extend_q8_kernel<D, FMT>) != cudaSuccess || fa.numRegs < (int)EQ_REGS_LAUNCH) {
-            set_error("prefix_extend_attention_q8: kernel built with %d registers per thread; the register split needs %d", fa.numRegs,
+            set_error("%s: kernel built with %d registers per thread; the register split needs %d", fn, fa.numRegs,
                       (int)EQ_REGS_LAUNCH);
             return (int)RX_ECUDA;
         }
@@ -963,7 +963,7 @@ static int launch_extend(const ExtendQ8Params& p, cudaStream_t s) {
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
-        set_error("prefix_extend_attention_q8: launch failed: %s", cudaGetErrorString(e));
+        set_error("%s: launch failed: %s", fn, cudaGetErrorString(e));
         return RX_ECUDA;
     }
     return RX_OK;
@@ -993,23 +993,24 @@ static void eq_params(ExtendQ8Params& p, const RowsQ8Args& a, const rx_attn_desc
     p.meta = (int4*)(p.part_lse + rows);
 }
 
-static int launch_extend(const ExtendQ8Params& p, const rx_attn_desc* d, const rx_q8_desc* q8, cudaStream_t stream) {
+static int launch_extend(const char* fn, const ExtendQ8Params& p, const rx_attn_desc* d, const rx_q8_desc* q8, cudaStream_t stream) {
     if (d->head_dim == 128)
-        return q8->format == RX_Q8_INT8 ? launch_extend<128, RX_Q8_INT8>(p, stream) : launch_extend<128, RX_Q8_E4M3>(p, stream);
-    return q8->format == RX_Q8_INT8 ? launch_extend<64, RX_Q8_INT8>(p, stream) : launch_extend<64, RX_Q8_E4M3>(p, stream);
+        return q8->format == RX_Q8_INT8 ? launch_extend<128, RX_Q8_INT8>(fn, p, stream) : launch_extend<128, RX_Q8_E4M3>(fn, p, stream);
+    return q8->format == RX_Q8_INT8 ? launch_extend<64, RX_Q8_INT8>(fn, p, stream) : launch_extend<64, RX_Q8_E4M3>(fn, p, stream);
 }
 
-int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream) {
-    const int dc = eq_device();
+int extend_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,
+                     cudaStream_t stream) {
+    const int dc = eq_device(fn);
     if (dc != RX_OK) return dc;
     const size_t need = extend_q8_bytes(d);
     RX_REQUIRE(ws && ws_bytes >= need && ((uintptr_t)ws & 255) == 0,
-               "prefix_extend_attention_q8: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", need, ws_bytes);
-    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - EQ_ROWS, "prefix_extend_attention_q8: too many rows in a request");
+               "%s: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", fn, need, ws_bytes);
+    RX_REQUIRE((int64_t)a.max_qo_len * (d->hq / d->hkv) < INT32_MAX - EQ_ROWS, "%s: too many rows in a request", fn);
     ExtendQ8Params p{};
     eq_params(p, a, d, q8, ws);
     p.q_map_ok = eq_rows_map(&p.q_map, a.q, d->hq, d->head_dim, p.group) ? 1 : 0;
-    return launch_extend(p, d, q8, stream);
+    return launch_extend(fn, p, d, q8, stream);
 }
 
 // A decode batch's groups as the kernels take them: SharedGroup per group, members (-1: not one), and the keys that each
@@ -1065,8 +1066,9 @@ size_t shared_q8_bytes(const rx_attn_desc* d, int32_t batch, int32_t num_groups)
     return shared_layout(d, batch, num_groups).total + extend_q8_bytes(d);
 }
 
-int shared_q8_launch(RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws, cudaStream_t stream) {
-    const int dc = eq_device();
+int shared_q8_launch(const char* fn, RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws,
+                     cudaStream_t stream) {
+    const int dc = eq_device(fn);
     if (dc != RX_OK) return dc;
     const SharedLayout L = shared_layout(d, a.batch, g->num_groups);
     unsigned char* w = (unsigned char*)ws;
@@ -1082,7 +1084,7 @@ int shared_q8_launch(RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8,
     a.shared_of = (const int32_t*)(w + L.of);
     a.shared_o = p.shared_o;
     a.shared_lse = p.shared_lse;
-    return launch_extend(p, d, q8, stream);
+    return launch_extend(fn, p, d, q8, stream);
 }
 
 }  // namespace rx

@@ -53,10 +53,12 @@ int rows_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, c
 // bf16 rows past what a tile of rows_q8.cu takes: the tensor-core kernel of extend_q8.cu and its workspace.
 constexpr int64_t ROWS_Q8_MOST = 16;
 size_t extend_q8_bytes(const rx_attn_desc* d);
-int extend_q8_launch(const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes, cudaStream_t stream);
+int extend_q8_launch(const char* fn, const RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, void* ws, size_t ws_bytes,
+                     cudaStream_t stream);
 
 // The shared runs of a decode batch's groups on that kernel; sets a's shared_* for the call of rows_q8_launch that does the rest.
 size_t shared_q8_bytes(const rx_attn_desc* d, int32_t batch, int32_t num_groups);
-int shared_q8_launch(RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws, cudaStream_t stream);
+int shared_q8_launch(const char* fn, RowsQ8Args& a, const rx_attn_desc* d, const rx_q8_desc* q8, const rx_shared_groups* g, void* ws,
+                     cudaStream_t stream);
 
 }  // namespace rx

@@ -5,6 +5,10 @@ The pages have no 8-bit cache; these stand beside kv_pool_write and the attentio
 """
 import ctypes
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import numpy as np
 import pytest
@@ -1162,3 +1166,30 @@ def test_write_q8_given_scales_of_any_size(dev, fmt, dt, s):
     want = codes_of(x[0], scales[0, :, 0], fmt)
     for p in pools:
         assert torch.equal(p[0].double(), want), (p[0].double() - want).nonzero()
+
+
+def test_q8_errors_name_the_call():
+    """Without a device, calls that pass all checks fail under their own names, decode with groups too.  (In a process that sees
+    no GPU, wherever it runs: the addresses are none.)"""
+    code = textwrap.dedent("""
+        import ctypes
+        from prefix_cached_kv_radix_gb300 import api
+        lib, by, A = api.load(), ctypes.byref, 0x1000
+        d, c = api.make_desc(api.RX_BF16, 8, 2, 128, 64, 0.1), api.q8_desc(api.RX_Q8_INT8)
+        g = api.rx_shared_groups()
+        g.num_groups, g.max_group_size, g.max_group_len = 1, 2, 8
+        g.d_group_indptr, g.d_group_members, g.d_group_len = A, A, A
+        def failed(fn, *args):
+            rc = getattr(lib, fn)(*args)
+            text = lib.rx_last_error().decode()
+            assert rc not in (api.RX_OK, api.RX_EINVAL) and text.startswith(fn + ":"), (fn, rc, text)
+        failed("decode_attention_q8", by(d), by(c), 2, A, A, 8, A, by(g), A, A, A, A, None, 8, A, 1 << 40, None, None)
+        failed("decode_attention_q8", by(d), by(c), 2, A, A, 8, A, None, A, A, A, A, None, 8, A, 1 << 40, None, None)
+        for rows in (1, 5):
+            failed("prefix_extend_attention_q8", by(d), by(c), 1, A, A, A, A, 8, A, A, A, A, None, rows, 8, A, 1 << 40, None, None)
+        failed("kv_pool_write_q8", by(d), by(c), 1, A, A, A, A, A, 256, A, 256, A, A, A, A, 8, 4, None, None)
+        failed("kv_pool_read_q8", by(d), by(c), 4, A, A, A, A, A, 256, A, 256, None, None)
+    """)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr
