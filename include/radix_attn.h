@@ -549,7 +549,8 @@ int kv_pool_read_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int64_t n, c
  *    desc->dtype f32 gives 32-bit results, on the tensor cores as well (queries and weighted probabilities in two 16-bit
  *    parts each); bf16 rounds the weighted probabilities to 11 bits (and takes the logarithm of V's scale, within 2^-15, into
  *    their exponent), those of a group's shared run to bf16 (as prefix_extend_attention_q8 does those of many rows).
- *  - A request of length 0 (a padded batch) gives a row of zeros and a log-sum-exp of -infinity.
+ *  - A request of length 0 (a padded batch) gives a row of zeros and a log-sum-exp of -infinity.  One of more than
+ *    2^31 - 2^16 keys: RX_DEV_BAD_LENGTH.
  *  - A key at a slot outside [0, num_slots) is reported and left out.
  *  - groups: as for decode_attention; used for bf16 rows (f32 rows read each request's own keys, with the same result).
  *    d_group_indptr does not decrease.  A group of bad boundaries or length is reported (RX_DEV_BAD_LENGTH) and its members
@@ -574,8 +575,8 @@ size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_
  *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most, for scales of 2^-100 and more: a product
  *    below 2^-126 has fewer bits, and one below 2^-134 is zero) where max_qo_len * hq / hkv is above 16, and as in decode below;
  *    f32 as in decode.
- *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request; it decides how far few rows over long
- *    contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned; what it is for the
+ *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request, as above 2^31 - 2^16; it decides how
+ *    far few rows over long contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned; what it is for the
  *    greatest batch and lengths serves all smaller calls). */
 int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q8, int32_t batch, const void* d_q,
                                const int64_t* d_qo_indptr, const int32_t* d_prefix_lens, const int32_t* d_req_to_token,

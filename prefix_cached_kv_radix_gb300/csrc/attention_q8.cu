@@ -1,4 +1,5 @@
 // The entry points of attention over 8-bit pools: argument checks, and which kernel takes a call.
+#include <algorithm>
 #include <cmath>
 
 #include "kv_q8.cuh"
@@ -25,6 +26,9 @@ static int attention_q8_pointers(const char* fn, const RowsQ8Args& a) {
     RX_REQUIRE(((uintptr_t)a.scales & 7) == 0, "%s: scales must be 8-byte aligned", fn);
     return RX_OK;
 }
+
+// The most keys of a request: the kernels count keys in 32 bits, and up to two stages' past the last.
+constexpr int32_t Q8_MOST_KEYS = INT32_MAX - 65535;
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -65,14 +69,14 @@ extern "C" int decode_attention_q8(const rx_attn_desc* desc, const rx_q8_desc* q
     if (rc != RX_OK || batch == 0) return rc;
     RX_REQUIRE(d_kv_lens, "%s: null device pointer", fn);
     RowsQ8Args a{d_q,  nullptr, nullptr, d_kv_lens, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool, (const uint8_t*)d_v_pool,
-                 (const float2*)d_scales, d_out, d_lse, batch, 1, max_kv_len, d_status};
+                 (const float2*)d_scales, d_out, d_lse, batch, 1, std::min(max_kv_len, Q8_MOST_KEYS), d_status};
     rc = attention_q8_pointers(fn, a);
     if (rc != RX_OK) return rc;
     if (uses_groups(desc, groups)) {
         RX_REQUIRE(groups->d_group_indptr && groups->d_group_members && groups->d_group_len && groups->max_group_size >= 1 &&
                        groups->max_group_len >= 1,
                    "%s: incomplete shared groups", fn);
-        const size_t own = up256(rows_q8_plan(desc, batch, 1, max_kv_len).bytes), need = own + shared_q8_bytes(desc, batch, groups->num_groups);
+        const size_t own = up256(rows_q8_plan(desc, batch, 1, a.max_kv_len).bytes), need = own + shared_q8_bytes(desc, batch, groups->num_groups);
         RX_REQUIRE(d_workspace && ws_bytes >= need && ((uintptr_t)d_workspace & 255) == 0,
                    "%s: a 256-byte aligned workspace of %zu bytes is needed (got %zu)", fn, need, ws_bytes);
         rc = shared_q8_launch(fn, a, desc, q8, groups, (unsigned char*)d_workspace + own, (cudaStream_t)stream);
@@ -91,7 +95,8 @@ extern "C" int prefix_extend_attention_q8(const rx_attn_desc* desc, const rx_q8_
     int rc = attention_q8_check(fn, desc, q8, batch, r2t_stride, max_qo_len, max_kv_len);
     if (rc != RX_OK || batch == 0 || max_qo_len == 0) return rc;
     const RowsQ8Args a{d_q,  d_qo_indptr, d_prefix_lens, nullptr, d_req_to_token, r2t_stride, (const uint8_t*)d_k_pool,
-                       (const uint8_t*)d_v_pool, (const float2*)d_scales, d_out, d_lse, batch, max_qo_len, max_kv_len, d_status};
+                       (const uint8_t*)d_v_pool, (const float2*)d_scales, d_out, d_lse, batch, max_qo_len, std::min(max_kv_len, Q8_MOST_KEYS),
+                       d_status};
     rc = attention_q8_pointers(fn, a);
     if (rc != RX_OK) return rc;
     if (many_rows(desc, max_qo_len)) return extend_q8_launch(fn, a, desc, q8, d_workspace, ws_bytes, (cudaStream_t)stream);

@@ -1193,3 +1193,32 @@ def test_q8_errors_name_the_call():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     got = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), capture_output=True, text=True)
     assert got.returncode == 0, got.stderr
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F])
+def test_attention_q8_lengths_near_the_32_bit_limit(dev, dt):
+    """Requests of more than 2^31 - 2^16 keys are refused on the device, before any of their slots is read: the table here holds the
+    first of its entries only."""
+    hq, hkv, d, most = 8, 2, 64, 2 ** 31 - 1
+    desc, cache = desc_of(dt, hq, hkv, d, 64), Cache(dev, INT8, 64, hkv, d, seed=1)
+    table = torch.zeros(4096, dtype=torch.int32, device=dev)
+    lib, by = api.load(), ctypes.byref
+    for length in (most, most - 1000, most - 65534):
+        st, out = torch.zeros(1, dtype=torch.int32, device=dev), torch.full((40, hq, d), 9.0, device=dev, dtype=dt)
+        q, lse = torch.zeros_like(out), torch.full((40, hq), 9.0, device=dev)
+        ws = torch.empty(api.decode_q8_workspace_bytes(desc, 1, most), dtype=torch.uint8, device=dev)
+        lens = i32([length], dev)
+        assert lib.decode_attention_q8(by(desc), by(cache.q8), 1, q.data_ptr(), table.data_ptr(), most, lens.data_ptr(), None,
+                                       cache.k.data_ptr(), cache.v.data_ptr(), cache.scales.data_ptr(), out.data_ptr(), lse.data_ptr(), most,
+                                       ws.data_ptr(), ws.numel(), st.data_ptr(), torch.cuda.current_stream().cuda_stream) == api.RX_OK
+        assert int(st) == api.RX_DEV_BAD_LENGTH and (out == 9.0).all() and (lse == 9.0).all()
+        for rows in (2, 40):
+            st.zero_()
+            ws = torch.empty(api.extend_q8_workspace_bytes(desc, 1, rows, most), dtype=torch.uint8, device=dev)
+            ind, pre = i64([0, rows], dev), i32([length - rows], dev)
+            assert lib.prefix_extend_attention_q8(by(desc), by(cache.q8), 1, q.data_ptr(), ind.data_ptr(), pre.data_ptr(), table.data_ptr(),
+                                                  most, cache.k.data_ptr(), cache.v.data_ptr(), cache.scales.data_ptr(), out.data_ptr(),
+                                                  lse.data_ptr(), rows, most, ws.data_ptr(), ws.numel(), st.data_ptr(),
+                                                  torch.cuda.current_stream().cuda_stream) == api.RX_OK
+            assert int(st) == api.RX_DEV_BAD_LENGTH and (out == 9.0).all() and (lse == 9.0).all()
