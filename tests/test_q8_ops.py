@@ -1222,3 +1222,94 @@ def test_attention_q8_lengths_near_the_32_bit_limit(dev, dt):
                                                   lse.data_ptr(), rows, most, ws.data_ptr(), ws.numel(), st.data_ptr(),
                                                   torch.cuda.current_stream().cuda_stream) == api.RX_OK
             assert int(st) == api.RX_DEV_BAD_LENGTH and (out == 9.0).all() and (lse == 9.0).all()
+
+
+# ============================================================================ what the tolerances and sizes above leave out
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (16, 8, 128)])
+def test_agree_f32_notices_a_part_left_out(hq, hkv, d):
+    """Queries or weights of one f16 part instead of two, here in the oracle: agree_f32 refuses either."""
+    cpu, n = torch.device("cpu"), 16
+    cache, q, r2t = one_product(cpu, INT8, n, hq, hkv, d, 1, 0)
+    k, v = cache.values(r2t[0])
+    want = attend(q, k, v, 1 / math.sqrt(d), n - 1)
+    agree_f32(want[0].float(), want, n)
+    with pytest.raises(AssertionError):
+        agree_f32(attend(q.half(), k, v, 1 / math.sqrt(d), n - 1)[0], want, n)
+    s = torch.einsum("hgd,khd->hgk", q[0].double().view(hkv, hq // hkv, d), k) / math.sqrt(d)
+    p = torch.exp(s - s.amax(-1, keepdim=True))
+    vs, codes = cache.scales[r2t[0].long(), :, 1].double(), v / cache.scales[r2t[0].long(), :, 1:].double()
+    w = p * vs.t()[:, None, :]
+    w = (w * (2.0 ** 14 / w.amax(-1, keepdim=True))).half().double() / (2.0 ** 14 / w.amax(-1, keepdim=True))
+    with pytest.raises(AssertionError):
+        agree_f32((torch.einsum("hgk,khd->hgd", w, codes) / p.sum(-1, keepdim=True)).reshape(1, hq, d), want, n)
+
+
+EIGHTS = [(8, 8, 64), (32, 8, 128), (24, 8, 64), (16, 16, 128)]
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d", EIGHTS)
+def test_attention_q8_kv_heads_by_eights(dev, fmt, dt, hq, hkv, d):
+    """Eight kv heads a CTA, a warp each: whole contexts of many requests, and a few long ones shared out."""
+    for lens in ([1, 0, 2, 15, 16, 17, 33, 40] * 30, [5000, 3, 2047]):
+        slots = sum(lens) + 9
+        r2t, used = table_of(lens, (max(lens) + 7) // 8 * 8, slots, dev)
+        cache = Cache(dev, fmt, slots, hkv, d, seed=hq)
+        poison(cache, used)
+        q, out, lse, st = decode(dev, cache, dt, hq, hkv, d, lens, r2t)
+        assert st == 0
+        for b in list(range(min(len(lens), 16))) + [len(lens) - 1]:
+            k, v = cache.values(r2t[b, :lens[b]])
+            agree(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], k, v, 1 / math.sqrt(d), lens[b] - 1), dt)
+    most = 16 * hkv // hq                        # as many tokens as make 16 rows
+    for lens, pre in (([most, 1, 0, most, 2] * 40, [0, 30, 5, 11, 1] * 40), ([most, 1], [4100, 700])):
+        total = [a + b for a, b in zip(lens, pre)]
+        slots = sum(total) + 9
+        r2t, used = table_of(total, (max(total) + 7) // 8 * 8, slots, dev)
+        cache = Cache(dev, fmt, slots, hkv, d, seed=hq)
+        poison(cache, used)
+        q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, lens, pre, r2t)
+        assert st == 0
+        few = min(len(lens), 10)
+        extend_agrees(cache, dt, d, lens[:few], pre[:few], r2t, q, out, lse)
+
+
+def cut_off(x):
+    """f32 numbers with the last bits of their float64 values cut off."""
+    y = x.float()
+    return torch.where(y.double().abs() > x.abs(), torch.nextafter(y, torch.zeros_like(y)), y)
+
+
+def long_sum_tolerance(stages):
+    """Of a sum of positive terms in 32 bits, relative: a stage's own sum is four instructions, each cut off at 17 * 2^-23; the
+    stages are added with rounding, independent and 2^-24 of the sum so far at most, which grows evenly: beyond 6 times the
+    square root of their squares' sum, stages / 3, with a probability below 2 e^-18; weights are off by 2^-21."""
+    return 4 * 17 * 2.0 ** -23 + 6 * math.sqrt(stages / 3) * 2.0 ** -24 + 2.0 ** -21
+
+
+def test_long_sums_tolerance_notices_sums_cut_off():
+    g, stages = torch.Generator().manual_seed(0), 1600
+    terms = torch.rand(stages, 64, generator=g, dtype=torch.float64) + 0.5
+    exact, rounded, cut = terms.sum(0), torch.zeros(64), torch.zeros(64)
+    for t in terms:
+        rounded = (rounded.double() + t).float()
+        cut = cut_off(cut.double() + t)
+    assert ((rounded.double() - exact).abs() / exact).max() < long_sum_tolerance(stages)
+    assert ((cut.double() - exact).abs() / exact).max() > long_sum_tolerance(stages)
+
+
+@gpu
+def test_decode_q8_f32_long_sums(dev):
+    """51200 keys that count alike: 1600 stages one after another, added with rounding and not cut off as the tensor core does."""
+    hq, hkv, d, n, b = 8, 8, 64, 51200, 300
+    cache = Cache(dev, INT8, n, hkv, d, seed=1)
+    bytes_of(cache.v).copy_(torch.randint(1, 128, cache.v.shape, device=dev, dtype=torch.uint8))
+    cache.scales[..., 1] = 1 + torch.rand(n, hkv, device=dev)
+    r2t = torch.randperm(n, device=dev).to(torch.int32)[None].repeat(b, 1)
+    q, out, lse, st = decode(dev, cache, F, hq, hkv, d, [n] * b, r2t, q=torch.zeros(b, hq, d, device=dev))
+    assert st == 0
+    want = cache.values(torch.arange(n, device=dev))[1].mean(0)
+    assert ((out.double() - want).abs() / want).max() < long_sum_tolerance(1600)
+    assert (lse.double() - math.log(n)).abs().max() < 2.0 ** -18 * (1 + math.log(n))
