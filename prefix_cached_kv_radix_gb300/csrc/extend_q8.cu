@@ -166,6 +166,26 @@ __device__ __forceinline__ void eq_locate(const ExtendQ8Params& p, int b, int64_
     j = (int)left;
 }
 
+// pt_wait for what may take an item's time: a Q buffer, the next item, the scores of a Q tile that the items before did without.
+// 2^31 keys, some of every tile at bad slots, take 73 s (4.4 us a tile, 2.3 without), so the bound is 133 s, in the timer's upper
+// word (no more code than pt_wait; a bound by the part's tiles cost short prompts 2 %).  The tensor core's warp and the
+// converters wait for single tiles, 2 s at most, and would end these waits too.
+__device__ __forceinline__ bool eq_wait_item(uint32_t bar, uint32_t parity, volatile int* abort) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        auto now = [] {
+            uint32_t t;
+            asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t));
+            return t;
+        };
+        const uint32_t t0 = now();
+        do ok = mbar_try_wait(bar, parity);
+        while (!ok && !*abort && now() - t0 < 32u);
+        if (!ok) *abort = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -289,10 +309,12 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
+    auto soon = [](uint32_t b, uint32_t parity, volatile int* abort) { return pt_wait(b, parity, abort); };
+    auto late = [](uint32_t b, uint32_t parity, volatile int* abort) { return eq_wait_item(b, parity, abort); };
     // The k-th item of this CTA, for a whole warp; false at the end.  The entry is free once every warp has read it.
-    auto take = [&](int k, EqItem& it) -> bool {
+    auto take = [&](int k, EqItem& it, auto wait) -> bool {
         const int e = k % EQ_RING;
-        if (!pt_wait(bar(LY::BAR_IF + e), (k / EQ_RING) & 1, abort_flag)) return false;
+        if (!wait(bar(LY::BAR_IF + e), (k / EQ_RING) & 1, abort_flag)) return false;
         const int4 a = ring[3 * e], c = ring[3 * e + 1], d = ring[3 * e + 2];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LY::BAR_IE + e));
@@ -343,8 +365,8 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
                     mbar_arrive(bar(LY::BAR_IF + e));
                 }
                 ++k;
-                if (quse0 > 0 && !(ok = pt_wait(bar(LY::BAR_QE), (quse0 - 1) & 1, abort_flag))) break;
-                if (ntiles > 1 && quse1 > 0 && !(ok = pt_wait(bar(LY::BAR_QE + 1), (quse1 - 1) & 1, abort_flag))) break;
+                if (quse0 > 0 && !(ok = eq_wait_item(bar(LY::BAR_QE), (quse0 - 1) & 1, abort_flag))) break;
+                if (ntiles > 1 && quse1 > 0 && !(ok = eq_wait_item(bar(LY::BAR_QE + 1), (quse1 - 1) & 1, abort_flag))) break;
                 quse0 += 1;
                 quse1 += ntiles > 1 ? 1 : 0;
                 // full 128-row tiles by TMA, one box per 64 columns; a ragged one row by row, two lanes a row, the rows
@@ -416,7 +438,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             int gt = 0, ic = 0, sc0 = 0, sc1 = 0;    // K/V tiles, items and score steps of Q tile 0 / 1 so far
             bool ok = true;
             EqItem it;
-            for (int k = 0; ok && take(k, it); ++k) {
+            for (int k = 0; ok && take(k, it, soon); ++k) {
                 const int nt = it.ntiles, nkv = it.j1 - it.j0;
                 ok = pt_wait(bar(LY::BAR_Q), ic & 1, abort_flag) && pt_wait(bar(LY::BAR_KF + gt % NK), (gt / NK) & 1, abort_flag);
                 ic += 1;
@@ -472,7 +494,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             // The tile whose codes are loaded next, and its slots: one tile ahead of the one being stored.
             EqItem it;
             int k = 0, j = 0;
-            bool have = take(0, it);
+            bool have = take(0, it, soon);
             if (have) j = it.j0;
             const int32_t* slots = nullptr;
             const uint8_t *kb = nullptr, *vb = nullptr;
@@ -498,7 +520,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             };
             auto next = [&]() {
                 if (++j == it.j1) {
-                    have = take(++k, it);
+                    have = take(++k, it, soon);
                     if (!have) return;
                     j = it.j0;
                     begin();
@@ -616,7 +638,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             }
             return x;
         };
-        for (int k = 0; ok && take(k, it); ++k) {
+        for (int k = 0; ok && take(k, it, late); ++k) {
             const int nkv = it.j1 - it.j0;
             if (t >= it.ntiles) {
                 gt += nkv;
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(EQ_THREADS, 1) extend_q8_kernel(const __grid_c
             }
             for (int j = 0; j < nkv; ++j, ++gt) {
                 const int vs = gt % NV;
-                if (!(ok = pt_wait(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag))) break;
+                if (!(ok = eq_wait_item(bar(LY::BAR_S + t), (sc + j) & 1, abort_flag))) break;
                 if (!(ok = pt_wait(bar(LY::BAR_VF + vs), (gt / NV) & 1, abort_flag))) break;     // the scales
                 tc_fence_after();
                 const float* kscale = reinterpret_cast<const float*>(gbase + LY::OFF_KS) + vs * EQ_BN + 2 * t4;

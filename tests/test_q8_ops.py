@@ -1313,3 +1313,28 @@ def test_decode_q8_f32_long_sums(dev):
     want = cache.values(torch.arange(n, device=dev))[1].mean(0)
     assert ((out.double() - want).abs() / want).max() < long_sum_tolerance(1600)
     assert (lse.double() - math.log(n)).abs().max() < 2.0 ** -18 * (1 + math.log(n))
+
+
+@gpu
+def test_extend_q8_items_of_seconds(dev):
+    """Items that take longer than any wait between a block's warps for a single tile may (2 s): two of 110 million keys a block, with a
+    bad slot in every tile.  One key outweighs the others by e^100, so every row is that key's value."""
+    hkv, d, rows, keys = 304, 64, 17, 110_000_000
+    desc, q8, slots = desc_of(BF, hkv, hkv, d, 4, scale=1.0), api.q8_desc(INT8), 4
+    k, v = (torch.zeros(slots, hkv, d, dtype=torch.int8, device=dev) for _ in range(2))
+    k[0, :, 0], k[1:, :, 0] = 100, -100
+    v[0] = torch.randint(-127, 128, (hkv, d), device=dev)
+    v[1:] = 127
+    scales = torch.full((slots, hkv, 2), 0.5, device=dev)
+    table = torch.ones(1, keys, dtype=torch.int32, device=dev)
+    table[0, ::128] = -1
+    table[0, keys - rows - 1] = 0
+    q = torch.zeros(rows, hkv, d, dtype=BF, device=dev)
+    q[..., 0] = 1.0
+    out, lse = torch.full_like(q, 9.0), torch.full((rows, hkv), 9.0, device=dev)
+    ws = torch.empty(api.extend_q8_workspace_bytes(desc, 1, rows, keys), dtype=torch.uint8, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    api.prefix_extend_attention_q8(desc, q8, 1, q, i64([0, rows], dev), i32([keys - rows], dev), table, k, v, scales, out, lse, rows, ws, st)
+    assert int(st) == api.RX_DEV_BAD_SLOT
+    assert torch.equal(out.float(), (v[0].float() * 0.5).expand(rows, hkv, d))
+    assert (lse - 50.0).abs().max() < 1e-3
