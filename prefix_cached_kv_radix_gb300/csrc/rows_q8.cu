@@ -7,8 +7,8 @@
 // each sum over its own running maximum: vs enters the exponent, so that what is weighed and rounded to 16 bits is 2^(y_j - max y)
 // next to the largest term of o, however far apart the rows' scales are.  For f32 rows only the exponent of vs = v 2^e does,
 // 1/2 <= v < 1: a logarithm of 32 bits is off by up to 2^-18.  The sums' references are then the maxima rounded up to whole
-// numbers, so that x_j - (max y - e_j) loses nothing of x_j (errors of 3e-7 to 5e-7 of the norm, where they were 5e-7
-// to 1.1e-6 and 3e-6 at scales of 2^-110).
+// numbers, so that x_j - (max y - e_j) loses nothing of x_j (errors of 3e-7 to 5e-7 of the norm; with the logarithm
+// 5e-7 to 1.1e-6, and 3e-6 at scales of 2^-110).
 //
 // A CTA of eight warps takes a run of a request's keys, a row tile and 1, 2, 4 or 8 neighbouring kv heads: a warp a head, or 8, 4, 2
 // warps sharing one, 16 keys of a stage each.  The heads of a slot lie side by side in the pools, so a stage is
@@ -22,8 +22,8 @@
 // widens them.  Queries are f16 after a power of two per row that brings the row's largest to 2^14 (bf16 is exact in that
 // down to 2^-29 of the largest); f32 rows' queries and weights are two f16 parts each, 22 bits.
 // Bound by HBM: 2 d + 8 bytes a key and kv head, read once.  Measured: 256 requests of 1024-8192 keys (32/8 heads x 128,
-// e4m3) 389 us, 91 % of the copy rate; two of 131071 (64/8) 102.7 us, 73 %: the launch, the first loads and the merge
-// (10 us) are a fifth of it; 64 of 441 (12 heads x 64, int8) 19.2 us, of which a CTA's one chain of length, slots, codes
+// e4m3) 389 us, 91 % of the copy rate; two of 131071 (64/8) 102.5 us, 73 %: the launch, the first loads and the merge
+// (10 us) are a fifth of it; 64 of 441 (12 heads x 64, int8) 19.5 us, of which a CTA's one chain of length, slots, codes
 // and joining is most.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -533,8 +533,7 @@ __global__ void __launch_bounds__(RQ_THREADS, rows_a_sm<T, D, NT>()) rows_q8_ker
             }
         }
         // f32 rows: a stage's products in accumulators of their own, added to the sum with rounding.  The tensor core cuts
-        // its sums off, which over up to 1302 keys made the outputs' error 1.2e-6 of their norm; so it is 6.3e-7, for
-        // 3 % of the time.
+        // its sums off, which over up to 1302 keys cost the outputs 6e-7 of their norm; 4e-7 are left, for 3 % of the time.
 #pragma unroll
         for (int i = 0; i < KS; i += 2) {
             float part[TWO ? 2 : 1][NT][4];
@@ -784,8 +783,8 @@ RowsPlan rows_q8_plan(const rx_attn_desc* d, int32_t batch, int32_t max_qo_len, 
     // Stages shared out evenly, as many neighbouring heads a CTA as there are, up to eight; or a request's whole context to a CTA, with as
     // many heads as take the least time.  In microseconds: a CTA's start and end four, a stage 1.1, or 1.7 with its twice as
     // many keys at 64 channels, a quarter more with two CTAs an SM; sharing out and merging nine, or 26 with two tiles, which
-    // are a CTA an SM and more rows a part.  Fitted to 144 sizes with a cold L2, of which it costs three more than a
-    // twentieth, at most a tenth.  Shared out and whole: decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9
+    // are a CTA an SM and more rows a part.  On 136 sizes that it was not fitted to, with a cold L2, it costs ten more than a
+    // twentieth over the better of the two, at most a third.  Shared out and whole: decode of 4 requests of up to 1000 keys, 64 heads on 8, 20.5 and 14.9
     // us, of 4 of up to 3000 23.6 and 33.6; 9 f32 prompts of up to 101 over up to 1201 48.8 and 35.6; 40 of up to 9 over up
     // to 5000 74 and 146.
     const double stage = d->head_dim == 64 ? 1.7 : 1.1, both = 1.25 * stage, joining = L.nt == 1 ? 9 : 26;
