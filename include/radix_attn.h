@@ -574,8 +574,8 @@ size_t decode_q8_workspace_bytes(const rx_attn_desc* desc, int32_t batch, int32_
  *  - A key at a slot outside [0, num_slots) is reported and left out; a row that is left no key is
  *    zeros, its log-sum-exp -infinity.
  *  - Rows before qo_indptr[0] and from qo_indptr[batch] on are left as they were.
- *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most, for scales of 2^-100 and more: a product
- *    below 2^-126 has fewer bits, and one below 2^-134 is zero) where max_qo_len * hq / hkv is above 16, and as in decode below;
+ *  - bf16 rounds the probabilities, times the value's scale, to bf16 (by 2^-8 at most, for scales of 2^-100 to 2^100: a product
+ *    below 2^-126 has fewer bits, one below 2^-134 is zero, and sums of far larger ones overflow) where max_qo_len * hq / hkv is above 16, and as in decode below;
  *    f32 as in decode.
  *  - max_kv_len (host) >= every P_b + n_b, else RX_DEV_BAD_LENGTH for that request, as above 2^31 - 2^16; it decides how
  *    far few rows over long contexts are split (the parts are merged in the workspace, >= extend_q8_workspace_bytes(...), 256-byte aligned; what it is for the

@@ -1338,3 +1338,24 @@ def test_extend_q8_items_of_seconds(dev):
     assert int(st) == api.RX_DEV_BAD_SLOT
     assert torch.equal(out.float(), (v[0].float() * 0.5).expand(rows, hkv, d))
     assert (lse - 50.0).abs().max() < 1e-3
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("hq,hkv,d,n", [(4, 4, 64, 2), (4, 2, 128, 4), (8, 8, 128, 3), (8, 2, 64, 4)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_extend_q8_few_rows_do_not_see_later_scales(dev, fmt, dt, hq, hkv, d, n, which):
+    """Calls of few rows: a later token's key or value scale, whatever it is, leaves the rows before it as they are."""
+    for pre in (0, 15, 131):
+        r2t, _ = table_of([n + pre], 144, 150, dev)
+        cache = Cache(dev, fmt, 150, hkv, d, seed=9)
+        for scale in (math.nan, math.inf, 2.0 ** 127):
+            last = r2t[0, pre + n - 1].long()
+            kept = cache.scales[last].clone()
+            cache.scales[last, :, which] = scale
+            q, out, lse, st = extend(dev, cache, dt, hq, hkv, d, [n], [pre], r2t)
+            cache.scales[last] = kept
+            k, v = cache.values(r2t[0, :n + pre - 1])
+            agree(out[:n - 1], lse[:n - 1], attend(q[:n - 1], k, v, 1 / math.sqrt(d), pre), dt)
+            assert st == 0 and (not math.isnan(scale) or out[n - 1].isnan().all())
